@@ -37,6 +37,8 @@ PA_STAGE_ALL = 7
 
 PA_DEV_TIMEOUT = 1
 PA_DEV_BAD_INDEX = 2
+PA_DEV_NO_PAGES = 4
+PA_DEV_NO_ROOM = 8
 
 DEFAULT_WORKSPACE_BYTES = 128 * 1024 * 1024  # the timing script's workspace size
 
@@ -45,7 +47,8 @@ EXPORTED = ("pagedattn_plan", "pagedattn_workspace_size", "pagedattn_run", "page
             "pagedattn_plan_destroy", "pagedattn_last_error", "pagedattn_device_status",
             "pagedattn_debug_plan_dump", "pagedattn_debug_gather", "pagedattn_version",
             "pagedattn_run_decode_noalloc", "pagedattn_noalloc_device_status", "pagedattn_plan_cascade",
-            "pagedattn_workspace_size_cascade")
+            "pagedattn_workspace_size_cascade", "pagedattn_build_tables", "pagedattn_kv4_append",
+            "pagedattn_kv4_workspace_size", "pagedattn_kv4_run", "pagedattn_status_word")
 
 
 class PagedAttnError(RuntimeError):
@@ -65,6 +68,43 @@ class Options(ctypes.Structure):
 _I32P = ctypes.POINTER(ctypes.c_int32)
 _lib = None
 _lock = threading.Lock()
+
+
+class TablesIn(ctypes.Structure):
+    """pagedattn_tables_in"""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("qo_lens", "kv_lens", "block_table", "free_pages", "free_count")] + \
+        [("block_table_stride", ctypes.c_int64)] + \
+        [(n, ctypes.c_int32) for n in ("block_table_width", "free_capacity", "batch_size", "page_size", "num_pages")]
+
+
+class TablesOut(ctypes.Structure):
+    """pagedattn_tables_out"""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("qo_indptr", "kv_page_indptr", "new_page_indptr", "kv_page_indices",
+                                               "kv_last_page_len", "kv_lens", "slot_mapping", "positions",
+                                               "free_count", "status")] + \
+        [(n, ctypes.c_int32) for n in ("max_tokens", "max_pages")]
+
+
+class Kv4CacheArgs(ctypes.Structure):
+    """pagedattn_kv4_cache"""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)] + \
+        [(n, ctypes.c_int32) for n in ("num_pages", "page_size", "num_kv_heads", "head_dim", "kv_layout")] + \
+        [("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+class Kv4Rows(ctypes.Structure):
+    """pagedattn_kv4_rows"""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("k_values", ctypes.c_void_p), ("v_values", ctypes.c_void_p),
+                ("slot_mapping", ctypes.c_void_p), ("status", ctypes.c_void_p), ("num_tokens", ctypes.c_int32),
+                ("dtype", ctypes.c_int)]
+
+
+class Kv4Batch(ctypes.Structure):
+    """pagedattn_kv4_batch"""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("qo_indptr", "kv_page_indptr", "kv_page_indices", "kv_last_page_len")] + \
+        [(n, ctypes.c_int32) for n in ("batch_size", "num_page_indices", "num_tokens", "max_qo_len", "num_qo_heads",
+                                       "causal")] + [("dtype", ctypes.c_int)]
 
 
 class PrefixGroups(ctypes.Structure):
@@ -126,6 +166,18 @@ def load() -> ctypes.CDLL:
         lib.pagedattn_run_decode_noalloc.restype = ctypes.c_int
         lib.pagedattn_noalloc_device_status.argtypes = [ctypes.c_void_p, _I32P]
         lib.pagedattn_noalloc_device_status.restype = ctypes.c_int
+        lib.pagedattn_build_tables.argtypes = [ctypes.POINTER(TablesIn), ctypes.POINTER(TablesOut), ctypes.c_void_p]
+        lib.pagedattn_build_tables.restype = ctypes.c_int
+        lib.pagedattn_kv4_append.argtypes = [ctypes.POINTER(Kv4CacheArgs), ctypes.POINTER(Kv4Rows), ctypes.c_void_p]
+        lib.pagedattn_kv4_append.restype = ctypes.c_int
+        lib.pagedattn_kv4_workspace_size.argtypes = [ctypes.c_int32] * 4 + [ctypes.POINTER(ctypes.c_size_t)]
+        lib.pagedattn_kv4_workspace_size.restype = ctypes.c_int
+        lib.pagedattn_kv4_run.argtypes = [ctypes.POINTER(Kv4CacheArgs), ctypes.POINTER(Kv4Batch), ctypes.c_void_p,
+                                          ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                          ctypes.c_size_t, ctypes.c_void_p]
+        lib.pagedattn_kv4_run.restype = ctypes.c_int
+        lib.pagedattn_status_word.argtypes = [ctypes.c_void_p, ctypes.c_void_p, _I32P]
+        lib.pagedattn_status_word.restype = ctypes.c_int
         lib.pagedattn_version.argtypes = []
         lib.pagedattn_version.restype = ctypes.c_char_p
         _lib = lib

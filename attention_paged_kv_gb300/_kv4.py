@@ -1,0 +1,303 @@
+"""Binding of the device-built tables and the 4-bit cache (include/pagedattn.h).
+
+A step of a serving loop, with no length on the host:
+
+    tables = BatchTables(batch_size, max_tokens, max_pages, page_size, num_pages)
+    cache = Kv4Cache(num_pages, page_size, num_kv_heads, head_dim)
+    attention = Kv4Attention(batch_size, max_tokens, num_qo_heads, num_kv_heads, head_dim, page_size, dtype)
+
+    tables.build(qo_lens, kv_lens, block_table, free_pages, free_count)
+    cache.append(k, v, tables.slot_mapping)
+    out, lse = attention.run(q, cache, tables)
+
+All three calls only launch kernels, so the step can be captured into a CUDA
+graph; `tables.build(qo_lens, tables.kv_lens, block_table, free_pages,
+tables.free_count)` then advances the lengths in place at each replay.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import _binding as _b
+from ._binding import PA_ERR_INVALID_ARG, PagedAttnError
+
+
+def _refuse(msg):
+    raise PagedAttnError(PA_ERR_INVALID_ARG, msg)
+
+
+def _is(t, name, dtype, shape, device):
+    """A contiguous tensor of this type and shape on this device, or an error."""
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+        _refuse(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on {device}")
+
+
+def _rows(t, name, shape, device):
+    """Tokens of contiguous [heads, head_dim] blocks at any stride; returns the stride."""
+    if tuple(t.shape) != shape or t.device != device:
+        _refuse(f"{name} must be of shape {list(shape)} on {device}")
+    n, h, d = shape
+    if t.stride(2) != 1 or (h > 1 and t.stride(1) != d):
+        _refuse(f"{name}: each token's [heads, head_dim] block must be contiguous")
+    return t.stride(0) if n > 1 else h * d
+
+
+class _On:
+    """The device's and the stream's context of one call.
+
+    Without a stream the device's current one is used.  With another one, the
+    tensors of the call are recorded on it, so that their memory is not given
+    away before it has passed the call.
+    """
+
+    def __init__(self, device, stream, tensors):
+        import torch
+        self._guard = None
+        current = torch.cuda.current_stream(device)
+        if stream is None:
+            stream = current
+        handle = int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+        if handle != current.cuda_stream:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(handle, device=device)
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
+            self._guard = torch.cuda.stream(stream)  # sets the device too
+        elif torch.cuda.current_device() != device.index:
+            self._guard = torch.cuda.device(device)
+        self.handle = handle
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+def _device(device):
+    import torch
+    device = torch.device("cuda") if device is None else torch.device(device)
+    if device.type != "cuda":
+        _refuse(f"device must be a CUDA device, not {device}")
+    return torch.device("cuda", torch.cuda.current_device() if device.index is None else device.index)
+
+
+def _status(word, stream):
+    with _On(word.device, stream, (word,)) as st:
+        flags = ctypes.c_int32(0)
+        rc = _b.load().pagedattn_status_word(word.data_ptr(), st, ctypes.byref(flags))
+    if rc not in (_b.PA_OK, _b.PA_ERR_TIMEOUT, _b.PA_ERR_DEVICE_CHECK):
+        _b.check(rc)
+    return int(flags.value)
+
+
+class BatchTables:
+    """Page tables, slot maps and positions of a step, built on the device.
+
+    Holds the outputs, all on the device: ``qo_indptr``, ``kv_page_indptr``,
+    ``new_page_indptr`` [batch_size + 1]; ``kv_page_indices`` [max_pages];
+    ``kv_last_page_len``, ``kv_lens`` [batch_size]; ``slot_mapping`` (int64),
+    ``positions`` [max_tokens]; ``free_count`` [1].
+    """
+
+    def __init__(self, batch_size, max_tokens, max_pages, page_size, num_pages, device=None):
+        import torch
+        self.batch_size, self.max_tokens, self.max_pages = int(batch_size), int(max_tokens), int(max_pages)
+        self.page_size, self.num_pages = int(page_size), int(num_pages)
+        if min(self.batch_size, self.max_tokens, self.max_pages) < 0:
+            _refuse("batch_size, max_tokens and max_pages must not be negative")
+        self.device = _device(device)
+        i32 = dict(dtype=torch.int32, device=self.device)
+        self.qo_indptr = torch.zeros(self.batch_size + 1, **i32)
+        self.kv_page_indptr = torch.zeros(self.batch_size + 1, **i32)
+        self.new_page_indptr = torch.zeros(self.batch_size + 1, **i32)
+        self.kv_page_indices = torch.full((self.max_pages,), -1, **i32)
+        self.kv_last_page_len = torch.zeros(self.batch_size, **i32)
+        self.kv_lens = torch.zeros(self.batch_size, **i32)
+        self.slot_mapping = torch.full((self.max_tokens,), -1, dtype=torch.int64, device=self.device)
+        self.positions = torch.zeros(self.max_tokens, **i32)
+        self.free_count = torch.zeros(1, **i32)
+        self.status = torch.zeros(1, **i32)
+        self._out = _b.TablesOut(*(getattr(self, n).data_ptr() for n, t in _b.TablesOut._fields_
+                                   if t is ctypes.c_void_p), self.max_tokens, self.max_pages)
+
+    def build(self, qo_lens, kv_lens, block_table, free_pages, free_count, stream=None):
+        """Builds the tables of a step; see pagedattn_build_tables.
+
+        qo_lens, kv_lens: int32 [batch_size]; block_table: int32 [batch_size,
+        width], rows contiguous; free_pages: int32, a stack of page ids whose
+        top is free_pages[free_count - 1]; free_count: int32 [1].  kv_lens may
+        be ``self.kv_lens`` and free_count ``self.free_count``: the step then
+        advances them in place.
+        """
+        import torch
+        i32, B, dev = torch.int32, self.batch_size, self.device
+        _is(qo_lens, "qo_lens", i32, (B,), dev)
+        _is(kv_lens, "kv_lens", i32, (B,), dev)
+        _is(free_count, "free_count", i32, (1,), dev)
+        _is(free_pages, "free_pages", i32, (free_pages.numel(),), dev)
+        if block_table.dtype != i32 or block_table.dim() != 2 or block_table.shape[0] != B or block_table.device != dev:
+            _refuse(f"block_table must be an int32 tensor of shape [{B}, width] on {dev}")
+        width = block_table.shape[1]
+        if width > 1 and block_table.stride(1) != 1:
+            _refuse("block_table: each row must be contiguous")
+        stride = block_table.stride(0) if B > 1 else width
+        a = _b.TablesIn(qo_lens.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(),
+                        free_count.data_ptr(), stride, width, free_pages.numel(), B, self.page_size, self.num_pages)
+        with _On(dev, stream, (qo_lens, kv_lens, block_table, free_pages, free_count)) as st:
+            _b.check(_b.load().pagedattn_build_tables(ctypes.byref(a), ctypes.byref(self._out), st))
+        return self
+
+    def device_status(self, stream=None) -> int:
+        """Waits for the stream; the PA_DEV_* bits since the last read, which clears them."""
+        return _status(self.status, stream)
+
+
+class Kv4Cache:
+    """A paged KV cache in 4 bits: e2m1 codes with an e4m3 scale for each 16 values along head_dim.
+
+    ``codes`` uint8 [num_pages, 2, page_size, num_kv_heads, head_dim / 2] and
+    ``scales`` uint8 [..., head_dim / 16] ("NHD"; "HND" exchanges page_size
+    and num_kv_heads); pass them to take over existing memory.  A value is
+    code * scale * k_scale (or v_scale).
+    """
+
+    def __init__(self, num_pages, page_size, num_kv_heads, head_dim, kv_layout="NHD", k_scale=1.0, v_scale=1.0,
+                 codes=None, scales=None, device=None):
+        import torch
+        self.num_pages, self.page_size = int(num_pages), int(page_size)
+        self.num_kv_heads, self.head_dim = int(num_kv_heads), int(head_dim)
+        self.kv_layout = _b.layout_code(kv_layout)
+        self.k_scale, self.v_scale = float(k_scale), float(v_scale)
+        mid = (self.num_kv_heads, self.page_size) if self.kv_layout == _b.PA_LAYOUT_HND else \
+            (self.page_size, self.num_kv_heads)
+        if min(self.num_pages, self.page_size, self.num_kv_heads) < 1 or self.head_dim not in (64, 128, 256):
+            _refuse("num_pages, page_size and num_kv_heads must be positive, head_dim 64, 128 or 256")
+        if device is None and codes is not None:
+            device = codes.device
+        self.device = _device(device)
+        for name, given, last in (("codes", codes, self.head_dim // 2), ("scales", scales, self.head_dim // 16)):
+            shape = (self.num_pages, 2, *mid, last)
+            if given is None:
+                given = torch.zeros(shape, dtype=torch.uint8, device=self.device)
+            _is(given, name, torch.uint8, shape, self.device)
+            setattr(self, name, given)
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._args = _b.Kv4CacheArgs(self.codes.data_ptr(), self.scales.data_ptr(), self.num_pages, self.page_size,
+                                     self.num_kv_heads, self.head_dim, self.kv_layout, self.k_scale, self.v_scale)
+
+    def append(self, k, v, slot_mapping, k_values=None, v_values=None, stream=None):
+        """Quantises the rows k, v [n, num_kv_heads, head_dim] into the slots of slot_mapping (int64 [n]).
+
+        Rows with a negative slot are skipped; the others' slots must be
+        distinct.  k and v may have any token stride that is a multiple of 8.
+        k_values, v_values (contiguous, of k's shape and type) receive the rows
+        as later reads see them.  See pagedattn_kv4_append.
+        """
+        import torch
+        dev, n = self.device, slot_mapping.shape[0] if slot_mapping.dim() else 0
+        shape = (n, self.num_kv_heads, self.head_dim)
+        ks, vs = _rows(k, "k", shape, dev), _rows(v, "v", shape, dev)
+        if v.dtype != k.dtype:
+            _refuse("k and v must be of one type")
+        _is(slot_mapping, "slot_mapping", torch.int64, (n,), dev)
+        for name, t in (("k_values", k_values), ("v_values", v_values)):
+            if t is not None:
+                _is(t, name, k.dtype, shape, dev)
+        a = _b.Kv4Rows(k.data_ptr(), v.data_ptr(), ks, vs, k_values.data_ptr() if k_values is not None else None,
+                       v_values.data_ptr() if v_values is not None else None, slot_mapping.data_ptr(),
+                       self.status.data_ptr(), n, _b.dtype_code(k.dtype))
+        with _On(dev, stream, (k, v, slot_mapping, k_values, v_values)) as st:
+            _b.check(_b.load().pagedattn_kv4_append(ctypes.byref(self._args), ctypes.byref(a), st))
+
+    def device_status(self, stream=None) -> int:
+        """Waits for the stream; the PA_DEV_* bits since the last read, which clears them."""
+        return _status(self.status, stream)
+
+
+class Kv4Attention:
+    """Attention over a Kv4Cache, through tables in device memory.
+
+    num_tokens: rows of q; max_qo_len: a bound of the requests' query lengths
+    (default num_tokens), by which the kernels are chosen: pass 1 for decode
+    steps.  Holds the workspace, so two runs that overlap on the device need
+    two objects.
+    """
+
+    def __init__(self, batch_size, num_tokens, num_qo_heads, num_kv_heads, head_dim, page_size, dtype, causal=True,
+                 max_qo_len=None, workspace=None, device=None):
+        import torch
+        self.batch_size, self.num_tokens = int(batch_size), int(num_tokens)
+        self.num_qo_heads, self.num_kv_heads = int(num_qo_heads), int(num_kv_heads)
+        self.head_dim, self.page_size = int(head_dim), int(page_size)
+        self.dtype_code, self.causal = _b.dtype_code(dtype), bool(causal)
+        self.max_qo_len = self.num_tokens if max_qo_len is None else int(max_qo_len)
+        if device is None and workspace is not None:
+            device = workspace.device
+        self.device = _device(device)
+        need = ctypes.c_size_t(0)
+        with torch.cuda.device(self.device):
+            _b.check(_b.load().pagedattn_kv4_workspace_size(self.num_qo_heads, self.num_kv_heads, self.head_dim,
+                                                            self.max_qo_len, ctypes.byref(need)))
+            if workspace is None:
+                workspace = torch.empty(need.value, dtype=torch.uint8, device=self.device)
+            if workspace.device != self.device or not workspace.is_contiguous():
+                _refuse(f"workspace must be a contiguous tensor on {self.device}")
+            self.workspace = workspace
+            self._ws_bytes = workspace.numel() * workspace.element_size()
+            if self._ws_bytes < need.value:
+                raise PagedAttnError(_b.PA_ERR_WORKSPACE_TOO_SMALL,
+                                     f"workspace needs {need.value} bytes, got {self._ws_bytes}")
+            self.status = workspace.view(-1).view(torch.uint8)[:4].view(torch.int32)
+            self.status.zero_()
+
+    def run(self, q, cache, tables, out=None, lse=None, return_lse=True, stream=None):
+        """out, lse of q [num_tokens, num_qo_heads, head_dim] (any token stride that is a multiple of 8).
+
+        tables: a BatchTables, or (qo_indptr, kv_page_indptr, kv_page_indices,
+        kv_last_page_len) as int32 device tensors.  See pagedattn_kv4_run.
+        """
+        import torch
+        dev, B, T = self.device, self.batch_size, self.num_tokens
+        shape = (T, self.num_qo_heads, self.head_dim)
+        stride = _rows(q, "q", shape, dev)
+        if _b.dtype_code(q.dtype) != self.dtype_code:
+            _refuse("q's dtype differs from the object's")
+        if cache.device != dev or (cache.num_kv_heads, cache.head_dim, cache.page_size) != \
+                (self.num_kv_heads, self.head_dim, self.page_size):
+            _refuse("the cache's heads, head_dim, page_size or device differ from the object's")
+        if isinstance(tables, BatchTables):
+            if tables.batch_size != B or tables.page_size != self.page_size or tables.device != dev:
+                _refuse("the tables' batch, page_size or device differ from the object's")
+            tables = (tables.qo_indptr, tables.kv_page_indptr, tables.kv_page_indices, tables.kv_last_page_len)
+        else:
+            i32 = torch.int32
+            qo_indptr, page_indptr, pages, last = tables
+            _is(qo_indptr, "qo_indptr", i32, (B + 1,), dev)
+            _is(page_indptr, "kv_page_indptr", i32, (B + 1,), dev)
+            _is(pages, "kv_page_indices", i32, (pages.numel(),), dev)
+            _is(last, "kv_last_page_len", i32, (B,), dev)
+        qo_indptr, page_indptr, pages, last = tables
+        with _On(dev, stream, (q, out, lse, *tables)) as st:
+            if out is None:
+                out = torch.empty(shape, dtype=q.dtype, device=dev)
+            else:
+                _is(out, "out", q.dtype, shape, dev)
+            if lse is not None:
+                _is(lse, "lse", torch.float32, shape[:2], dev)
+            elif return_lse:
+                lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
+            a = _b.Kv4Batch(qo_indptr.data_ptr(), page_indptr.data_ptr(), pages.data_ptr(), last.data_ptr(), B,
+                            pages.numel(), T, self.max_qo_len, self.num_qo_heads, int(self.causal), self.dtype_code)
+            _b.check(_b.load().pagedattn_kv4_run(ctypes.byref(cache._args), ctypes.byref(a), q.data_ptr(), stride,
+                                                 out.data_ptr(), lse.data_ptr() if lse is not None else None,
+                                                 self.workspace.data_ptr(), self._ws_bytes, st))
+        return out, lse
+
+    def device_status(self, stream=None) -> int:
+        """Waits for the stream; the PA_DEV_* bits since the last read, which clears them."""
+        return _status(self.status, stream)

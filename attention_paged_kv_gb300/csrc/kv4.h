@@ -1,0 +1,103 @@
+// Host-side internals of the device-built tables and the 4-bit cache:
+// kernel parameters and launchers.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "../../include/pagedattn.h"
+
+namespace pa {
+
+// ---------------------------------------------------------------------------
+// tables.cu
+
+struct TablesParams {
+  const int32_t* qo_lens;     // [batch]
+  const int32_t* kv_lens;     // [batch], before this step's tokens
+  int32_t* block_table;       // [batch, table_width]
+  const int32_t* free_pages;  // [free_capacity], the top of the stack at free_count - 1
+  const int32_t* free_count;
+  int32_t *qo_indptr, *kv_page_indptr, *new_page_indptr;      // [batch + 1]
+  int32_t *kv_page_indices, *kv_last_page_len, *kv_lens_out;  // [max_pages], [batch], [batch]
+  int64_t* slot_mapping;                                      // [max_tokens]
+  int32_t* positions;                                         // [max_tokens]
+  int32_t* free_count_out;
+  int32_t* status;
+  int64_t table_stride;
+  int32_t table_width, free_capacity, batch, ps, ps_shift, num_pages, max_tokens, max_pages;
+};
+
+// The longest list (tokens or pages) that the scan's one CTA fills itself.
+constexpr int kTablesOneLaunch = 4096;
+
+cudaError_t launch_tables(const TablesParams& p, int num_sms, cudaStream_t stream);
+
+// ---------------------------------------------------------------------------
+// kv4_append.cu
+
+// Offsets of a 4-bit cache's rows.  A row is (page, half, slot, kv head):
+// half 0 = K, 1 = V.  In units of rows:
+//   ((page * 2 + half) * ps * Hkv) + slot * slot_rows + head * head_rows
+struct Kv4Geom {
+  int32_t Hkv, ps, ps_shift, num_pages;
+  int32_t slot_rows, head_rows;  // NHD: Hkv, 1; HND: 1, ps
+};
+
+struct Kv4AppendParams {
+  uint8_t *codes, *scales;
+  const void *k, *v;
+  void *k_values, *v_values;  // nullptr: not wanted
+  const int64_t* slots;
+  int32_t* status;
+  int64_t k_stride, v_stride;  // elements between tokens
+  Kv4Geom g;
+  float k_scale, v_scale;
+  int32_t n;  // tokens
+};
+
+cudaError_t launch_kv4_append(const Kv4AppendParams& p, int D, int dtype, int num_sms, cudaStream_t stream);
+
+// ---------------------------------------------------------------------------
+// kv4_attn.cu
+
+// One split (request, row tile) as the merge needs it, at the first unit of
+// the slice that begins inside it.
+struct Kv4Split {
+  int32_t valid, qo_row0, rows, row_tile;  // first q row (token) of the request, its packed rows, row tile
+  int64_t u0, u1, per_slice;               // units of the row tile, units of a slice
+};
+
+struct Kv4Params {
+  const void* q;
+  void* out;
+  float* lse;
+  const uint8_t *codes, *scales;
+  const int32_t *qo_indptr, *page_indptr, *pages, *last_page_len;
+  int32_t* status;
+  Kv4Split* splits;  // [slices], then the partial states below
+  float* part_o;     // [slices * Hkv * 2][rows of a tile][D], each normalised
+  float* part_lse;   // [slices * Hkv * 2][rows of a tile], base-2, v_scale not in it
+  int64_t q_stride;  // elements between tokens
+  Kv4Geom g;
+  int32_t batch, num_tokens, num_page_indices, Hq, G, causal, slices;
+  int32_t small_rows;  // requests of more packed rows are the prefill kernel's
+  float scale_log2;    // log2(e) / sqrt(D) * k_scale
+  float v_scale;
+};
+
+struct Kv4Shape {  // what the launch and its workspace depend on
+  int32_t D, Hkv, G, num_sms, max_rows;  // max_rows: packed rows of the longest request
+};
+
+// Bytes of a run's workspace, and where its parts lie in it.
+struct Kv4Layout {
+  int32_t slices;
+  size_t off_splits, off_part_o, off_part_lse, total;
+};
+Kv4Layout kv4_layout(const Kv4Shape& s);
+
+cudaError_t launch_kv4_attention(const Kv4Params& p, const Kv4Shape& s, int dtype, cudaStream_t stream);
+
+}  // namespace pa

@@ -120,6 +120,8 @@ typedef struct {
 /* Status bits the kernels OR into the device status word. */
 #define PA_DEV_TIMEOUT 1
 #define PA_DEV_BAD_INDEX 2
+#define PA_DEV_NO_PAGES 4 /* build_tables: the free stack holds too few pages            */
+#define PA_DEV_NO_ROOM 8  /* build_tables: block_table_width, max_tokens or max_pages     */
 
 /*
  * Build the work partition for one batch ("auxiliary data structures" that
@@ -341,6 +343,173 @@ PAGEDATTN_API pagedattn_status pagedattn_run_decode_noalloc(pagedattn_plan_t pla
  * nothing; the next no-alloc call clears the word.
  */
 PAGEDATTN_API pagedattn_status pagedattn_noalloc_device_status(pagedattn_stream_t stream, int32_t* flags);
+
+/* ------------------------------------------------------------------------
+ * A decode step without the host: page tables built on the device, a cache
+ * held in 4 bits, and attention over it.
+ *
+ * The entries below keep every length on the device, so that a whole step
+ * (tables, append, attention) can be captured into one CUDA graph and
+ * replayed while the requests grow.  All are asynchronous on `stream`,
+ * allocate nothing and keep nothing between calls but what is documented;
+ * pointers belong to the current device.  Two calls may overlap on the
+ * device unless one writes what the other uses (outputs, cache rows, or the
+ * workspace of pagedattn_kv4_run).
+ *
+ * Kernels OR PA_DEV_* bits into a status word in device memory that the
+ * caller zeroes once and reads with pagedattn_status_word.
+ */
+
+/* Inputs of pagedattn_build_tables.  All arrays are device memory. */
+typedef struct {
+  const int32_t* qo_lens;     /* [batch_size] tokens that each request appends, >= 0     */
+  const int32_t* kv_lens;     /* [batch_size] tokens that it has cached already, >= 0    */
+  int32_t* block_table;       /* [batch_size][block_table_width] page ids, row b's first
+                                 ceil(kv_lens[b] / page_size) held already; this step's
+                                 new pages are entered behind them                       */
+  const int32_t* free_pages;  /* [free_capacity] a stack of free page ids: the first
+                                 *free_count are free and the top is the last of them    */
+  const int32_t* free_count;  /* [1]                                                     */
+  int64_t block_table_stride; /* entries between rows, >= block_table_width              */
+  int32_t block_table_width, free_capacity, batch_size;
+  int32_t page_size;          /* a power of two in [1, 128]                              */
+  int32_t num_pages;          /* page ids lie in [0, num_pages)                          */
+} pagedattn_tables_in;
+
+/* Outputs of pagedattn_build_tables.  All arrays are device memory. */
+typedef struct {
+  int32_t* qo_indptr;        /* [batch_size + 1] exclusive sums of qo_lens               */
+  int32_t* kv_page_indptr;   /* [batch_size + 1] exclusive sums of the pages, new ones
+                                included                                                 */
+  int32_t* new_page_indptr;  /* [batch_size + 1] exclusive sums of the pages taken       */
+  int32_t* kv_page_indices;  /* [max_pages] the requests' pages one after the other;
+                                entries from kv_page_indptr[batch_size] on are left      */
+  int32_t* kv_last_page_len; /* [batch_size] slots of the last page, 0 without pages     */
+  int32_t* kv_lens;          /* [batch_size] kv_lens + qo_lens; may be the input array   */
+  int64_t* slot_mapping;     /* [max_tokens] page * page_size + slot of each new token,
+                                request after request; -1 from qo_indptr[batch_size] on  */
+  int32_t* positions;        /* [max_tokens] its position in its request; 0 from there on */
+  int32_t* free_count;       /* [1] pages left on the stack; may be the input array      */
+  int32_t* status;           /* [1] status word                                          */
+  int32_t max_tokens, max_pages;
+} pagedattn_tables_out;
+
+/*
+ * The tables of one step from its requests' lengths.  Request b needs
+ * ceil((kv_lens[b] + qo_lens[b]) / page_size) pages; those it lacks come off
+ * the top of the free stack in request order (the n-th page taken by the
+ * whole batch is free_pages[*free_count - 1 - n]).  Requests of no tokens
+ * and no pages are allowed.  The outputs are what pagedattn_plan takes (after
+ * a copy to the host) and what pagedattn_kv4_append and pagedattn_kv4_run
+ * read in place.
+ *
+ * All or nothing: where a length is negative or their sum passes 2^31 - 1
+ * (PA_DEV_BAD_INDEX), the stack is short (PA_DEV_NO_PAGES), or a row of the
+ * block table, max_tokens or max_pages is (PA_DEV_NO_ROOM), the outputs are
+ * those of an empty batch (indptr all 0, slot_mapping all -1, kv_lens and
+ * free_count as they were) and the block table is left alone.  A page id
+ * outside [0, num_pages) raises PA_DEV_BAD_INDEX and its tokens get slot -1.
+ */
+PAGEDATTN_API pagedattn_status pagedattn_build_tables(const pagedattn_tables_in* in, const pagedattn_tables_out* out,
+                                        pagedattn_stream_t stream);
+
+/*
+ * A paged cache of 4-bit keys and values: e2m1 codes, two to a byte (the even
+ * element of head_dim in the low four bits), and an e4m3 scale for each 16
+ * elements along head_dim.  A value is code * scale * k_scale (or v_scale).
+ *   NHD  codes [num_pages][2][page_size][num_kv_heads][head_dim / 2]
+ *        scales[num_pages][2][page_size][num_kv_heads][head_dim / 16]
+ *   HND  the same with page_size and num_kv_heads exchanged
+ * Both device memory, 16-byte aligned.  Memory of slots that were never
+ * written may hold anything.
+ */
+typedef struct {
+  void* codes;
+  void* scales;
+  int32_t num_pages, page_size, num_kv_heads;
+  int32_t head_dim;  /* 64, 128 or 256                       */
+  int32_t kv_layout; /* PA_LAYOUT_NHD or PA_LAYOUT_HND       */
+  float k_scale, v_scale;  /* in [1e-30, 1e30]               */
+} pagedattn_kv4_cache;
+
+/* Rows for pagedattn_kv4_append. */
+typedef struct {
+  const void* k;               /* device, dtype[num_tokens][num_kv_heads][head_dim], tokens
+                                  k_stride elements apart (slices of a fused projection's
+                                  output), 16-byte aligned                                  */
+  const void* v;
+  int64_t k_stride, v_stride;  /* multiples of 8                                            */
+  void* k_values;              /* NULL, or device, dtype[num_tokens][num_kv_heads][head_dim]
+                                  contiguous: the rows as later reads see them             */
+  void* v_values;
+  const int64_t* slot_mapping; /* device, [num_tokens] page * page_size + slot; a row with a
+                                  negative slot is skipped                                  */
+  int32_t* status;             /* device, status word                                       */
+  int32_t num_tokens;
+  pagedattn_dtype dtype;
+} pagedattn_kv4_rows;
+
+/*
+ * Quantise rows into the cache.  Per block of 16 elements, with g the cache's
+ * scale of K or V, each step rounded to nearest even: scale = e4m3(amax / (6 g)),
+ * at most 448; code = e2m1(x / (scale * g)), beyond 6 to 6, and 0 where the
+ * scale is 0.  A block with a NaN reads back as NaN; an infinity becomes the
+ * block's largest value.  Slots at num_pages * page_size or beyond are skipped
+ * and raise PA_DEV_BAD_INDEX.  The non-negative slots of one call must be
+ * distinct: two rows for one slot may leave a mixture of both there.
+ */
+PAGEDATTN_API pagedattn_status pagedattn_kv4_append(const pagedattn_kv4_cache* cache, const pagedattn_kv4_rows* rows,
+                                      pagedattn_stream_t stream);
+
+/* The batch that pagedattn_kv4_run attends for.  Arrays are device memory. */
+typedef struct {
+  const int32_t* qo_indptr;        /* [batch_size + 1]                                    */
+  const int32_t* kv_page_indptr;   /* [batch_size + 1]                                    */
+  const int32_t* kv_page_indices;  /* [num_page_indices]                                  */
+  const int32_t* kv_last_page_len; /* [batch_size]                                        */
+  int32_t batch_size, num_page_indices;
+  int32_t num_tokens;              /* rows of q, out and lse, >= qo_indptr[batch_size]    */
+  int32_t max_qo_len;              /* bound of the requests' query lengths: chooses the
+                                      kernels (a longer request is computed too, slower)  */
+  int32_t num_qo_heads, causal;
+  pagedattn_dtype dtype;           /* of q and out                                        */
+} pagedattn_kv4_batch;
+
+/* Bytes of workspace that pagedattn_kv4_run needs on the current device. */
+PAGEDATTN_API pagedattn_status pagedattn_kv4_workspace_size(int32_t num_qo_heads, int32_t num_kv_heads,
+                                              int32_t head_dim, int32_t max_qo_len, size_t* bytes);
+
+/*
+ * Attention as pagedattn_run computes it (see the top of this file), over a
+ * 4-bit cache and with the batch's tables in device memory.  Any group size
+ * num_qo_heads / num_kv_heads up to 128; any lengths.  A row that sees no key
+ * (kv_len 0, or causal with qo_len > kv_len) gets zeros and lse = -inf.  Rows
+ * of q from qo_indptr[batch_size] on are not read, and rows of out and lse
+ * not written.
+ *
+ * q         device, dtype[num_tokens][num_qo_heads][head_dim], tokens q_stride
+ *           elements apart (a multiple of 8), 16-byte aligned.
+ * out       device, dtype[num_tokens][num_qo_heads][head_dim], 16-byte aligned.
+ * lse       device, float[num_tokens][num_qo_heads], or NULL.
+ * workspace device, 256-byte aligned, pagedattn_kv4_workspace_size() bytes.  Its
+ *           first word is the status word: zero it once.  Calls that overlap on
+ *           the device need different workspaces.
+ *
+ * A table entry that cannot be (indptr out of order or out of range, a last
+ * page length outside [1, page_size]) leaves its request's rows unwritten, a
+ * page id outside [0, num_pages) is read as page 0; both raise
+ * PA_DEV_BAD_INDEX.
+ */
+PAGEDATTN_API pagedattn_status pagedattn_kv4_run(const pagedattn_kv4_cache* cache, const pagedattn_kv4_batch* batch,
+                                   const void* q, int64_t q_stride, void* out, float* lse, void* workspace,
+                                   size_t workspace_bytes, pagedattn_stream_t stream);
+
+/*
+ * Wait for `stream`, read the status word *word (device memory) into *flags
+ * and clear it.  Returns PA_ERR_TIMEOUT / PA_ERR_DEVICE_CHECK when a bit is
+ * set, PA_OK otherwise.
+ */
+PAGEDATTN_API pagedattn_status pagedattn_status_word(int32_t* word, pagedattn_stream_t stream, int32_t* flags);
 
 /* Library version as "major.minor.patch". */
 PAGEDATTN_API const char* pagedattn_version(void);

@@ -14,6 +14,8 @@ Modules:
   (page, slot) walk of the page table.
 * ``oracle.plan_ref``  -- a restatement of the planner's partition rules that
   produces the plan metadata bit for bit.
+* ``oracle.kv4``       -- the device-built tables, the 4-bit cache's format and
+  the attention over it.
 
 Parity status: every function here is pinned by ``tests/test_oracle_*.py``
 (closed forms, a library special case, invariants, brute force and planted
