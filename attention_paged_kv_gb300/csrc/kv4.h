@@ -98,6 +98,10 @@ struct Kv4Layout {
 };
 Kv4Layout kv4_layout(const Kv4Shape& s);
 
+// Requests of more packed rows than this go to the tensor-core kernel.
+constexpr int kKv4SmallRows = 32;
+
+cudaError_t launch_kv4_prefill(const Kv4Params& p, const Kv4Shape& s, int dtype, cudaStream_t stream);
 cudaError_t launch_kv4_attention(const Kv4Params& p, const Kv4Shape& s, int dtype, cudaStream_t stream);
 
 }  // namespace pa

@@ -254,10 +254,16 @@ pagedattn_status pagedattn_kv4_run(const pagedattn_kv4_cache* cache, const paged
   p.G = shape.G;
   p.causal = batch->causal ? 1 : 0;
   p.slices = lay.slices;
-  p.small_rows = 0x7FFFFFFF;
+  // the bound alone decides whether the tensor-core kernel is launched; where
+  // it is not, the small-query kernel takes every request
+  const bool prefill = shape.max_rows > pa::kKv4SmallRows;
+  p.small_rows = prefill ? pa::kKv4SmallRows : 0x7FFFFFFF;
   p.scale_log2 = float(1.4426950408889634 / std::sqrt(double(cache->head_dim)) * double(cache->k_scale));
   p.v_scale = cache->v_scale;
-  cudaError_t e = pa::launch_kv4_attention(p, shape, batch->dtype, reinterpret_cast<cudaStream_t>(stream));
+  cudaError_t e = cudaSuccess;
+  if (prefill) e = pa::launch_kv4_prefill(p, shape, batch->dtype, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_err(e, "4-bit prefill launch");
+  e = pa::launch_kv4_attention(p, shape, batch->dtype, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_err(e, "4-bit attention launch");
   return PA_OK;
 }

@@ -35,12 +35,10 @@
 //        fragment's (key, key + 1) pair.
 // So the cache goes from global memory to registers and into the MMA without
 // shared memory.
-#include <climits>
 #include <cstring>
 
-#include "common.cuh"
 #include "internal.h"
-#include "kv4.h"
+#include "kv4_common.cuh"
 
 namespace pa {
 namespace {
@@ -57,29 +55,6 @@ __device__ __forceinline__ float ex2f(float x) {
   return y;
 }
 
-// ---------------------------------------------------------------------------
-// the batch as the kernels read it
-
-struct Req {
-  int qo_start, qo_len, page_start, kv_len;
-};
-
-// Request b, checked: one whose entries cannot be is empty (its rows are not
-// written) and raises PA_DEV_BAD_INDEX.
-__device__ __forceinline__ Req load_req(const Kv4Params& p, int b) {
-  const int q0 = p.qo_indptr[b], q1 = p.qo_indptr[b + 1];
-  const int p0 = p.page_indptr[b], p1 = p.page_indptr[b + 1];
-  const int last = p.last_page_len[b];
-  const long long kv = p1 > p0 ? static_cast<long long>(p1 - p0 - 1) * p.g.ps + last : 0;
-  const bool ok = q0 >= 0 && q1 >= q0 && q1 <= p.num_tokens && p0 >= 0 && p1 >= p0 && p1 <= p.num_page_indices &&
-                  (p1 == p0 || (last >= 1 && last <= p.g.ps)) && kv <= INT_MAX - 256;
-  if (!ok) {
-    atomicOr(p.status, PA_DEV_BAD_INDEX);
-    return Req{0, 0, 0, 0};
-  }
-  return Req{q0, q1 - q0, p0, static_cast<int>(kv)};
-}
-
 __device__ __forceinline__ int row_tiles(const Kv4Params& p, const Req& r, int tile_rows) {
   const int rows = r.qo_len * p.G;
   return rows > p.small_rows ? 0 : (rows + tile_rows - 1) / tile_rows;
@@ -89,27 +64,6 @@ __device__ __forceinline__ int key_units(const Req& r) { return max(1, (r.kv_len
 // ---------------------------------------------------------------------------
 // 4-bit fragments
 
-// The 8 codes of a word as four (even, odd) fp16 pairs.
-__device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&h)[4]) {
-  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(w));
-}
-__device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t two) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
-  return h;
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
-  const __half2 r = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
 // (a & m) | (b & ~m): low nibbles of a, high nibbles of b.
 __device__ __forceinline__ uint32_t select_nibbles(uint32_t a, uint32_t b) {
   return (a & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u);
@@ -382,10 +336,9 @@ __global__ void __launch_bounds__(kThreads, SmallCfg<D, NT>::CTAS) kv4_small_ker
             top = max(top, max(qf[nt][j][i] & 0x7FFFu, (qf[nt][j][i] >> 16) & 0x7FFFu));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e = static_cast<int>(top >> 7);  // exponent field; 0 and 255 (zero, subnormal; inf, NaN) stay
-        const int up = (e == 0 || e == 255) ? 0 : min(140 - e, 126);
-        const float mul = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-        my *= __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+        const int up = bf16_row_shift(top);
+        const float mul = pow2(up);
+        my *= pow2(-up);
 #pragma unroll
         for (int j = 0; j < D / 16; ++j)
 #pragma unroll

@@ -1,0 +1,568 @@
+// Tensor-core attention of long query chunks over the 4-bit paged cache
+// (sm_103a: tcgen05 + TMEM).
+//
+// One CTA takes NT tiles of 128 packed query rows (token major, the G heads
+// of a kv head minor; any G) of one request and one kv head, against all keys
+// that its last row sees.  The work is found on the device: every CTA sums
+// the requests' tiles and looks its own up; the grid is the host's upper
+// bound, and the CTAs behind the last tile leave at once.  Tiles are taken
+// from the last one down: under a causal mask the last are the longest.
+//
+// Warp roles (4 warps each; register shares after setmaxnreg):
+//   warpgroup x < NT  softmax, correction and epilogue of tile x: thread i
+//                     owns row i = TMEM lane i.  It also loads its q row,
+//                     brings it to fp16 (bf16 rows by an exact power of two,
+//                     see kv4_attn.cu) and stores it as the MMA's operand.
+//   warpgroup NT      dequantisation: thread i owns key i of every 128-key
+//                     tile; it loads the key's codes and scales a tile ahead,
+//                     straight from its page, and writes the fp16 rows of K
+//                     and V (exact values: code * scale has 6 bits) into the
+//                     128-byte swizzled layout that the MMAs read.  Rows past
+//                     the last key are written as zeros, so that whatever
+//                     their memory holds cannot pass through P = 0.
+//   warpgroup NT + 1  one thread issues the MMAs: S_x = Q_x K^T, O_x += P_x V,
+//                     all fp16 with fp32 sums in TMEM.  P is fp16 whatever q's
+//                     type (2^-11 relative), so no row needs P in two parts.
+// Per key tile j it issues PV_A(j), S_A(j+1), PV_B(j), S_B(j+1): one tile's
+// MMAs run while the other tile's rows are in their softmax.
+//
+// TMEM: S_x (fp32 128 x 128) at 128 x, O_x (fp32 128 x D) after them; P_x
+// overwrites the first 64 columns of S_x.
+#include <cstring>
+
+#include "internal.h"
+#include "kv4_common.cuh"
+
+namespace pa {
+namespace {
+
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int D, int NT>
+struct PreCfg {
+  static_assert(NT == 1 || (NT == 2 && D <= 128), "two tiles need 2 x (128 + D) <= 512 TMEM columns");
+  static constexpr int THREADS = 128 * (NT + 2);
+  static constexpr int WARP_DQ = 4 * NT, WARP_MMA = 4 * NT + 4;
+  static constexpr int NKB = D / 64;      // 128-byte column blocks of a row
+  static constexpr int BLK = 128 * 128;   // one 128-row x 128-byte block
+  static constexpr int TILE = NKB * BLK;  // 128 rows of Q, K or V
+  static constexpr int NST = D == 256 ? 1 : 2;
+  static constexpr int OFF_K = NT * TILE;
+  static constexpr int OFF_V = OFF_K + NST * TILE;
+  static constexpr int OFF_BAR = OFF_V + NST * TILE;
+  static constexpr int SMEM = OFF_BAR + 256 + 1024;  // barriers + alignment slack
+  static_assert(SMEM <= 232448, "shared memory per CTA");
+  static constexpr int O_COL = NT * 128;
+  static constexpr uint32_t TMEM_COLS = (NT * (128 + D) <= 256) ? 256u : 512u;
+  // registers: with two tiles the launch gives 512 threads 128 each, handed
+  // over as 2 x 176 (softmax) + 104 (dequantisation) + 56 (MMA) = 4 x 128
+  static constexpr int LAUNCH_REGS = 128;
+};
+
+template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A key's codes and scales of K or V.
+template <int D>
+struct Row4 {
+  uint4 codes[D / 32];
+  uint32_t scales[D / 64];
+};
+
+template <int D>
+__device__ __forceinline__ void load_row4(Row4<D>& r, const Kv4Params& p, int64_t row, bool live) {
+  if (live) {
+    const uint4* c = reinterpret_cast<const uint4*>(p.codes + row * (D / 2));
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) r.codes[i] = __ldg(c + i);
+    const uint32_t* s = reinterpret_cast<const uint32_t*>(p.scales + row * (D / 16));
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) r.scales[i] = __ldg(s + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) r.codes[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) r.scales[i] = 0;
+  }
+}
+
+// Row `key` of a tile at `dst` in fp16, 128-byte swizzled.
+template <int D>
+__device__ __forceinline__ void store_row4(uint8_t* dst, const Row4<D>& r, int key) {
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {  // 32 dims: two scales, four 16-byte chunks
+    const uint32_t words[4] = {r.codes[i].x, r.codes[i].y, r.codes[i].z, r.codes[i].w};
+    const uint32_t two = r.scales[i >> 1] >> (16 * (i & 1));
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const uint32_t s = e4m3x2_f16(((two >> (8 * (w >> 1))) & 0xFFu) * 0x101u);
+      uint32_t h[4];
+      e2m1x8(words[w], h);
+      const int c = (i & 1) * 4 + w;  // 16-byte chunk of the 128-byte block
+      *reinterpret_cast<uint4*>(dst + (i >> 1) * (128 * 128) + key * 128 + ((c ^ (key & 7)) << 4)) =
+          make_uint4(mul_f16x2(h[0], s), mul_f16x2(h[1], s), mul_f16x2(h[2], s), mul_f16x2(h[3], s));
+    }
+  }
+}
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, 1) kv4_prefill_kernel(const Kv4Params p) {
+  using C = PreCfg<D, NT>;
+  constexpr int NST = C::NST;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ int warp_sums[32], found_b, found_tile;
+  pdl_wait();  // q, the cache and the tables may come from the kernel before
+
+  // ---- the item: tile from the end, kv head
+  const int h = blockIdx.x % p.g.Hkv;
+  auto tiles_of = [&](int b) -> int {
+    const Req r = load_req(p, b);
+    const int rows = r.qo_len * p.G;
+    return rows > p.small_rows ? (rows + NT * kQRows - 1) / (NT * kQRows) : 0;
+  };
+  auto sum_before = [&](int v, int* total) -> int {  // exclusive sum over the block
+    int x = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
+    }
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    int before = x - v, all = 0;
+#pragma unroll
+    for (int w = 0; w < C::THREADS / 32; ++w) {
+      if (w < warp) before += warp_sums[w];
+      all += warp_sums[w];
+    }
+    __syncthreads();
+    *total = all;
+    return before;
+  };
+  int mine = 0;
+  for (int b = tid; b < p.batch; b += C::THREADS) mine += tiles_of(b);
+  int total;
+  int before = sum_before(mine, &total);
+  const int item = total - 1 - static_cast<int>(blockIdx.x) / p.g.Hkv;
+  if (item < 0) return;
+  for (int b0 = 0, base = 0; b0 < p.batch; b0 += C::THREADS) {
+    int v = mine, all = total;
+    if (p.batch > C::THREADS) {
+      v = b0 + tid < p.batch ? tiles_of(b0 + tid) : 0;
+      before = base + sum_before(v, &all);
+    }
+    if (v > 0 && before <= item && item < before + v) {
+      found_b = b0 + tid;
+      found_tile = item - before;
+    }
+    base += all;
+    if (item < base) break;
+  }
+
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* full_k = bars;             // [NST] K tile written
+  uint64_t* full_v = bars + NST;       // [NST] V tile written
+  uint64_t* empty_k = bars + 2 * NST;  // [NST] every S MMA done with the slot
+  uint64_t* empty_v = bars + 3 * NST;  // [NST] every PV MMA done with the slot
+  uint64_t* q_full = bars + 4 * NST;   // the Q tiles written
+  uint64_t* s_full = q_full + 1;       // [2] S_x done
+  uint64_t* p_full = s_full + 2;       // [2] P_x (and O_x's correction) written
+  uint64_t* o_done = p_full + 2;       // [2] the last PV_x done
+  uint64_t* fin = o_done + 2;          // every MMA retired
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 24);
+  volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
+  if (tid == 0) {
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(&full_k[i], 4);
+      mbar_init(&full_v[i], 4);
+      mbar_init(&empty_k[i], 1);
+      mbar_init(&empty_v[i], 1);
+    }
+    mbar_init(q_full, 4 * NT);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_done[i], 1);
+    }
+    mbar_init(fin, 1);
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == C::WARP_MMA) tmem_alloc(tmem_slot, C::TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  const Req rq = load_req(p, found_b);
+  const int row0 = found_tile * NT * kQRows;  // first packed row of the item
+  const int rows = min(NT * kQRows, rq.qo_len * p.G - row0);
+  const bool has_b = NT == 2 && rows > kQRows;
+  const int shift = rq.kv_len - rq.qo_len + 1;
+  const int key_end = p.causal ? max(0, min(rq.kv_len, shift + (row0 + rows - 1) / p.G)) : rq.kv_len;
+  const int nkt = (key_end + kKvTile - 1) / kKvTile;
+  constexpr long long kLimit = PA_WAIT_LIMIT_CYCLES;
+
+  if (warp >= C::WARP_DQ && warp < C::WARP_DQ + 4) {
+    // ---------------------------------------------------------------- dequantisation
+    if constexpr (NT == 2) regs_down<104>();
+    const int r = tid - 32 * C::WARP_DQ;  // key of the tile
+    const int32_t* ids = p.pages + rq.page_start;
+    const int64_t half_rows = static_cast<int64_t>(p.g.ps) * p.g.Hkv;
+    auto page_of = [&](int j) -> int {
+      const int key = j * kKvTile + r;
+      return key < key_end ? __ldg(ids + (key >> p.g.ps_shift)) : 0;
+    };
+    auto row_of = [&](int j, int pid) -> int64_t {  // the K row; V's lies half_rows behind it
+      const int key = j * kKvTile + r;
+      if (static_cast<unsigned>(pid) >= static_cast<unsigned>(p.g.num_pages)) {
+        atomicOr(p.status, PA_DEV_BAD_INDEX);
+        pid = 0;
+      }
+      return static_cast<int64_t>(pid) * 2 * half_rows + static_cast<int64_t>(key & (p.g.ps - 1)) * p.g.slot_rows +
+             static_cast<int64_t>(h) * p.g.head_rows;
+    };
+    Row4<D> k4, v4;
+    int64_t at = row_of(0, page_of(0));
+    load_row4(k4, p, at, r < key_end);
+    load_row4(v4, p, at + half_rows, r < key_end);
+    int next_page = page_of(1);
+    for (int j = 0; j < nkt; ++j) {
+      const int st = j % NST;
+      const uint32_t parity = ((j / NST) - 1) & 1;
+      const bool more = (j + 1) * kKvTile + r < key_end;
+      at = row_of(j + 1, next_page);
+      next_page = page_of(j + 2);
+      if (j >= NST && !warp_wait(&empty_k[st], parity, abort_flag, p.status, kLimit)) break;
+      store_row4<D>(smem + C::OFF_K + st * C::TILE, k4, r);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full_k[st]);
+      load_row4(k4, p, at, more);
+      if (j >= NST && !warp_wait(&empty_v[st], parity, abort_flag, p.status, kLimit)) break;
+      store_row4<D>(smem + C::OFF_V + st * C::TILE, v4, r);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full_v[st]);
+      load_row4(v4, p, at + half_rows, more);
+    }
+  } else if (warp >= C::WARP_MMA) {
+    // ---------------------------------------------------------------- MMA issuer
+    if constexpr (NT == 2) regs_down<56>();
+    if (warp == C::WARP_MMA && lane == 0 && nkt > 0) {
+      const uint32_t id_s = idesc_f16(0, 0, 0, 128, 128);
+      const uint32_t id_o = idesc_f16(0, 0, 1, 128, D);
+      const uint64_t dq0 = smem_desc_sw128(sbase, 16, 1024);
+      const uint64_t dk0 = smem_desc_sw128(sbase + C::OFF_K, 16, 1024);
+      const uint64_t dv0 = smem_desc_sw128(sbase + C::OFF_V, C::BLK, 1024);
+      auto issue_s = [&](int x, int st) {
+        const uint64_t qd = dq0 + uint64_t(x) * (C::TILE >> 4);
+        const uint64_t kd = dk0 + uint64_t(st) * (C::TILE >> 4);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = ((k >> 2) * C::BLK + (k & 3) * 32) >> 4;
+          tc_mma_ss(tmem + x * 128, qd + off, kd + off, id_s, k > 0 ? 1u : 0u);
+        }
+        tc_commit(&s_full[x]);
+      };
+      auto issue_pv = [&](int x, int j, int st) {
+        const uint64_t vd = dv0 + uint64_t(st) * (C::TILE >> 4);
+#pragma unroll
+        for (int k = 0; k < kKvTile / 16; ++k)
+          tc_mma_ts(tmem + C::O_COL + x * 128, tmem + x * 128 + k * 8, vd + (k * 2048 >> 4), id_o,
+                    (j > 0 || k > 0) ? 1u : 0u);
+        if (j == nkt - 1) tc_commit(&o_done[x]);
+      };
+      bool ok = spin_wait(q_full, 0, abort_flag, p.status, kLimit);
+      if (ok) ok = spin_wait(&full_k[0], 0, abort_flag, p.status, kLimit);
+      if (ok) {
+        tc_fence_after();
+        issue_s(0, 0);
+        if (has_b) issue_s(1, 0);
+        tc_commit(&empty_k[0]);
+      }
+      for (int j = 0; ok && j < nkt; ++j) {
+        const int st = j % NST, st1 = (j + 1) % NST;
+        const bool more = j + 1 < nkt;
+        ok = spin_wait(&p_full[0], j & 1, abort_flag, p.status, kLimit);
+        if (ok) ok = spin_wait(&full_v[st], (j / NST) & 1, abort_flag, p.status, kLimit);
+        if (!ok) break;
+        tc_fence_after();
+        issue_pv(0, j, st);
+        if (more) {
+          ok = spin_wait(&full_k[st1], ((j + 1) / NST) & 1, abort_flag, p.status, kLimit);
+          if (!ok) break;
+          tc_fence_after();
+          issue_s(0, st1);
+          if (!has_b) tc_commit(&empty_k[st1]);
+        }
+        if (has_b) {
+          ok = spin_wait(&p_full[1], j & 1, abort_flag, p.status, kLimit);
+          if (!ok) break;
+          tc_fence_after();
+          issue_pv(1, j, st);
+        }
+        tc_commit(&empty_v[st]);
+        if (has_b && more) {
+          issue_s(1, st1);
+          tc_commit(&empty_k[st1]);
+        }
+      }
+      tc_commit(fin);
+      drain_wait(fin, 0);
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- softmax warps
+    if constexpr (NT == 2) regs_up<176>();
+    const int x = warp >> 2;
+    const int r = tid & 127;
+    const int pr = row0 + x * kQRows + r;  // packed row of the request
+    const bool row_valid = x * kQRows + r < rows;
+    const bool active = x == 0 || has_b;
+    const int64_t qtok = static_cast<int64_t>(rq.qo_start) + pr / p.G;
+    const int qhead = h * p.G + pr % p.G;
+    int row_end = p.causal ? shift + pr / p.G : rq.kv_len;
+    row_end = row_valid ? min(row_end, key_end) : 0;
+    float sl2 = p.scale_log2;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_col = tmem + lane_base + x * 128;
+    const uint32_t o_col = tmem + lane_base + C::O_COL + x * 128;
+    uint8_t* q_row = smem + x * C::TILE + r * 128;  // chunk c of block kb at kb * BLK + ((c ^ (r & 7)) << 4)
+
+    if (active) {  // the row of q as fp16
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + qtok * p.q_stride +
+                                                        static_cast<int64_t>(qhead) * D);
+      float mul = 1.f;
+      if constexpr (Elt<T>::kBf16) {
+        uint32_t top = 0;
+        if (row_valid) {
+#pragma unroll 8
+          for (int i = 0; i < D / 8; ++i) {
+            const uint4 w = src[i];
+            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = max(top, max(ws[e] & 0x7FFFu, (ws[e] >> 16) & 0x7FFFu));
+          }
+        }
+        const int up = bf16_row_shift(top);
+        mul = pow2(up);
+        sl2 *= pow2(-up);
+      }
+#pragma unroll 8
+      for (int i = 0; i < D / 8; ++i) {
+        uint4 w = row_valid ? src[i] : make_uint4(0, 0, 0, 0);
+        if constexpr (Elt<T>::kBf16) {
+          uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = Elt<T>::to_f2(ws[e]);
+            ws[e] = pack_f16x2(f.x * mul, f.y * mul);
+          }
+          w = make_uint4(ws[0], ws[1], ws[2], ws[3]);
+        }
+        *reinterpret_cast<uint4*>(q_row + (i >> 3) * C::BLK + (((i & 7) ^ (r & 7)) << 4)) = w;
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(q_full);
+
+    float m_ref = -INFINITY, l_sum = 0.f;
+    bool ok = active;
+    for (int j = 0; ok && j < nkt; ++j) {
+      ok = warp_wait(&s_full[x], j & 1, abort_flag, p.status, kLimit);
+      if (!ok) break;
+      tc_fence_after();
+      const int lim = row_end - j * kKvTile;
+      // the whole S row in registers: four loads, one wait
+      uint32_t s[128];
+      tmem_ld32(s_col + 0, *reinterpret_cast<uint32_t(*)[32]>(s + 0));
+      tmem_ld32(s_col + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+      tmem_ld32(s_col + 64, *reinterpret_cast<uint32_t(*)[32]>(s + 64));
+      tmem_ld32(s_col + 96, *reinterpret_cast<uint32_t(*)[32]>(s + 96));
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 128; ++i) asm volatile("" : "+r"(s[i]));
+      if (lim < kKvTile) {
+#pragma unroll
+        for (int i = 0; i < 128; ++i)
+          if (i >= lim) s[i] = __float_as_uint(-INFINITY);
+      }
+      float m43[43];
+#pragma unroll
+      for (int u = 0; u < 42; ++u)
+        m43[u] = fmax3(__uint_as_float(s[3 * u]), __uint_as_float(s[3 * u + 1]), __uint_as_float(s[3 * u + 2]));
+      m43[42] = fmaxf(__uint_as_float(s[126]), __uint_as_float(s[127]));
+      float m15[15];
+#pragma unroll
+      for (int u = 0; u < 14; ++u) m15[u] = fmax3(m43[3 * u], m43[3 * u + 1], m43[3 * u + 2]);
+      m15[14] = m43[42];
+      float m5[5];
+#pragma unroll
+      for (int u = 0; u < 5; ++u) m5[u] = fmax3(m15[3 * u], m15[3 * u + 1], m15[3 * u + 2]);
+      const float mx2 = fmax3(fmax3(m5[0], m5[1], m5[2]), m5[3], m5[4]) * sl2;
+      // the reference maximum moves when it grows by more than 8 (log2 units):
+      // P stays below 2^8, which fp16 and the fp32 sums carry
+      float alpha = 1.f;
+      bool resc = false;
+      if (mx2 > m_ref + 8.f) {
+        if (m_ref != -INFINITY) {
+          alpha = ex2(m_ref - mx2);
+          resc = true;
+        }
+        m_ref = mx2;
+      }
+      const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
+      const float2 sc2 = make_float2(sl2, sl2), nm2 = make_float2(-m_use, -m_use);
+      float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t ph[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int k = 32 * c + 2 * i;
+          const float2 t2 = __ffma2_rn(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), sc2, nm2);
+          const float a = ex2(t2.x), b = ex2(t2.y);
+          acc[(i >> 2) & 1] = __fadd2_rn(acc[(i >> 2) & 1], make_float2(a, b));
+          ph[i] = pack_f16x2(a, b);
+        }
+        tmem_st16(s_col + c * 16, ph);
+      }
+      // PV_x(j-1) is complete: it was issued before S_x(j), whose commit
+      // tracks every MMA issued before it, so O may be rescaled
+      if (__any_sync(0xffffffffu, resc)) {
+#pragma unroll
+        for (int c4 = 0; c4 < D / 32; ++c4) {
+          uint32_t o[32];
+          tmem_ld32(o_col + c4 * 32, o);
+          tmem_wait_ld(o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+          tmem_st32(o_col + c4 * 32, o);
+        }
+      }
+      const float2 sum = __fadd2_rn(acc[0], acc[1]);
+      l_sum = l_sum * alpha + (sum.x + sum.y);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[x]);
+    }
+
+    // ---------------------------------------------------------------- epilogue
+    if (ok && nkt > 0) ok = warp_wait(&o_done[x], 0, abort_flag, p.status, kLimit);
+    if (ok) {
+      tc_fence_after();
+      const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
+      // a row that sees no key: zeros, and -inf as its lse
+      const float inv = l_sum == 0.f ? 0.f : p.v_scale / l_sum;
+      if (row_valid && p.lse)
+        p.lse[qtok * p.Hq + qhead] = l_sum == 0.f ? -INFINITY : (m_use + __log2f(l_sum)) * kLn2;
+      // O scaled and rounded into the row of q's slot (free since the last S
+      // MMA); then each warp writes its 32 rows, whole rows at a time
+#pragma unroll
+      for (int c4 = 0; c4 < D / 32; ++c4) {
+        uint32_t o[32];
+        if (nkt > 0) {
+          tmem_ld32(o_col + c4 * 32, o);
+          tmem_wait_ld(o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0;
+        }
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float* f = reinterpret_cast<const float*>(o) + 8 * v;
+          const int c = (c4 & 1) * 4 + v;
+          *reinterpret_cast<uint4*>(q_row + (c4 >> 1) * C::BLK + ((c ^ (r & 7)) << 4)) =
+              make_uint4(Elt<T>::from_f2(f[0] * inv, f[1] * inv), Elt<T>::from_f2(f[2] * inv, f[3] * inv),
+                         Elt<T>::from_f2(f[4] * inv, f[5] * inv), Elt<T>::from_f2(f[6] * inv, f[7] * inv));
+        }
+      }
+      __syncwarp();
+      constexpr int LPR = D / 8;        // lanes of a row
+      constexpr int RPI = 32 / LPR;     // rows of an access
+      const int c = lane % LPR;
+#pragma unroll 4
+      for (int i = 0; i < 32 / RPI; ++i) {
+        const int rr = (warp & 3) * 32 + i * RPI + lane / LPR;  // row of the tile
+        if (x * kQRows + rr >= rows) break;
+        const uint4 w = *reinterpret_cast<const uint4*>(smem + x * C::TILE + (c >> 3) * C::BLK + rr * 128 +
+                                                        (((c & 7) ^ (rr & 7)) << 4));
+        const int pr2 = row0 + x * kQRows + rr;
+        const int64_t row = (static_cast<int64_t>(rq.qo_start) + pr2 / p.G) * p.Hq + h * p.G + pr2 % p.G;
+        *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + row * D + c * 8) = w;
+      }
+    }
+  }
+
+  // ---------------------------------------------------------------- teardown
+  // a softmax warp that gave up between its P stores and their wait still
+  // has TMEM stores in flight: they complete before TMEM is released
+  if (warp < C::WARP_DQ) tmem_wait_st();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::WARP_MMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+template <typename T, int D, int NT>
+cudaError_t launch_d(const Kv4Params& p, cudaStream_t stream) {
+  using C = PreCfg<D, NT>;
+  auto* kernel = kv4_prefill_kernel<T, D, NT>;
+  static std::atomic<uint64_t> attr_set{0};
+  cudaError_t e = set_smem_once(attr_set, reinterpret_cast<const void*>(kernel), C::SMEM);
+  if (e != cudaSuccess) return e;
+  if (NT == 2) {
+    // the register hand-over adds up to what the launch gives: a build that
+    // gives less would wait forever
+    static std::atomic<int> regs{0};
+    int n = regs.load(std::memory_order_relaxed);
+    if (n == 0) {
+      cudaFuncAttributes at;
+      e = cudaFuncGetAttributes(&at, kernel);
+      if (e != cudaSuccess) return e;
+      n = at.numRegs;
+      regs.store(n, std::memory_order_relaxed);
+    }
+    if (n != C::LAUNCH_REGS) return cudaErrorLaunchOutOfResources;
+  }
+  // at most one tile more than its rows need for each request that has any
+  const int64_t tile = int64_t(NT) * kQRows;
+  const int64_t rows = int64_t(p.num_tokens) * p.G;
+  const int64_t some = rows / (p.small_rows + 1);  // requests of more rows than the small kernel takes
+  const int64_t tiles = rows / tile + (some < p.batch ? some : p.batch);
+  if (tiles == 0) return cudaSuccess;
+  if (tiles * p.g.Hkv > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  return launch_pdl(kernel, unsigned(tiles * p.g.Hkv), unsigned(C::THREADS), size_t(C::SMEM), stream, p);
+}
+
+template <typename T>
+cudaError_t launch_t(const Kv4Params& p, int D, cudaStream_t stream) {
+  switch (D) {
+    case 64: return launch_d<T, 64, 2>(p, stream);
+    case 128: return launch_d<T, 128, 2>(p, stream);
+    default: return launch_d<T, 256, 1>(p, stream);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_prefill(const Kv4Params& p, const Kv4Shape& s, int dtype, cudaStream_t stream) {
+  return dtype == PA_BF16 ? launch_t<__nv_bfloat16>(p, s.D, stream) : launch_t<__half>(p, s.D, stream);
+}
+
+}  // namespace pa
