@@ -55,7 +55,7 @@ struct PreCfg {
   static constexpr int O_COL = NT * 128;
   static constexpr uint32_t TMEM_COLS = (NT * (128 + D) <= 256) ? 256u : 512u;
   // registers: with two tiles the launch gives 512 threads 128 each, handed
-  // over as 2 x 176 (softmax) + 104 (dequantisation) + 56 (MMA) = 4 x 128
+  // over as 2 x 168 (softmax) + 88 (dequantisation) + 88 (MMA) = 4 x 128;
   static constexpr int LAUNCH_REGS = 128;
 };
 
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, 1) kv4_prefill_kernel(
 
   if (warp >= C::WARP_DQ && warp < C::WARP_DQ + 4) {
     // ---------------------------------------------------------------- dequantisation
-    if constexpr (NT == 2) regs_down<104>();
+    if constexpr (NT == 2) regs_down<88>();
     const int r = tid - 32 * C::WARP_DQ;  // key of the tile
     const int32_t* ids = p.pages + rq.page_start;
     const int64_t half_rows = static_cast<int64_t>(p.g.ps) * p.g.Hkv;
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, 1) kv4_prefill_kernel(
     }
   } else if (warp >= C::WARP_MMA) {
     // ---------------------------------------------------------------- MMA issuer
-    if constexpr (NT == 2) regs_down<56>();
+    if constexpr (NT == 2) regs_down<88>();
     if (warp == C::WARP_MMA && lane == 0 && nkt > 0) {
       const uint32_t id_s = idesc_f16(0, 0, 0, 128, 128);
       const uint32_t id_o = idesc_f16(0, 0, 1, 128, D);
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, 1) kv4_prefill_kernel(
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- softmax warps
-    if constexpr (NT == 2) regs_up<176>();
+    if constexpr (NT == 2) regs_up<168>();
     const int x = warp >> 2;
     const int r = tid & 127;
     const int pr = row0 + x * kQRows + r;  // packed row of the request
