@@ -166,13 +166,14 @@ def load() -> ctypes.CDLL:
         lib.pagedattn_run_decode_noalloc.restype = ctypes.c_int
         lib.pagedattn_noalloc_device_status.argtypes = [ctypes.c_void_p, _I32P]
         lib.pagedattn_noalloc_device_status.restype = ctypes.c_int
-        lib.pagedattn_build_tables.argtypes = [ctypes.POINTER(TablesIn), ctypes.POINTER(TablesOut), ctypes.c_void_p]
+        # the argument structures come as ctypes structures or packed bytes
+        lib.pagedattn_build_tables.argtypes = [ctypes.c_void_p] * 3
         lib.pagedattn_build_tables.restype = ctypes.c_int
-        lib.pagedattn_kv4_append.argtypes = [ctypes.POINTER(Kv4CacheArgs), ctypes.POINTER(Kv4Rows), ctypes.c_void_p]
+        lib.pagedattn_kv4_append.argtypes = [ctypes.c_void_p] * 3
         lib.pagedattn_kv4_append.restype = ctypes.c_int
         lib.pagedattn_kv4_workspace_size.argtypes = [ctypes.c_int32] * 4 + [ctypes.POINTER(ctypes.c_size_t)]
         lib.pagedattn_kv4_workspace_size.restype = ctypes.c_int
-        lib.pagedattn_kv4_run.argtypes = [ctypes.POINTER(Kv4CacheArgs), ctypes.POINTER(Kv4Batch), ctypes.c_void_p,
+        lib.pagedattn_kv4_run.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                           ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                           ctypes.c_size_t, ctypes.c_void_p]
         lib.pagedattn_kv4_run.restype = ctypes.c_int

@@ -17,65 +17,65 @@ tables.free_count)` then advances the lengths in place at each replay.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 from . import _binding as _b
 from ._binding import PA_ERR_INVALID_ARG, PagedAttnError
+
+# The arguments' structures (include/pagedattn.h) packed directly: a ctypes
+# structure of this size costs a third of a small launch to fill.
+_TABLES_IN = struct.Struct("@5Pq5i0P")
+_KV4_ROWS = struct.Struct("@2P2q4P2i")
+_KV4_BATCH = struct.Struct("@4P7i0P")
 
 
 def _refuse(msg):
     raise PagedAttnError(PA_ERR_INVALID_ARG, msg)
 
 
-def _is(t, name, dtype, shape, device):
-    """A contiguous tensor of this type and shape on this device, or an error."""
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
-        _refuse(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on {device}")
+def _is(t, name, dtype, shape, index):
+    """A contiguous tensor of this type and shape on device `index`, or an error."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != index:
+        _refuse(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on cuda:{index}")
 
 
-def _rows(t, name, shape, device):
+def _rows(t, name, shape, index):
     """Tokens of contiguous [heads, head_dim] blocks at any stride; returns the stride."""
-    if tuple(t.shape) != shape or t.device != device:
-        _refuse(f"{name} must be of shape {list(shape)} on {device}")
+    if t.shape != shape or t.get_device() != index:
+        _refuse(f"{name} must be of shape {list(shape)} on cuda:{index}")
     n, h, d = shape
-    if t.stride(2) != 1 or (h > 1 and t.stride(1) != d):
+    st = t.stride()
+    if st[2] != 1 or (h > 1 and st[1] != d):
         _refuse(f"{name}: each token's [heads, head_dim] block must be contiguous")
-    return t.stride(0) if n > 1 else h * d
+    return st[0] if n > 1 else h * d
 
 
-class _On:
-    """The device's and the stream's context of one call.
+def _on(index, stream, tensors=()):
+    """(stream handle, context or None) for a call on device `index`.
 
     Without a stream the device's current one is used.  With another one, the
     tensors of the call are recorded on it, so that their memory is not given
-    away before it has passed the call.
+    away before it has passed the call.  The context makes device and stream
+    current where they are not.
     """
-
-    def __init__(self, device, stream, tensors):
-        import torch
-        self._guard = None
-        current = torch.cuda.current_stream(device)
-        if stream is None:
-            stream = current
+    import torch
+    current = torch._C._cuda_getCurrentRawStream(index)
+    if stream is None:
+        handle = current
+    else:
         handle = int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
-        if handle != current.cuda_stream:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(handle, device=device)
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(stream)
-            self._guard = torch.cuda.stream(stream)  # sets the device too
-        elif torch.cuda.current_device() != device.index:
-            self._guard = torch.cuda.device(device)
-        self.handle = handle
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
+    if handle != current:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(handle, device=index)
+        if stream.device.index != index:
+            _refuse(f"the stream is not one of cuda:{index}")
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+        return handle, torch.cuda.stream(stream)  # sets the device too
+    if torch.cuda.current_device() != index:
+        return handle, torch.cuda.device(index)
+    return handle, None
 
 
 def _device(device):
@@ -86,12 +86,24 @@ def _device(device):
     return torch.device("cuda", torch.cuda.current_device() if device.index is None else device.index)
 
 
+def _call(guard, function, *args):
+    if guard is None:
+        status = function(*args)
+    else:
+        with guard:
+            status = function(*args)
+    if status != _b.PA_OK:
+        _b.check(status)
+
+
 def _status(word, stream):
-    with _On(word.device, stream, (word,)) as st:
-        flags = ctypes.c_int32(0)
-        rc = _b.load().pagedattn_status_word(word.data_ptr(), st, ctypes.byref(flags))
-    if rc not in (_b.PA_OK, _b.PA_ERR_TIMEOUT, _b.PA_ERR_DEVICE_CHECK):
-        _b.check(rc)
+    flags = ctypes.c_int32(0)
+    handle, guard = _on(word.get_device(), stream, (word,))
+    try:
+        _call(guard, _b.load().pagedattn_status_word, word.data_ptr(), handle, ctypes.byref(flags))
+    except PagedAttnError as e:
+        if e.status not in (_b.PA_ERR_TIMEOUT, _b.PA_ERR_DEVICE_CHECK):
+            raise
     return int(flags.value)
 
 
@@ -110,7 +122,9 @@ class BatchTables:
         self.page_size, self.num_pages = int(page_size), int(num_pages)
         if min(self.batch_size, self.max_tokens, self.max_pages) < 0:
             _refuse("batch_size, max_tokens and max_pages must not be negative")
+        self._lib = _b.load()
         self.device = _device(device)
+        self._index = self.device.index
         i32 = dict(dtype=torch.int32, device=self.device)
         self.qo_indptr = torch.zeros(self.batch_size + 1, **i32)
         self.kv_page_indptr = torch.zeros(self.batch_size + 1, **i32)
@@ -134,22 +148,22 @@ class BatchTables:
         be ``self.kv_lens`` and free_count ``self.free_count``: the step then
         advances them in place.
         """
-        import torch
-        i32, B, dev = torch.int32, self.batch_size, self.device
-        _is(qo_lens, "qo_lens", i32, (B,), dev)
-        _is(kv_lens, "kv_lens", i32, (B,), dev)
-        _is(free_count, "free_count", i32, (1,), dev)
-        _is(free_pages, "free_pages", i32, (free_pages.numel(),), dev)
-        if block_table.dtype != i32 or block_table.dim() != 2 or block_table.shape[0] != B or block_table.device != dev:
-            _refuse(f"block_table must be an int32 tensor of shape [{B}, width] on {dev}")
-        width = block_table.shape[1]
-        if width > 1 and block_table.stride(1) != 1:
+        i32, B, at, cap = self.qo_indptr.dtype, self.batch_size, self._index, free_pages.numel()
+        _is(qo_lens, "qo_lens", i32, (B,), at)
+        _is(kv_lens, "kv_lens", i32, (B,), at)
+        _is(free_count, "free_count", i32, (1,), at)
+        _is(free_pages, "free_pages", i32, (cap,), at)
+        if block_table.dtype != i32 or block_table.dim() != 2 or block_table.shape[0] != B or \
+                block_table.get_device() != at:
+            _refuse(f"block_table must be an int32 tensor of shape [{B}, width] on cuda:{at}")
+        width, (row, col) = block_table.shape[1], block_table.stride()
+        if width > 1 and col != 1:
             _refuse("block_table: each row must be contiguous")
-        stride = block_table.stride(0) if B > 1 else width
-        a = _b.TablesIn(qo_lens.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(),
-                        free_count.data_ptr(), stride, width, free_pages.numel(), B, self.page_size, self.num_pages)
-        with _On(dev, stream, (qo_lens, kv_lens, block_table, free_pages, free_count)) as st:
-            _b.check(_b.load().pagedattn_build_tables(ctypes.byref(a), ctypes.byref(self._out), st))
+        handle, guard = _on(at, stream, (qo_lens, kv_lens, block_table, free_pages, free_count))
+        _call(guard, self._lib.pagedattn_build_tables,
+              _TABLES_IN.pack(qo_lens.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(),
+                              free_count.data_ptr(), row if B > 1 else width, width, cap, B, self.page_size,
+                              self.num_pages), ctypes.byref(self._out), handle)
         return self
 
     def device_status(self, stream=None) -> int:
@@ -179,14 +193,17 @@ class Kv4Cache:
             _refuse("num_pages, page_size and num_kv_heads must be positive, head_dim 64, 128 or 256")
         if device is None and codes is not None:
             device = codes.device
+        self._lib = _b.load()
         self.device = _device(device)
+        self._index = self.device.index
         for name, given, last in (("codes", codes, self.head_dim // 2), ("scales", scales, self.head_dim // 16)):
             shape = (self.num_pages, 2, *mid, last)
             if given is None:
                 given = torch.zeros(shape, dtype=torch.uint8, device=self.device)
-            _is(given, name, torch.uint8, shape, self.device)
+            _is(given, name, torch.uint8, shape, self._index)
             setattr(self, name, given)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._status_ptr = self.status.data_ptr()
         self._args = _b.Kv4CacheArgs(self.codes.data_ptr(), self.scales.data_ptr(), self.num_pages, self.page_size,
                                      self.num_kv_heads, self.head_dim, self.kv_layout, self.k_scale, self.v_scale)
 
@@ -199,20 +216,23 @@ class Kv4Cache:
         as later reads see them.  See pagedattn_kv4_append.
         """
         import torch
-        dev, n = self.device, slot_mapping.shape[0] if slot_mapping.dim() else 0
+        at, n = self._index, slot_mapping.shape[0] if slot_mapping.dim() else 0
         shape = (n, self.num_kv_heads, self.head_dim)
-        ks, vs = _rows(k, "k", shape, dev), _rows(v, "v", shape, dev)
+        k_stride, v_stride = _rows(k, "k", shape, at), _rows(v, "v", shape, at)
         if v.dtype != k.dtype:
             _refuse("k and v must be of one type")
-        _is(slot_mapping, "slot_mapping", torch.int64, (n,), dev)
-        for name, t in (("k_values", k_values), ("v_values", v_values)):
-            if t is not None:
-                _is(t, name, k.dtype, shape, dev)
-        a = _b.Kv4Rows(k.data_ptr(), v.data_ptr(), ks, vs, k_values.data_ptr() if k_values is not None else None,
-                       v_values.data_ptr() if v_values is not None else None, slot_mapping.data_ptr(),
-                       self.status.data_ptr(), n, _b.dtype_code(k.dtype))
-        with _On(dev, stream, (k, v, slot_mapping, k_values, v_values)) as st:
-            _b.check(_b.load().pagedattn_kv4_append(ctypes.byref(self._args), ctypes.byref(a), st))
+        _is(slot_mapping, "slot_mapping", torch.int64, (n,), at)
+        if k_values is not None:
+            _is(k_values, "k_values", k.dtype, shape, at)
+        if v_values is not None:
+            _is(v_values, "v_values", k.dtype, shape, at)
+        rows = _KV4_ROWS.pack(k.data_ptr(), v.data_ptr(), k_stride, v_stride,
+                              0 if k_values is None else k_values.data_ptr(),
+                              0 if v_values is None else v_values.data_ptr(), slot_mapping.data_ptr(),
+                              self._status_ptr, n,
+                              _b.PA_BF16 if k.dtype == torch.bfloat16 else _b.dtype_code(k.dtype))
+        handle, guard = _on(at, stream, (k, v, slot_mapping, k_values, v_values))
+        _call(guard, self._lib.pagedattn_kv4_append, ctypes.byref(self._args), rows, handle)
 
     def device_status(self, stream=None) -> int:
         """Waits for the stream; the PA_DEV_* bits since the last read, which clears them."""
@@ -238,7 +258,11 @@ class Kv4Attention:
         self.max_qo_len = self.num_tokens if max_qo_len is None else int(max_qo_len)
         if device is None and workspace is not None:
             device = workspace.device
+        self._lib = _b.load()
         self.device = _device(device)
+        self._index = self.device.index
+        self._dtype = (torch.float16, torch.bfloat16)[self.dtype_code]
+        self._shape = (self.num_tokens, self.num_qo_heads, self.head_dim)
         need = ctypes.c_size_t(0)
         with torch.cuda.device(self.device):
             _b.check(_b.load().pagedattn_kv4_workspace_size(self.num_qo_heads, self.num_kv_heads, self.head_dim,
@@ -252,6 +276,7 @@ class Kv4Attention:
             if self._ws_bytes < need.value:
                 raise PagedAttnError(_b.PA_ERR_WORKSPACE_TOO_SMALL,
                                      f"workspace needs {need.value} bytes, got {self._ws_bytes}")
+            self._ws_ptr = workspace.data_ptr()
             self.status = workspace.view(-1).view(torch.uint8)[:4].view(torch.int32)
             self.status.zero_()
 
@@ -262,40 +287,51 @@ class Kv4Attention:
         kv_last_page_len) as int32 device tensors.  See pagedattn_kv4_run.
         """
         import torch
-        dev, B, T = self.device, self.batch_size, self.num_tokens
-        shape = (T, self.num_qo_heads, self.head_dim)
-        stride = _rows(q, "q", shape, dev)
-        if _b.dtype_code(q.dtype) != self.dtype_code:
+        at, B, shape = self._index, self.batch_size, self._shape
+        stride = _rows(q, "q", shape, at)
+        if q.dtype != self._dtype:
             _refuse("q's dtype differs from the object's")
-        if cache.device != dev or (cache.num_kv_heads, cache.head_dim, cache.page_size) != \
-                (self.num_kv_heads, self.head_dim, self.page_size):
+        if cache._index != at or cache.num_kv_heads != self.num_kv_heads or cache.head_dim != self.head_dim or \
+                cache.page_size != self.page_size:
             _refuse("the cache's heads, head_dim, page_size or device differ from the object's")
         if isinstance(tables, BatchTables):
-            if tables.batch_size != B or tables.page_size != self.page_size or tables.device != dev:
+            if tables.batch_size != B or tables.page_size != self.page_size or tables._index != at:
                 _refuse("the tables' batch, page_size or device differ from the object's")
-            tables = (tables.qo_indptr, tables.kv_page_indptr, tables.kv_page_indices, tables.kv_last_page_len)
+            qo_indptr, page_indptr, pages, last = tables = (tables.qo_indptr, tables.kv_page_indptr,
+                                                            tables.kv_page_indices, tables.kv_last_page_len)
+            nnz = pages.shape[0]
         else:
-            i32 = torch.int32
             qo_indptr, page_indptr, pages, last = tables
-            _is(qo_indptr, "qo_indptr", i32, (B + 1,), dev)
-            _is(page_indptr, "kv_page_indptr", i32, (B + 1,), dev)
-            _is(pages, "kv_page_indices", i32, (pages.numel(),), dev)
-            _is(last, "kv_last_page_len", i32, (B,), dev)
-        qo_indptr, page_indptr, pages, last = tables
-        with _On(dev, stream, (q, out, lse, *tables)) as st:
-            if out is None:
-                out = torch.empty(shape, dtype=q.dtype, device=dev)
-            else:
-                _is(out, "out", q.dtype, shape, dev)
-            if lse is not None:
-                _is(lse, "lse", torch.float32, shape[:2], dev)
-            elif return_lse:
-                lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
-            a = _b.Kv4Batch(qo_indptr.data_ptr(), page_indptr.data_ptr(), pages.data_ptr(), last.data_ptr(), B,
-                            pages.numel(), T, self.max_qo_len, self.num_qo_heads, int(self.causal), self.dtype_code)
-            _b.check(_b.load().pagedattn_kv4_run(ctypes.byref(cache._args), ctypes.byref(a), q.data_ptr(), stride,
-                                                 out.data_ptr(), lse.data_ptr() if lse is not None else None,
-                                                 self.workspace.data_ptr(), self._ws_bytes, st))
+            nnz, i32 = pages.numel(), torch.int32
+            _is(qo_indptr, "qo_indptr", i32, (B + 1,), at)
+            _is(page_indptr, "kv_page_indptr", i32, (B + 1,), at)
+            _is(pages, "kv_page_indices", i32, (nnz,), at)
+            _is(last, "kv_last_page_len", i32, (B,), at)
+        if out is not None:
+            _is(out, "out", q.dtype, shape, at)
+        if lse is not None:
+            _is(lse, "lse", torch.float32, shape[:2], at)
+        handle, guard = _on(at, stream, (q, out, lse, *tables))
+        if guard is None:
+            return self._launch(q, stride, cache, qo_indptr, page_indptr, pages, last, nnz, out, lse, return_lse, handle)
+        with guard:  # the outputs are allocated on the stream that writes them
+            return self._launch(q, stride, cache, qo_indptr, page_indptr, pages, last, nnz, out, lse, return_lse, handle)
+
+    def _launch(self, q, stride, cache, qo_indptr, page_indptr, pages, last, nnz, out, lse, return_lse, handle):
+        import torch
+        shape = self._shape
+        if out is None:
+            out = torch.empty(shape, dtype=self._dtype, device=self.device)
+        if lse is None and return_lse:
+            lse = torch.empty(shape[:2], dtype=torch.float32, device=self.device)
+        batch = _KV4_BATCH.pack(qo_indptr.data_ptr(), page_indptr.data_ptr(), pages.data_ptr(), last.data_ptr(),
+                                self.batch_size, nnz, shape[0], self.max_qo_len, shape[1], self.causal,
+                                self.dtype_code)
+        status = self._lib.pagedattn_kv4_run(ctypes.byref(cache._args), batch, q.data_ptr(), stride, out.data_ptr(),
+                                             None if lse is None else lse.data_ptr(), self._ws_ptr, self._ws_bytes,
+                                             handle)
+        if status != _b.PA_OK:
+            _b.check(status)
         return out, lse
 
     def device_status(self, stream=None) -> int:
