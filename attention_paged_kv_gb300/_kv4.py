@@ -278,7 +278,7 @@ class Kv4Attention:
                                      f"workspace needs {need.value} bytes, got {self._ws_bytes}")
             self._ws_ptr = workspace.data_ptr()
             self.status = workspace.view(-1).view(torch.uint8)[:4].view(torch.int32)
-            self.status.zero_()
+            workspace.zero_()
 
     def run(self, q, cache, tables, out=None, lse=None, return_lse=True, stream=None):
         """out, lse of q [num_tokens, num_qo_heads, head_dim] (any token stride that is a multiple of 8).

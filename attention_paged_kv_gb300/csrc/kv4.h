@@ -62,13 +62,6 @@ cudaError_t launch_kv4_append(const Kv4AppendParams& p, int D, int dtype, int nu
 // ---------------------------------------------------------------------------
 // kv4_attn.cu
 
-// One split (request, row tile) as the merge needs it, at the first unit of
-// the slice that begins inside it.
-struct Kv4Split {
-  int32_t valid, qo_row0, rows, row_tile;  // first q row (token) of the request, its packed rows, row tile
-  int64_t u0, u1, per_slice;               // units of the row tile, units of a slice
-};
-
 struct Kv4Params {
   const void* q;
   void* out;
@@ -76,7 +69,7 @@ struct Kv4Params {
   const uint8_t *codes, *scales;
   const int32_t *qo_indptr, *page_indptr, *pages, *last_page_len;
   int32_t* status;
-  Kv4Split* splits;  // [slices], then the partial states below
+  int32_t* counters; // [slices * Hkv]: parts written of the row tile that slice's first boundary cuts
   float* part_o;     // [slices * Hkv * 2][rows of a tile][D], each normalised
   float* part_lse;   // [slices * Hkv * 2][rows of a tile], base-2, v_scale not in it
   int64_t q_stride;  // elements between tokens
@@ -94,7 +87,7 @@ struct Kv4Shape {  // what the launch and its workspace depend on
 // Bytes of a run's workspace, and where its parts lie in it.
 struct Kv4Layout {
   int32_t slices;
-  size_t off_splits, off_part_o, off_part_lse, total;
+  size_t off_counters, off_part_o, off_part_lse, total;
 };
 Kv4Layout kv4_layout(const Kv4Shape& s);
 

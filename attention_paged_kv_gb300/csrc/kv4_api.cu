@@ -243,7 +243,7 @@ pagedattn_status pagedattn_kv4_run(const pagedattn_kv4_cache* cache, const paged
   p.pages = batch->kv_page_indices;
   p.last_page_len = batch->kv_last_page_len;
   p.status = reinterpret_cast<int32_t*>(ws);
-  p.splits = reinterpret_cast<pa::Kv4Split*>(ws + lay.off_splits);
+  p.counters = reinterpret_cast<int32_t*>(ws + lay.off_counters);
   p.part_o = reinterpret_cast<float*>(ws + lay.off_part_o);
   p.part_lse = reinterpret_cast<float*>(ws + lay.off_part_lse);
   p.q_stride = q_stride;
@@ -253,7 +253,12 @@ pagedattn_status pagedattn_kv4_run(const pagedattn_kv4_cache* cache, const paged
   p.Hq = batch->num_qo_heads;
   p.G = shape.G;
   p.causal = batch->causal ? 1 : 0;
-  p.slices = lay.slices;
+  // no more slices than the tables can hold work for (the workspace's layout
+  // stays): 64-key units of at most this many row tiles, 4 to a slice
+  const int64_t tiles = int64_t(batch->num_tokens) * shape.G / 8 + 1;
+  const int64_t key_units = int64_t(batch->num_page_indices) * cache->page_size / 64 + batch->batch_size;
+  const int64_t most = (key_units * tiles + 3) / 4;
+  p.slices = most < lay.slices ? int32_t(most) : lay.slices;
   // the bound alone decides whether the tensor-core kernel is launched; where
   // it is not, the small-query kernel takes every request
   const bool prefill = shape.max_rows > pa::kKv4SmallRows;

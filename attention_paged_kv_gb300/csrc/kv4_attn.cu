@@ -43,11 +43,13 @@
 namespace pa {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 constexpr int kUnitKeys = 64;
 constexpr int kMinUnits = 4;  // of a slice: below 256 keys a split costs more than it spreads
+constexpr int kStepKeys = 32;
+constexpr int kKeptReqs = 128;  // requests of a slice kept in shared memory
 constexpr float kLn2f = 0.6931471805599453f;
+// A running maximum before any key: finite, so that it can be subtracted.
+constexpr float kNone = -3.0e38f;
 
 __device__ __forceinline__ float ex2f(float x) {
   float y;
@@ -81,104 +83,122 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <int BYTES> struct Piece;  // a lane's contiguous codes of one row
-template <> struct Piece<4> { uint32_t w[1]; };
-template <> struct Piece<8> { uint32_t w[2]; };
-template <> struct Piece<16> { uint32_t w[4]; };
-template <> struct Piece<32> { uint32_t w[8]; };
-
+// BYTES of shared memory at `at` in registers.
 template <int BYTES>
-__device__ __forceinline__ Piece<BYTES> load_piece(const uint8_t* src) {
-  Piece<BYTES> r;
+__device__ __forceinline__ void lds(uint32_t (&r)[BYTES / 4], uint32_t at) {
   if constexpr (BYTES == 4) {
-    r.w[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r[0]) : "r"(at));
   } else if constexpr (BYTES == 8) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
-    r.w[0] = v.x;
-    r.w[1] = v.y;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(at));
   } else {
-#pragma unroll
-    for (int i = 0; i < BYTES / 16; ++i) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + i);
-      r.w[4 * i] = v.x;
-      r.w[4 * i + 1] = v.y;
-      r.w[4 * i + 2] = v.z;
-      r.w[4 * i + 3] = v.w;
-    }
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at));
   }
-  return r;
 }
+// 1, 2 or 4 bytes of shared memory.
 template <int BYTES>
-__device__ __forceinline__ uint32_t load_scales(const uint8_t* src) {
-  if constexpr (BYTES == 1) return __ldg(src);
-  if constexpr (BYTES == 2) return __ldg(reinterpret_cast<const unsigned short*>(src));
-  return __ldg(reinterpret_cast<const uint32_t*>(src));
+__device__ __forceinline__ uint32_t lds_scales(uint32_t at) {
+  if constexpr (BYTES == 4) {
+    uint32_t r;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(at));
+    return r;
+  } else {
+    uint16_t r;
+    if constexpr (BYTES == 2) asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(at));
+    else asm volatile("ld.shared.u8 %0, [%1];" : "=h"(r) : "r"(at));
+    return r;
+  }
 }
+// cp.async of N bytes (through L2 alone where N = 16); zeros where !live.
+template <int N>
+__device__ __forceinline__ void cp_async(uint32_t dst, const uint8_t* src, bool live = true) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(live ? N : 0), "n"(N)
+                 : "memory");
+}
+template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// What a lane holds of 16 keys.
+// A stage: 32 keys of one kv head in shared memory, K codes, V codes, K
+// scales, V scales.  The rows of codes are 16-byte chunks whose place in the
+// row is exclusive-ored with swizzle(row), and row r of each 8-row group of an
+// MMA is the group's key order(r); both are chosen so that neither K's
+// reads (rows r, r + 1, ... whole) nor V's (the even or the odd rows, one
+// chunk of each) meet in a bank.
 template <int D>
-struct KeyStep {
-  static constexpr int KB = D / 8;                      // bytes of a K row: D/4 dims
-  static constexpr int VB = D / 16;                     // bytes of a V row: D/8 dims
-  static constexpr int KS = D / 64;                     // their scales
+struct Stage {
+  static constexpr int ROW = D / 2, SROW = D / 16;
+  static constexpr int OFF_V = kStepKeys * ROW, OFF_KS = 2 * OFF_V, OFF_VS = OFF_KS + kStepKeys * SROW;
+  static constexpr int BYTES = OFF_VS + kStepKeys * SROW;
+  static constexpr int KB = D / 8;   // bytes of a K row that a lane reads: D/4 dims
+  static constexpr int VB = D / 16;  // of a V row: D/8 dims
+  static constexpr int KS = D / 64;  // their scales
   static constexpr int VS = D >= 128 ? D / 128 : 1;
-  Piece<KB> k[2];  // keys g, g + 8
-  Piece<VB> v[4];  // keys 2t, 2t + 1, 2t + 8, 2t + 9
-  uint32_t ks[2], vs[4];
+  static constexpr int LANES = ROW / 16;  // lanes that copy a row
+  static __device__ __forceinline__ int swizzle(int row) {
+    if constexpr (D == 64) return 0;
+    if constexpr (D == 128) return row & 2;
+    return ((row & 3) << 1) | ((row >> 2) & 1);
+  }
+  static __device__ __forceinline__ int order(int r) {  // r in [0, 8)
+    const int t = r >> 1;
+    return r & 1 ? 4 + (t ^ (D == 64 ? 2 : 1)) : t;
+  }
 };
 
+// Stages and CTAs of an SM by head_dim and 8-row groups of a tile: O^T takes
+// D / 4 registers a lane for each group, q's fragments D / 8 (kept in shared
+// memory at 4 groups).
 template <int D, int NT>
 struct SmallCfg {
   static constexpr int ROWS = 8 * NT;
-  static constexpr int O_STRIDE = D + 4;  // floats of a row in the combine buffer
-  static constexpr int SMEM = kWarps * ROWS * O_STRIDE * 4 + 2 * kWarps * ROWS * 4;
-  static constexpr int CTAS = D == 256 ? 1 : 2;  // of an SM
+  static constexpr int WARPS = D * NT == 256 && D < 256 ? 6 : 8;  // 168 registers a thread, or 128 (255 for one CTA)
+  static constexpr int THREADS = 32 * WARPS;
+  static constexpr int CTAS = D * NT <= 256 && D < 256 ? 2 : 1;
+  static constexpr bool Q_SMEM = NT * D >= 512;
+  static constexpr int STAGES = CTAS == 1 && D < 256 ? 5 : (D == 64 ? 5 : (WARPS == 6 ? 4 : 3));
+  static constexpr int RING = WARPS * STAGES * Stage<D>::BYTES;
+  // after the loop the states of the warps take the ring's place (floats)
+  static constexpr int O_STRIDE = D + 4;
+  static constexpr int STATES = WARPS * ROWS * O_STRIDE * 4;
+  static constexpr int OFF_M = RING > STATES ? RING : STATES;
+  static constexpr int OFF_L = OFF_M + WARPS * ROWS * 4;
+  static constexpr int OFF_Q = OFF_L + WARPS * ROWS * 4;
+  static constexpr int SMEM = OFF_Q + (Q_SMEM ? NT * (D / 16) * 256 : 0);
+  static_assert(CTAS * (SMEM + kKeptReqs * 16 + 256 + 1024) <= 233472, "shared memory per SM");
 };
 
-// Sum over the block (every thread gets it).
-__device__ __forceinline__ long long block_sum(long long v, long long* scratch) {
-#pragma unroll
-  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-  __syncthreads();
-  long long s = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) s += scratch[w];
-  __syncthreads();
-  return s;
-}
-
-template <typename T, int D, int NT, bool kSmallPage>
-__global__ void __launch_bounds__(kThreads, SmallCfg<D, NT>::CTAS) kv4_small_kernel(const Kv4Params p) {
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTAS) kv4_small_kernel(const Kv4Params p) {
   using C = SmallCfg<D, NT>;
-  using Step = KeyStep<D>;
-  extern __shared__ float smem_f[];
-  float* o_s = smem_f;                                    // [warps][rows][O_STRIDE]
-  float* m_s = smem_f + kWarps * C::ROWS * C::O_STRIDE;   // [warps][rows]
-  float* l_s = m_s + kWarps * C::ROWS;                    // [warps][rows]
+  using St = Stage<D>;
+  constexpr int kThreads = C::THREADS, kWarps = C::WARPS;
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* o_s = reinterpret_cast<float*>(smem);             // [warps][rows][O_STRIDE]
+  float* m_s = reinterpret_cast<float*>(smem + C::OFF_M);  // [warps][rows]
+  float* l_s = reinterpret_cast<float*>(smem + C::OFF_L);  // [warps][rows]
+  uint2* q_s = reinterpret_cast<uint2*>(smem + C::OFF_Q);  // Q_SMEM: [NT][D / 16][lane] fragments
   __shared__ long long scratch[kWarps];
+  __shared__ Req req_s[kKeptReqs];  // the slice's first requests, where its scan met them
   __shared__ long long found_u;
-  __shared__ int found_b;
+  __shared__ int found_b, last_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int h = blockIdx.x % p.g.Hkv, slice = blockIdx.x / p.g.Hkv;
   pdl_wait();
 
   // ---- the slice's units [u, u_end) and the request that they begin in
-  auto units_of = [&](int b) -> long long {
-    const Req r = load_req(p, b);
+  auto units_of = [&](const Req& r) -> long long {
     return static_cast<long long>(row_tiles(p, r, C::ROWS)) * key_units(r);
   };
-  long long mine = 0;
-  for (int b = tid; b < p.batch; b += kThreads) mine += units_of(b);
-  const long long total = block_sum(mine, scratch);
-  const long long per_slice = max(static_cast<long long>(kMinUnits), (total + p.slices - 1) / p.slices);
-  long long u = slice * per_slice;
-  const long long u_end = min(total, u + per_slice);
-  if (h == 0 && tid == 0 && (u >= u_end || slice == 0)) p.splits[slice].valid = 0;
-  if (u >= u_end) return;
-  long long base = 0;  // units before the chunk of requests
-  for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
-    const long long v = b0 + tid < p.batch ? (p.batch <= kThreads ? mine : units_of(b0 + tid)) : 0;
+  Req mine{0, 0, 0, 0};
+  long long units = 0;
+  for (int b = tid; b < p.batch; b += kThreads) {
+    mine = load_req(p, b);
+    units += units_of(mine);
+  }
+  auto sum_before = [&](long long v, long long* all) -> long long {  // exclusive sum over the block
     long long x = v;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -187,24 +207,66 @@ __global__ void __launch_bounds__(kThreads, SmallCfg<D, NT>::CTAS) kv4_small_ker
     }
     if (lane == 31) scratch[warp] = x;
     __syncthreads();
-    long long before = base, all = 0;
+    long long before = x - v, sum = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) before += scratch[w];
-      all += scratch[w];
-    }
-    const long long first = before + x - v;
-    if (v > 0 && first <= u && u < first + v) {
-      found_b = b0 + tid;
-      found_u = first;
+      sum += scratch[w];
     }
     __syncthreads();
+    *all = sum;
+    return before;
+  };
+  long long total;
+  long long before = sum_before(units, &total);
+  const long long per_slice = max(static_cast<long long>(kMinUnits), (total + p.slices - 1) / p.slices);
+  long long u = slice * per_slice;
+  const long long u_end = min(total, u + per_slice);
+  if (u >= u_end) return;
+  int chunk = 0;  // first request of the threads' `mine`
+  for (long long base = 0; chunk < p.batch; chunk += kThreads) {
+    long long v = units, all = total;
+    if (p.batch > kThreads) {
+      mine = Req{0, 0, 0, 0};
+      if (chunk + tid < p.batch) mine = load_req(p, chunk + tid);
+      v = units_of(mine);
+      before = base + sum_before(v, &all);
+    }
     base += all;
-    if (u < base) break;
+    if (u >= base) continue;
+    if (v > 0 && before <= u && u < before + v) {
+      found_b = chunk + tid;
+      found_u = before;
+    }
+    break;
   }
-  int b = found_b;  // always found: u < total
+  __syncthreads();
+  const int first_b = found_b;  // always found: u < total
+  if (chunk + tid >= first_b && chunk + tid - first_b < kKeptReqs) req_s[chunk + tid - first_b] = mine;
+  __syncthreads();
+  const int kept_b = min(first_b + kKeptReqs, chunk + kThreads);
+  int b = first_b;
   long long req_u = found_u;  // the request's first unit
-  Req rq = load_req(p, b);
+  Req rq = req_s[0];
+
+  // ---- where a lane copies to and reads from in a stage
+  const uint32_t page_bytes = static_cast<uint32_t>(p.g.ps) * p.g.Hkv * D;  // K and V codes of a page, at most 2^31
+  const uint32_t slot_bytes = static_cast<uint32_t>(p.g.slot_rows) * (D / 2);
+  const int copy_row = lane / St::LANES, copy_chunk = lane % St::LANES;
+  const uint8_t* codes_h = p.codes + static_cast<int64_t>(h) * p.g.head_rows * (D / 2) + copy_chunk * 16;
+  const uint8_t* scales_h = p.scales + static_cast<int64_t>(h) * p.g.head_rows * (D / 16);
+  const uint32_t ring = smem_u32(smem) + warp * C::STAGES * St::BYTES;
+  const uint32_t copy_to = copy_row * St::ROW + ((copy_chunk ^ St::swizzle(copy_row & 7)) << 4);
+  const int k_row = St::order(g);  // + 8 i
+  const uint32_t k_at = k_row * St::ROW + ((((t * St::KB) >> 4) ^ St::swizzle(k_row)) << 4) + ((t * St::KB) & 15);
+  uint32_t v_at[2];  // rows 2t and 2t + 1, + 8 i
+  int v_row[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    v_row[e] = St::order(2 * t + e);
+    v_at[e] = St::OFF_V + v_row[e] * St::ROW + ((((g * St::VB) >> 4) ^ St::swizzle(v_row[e])) << 4) +
+              ((g * St::VB) & 15);
+  }
 
   // ---- row tiles, one after the other
   bool first_segment = true;
@@ -214,102 +276,64 @@ __global__ void __launch_bounds__(kThreads, SmallCfg<D, NT>::CTAS) kv4_small_ker
     const long long tile_u = req_u + static_cast<long long>(rt) * kts;
     const int unit0 = static_cast<int>(u - tile_u);
     const long long seg_end = min(u_end, tile_u + kts);
-    const int rows = min(C::ROWS, rq.qo_len * p.G - rt * C::ROWS);
     const int row0 = rt * C::ROWS;
+    const int rows = min(C::ROWS, rq.qo_len * p.G - row0);
     // keys that some row of the tile sees, and those that every row sees
     const int shift = rq.kv_len - rq.qo_len + 1;
     const int seen_end = p.causal ? max(0, shift + (row0 + rows - 1) / p.G) : rq.kv_len;
     const int all_end = p.causal ? shift + row0 / p.G : rq.kv_len;
     const int key_a = unit0 * kUnitKeys;
     const int key_b = min(static_cast<int>(seg_end - tile_u) * kUnitKeys, seen_end);
-    const int steps = key_b > key_a ? (key_b - key_a + 15) / 16 : 0;
+    const int steps = key_b > key_a ? (key_b - key_a + kStepKeys - 1) / kStepKeys : 0;
 
-    if (h == 0 && tid == 0 && first_segment && slice > 0) {
-      Kv4Split s;
-      s.valid = u > tile_u;
-      s.qo_row0 = rq.qo_start;
-      s.rows = rq.qo_len * p.G;
-      s.row_tile = rt;
-      s.u0 = tile_u;
-      s.u1 = tile_u + kts;
-      s.per_slice = per_slice;
-      p.splits[slice] = s;
-    }
-
-    // page ids two steps ahead, codes one
+    // page of key `lane` of a step; keys that no row sees have none
     const int32_t* page_ids = p.pages + rq.page_start;
-    auto step_page = [&](int s) -> int {  // kSmallPage: of key (lane & 15) of the step
-      if (s >= steps) return 0;
-      const int key = key_a + s * 16;
-      int pid;
-      if constexpr (kSmallPage)
-        pid = __ldg(page_ids + (min(key + (lane & 15), rq.kv_len - 1) >> p.g.ps_shift));
-      else
-        pid = __ldg(page_ids + (key >> p.g.ps_shift));
-      return pid;
+    auto step_page = [&](int s) -> int {
+      const int key = key_a + s * kStepKeys + lane;
+      return s < steps && key < key_b ? __ldg(page_ids + (key >> p.g.ps_shift)) : 0;
     };
-    const int64_t half_rows = static_cast<int64_t>(p.g.ps) * p.g.Hkv;
-    const int64_t head_off = static_cast<int64_t>(h) * p.g.head_rows;
-    auto load_step = [&](Step& f, int s, int pid) {
-      if (s >= steps) return;
-      if (static_cast<unsigned>(pid) >= static_cast<unsigned>(p.g.num_pages)) {
-        atomicOr(p.status, PA_DEV_BAD_INDEX);
-        pid = 0;
+    // copies step s into its stage; `pids` from step_page(s)
+    auto copy_step = [&](int s, int pids) {
+      if (s < steps) {
+        if (static_cast<unsigned>(pids) >= static_cast<unsigned>(p.g.num_pages)) {
+          atomicOr(p.status, PA_DEV_BAD_INDEX);
+          pids = 0;
+        }
+        const int key = key_a + s * kStepKeys;
+        const uint32_t st = ring + ((s / kWarps) % C::STAGES) * St::BYTES;
+        const bool tail = key + kStepKeys > key_b;  // rows of keys that no row sees are zeros
+#pragma unroll
+        for (int i = 0; i < St::LANES; ++i) {
+          constexpr int RPP = 32 / St::LANES;
+          const int r = i * RPP + copy_row;
+          const uint32_t pid = __shfl_sync(0xffffffffu, pids, r);
+          const uint32_t slot = (key + r) & (p.g.ps - 1);
+          const uint8_t* src = codes_h + static_cast<uint64_t>(pid) * page_bytes + static_cast<uint64_t>(slot) * slot_bytes;
+          // (the swizzle of a 4-row pass changes with bit 2 of its first row)
+          const uint32_t dst = st + ((copy_to + i * RPP * St::ROW) ^ (D == 256 ? (i & 1) << 4 : 0));
+          const bool live = !tail || key + r < key_b;
+          cp_async<16>(dst, src, live);
+          cp_async<16>(dst + St::OFF_V, src + (page_bytes >> 1), live);
+        }
+        const uint32_t slot = (key + lane) & (p.g.ps - 1);
+        const uint8_t* src = scales_h + static_cast<uint64_t>(static_cast<uint32_t>(pids)) * (page_bytes >> 3) +
+                             static_cast<uint64_t>(slot) * (slot_bytes >> 3);
+        const bool live = !tail || key + lane < key_b;
+        cp_async<St::SROW>(st + St::OFF_KS + lane * St::SROW, src, live);
+        cp_async<St::SROW>(st + St::OFF_VS + lane * St::SROW, src + (page_bytes >> 4), live);
       }
-      const int key = key_a + s * 16;
-      if constexpr (kSmallPage) {
-        auto row_of = [&](int i, int half) {
-          const int id = __shfl_sync(0xffffffffu, pid, i);
-          const int slot = min(key + i, rq.kv_len - 1) & (p.g.ps - 1);
-          return (static_cast<int64_t>(id) * 2 + half) * half_rows + static_cast<int64_t>(slot) * p.g.slot_rows +
-                 head_off;
-        };
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int64_t row = row_of(g + 8 * i, 0);
-          f.k[i] = load_piece<Step::KB>(p.codes + row * (D / 2) + t * Step::KB);
-          f.ks[i] = load_scales<Step::KS>(p.scales + row * (D / 16) + t * Step::KS);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int64_t row = row_of(2 * t + (i & 1) + 8 * (i >> 1), 1);
-          f.v[i] = load_piece<Step::VB>(p.codes + row * (D / 2) + g * Step::VB);
-          f.vs[i] = load_scales<Step::VS>(p.scales + row * (D / 16) + (g * D / 8) / 16);
-        }
-      } else {
-        // pages of 16 slots or more: the step's 16 slots are all in one page
-        // (those past the last key too, so nothing has to be clamped)
-        const int64_t row = static_cast<int64_t>(pid) * 2 * half_rows +
-                            static_cast<int64_t>(key & (p.g.ps - 1)) * p.g.slot_rows + head_off;
-        const uint8_t* kc = p.codes + row * (D / 2);
-        const uint8_t* ksc = p.scales + row * (D / 16);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = (g + 8 * i) * p.g.slot_rows;
-          f.k[i] = load_piece<Step::KB>(kc + static_cast<int64_t>(r) * (D / 2) + t * Step::KB);
-          f.ks[i] = load_scales<Step::KS>(ksc + static_cast<int64_t>(r) * (D / 16) + t * Step::KS);
-        }
-        const uint8_t* vc = kc + half_rows * (D / 2);
-        const uint8_t* vsc = ksc + half_rows * (D / 16);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = (2 * t + (i & 1) + 8 * (i >> 1)) * p.g.slot_rows;
-          f.v[i] = load_piece<Step::VB>(vc + static_cast<int64_t>(r) * (D / 2) + g * Step::VB);
-          f.vs[i] = load_scales<Step::VS>(vsc + static_cast<int64_t>(r) * (D / 16) + (g * D / 8) / 16);
-        }
-      }
+      cp_async_commit();
     };
-    int pid0 = step_page(warp), pid1 = step_page(warp + kWarps);
-    Step cur, nxt;
-    load_step(cur, warp, pid0);
+    int pids[C::STAGES];
+#pragma unroll
+    for (int i = 0; i < C::STAGES; ++i) pids[i] = step_page(warp + i * kWarps);
 
     // q fragments (row n = g of each 8-row group, dims [t D/4, (t+1) D/4)) and
     // the logit factors of rows 2t, 2t + 1
-    uint32_t qf[NT][D / 16][2];
+    uint32_t qf[C::Q_SMEM ? 1 : NT][D / 16][2];
     float fac[NT][2];
     int lim[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    auto load_q = [&](int nt, uint32_t (&f)[D / 16][2]) -> float {  // returns the row's factor
       const int n = nt * 8 + g, r = row0 + n;
       float my = p.scale_log2;
       if (n < rows) {
@@ -318,22 +342,21 @@ __global__ void __launch_bounds__(kThreads, SmallCfg<D, NT>::CTAS) kv4_small_ker
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           const uint4 w = *(reinterpret_cast<const uint4*>(src) + c);
-          qf[nt][2 * c][0] = w.x;
-          qf[nt][2 * c][1] = w.y;
-          qf[nt][2 * c + 1][0] = w.z;
-          qf[nt][2 * c + 1][1] = w.w;
+          f[2 * c][0] = w.x;
+          f[2 * c][1] = w.y;
+          f[2 * c + 1][0] = w.z;
+          f[2 * c + 1][1] = w.w;
         }
       } else {
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) qf[nt][j][0] = qf[nt][j][1] = 0;
+        for (int j = 0; j < D / 16; ++j) f[j][0] = f[j][1] = 0;
       }
       if constexpr (Elt<T>::kBf16) {
         uint32_t top = 0;  // the largest magnitude's bf16 bits
 #pragma unroll
         for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            top = max(top, max(qf[nt][j][i] & 0x7FFFu, (qf[nt][j][i] >> 16) & 0x7FFFu));
+          for (int i = 0; i < 2; ++i) top = max(top, max(f[j][i] & 0x7FFFu, (f[j][i] >> 16) & 0x7FFFu));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int up = bf16_row_shift(top);
@@ -343,13 +366,38 @@ __global__ void __launch_bounds__(kThreads, SmallCfg<D, NT>::CTAS) kv4_small_ker
         for (int j = 0; j < D / 16; ++j)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float2 f = Elt<T>::to_f2(qf[nt][j][i]);
-            qf[nt][j][i] = pack_f16x2(f.x * mul, f.y * mul);
+            const float2 x = Elt<T>::to_f2(f[j][i]);
+            f[j][i] = pack_f16x2(x.x * mul, x.y * mul);
           }
       }
+      return my;
+    };
+    if constexpr (C::Q_SMEM) {
+      // warp nt makes row group nt's fragments for all
+      if (warp < NT) {
+        const float my = load_q(warp, qf[0]);
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) q_s[(warp * (D / 16) + j) * 32 + lane] = make_uint2(qf[0][j][0], qf[0][j][1]);
+        if (t == 0) m_s[warp * 8 + g] = my;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        fac[nt][0] = m_s[nt * 8 + 2 * t];
+        fac[nt][1] = m_s[nt * 8 + 2 * t + 1];
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < C::STAGES - 1; ++i) copy_step(warp + i * kWarps, pids[i]);
+    int next_pids = pids[C::STAGES - 1];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float my = 0.f;
+      if constexpr (!C::Q_SMEM) my = load_q(nt, qf[nt]);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        fac[nt][i] = __shfl_sync(0xffffffffu, my, (2 * t + i) * 4);
+        if constexpr (!C::Q_SMEM) fac[nt][i] = __shfl_sync(0xffffffffu, my, (2 * t + i) * 4);
         const int r2 = row0 + nt * 8 + 2 * t + i;
         lim[nt][i] = p.causal ? min(shift + r2 / p.G, rq.kv_len) : rq.kv_len;
       }
@@ -362,55 +410,109 @@ __global__ void __launch_bounds__(kThreads, SmallCfg<D, NT>::CTAS) kv4_small_ker
       for (int i = 0; i < D / 16; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
-      m[nt][0] = m[nt][1] = -INFINITY;
+      m[nt][0] = m[nt][1] = kNone;
       l[nt][0] = l[nt][1] = 0.f;
     }
 
-    auto compute = [&](Step& f, int s) {
-      const int key = key_a + s * 16;
-      float sc[NT][4];
+    for (int s = warp; s < steps; s += kWarps) {
+      const int key = key_a + s * kStepKeys;
+      // the step's stage has landed, and every lane is done with the one
+      // that the copies below overwrite
+      cp_async_wait<C::STAGES - 2>();
+      __syncwarp();
+      copy_step(s + (C::STAGES - 1) * kWarps, next_pids);
+      next_pids = step_page(s + C::STAGES * kWarps);
+      const uint32_t st = ring + ((s / kWarps) % C::STAGES) * St::BYTES;
+      // ---- S^T = K q^T
+      float sc[NT][2][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int w = 0; w < Step::KB / 4; ++w) {  // 8 dims of each of the two keys
-        uint32_t a[4], c[4];
-        e2m1x8(f.k[0].w[w], a);
-        e2m1x8(f.k[1].w[w], c);
-        const uint32_t b0 = (f.ks[0] >> (8 * (w >> 1))) & 0xFFu, b1 = (f.ks[1] >> (8 * (w >> 1))) & 0xFFu;
-        const uint32_t s0 = e4m3x2_f16(b0 * 0x101u), s1 = e4m3x2_f16(b1 * 0x101u);
+        for (int n = 0; n < 2; ++n) sc[nt][n][0] = sc[nt][n][1] = sc[nt][n][2] = sc[nt][n][3] = 0.f;
+      uint32_t ks[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          a[i] = mul_f16x2(a[i], s0);
-          c[i] = mul_f16x2(c[i], s1);
-        }
+      for (int i = 0; i < 4; ++i) ks[i] = lds_scales<St::KS>(st + St::OFF_KS + (k_row + 8 * i) * St::SROW + t * St::KS);
+#pragma unroll
+      for (int w16 = 0; w16 < (St::KB + 15) / 16; ++w16) {  // 16 bytes (or all 8) of each key
+      constexpr int LB = St::KB < 16 ? St::KB : 16;
+      uint32_t kw[4][LB / 4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) lds<LB>(kw[i], st + ((k_at + i * 8 * St::ROW) ^ (w16 << 4)));
+#pragma unroll
+      for (int wi = 0; wi < LB / 4; ++wi) {  // 8 dims of each key
+        const int w = w16 * 4 + wi;
+        uint2 q0[NT], q1[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma_f16(sc[nt], a[0], c[0], a[1], c[1], qf[nt][2 * w][0], qf[nt][2 * w][1]);
-          mma_f16(sc[nt], a[2], c[2], a[3], c[3], qf[nt][2 * w + 1][0], qf[nt][2 * w + 1][1]);
+          if constexpr (C::Q_SMEM) {
+            q0[nt] = q_s[(nt * (D / 16) + 2 * w) * 32 + lane];
+            q1[nt] = q_s[(nt * (D / 16) + 2 * w + 1) * 32 + lane];
+          } else {
+            q0[nt] = make_uint2(qf[nt][2 * w][0], qf[nt][2 * w][1]);
+            q1[nt] = make_uint2(qf[nt][2 * w + 1][0], qf[nt][2 * w + 1][1]);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          uint32_t a[4], c[4];
+          e2m1x8(kw[2 * n][wi], a);
+          e2m1x8(kw[2 * n + 1][wi], c);
+          const uint32_t twice = (w >> 1) * 0x1111u;  // the scale's byte, twice
+          const uint32_t s0 = e4m3x2_f16(__byte_perm(ks[2 * n], 0, twice));
+          const uint32_t s1 = e4m3x2_f16(__byte_perm(ks[2 * n + 1], 0, twice));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            a[i] = mul_f16x2(a[i], s0);
+            c[i] = mul_f16x2(c[i], s1);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_f16(sc[nt][n], a[0], c[0], a[1], c[1], q0[nt].x, q0[nt].y);
+            mma_f16(sc[nt][n], a[2], c[2], a[3], c[3], q1[nt].x, q1[nt].y);
+          }
         }
       }
-      uint32_t pb[NT][2];
-      const bool edge = key + 16 > all_end;  // some row does not see every key of the step
+      }
+      // ---- softmax
+      uint32_t pb[NT][2][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float x[4];
+        float x[2][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[e] = sc[nt][e] * fac[nt][e & 1];
-          if (edge && key + g + 8 * (e >> 1) >= lim[nt][e & 1]) x[e] = -INFINITY;
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[n][e] = fmaf(sc[nt][n][e], fac[nt][e & 1], -m[nt][e & 1]);
+        if (key + kStepKeys > all_end) {  // some row does not see every key of the step
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (key + 16 * n + k_row + 8 * (e >> 1) >= lim[nt][e & 1]) x[n][e] = -INFINITY;
         }
         // the reference maximum moves when a logit passes it by 8 (in log2
         // units): P stays below 2^8, which fp16 and the fp32 sums carry
-        const bool grow = fmaxf(x[0], x[2]) > m[nt][0] + 8.f || fmaxf(x[1], x[3]) > m[nt][1] + 8.f;
-        if (__any_sync(0xffffffffu, grow)) {
+        const float top = fmax3(fmax3(x[0][0], x[0][1], x[0][2]), fmax3(x[0][3], x[1][0], x[1][1]),
+                                fmaxf(x[1][2], x[1][3]));
+        if (__any_sync(0xffffffffu, top > 8.f)) {
+          // from the logits again: subtracting kNone has lost their bits
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float top = fmaxf(x[i], x[i + 2]);
+            float y = m[nt][i];
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            const float now = fmaxf(m[nt][i], top);
-            const float alpha = now == m[nt][i] ? 1.f : ex2f(m[nt][i] - now);
-            m[nt][i] = now;
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int e = i; e < 4; e += 2) {
+                x[n][e] = x[n][e] == -INFINITY ? -INFINITY : sc[nt][n][e] * fac[nt][i];
+                y = fmaxf(y, x[n][e]);
+              }
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
+            const float alpha = ex2f(m[nt][i] - y);
+            m[nt][i] = y;
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int e = i; e < 4; e += 2) x[n][e] -= y;
             l[nt][i] *= alpha;
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
@@ -420,50 +522,51 @@ __global__ void __launch_bounds__(kThreads, SmallCfg<D, NT>::CTAS) kv4_small_ker
           }
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float ref = m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1];
-          x[e] = ex2f(x[e] - ref);
-          l[nt][e & 1] += x[e];
+        for (int n = 0; n < 2; ++n) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[n][e] = ex2f(x[n][e]);
+            l[nt][e & 1] += x[n][e];
+          }
+          pb[nt][n][0] = movmatrix(pack_f16x2(x[n][0], x[n][1]));
+          pb[nt][n][1] = movmatrix(pack_f16x2(x[n][2], x[n][3]));
         }
-        pb[nt][0] = movmatrix(pack_f16x2(x[0], x[1]));
-        pb[nt][1] = movmatrix(pack_f16x2(x[2], x[3]));
       }
-      if (key + 16 > seen_end) {
-        // slots past the last key may hold anything: a NaN scale would pass
-        // through P = 0
+      // ---- O^T += V^T P^T
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (key + 2 * t + (i & 1) + 8 * (i >> 1) >= seen_end) f.vs[i] = 0;
-      }
-#pragma unroll
-      for (int w = 0; w < Step::VB / 4; ++w) {  // 8 dims of each of the four keys
-        const int sh = 8 * (w >> 1);
-        const uint32_t s01 = e4m3x2_f16(((f.vs[0] >> sh) & 0xFFu) | (((f.vs[1] >> sh) & 0xFFu) << 8));
-        const uint32_t s89 = e4m3x2_f16(((f.vs[2] >> sh) & 0xFFu) | (((f.vs[3] >> sh) & 0xFFu) << 8));
-        uint32_t a[4], b[4], c[4], d[4];
-        e2m1x8(select_nibbles(f.v[0].w[w], f.v[1].w[w] << 4), a);
-        e2m1x8(select_nibbles(f.v[0].w[w] >> 4, f.v[1].w[w]), b);
-        e2m1x8(select_nibbles(f.v[2].w[w], f.v[3].w[w] << 4), c);
-        e2m1x8(select_nibbles(f.v[2].w[w] >> 4, f.v[3].w[w]), d);
+      for (int n = 0; n < 2; ++n) {
+        uint32_t vw[4][St::VB / 4], vs[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          a[i] = mul_f16x2(a[i], s01);
-          b[i] = mul_f16x2(b[i], s01);
-          c[i] = mul_f16x2(c[i], s89);
-          d[i] = mul_f16x2(d[i], s89);
+          const int more = 16 * n + 8 * (i >> 1);
+          lds<St::VB>(vw[i], st + v_at[i & 1] + more * St::ROW);
+          vs[i] = lds_scales<St::VS>(st + St::OFF_VS + (v_row[i & 1] + more) * St::SROW + g * St::VB / 8);
+        }
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][4 * w + i], a[i], b[i], c[i], d[i], pb[nt][0], pb[nt][1]);
+        for (int w = 0; w < St::VB / 4; ++w) {  // 8 dims of each key
+          const uint32_t pair = (w >> 1) * 0x11u + 0x40u;  // byte w >> 1 of two keys' scales
+          const uint32_t s01 = e4m3x2_f16(__byte_perm(vs[0], vs[1], pair));
+          const uint32_t s89 = e4m3x2_f16(__byte_perm(vs[2], vs[3], pair));
+          uint32_t a[4], b4[4], c[4], d[4];
+          e2m1x8(select_nibbles(vw[0][w], vw[1][w] << 4), a);
+          e2m1x8(select_nibbles(vw[0][w] >> 4, vw[1][w]), b4);
+          e2m1x8(select_nibbles(vw[2][w], vw[3][w] << 4), c);
+          e2m1x8(select_nibbles(vw[2][w] >> 4, vw[3][w]), d);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            a[i] = mul_f16x2(a[i], s01);
+            b4[i] = mul_f16x2(b4[i], s01);
+            c[i] = mul_f16x2(c[i], s89);
+            d[i] = mul_f16x2(d[i], s89);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_f16(o[nt][4 * w + i], a[i], b4[i], c[i], d[i], pb[nt][n][0], pb[nt][n][1]);
+          }
         }
       }
-    };
-    for (int s = warp; s < steps; s += 2 * kWarps) {
-      pid0 = step_page(s + 2 * kWarps);
-      load_step(nxt, s + kWarps, pid1);
-      compute(cur, s);
-      pid1 = step_page(s + 3 * kWarps);
-      load_step(cur, s + 2 * kWarps, pid0);
-      if (s + kWarps < steps) compute(nxt, s + kWarps);
     }
+    cp_async_wait<0>();
+    __syncthreads();  // the states take the ring's place
 
     // ---- the warps' states are joined
 #pragma unroll
@@ -485,18 +588,21 @@ __global__ void __launch_bounds__(kThreads, SmallCfg<D, NT>::CTAS) kv4_small_ker
       }
     __syncthreads();
     const bool whole = unit0 == 0 && seg_end == tile_u + kts;
+    auto out_row = [&](int n) -> int64_t {
+      const int r = row0 + n;
+      return static_cast<int64_t>(rq.qo_start + r / p.G) * p.Hq + h * p.G + r % p.G;
+    };
     const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (first_segment ? 0 : 1)) * C::ROWS;
     for (int i = tid; i < rows * (D / 4); i += kThreads) {
       const int n = i / (D / 4), d = (i % (D / 4)) * 4;
-      float top = -INFINITY;
+      float top = kNone;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) top = fmaxf(top, m_s[w * C::ROWS + n]);
-      const float ref = top == -INFINITY ? 0.f : top;
       float sum = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float a = ex2f(m_s[w * C::ROWS + n] - ref);
+        const float a = ex2f(m_s[w * C::ROWS + n] - top);
         const float4 v = *reinterpret_cast<const float4*>(o_s + (w * C::ROWS + n) * C::O_STRIDE + d);
         sum += a * l_s[w * C::ROWS + n];
         acc.x += a * v.x;
@@ -506,20 +612,103 @@ __global__ void __launch_bounds__(kThreads, SmallCfg<D, NT>::CTAS) kv4_small_ker
       }
       // a row that sees no key: zeros, and -inf as its lse
       const float inv = sum == 0.f ? 0.f : (whole ? p.v_scale : 1.f) / sum;
-      const float lse2 = sum == 0.f ? -INFINITY : ref + log2f(sum);
+      const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum);
       acc.x *= inv;
       acc.y *= inv;
       acc.z *= inv;
       acc.w *= inv;
       if (whole) {
-        const int r = row0 + n;
-        const int64_t row = static_cast<int64_t>(rq.qo_start + r / p.G) * p.Hq + h * p.G + r % p.G;
+        const int64_t row = out_row(n);
         *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + row * D + d) =
             make_uint2(Elt<T>::from_f2(acc.x, acc.y), Elt<T>::from_f2(acc.z, acc.w));
         if (d == 0 && p.lse) p.lse[row] = lse2 * kLn2f;
       } else {
         *reinterpret_cast<float4*>(p.part_o + (part + n) * D + d) = acc;
         if (d == 0) p.part_lse[part + n] = lse2;
+      }
+    }
+    if (!whole) {
+      // ---- the last slice of a cut row tile joins its parts:
+      // o = sum_s 2^(lse_s - lse) o_s.  The sum's order is the slices', so
+      // the result does not depend on which one comes last.
+      const int sa = static_cast<int>(tile_u / per_slice), sb = static_cast<int>((tile_u + kts - 1) / per_slice);
+      const bool sa_first = tile_u == sa * per_slice;
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        int32_t* count = p.counters + (sa + 1) * p.g.Hkv + h;
+        const int before_me = atomicAdd(count, 1);
+        last_s = before_me == sb - sa;
+        if (last_s) *count = 0;  // for the next run
+      }
+      __syncthreads();
+      if (last_s) {
+        __threadfence();
+        auto part_row = [&](int sl) -> int64_t {
+          const int which = (sl == sa && !sa_first) ? 1 : 0;
+          return ((static_cast<int64_t>(sl) * p.g.Hkv + h) * 2 + which) * C::ROWS;
+        };
+        constexpr int COLS = D / 4;                              // float4 columns of a row
+        constexpr int GROUPS = kThreads / COLS;                  // rows x part groups at a time
+        constexpr int RP = GROUPS < C::ROWS ? GROUPS : C::ROWS;  // rows at a time
+        constexpr int PG = GROUPS / RP;                          // groups that share a row's parts
+        float4* acc_s = reinterpret_cast<float4*>(o_s);          // [threads]
+        float2* ms_s = reinterpret_cast<float2*>(acc_s + kThreads);  // [threads]
+        const int col = tid % COLS, grp = tid / COLS, pg = grp / RP;
+        for (int n0 = 0; n0 < rows; n0 += RP) {
+          const int n = n0 + grp % RP;
+          const bool in = n < rows && pg < PG;
+          float top = kNone, sum = 0.f;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (in) {
+#pragma unroll 4
+            for (int sl = sa + pg; sl <= sb; sl += PG) top = fmaxf(top, __ldcg(p.part_lse + part_row(sl) + n));
+#pragma unroll 4
+            for (int sl = sa + pg; sl <= sb; sl += PG) {
+              const int64_t row = part_row(sl) + n;
+              const float a = ex2f(__ldcg(p.part_lse + row) - top);
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + row * D + col * 4));
+              sum += a;
+              acc.x += a * v.x;
+              acc.y += a * v.y;
+              acc.z += a * v.z;
+              acc.w += a * v.w;
+            }
+          }
+          if constexpr (PG > 1) {
+            acc_s[tid] = acc;
+            ms_s[tid] = make_float2(top, sum);
+            __syncthreads();
+            if (in && pg == 0) {
+              float all = kNone;
+#pragma unroll
+              for (int k = 0; k < PG; ++k) all = fmaxf(all, ms_s[tid + k * RP * COLS].x);
+              sum = 0.f;
+              acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+              for (int k = 0; k < PG; ++k) {
+                const int at = tid + k * RP * COLS;
+                const float2 ms = ms_s[at];
+                const float a = ex2f(ms.x - all);
+                const float4 v = acc_s[at];
+                sum += a * ms.y;
+                acc.x += a * v.x;
+                acc.y += a * v.y;
+                acc.z += a * v.z;
+                acc.w += a * v.w;
+              }
+              top = all;
+            }
+            __syncthreads();
+          }
+          if (in && pg == 0) {
+            const float inv = sum == 0.f ? 0.f : p.v_scale / sum;
+            const int64_t row = out_row(n);
+            *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + row * D + col * 4) = make_uint2(
+                Elt<T>::from_f2(acc.x * inv, acc.y * inv), Elt<T>::from_f2(acc.z * inv, acc.w * inv));
+            if (col == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2f;
+          }
+        }
       }
     }
     __syncthreads();  // the buffers are the next row tile's
@@ -529,122 +718,48 @@ __global__ void __launch_bounds__(kThreads, SmallCfg<D, NT>::CTAS) kv4_small_ker
       req_u += static_cast<long long>(row_tiles(p, rq, C::ROWS)) * kts;
       do {
         if (++b >= p.batch) return;
-        rq = load_req(p, b);
+        rq = b < kept_b ? req_s[b - first_b] : load_req(p, b);
       } while (row_tiles(p, rq, C::ROWS) == 0);
     }
   }
 }
 
-// One CTA per slice boundary and kv head: where the boundary is the first one
-// inside a row tile, the partial states of all slices that the tile spans are
-// joined, o = sum_s 2^(lse_s - lse) o_s.
-constexpr int kMergeThreads = 512;
-
-template <typename T, int D, int ROWS>
-__global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(const Kv4Params p) {
-  constexpr int COLS = D / 4;                        // float4 columns of a row
-  constexpr int GROUPS = kMergeThreads / COLS;       // rows x part groups at a time
-  constexpr int RP = GROUPS < ROWS ? GROUPS : ROWS;  // rows at a time
-  constexpr int PG = GROUPS / RP;                    // groups that share a row's parts
-  __shared__ float4 acc_s[kMergeThreads];
-  __shared__ float sum_s[kMergeThreads], top_s[kMergeThreads];
-  pdl_wait();
-  const int h = blockIdx.x % p.g.Hkv, slice = blockIdx.x / p.g.Hkv + 1;
-  const Kv4Split s = p.splits[slice];
-  if (!s.valid) return;
-  const int sa = static_cast<int>(s.u0 / s.per_slice), sb = static_cast<int>((s.u1 - 1) / s.per_slice);
-  if (sa != slice - 1) return;  // an earlier boundary's
-  const bool sa_first = s.u0 == sa * s.per_slice;
-  auto part_row = [&](int sl) {
-    const int which = (sl == sa && !sa_first) ? 1 : 0;
-    return ((static_cast<int64_t>(sl) * p.g.Hkv + h) * 2 + which) * ROWS;
-  };
-  const int col = threadIdx.x % COLS, grp = threadIdx.x / COLS, pg = grp / RP;
-  const int rows = min(ROWS, s.rows - s.row_tile * ROWS);
-  for (int n0 = 0; n0 < rows; n0 += RP) {
-    const int n = n0 + grp % RP;
-    const bool in = n < rows && pg < PG;
-    float top = -INFINITY, sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (in) {
-      for (int sl = sa + pg; sl <= sb; sl += PG) top = fmaxf(top, p.part_lse[part_row(sl) + n]);
-      const float ref = top == -INFINITY ? 0.f : top;
-#pragma unroll 4
-      for (int sl = sa + pg; sl <= sb; sl += PG) {
-        const int64_t row = part_row(sl) + n;
-        const float a = ex2f(p.part_lse[row] - ref);
-        const float4 v = *reinterpret_cast<const float4*>(p.part_o + row * D + col * 4);
-        sum += a;
-        acc.x += a * v.x;
-        acc.y += a * v.y;
-        acc.z += a * v.z;
-        acc.w += a * v.w;
-      }
-    }
-    acc_s[threadIdx.x] = acc;
-    sum_s[threadIdx.x] = sum;
-    top_s[threadIdx.x] = top;
-    __syncthreads();
-    if (in && pg == 0) {
-      float all = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < PG; ++k) all = fmaxf(all, top_s[threadIdx.x + k * RP * COLS]);
-      const float ref = all == -INFINITY ? 0.f : all;
-      sum = 0.f;
-      acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int k = 0; k < PG; ++k) {
-        const int at = threadIdx.x + k * RP * COLS;
-        const float a = ex2f(top_s[at] - ref);  // 0 where the group had no part
-        const float4 v = acc_s[at];
-        sum += a * sum_s[at];
-        acc.x += a * v.x;
-        acc.y += a * v.y;
-        acc.z += a * v.z;
-        acc.w += a * v.w;
-      }
-      const float inv = sum == 0.f ? 0.f : p.v_scale / sum;
-      const int r = s.row_tile * ROWS + n;
-      const int64_t row = static_cast<int64_t>(s.qo_row0 + r / p.G) * p.Hq + h * p.G + r % p.G;
-      *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + row * D + col * 4) = make_uint2(
-          Elt<T>::from_f2(acc.x * inv, acc.y * inv), Elt<T>::from_f2(acc.z * inv, acc.w * inv));
-      if (col == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2f;
-    }
-    __syncthreads();
-  }
+// 8-row groups of a tile: as many as the longest request needs, of 1, 2 or 4
+// (the registers of head_dim 256 allow one).
+int row_groups(const Kv4Shape& s) {
+  if (s.D == 256 || s.max_rows <= 8) return 1;
+  return s.max_rows <= 16 ? 2 : 4;
 }
-
-// Packed rows of a tile: 8 where no request has more (or the registers of
-// head_dim 256 allow no more), else 16.
-int tile_rows(const Kv4Shape& s) { return s.max_rows <= 8 || s.D == 256 ? 8 : 16; }
 
 template <typename T, int D, int NT>
 cudaError_t launch_small(const Kv4Params& p, cudaStream_t stream) {
   using C = SmallCfg<D, NT>;
   const unsigned grid = static_cast<unsigned>(p.slices) * p.g.Hkv;
-  static std::atomic<uint64_t> set_a{0}, set_b{0};
-  cudaError_t e;
-  if (p.g.ps < 16) {
-    auto* k = kv4_small_kernel<T, D, NT, true>;
-    e = set_smem_once(set_a, reinterpret_cast<const void*>(k), C::SMEM);
-    if (e == cudaSuccess) e = launch_pdl(k, grid, unsigned(kThreads), size_t(C::SMEM), stream, p);
+  static std::atomic<uint64_t> set{0};
+  auto* k = kv4_small_kernel<T, D, NT>;
+  cudaError_t e = set_smem_once(set, reinterpret_cast<const void*>(k), C::SMEM);
+  return e != cudaSuccess ? e : launch_pdl(k, grid, unsigned(C::THREADS), size_t(C::SMEM), stream, p);
+}
+
+template <typename T, int D>
+cudaError_t launch_d(const Kv4Params& p, const Kv4Shape& s, cudaStream_t stream) {
+  if constexpr (D == 256) {
+    return launch_small<T, 256, 1>(p, stream);
   } else {
-    auto* k = kv4_small_kernel<T, D, NT, false>;
-    e = set_smem_once(set_b, reinterpret_cast<const void*>(k), C::SMEM);
-    if (e == cudaSuccess) e = launch_pdl(k, grid, unsigned(kThreads), size_t(C::SMEM), stream, p);
+    switch (row_groups(s)) {
+      case 1: return launch_small<T, D, 1>(p, stream);
+      case 2: return launch_small<T, D, 2>(p, stream);
+      default: return launch_small<T, D, 4>(p, stream);
+    }
   }
-  if (e != cudaSuccess || p.slices < 2) return e;
-  return launch_pdl(kv4_merge_kernel<T, D, C::ROWS>, static_cast<unsigned>(p.slices - 1) * p.g.Hkv,
-                    unsigned(kMergeThreads), size_t(0), stream, p);
 }
 
 template <typename T>
 cudaError_t launch_t(const Kv4Params& p, const Kv4Shape& s, cudaStream_t stream) {
-  const bool wide = tile_rows(s) == 16;
   switch (s.D) {
-    case 64: return wide ? launch_small<T, 64, 2>(p, stream) : launch_small<T, 64, 1>(p, stream);
-    case 128: return wide ? launch_small<T, 128, 2>(p, stream) : launch_small<T, 128, 1>(p, stream);
-    default: return launch_small<T, 256, 1>(p, stream);
+    case 64: return launch_d<T, 64>(p, s, stream);
+    case 128: return launch_d<T, 128>(p, s, stream);
+    default: return launch_d<T, 256>(p, s, stream);
   }
 }
 
@@ -654,12 +769,15 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 Kv4Layout kv4_layout(const Kv4Shape& s) {
   Kv4Layout l;
-  const int per_sm = s.D == 256 ? 1 : 2;
+  const int nt = row_groups(s);
+  const int per_sm = s.D * nt <= 256 && s.D < 256 ? 2 : 1;  // SmallCfg::CTAS
   const int slices = per_sm * s.num_sms / s.Hkv;
   l.slices = slices > 0 ? slices : 1;
-  const size_t rows = size_t(l.slices) * s.Hkv * 2 * tile_rows(s);
-  l.off_splits = 256;  // after the status word
-  l.off_part_o = up256(l.off_splits + size_t(l.slices) * sizeof(Kv4Split));
+  const size_t rows = size_t(l.slices) * s.Hkv * 2 * 8 * nt;
+  l.off_counters = 256;  // after the status word
+  // the counters' place is the same for every shape: they have to stay zero
+  // between runs (more than two slices a kv head and SM there never are)
+  l.off_part_o = up256(l.off_counters + size_t(2) * s.num_sms * sizeof(int32_t));
   l.off_part_lse = up256(l.off_part_o + rows * s.D * sizeof(float));
   l.total = up256(l.off_part_lse + rows * sizeof(float));
   return l;

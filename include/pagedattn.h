@@ -491,9 +491,10 @@ PAGEDATTN_API pagedattn_status pagedattn_kv4_workspace_size(int32_t num_qo_heads
  *           elements apart (a multiple of 8), 16-byte aligned.
  * out       device, dtype[num_tokens][num_qo_heads][head_dim], 16-byte aligned.
  * lse       device, float[num_tokens][num_qo_heads], or NULL.
- * workspace device, 256-byte aligned, pagedattn_kv4_workspace_size() bytes.  Its
- *           first word is the status word: zero it once.  Calls that overlap on
- *           the device need different workspaces.
+ * workspace device, 256-byte aligned, pagedattn_kv4_workspace_size() bytes: zero
+ *           it once, before its first run.  Its first word is the status word.
+ *           Calls that overlap on the device need different workspaces; runs of
+ *           other shapes or batches may share one, one after the other.
  *
  * A table entry that cannot be (indptr out of order or out of range, a last
  * page length outside [1, page_size]) leaves its request's rows unwritten, a
