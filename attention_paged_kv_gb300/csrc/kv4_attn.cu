@@ -36,6 +36,7 @@
 // So the cache goes from global memory to registers and into the MMA without
 // shared memory.
 #include <cstring>
+#include <type_traits>
 
 #include "internal.h"
 #include "kv4_common.cuh"
@@ -83,7 +84,15 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// BYTES of shared memory at `at` in registers.
+// The same with a zero sum to start from.
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 template <int BYTES>
 __device__ __forceinline__ void lds(uint32_t (&r)[BYTES / 4], uint32_t at) {
   if constexpr (BYTES == 4) {
@@ -99,20 +108,23 @@ __device__ __forceinline__ void lds(uint32_t (&r)[BYTES / 4], uint32_t at) {
 // 1, 2 or 4 bytes of shared memory.
 template <int BYTES>
 __device__ __forceinline__ uint32_t lds_scales(uint32_t at) {
-  if constexpr (BYTES == 4) {
-    uint32_t r;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(at));
-    return r;
-  } else {
-    uint16_t r;
-    if constexpr (BYTES == 2) asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(at));
-    else asm volatile("ld.shared.u8 %0, [%1];" : "=h"(r) : "r"(at));
-    return r;
-  }
+  uint32_t r;
+  if constexpr (BYTES == 4) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(at));
+  else if constexpr (BYTES == 2) asm volatile("ld.shared.u16 %0, [%1];" : "=r"(r) : "r"(at));
+  else asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(at));
+  return r;
 }
-// cp.async of N bytes (through L2 alone where N = 16); zeros where !live.
+// cp.async of N bytes (through L2 alone where N = 16), and one that writes
+// zeros where !live.
 template <int N>
-__device__ __forceinline__ void cp_async(uint32_t dst, const uint8_t* src, bool live = true) {
+__device__ __forceinline__ void cp_async(uint32_t dst, const uint8_t* src) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_or_zero(uint32_t dst, const uint8_t* src, bool live) {
   if constexpr (N == 16)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
   else
@@ -292,35 +304,49 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
       const int key = key_a + s * kStepKeys + lane;
       return s < steps && key < key_b ? __ldg(page_ids + (key >> p.g.ps_shift)) : 0;
     };
-    // copies step s into its stage; `pids` from step_page(s)
-    auto copy_step = [&](int s, int pids) {
+    // copies step s into the stage at `st`; `pids` from step_page(s)
+    auto copy_rows = [&](int key, uint32_t st, int pids, auto tail) {
+      constexpr bool kTail = decltype(tail)::value;  // rows of keys that no row sees are zeros
+#pragma unroll
+      for (int i = 0; i < St::LANES; ++i) {
+        constexpr int RPP = 32 / St::LANES;
+        const int r = i * RPP + copy_row;
+        const uint32_t pid = __shfl_sync(0xffffffffu, pids, r);
+        const uint32_t slot = (key + r) & (p.g.ps - 1);
+        const uint8_t* src = codes_h + static_cast<uint64_t>(pid) * page_bytes + static_cast<uint64_t>(slot) * slot_bytes;
+        // (the swizzle of a 4-row pass changes with bit 2 of its first row)
+        const uint32_t dst = st + ((copy_to + i * RPP * St::ROW) ^ (D == 256 ? (i & 1) << 4 : 0));
+        if constexpr (kTail) {
+          const bool live = key + r < key_b;
+          cp_async_or_zero<16>(dst, src, live);
+          cp_async_or_zero<16>(dst + St::OFF_V, src + (page_bytes >> 1), live);
+        } else {
+          cp_async<16>(dst, src);
+          cp_async<16>(dst + St::OFF_V, src + (page_bytes >> 1));
+        }
+      }
+      const uint32_t slot = (key + lane) & (p.g.ps - 1);
+      const uint8_t* src = scales_h + static_cast<uint64_t>(static_cast<uint32_t>(pids)) * (page_bytes >> 3) +
+                           static_cast<uint64_t>(slot) * (slot_bytes >> 3);
+      const uint32_t dst = st + St::OFF_KS + lane * St::SROW;
+      if constexpr (kTail) {
+        const bool live = key + lane < key_b;
+        cp_async_or_zero<St::SROW>(dst, src, live);
+        cp_async_or_zero<St::SROW>(dst + St::OFF_VS - St::OFF_KS, src + (page_bytes >> 4), live);
+      } else {
+        cp_async<St::SROW>(dst, src);
+        cp_async<St::SROW>(dst + St::OFF_VS - St::OFF_KS, src + (page_bytes >> 4));
+      }
+    };
+    auto copy_step = [&](int s, uint32_t st, int pids) {
       if (s < steps) {
         if (static_cast<unsigned>(pids) >= static_cast<unsigned>(p.g.num_pages)) {
           atomicOr(p.status, PA_DEV_BAD_INDEX);
           pids = 0;
         }
         const int key = key_a + s * kStepKeys;
-        const uint32_t st = ring + ((s / kWarps) % C::STAGES) * St::BYTES;
-        const bool tail = key + kStepKeys > key_b;  // rows of keys that no row sees are zeros
-#pragma unroll
-        for (int i = 0; i < St::LANES; ++i) {
-          constexpr int RPP = 32 / St::LANES;
-          const int r = i * RPP + copy_row;
-          const uint32_t pid = __shfl_sync(0xffffffffu, pids, r);
-          const uint32_t slot = (key + r) & (p.g.ps - 1);
-          const uint8_t* src = codes_h + static_cast<uint64_t>(pid) * page_bytes + static_cast<uint64_t>(slot) * slot_bytes;
-          // (the swizzle of a 4-row pass changes with bit 2 of its first row)
-          const uint32_t dst = st + ((copy_to + i * RPP * St::ROW) ^ (D == 256 ? (i & 1) << 4 : 0));
-          const bool live = !tail || key + r < key_b;
-          cp_async<16>(dst, src, live);
-          cp_async<16>(dst + St::OFF_V, src + (page_bytes >> 1), live);
-        }
-        const uint32_t slot = (key + lane) & (p.g.ps - 1);
-        const uint8_t* src = scales_h + static_cast<uint64_t>(static_cast<uint32_t>(pids)) * (page_bytes >> 3) +
-                             static_cast<uint64_t>(slot) * (slot_bytes >> 3);
-        const bool live = !tail || key + lane < key_b;
-        cp_async<St::SROW>(st + St::OFF_KS + lane * St::SROW, src, live);
-        cp_async<St::SROW>(st + St::OFF_VS + lane * St::SROW, src + (page_bytes >> 4), live);
+        if (key + kStepKeys <= key_b) copy_rows(key, st, pids, std::false_type{});
+        else copy_rows(key, st, pids, std::true_type{});
       }
       cp_async_commit();
     };
@@ -389,7 +415,7 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
       __syncthreads();
     }
 #pragma unroll
-    for (int i = 0; i < C::STAGES - 1; ++i) copy_step(warp + i * kWarps, pids[i]);
+    for (int i = 0; i < C::STAGES - 1; ++i) copy_step(warp + i * kWarps, ring + i * St::BYTES, pids[i]);
     int next_pids = pids[C::STAGES - 1];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -414,21 +440,23 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
       l[nt][0] = l[nt][1] = 0.f;
     }
 
-    for (int s = warp; s < steps; s += kWarps) {
+    // One step; kEdge: some row does not see every key of it.
+    uint32_t st_read = ring, st_write = ring + (C::STAGES - 1) * St::BYTES;
+    const uint32_t ring_end = ring + C::STAGES * St::BYTES;
+    auto step = [&](int s, auto edge) {
+      constexpr bool kEdge = decltype(edge)::value;
       const int key = key_a + s * kStepKeys;
       // the step's stage has landed, and every lane is done with the one
       // that the copies below overwrite
       cp_async_wait<C::STAGES - 2>();
       __syncwarp();
-      copy_step(s + (C::STAGES - 1) * kWarps, next_pids);
+      copy_step(s + (C::STAGES - 1) * kWarps, st_write, next_pids);
       next_pids = step_page(s + C::STAGES * kWarps);
-      const uint32_t st = ring + ((s / kWarps) % C::STAGES) * St::BYTES;
+      const uint32_t st = st_read;
+      st_write = st;
+      st_read = st + St::BYTES == ring_end ? ring : st + St::BYTES;
       // ---- S^T = K q^T
       float sc[NT][2][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int n = 0; n < 2; ++n) sc[nt][n][0] = sc[nt][n][1] = sc[nt][n][2] = sc[nt][n][3] = 0.f;
       uint32_t ks[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) ks[i] = lds_scales<St::KS>(st + St::OFF_KS + (k_row + 8 * i) * St::SROW + t * St::KS);
@@ -467,7 +495,8 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            mma_f16(sc[nt][n], a[0], c[0], a[1], c[1], q0[nt].x, q0[nt].y);
+            if (w == 0) mma_f16_first(sc[nt][n], a[0], c[0], a[1], c[1], q0[nt].x, q0[nt].y);
+            else mma_f16(sc[nt][n], a[0], c[0], a[1], c[1], q0[nt].x, q0[nt].y);
             mma_f16(sc[nt][n], a[2], c[2], a[3], c[3], q1[nt].x, q1[nt].y);
           }
         }
@@ -482,7 +511,7 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
         for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[n][e] = fmaf(sc[nt][n][e], fac[nt][e & 1], -m[nt][e & 1]);
-        if (key + kStepKeys > all_end) {  // some row does not see every key of the step
+        if constexpr (kEdge) {
 #pragma unroll
           for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -564,7 +593,10 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
           }
         }
       }
-    }
+    };
+    int s = warp;
+    for (; s < steps && key_a + (s + 1) * kStepKeys <= all_end; s += kWarps) step(s, std::false_type{});
+    for (; s < steps; s += kWarps) step(s, std::true_type{});
     cp_async_wait<0>();
     __syncthreads();  // the states take the ring's place
 
