@@ -74,19 +74,19 @@ struct Kv4Params {
   float* part_lse;   // [slices * Hkv * 2][rows of a tile], base-2, v_scale not in it
   int64_t q_stride;  // elements between tokens
   Kv4Geom g;
-  int32_t batch, num_tokens, num_page_indices, Hq, G, causal, slices;
+  int32_t batch, num_tokens, num_page_indices, Hq, G, causal, slices, cta_heads;
   int32_t small_rows;  // requests of more packed rows are the prefill kernel's
   float scale_log2;    // log2(e) / sqrt(D) * k_scale
   float v_scale;
 };
 
 struct Kv4Shape {  // what the launch and its workspace depend on
-  int32_t D, Hkv, G, num_sms, max_rows;  // max_rows: packed rows of the longest request
+  int32_t D, Hkv, G, num_sms, max_rows, batch;  // max_rows: packed rows of the longest request
 };
 
 // Bytes of a run's workspace, and where its parts lie in it.
 struct Kv4Layout {
-  int32_t slices;
+  int32_t slices, cta_heads;
   size_t off_counters, off_part_o, off_part_lse, total;
 };
 Kv4Layout kv4_layout(const Kv4Shape& s);

@@ -189,6 +189,7 @@ pagedattn_status pagedattn_kv4_workspace_size(int32_t num_qo_heads, int32_t num_
   shape.G = num_qo_heads / num_kv_heads;
   const int64_t rows = int64_t(max_qo_len) * shape.G;
   shape.max_rows = rows < (1 << 30) ? int32_t(rows) : (1 << 30);
+  shape.batch = 1;
   *bytes = pa::kv4_layout(shape).total;
   return PA_OK;
 }
@@ -219,6 +220,7 @@ pagedattn_status pagedattn_kv4_run(const pagedattn_kv4_cache* cache, const paged
   shape.G = batch->num_qo_heads / cache->num_kv_heads;
   const int64_t rows = int64_t(batch->max_qo_len) * shape.G;
   shape.max_rows = rows < (1 << 30) ? int32_t(rows) : (1 << 30);
+  shape.batch = batch->batch_size;
   const pa::Kv4Layout lay = pa::kv4_layout(shape);
   if (workspace_bytes < lay.total)
     return set_err(PA_ERR_WORKSPACE_TOO_SMALL, "workspace needs " + std::to_string(lay.total) + " bytes, got " +
@@ -259,6 +261,7 @@ pagedattn_status pagedattn_kv4_run(const pagedattn_kv4_cache* cache, const paged
   const int64_t key_units = int64_t(batch->num_page_indices) * cache->page_size / 64 + batch->batch_size;
   const int64_t most = (key_units * tiles + 3) / 4;
   p.slices = most < lay.slices ? int32_t(most) : lay.slices;
+  p.cta_heads = lay.cta_heads;
   // the bound alone decides whether the tensor-core kernel is launched; where
   // it is not, the small-query kernel takes every request
   const bool prefill = shape.max_rows > pa::kKv4SmallRows;

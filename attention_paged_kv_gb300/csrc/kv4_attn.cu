@@ -160,25 +160,25 @@ struct Stage {
   }
 };
 
-// Stages and CTAs of an SM by head_dim and 8-row groups of a tile: O^T takes
-// D / 4 registers a lane for each group, q's fragments D / 8 (kept in shared
-// memory at 4 groups).
+// Warps of a CTA and CTAs of an SM by head_dim and 8-row groups of a tile:
+// O^T takes D / 4 registers a lane for each group, q's fragments D / 8 (kept
+// in shared memory where that passes 64).
+constexpr int small_ctas(int D, int nt) { return D < 256 && D * nt <= 256 && nt < 4 ? 2 : 1; }
+constexpr int small_warps(int D, int nt) { return small_ctas(D, nt) == 2 && D * nt == 256 ? 6 : 8; }
+
 template <int D, int NT>
 struct SmallCfg {
   static constexpr int ROWS = 8 * NT;
-  static constexpr int WARPS = D * NT == 256 && D < 256 ? 6 : 8;  // 168 registers a thread, or 128 (255 for one CTA)
+  static constexpr int WARPS = small_warps(D, NT);
   static constexpr int THREADS = 32 * WARPS;
-  static constexpr int CTAS = D * NT <= 256 && D < 256 ? 2 : 1;
+  static constexpr int CTAS = small_ctas(D, NT);
   static constexpr bool Q_SMEM = NT * D >= 512;
-  static constexpr int STAGES = CTAS == 1 && D < 256 ? 5 : (D == 64 ? 5 : (WARPS == 6 ? 4 : 3));
-  static constexpr int RING = WARPS * STAGES * Stage<D>::BYTES;
-  // after the loop the states of the warps take the ring's place (floats)
+  static constexpr int STAGES = D == 256 ? 3 : (CTAS == 1 ? 5 : (D == 64 ? 5 : (WARPS == 6 ? 4 : 3)));
+  static constexpr int RING = STAGES * Stage<D>::BYTES;  // of a warp
+  // after its loop a warp's state takes its ring's place (floats)
   static constexpr int O_STRIDE = D + 4;
-  static constexpr int STATES = WARPS * ROWS * O_STRIDE * 4;
-  static constexpr int OFF_M = RING > STATES ? RING : STATES;
-  static constexpr int OFF_L = OFF_M + WARPS * ROWS * 4;
-  static constexpr int OFF_Q = OFF_L + WARPS * ROWS * 4;
-  static constexpr int SMEM = OFF_Q + (Q_SMEM ? NT * (D / 16) * 256 : 0);
+  static_assert(ROWS * (O_STRIDE + 2) * 4 <= RING, "a warp's state fits its ring");
+  static constexpr int SMEM = WARPS * RING + (Q_SMEM ? NT * (D / 16) * 256 + ROWS * 4 : 0);
   static_assert(CTAS * (SMEM + kKeptReqs * 16 + 256 + 1024) <= 233472, "shared memory per SM");
 };
 
@@ -188,16 +188,23 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
   using St = Stage<D>;
   constexpr int kThreads = C::THREADS, kWarps = C::WARPS;
   extern __shared__ __align__(128) uint8_t smem[];
-  float* o_s = reinterpret_cast<float*>(smem);             // [warps][rows][O_STRIDE]
-  float* m_s = reinterpret_cast<float*>(smem + C::OFF_M);  // [warps][rows]
-  float* l_s = reinterpret_cast<float*>(smem + C::OFF_L);  // [warps][rows]
-  uint2* q_s = reinterpret_cast<uint2*>(smem + C::OFF_Q);  // Q_SMEM: [NT][D / 16][lane] fragments
   __shared__ long long scratch[kWarps];
   __shared__ Req req_s[kKeptReqs];  // the slice's first requests, where its scan met them
   __shared__ long long found_u;
-  __shared__ int found_b, last_s;
+  __shared__ int found_b, last_s[8];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int h = blockIdx.x % p.g.Hkv, slice = blockIdx.x / p.g.Hkv;
+  // the CTA's kv heads, and the warp's: `team` warps share one and take every
+  // team-th step each
+  const int cta_heads = C::Q_SMEM ? 1 : p.cta_heads;
+  const int groups = p.g.Hkv / cta_heads;
+  const int slice = blockIdx.x / groups, cta_head = warp % cta_heads;
+  const int h = (blockIdx.x % groups) * cta_heads + cta_head;
+  const int team = kWarps / cta_heads, member = warp / cta_heads;
+  const int rank = member * 32 + lane;  // of the team's threads
+  auto team_sync = [&]() {
+    if (team == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + cta_head), "r"(team * 32) : "memory");
+  };
   pdl_wait();
 
   // ---- the slice's units [u, u_end) and the request that they begin in
@@ -267,7 +274,13 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
   const int copy_row = lane / St::LANES, copy_chunk = lane % St::LANES;
   const uint8_t* codes_h = p.codes + static_cast<int64_t>(h) * p.g.head_rows * (D / 2) + copy_chunk * 16;
   const uint8_t* scales_h = p.scales + static_cast<int64_t>(h) * p.g.head_rows * (D / 16);
-  const uint32_t ring = smem_u32(smem) + warp * C::STAGES * St::BYTES;
+  const uint32_t ring = smem_u32(smem) + warp * C::RING;
+  // states: of member w of the team at w * team_step
+  float* o_s = reinterpret_cast<float*>(smem + cta_head * C::RING);  // [rows][O_STRIDE], then m and l of each row
+  const int team_step = cta_heads * C::RING / 4;
+  constexpr int OFF_ML = C::ROWS * C::O_STRIDE;
+  uint2* q_s = reinterpret_cast<uint2*>(smem + kWarps * C::RING);  // Q_SMEM: [NT][D / 16][lane], then the rows' factors
+  float* fac_s = reinterpret_cast<float*>(q_s + NT * (D / 16) * 32);
   const uint32_t copy_to = copy_row * St::ROW + ((copy_chunk ^ St::swizzle(copy_row & 7)) << 4);
   const int k_row = St::order(g);  // + 8 i
   const uint32_t k_at = k_row * St::ROW + ((((t * St::KB) >> 4) ^ St::swizzle(k_row)) << 4) + ((t * St::KB) & 15);
@@ -352,7 +365,7 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
     };
     int pids[C::STAGES];
 #pragma unroll
-    for (int i = 0; i < C::STAGES; ++i) pids[i] = step_page(warp + i * kWarps);
+    for (int i = 0; i < C::STAGES; ++i) pids[i] = step_page(member + i * team);
 
     // q fragments (row n = g of each 8-row group, dims [t D/4, (t+1) D/4)) and
     // the logit factors of rows 2t, 2t + 1
@@ -399,23 +412,22 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
       return my;
     };
     if constexpr (C::Q_SMEM) {
-      // warp nt makes row group nt's fragments for all
+      // warp nt makes row group nt's fragments for all (the CTA has one head)
       if (warp < NT) {
         const float my = load_q(warp, qf[0]);
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) q_s[(warp * (D / 16) + j) * 32 + lane] = make_uint2(qf[0][j][0], qf[0][j][1]);
-        if (t == 0) m_s[warp * 8 + g] = my;
+        if (t == 0) fac_s[warp * 8 + g] = my;
       }
-      __syncthreads();
+      team_sync();
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        fac[nt][0] = m_s[nt * 8 + 2 * t];
-        fac[nt][1] = m_s[nt * 8 + 2 * t + 1];
+        fac[nt][0] = fac_s[nt * 8 + 2 * t];
+        fac[nt][1] = fac_s[nt * 8 + 2 * t + 1];
       }
-      __syncthreads();
     }
 #pragma unroll
-    for (int i = 0; i < C::STAGES - 1; ++i) copy_step(warp + i * kWarps, ring + i * St::BYTES, pids[i]);
+    for (int i = 0; i < C::STAGES - 1; ++i) copy_step(member + i * team, ring + i * St::BYTES, pids[i]);
     int next_pids = pids[C::STAGES - 1];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -450,8 +462,8 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
       // that the copies below overwrite
       cp_async_wait<C::STAGES - 2>();
       __syncwarp();
-      copy_step(s + (C::STAGES - 1) * kWarps, st_write, next_pids);
-      next_pids = step_page(s + C::STAGES * kWarps);
+      copy_step(s + (C::STAGES - 1) * team, st_write, next_pids);
+      next_pids = step_page(s + C::STAGES * team);
       const uint32_t st = st_read;
       st_write = st;
       st_read = st + St::BYTES == ring_end ? ring : st + St::BYTES;
@@ -594,13 +606,14 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
         }
       }
     };
-    int s = warp;
-    for (; s < steps && key_a + (s + 1) * kStepKeys <= all_end; s += kWarps) step(s, std::false_type{});
-    for (; s < steps; s += kWarps) step(s, std::true_type{});
-    cp_async_wait<0>();
-    __syncthreads();  // the states take the ring's place
+    int s = member;
+    for (; s < steps && key_a + (s + 1) * kStepKeys <= all_end; s += team) step(s, std::false_type{});
+    for (; s < steps; s += team) step(s, std::true_type{});
 
-    // ---- the warps' states are joined
+    // ---- the team's states are joined
+    cp_async_wait<0>();
+    __syncwarp();
+    float* mine_s = o_s + member * team_step;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -608,35 +621,31 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], d);
         const int n = nt * 8 + 2 * t + i;
-        if (g == 0) {
-          m_s[warp * C::ROWS + n] = m[nt][i];
-          l_s[warp * C::ROWS + n] = l[nt][i];
-        }
-        float* dst = o_s + (warp * C::ROWS + n) * C::O_STRIDE + g * (D / 8);
+        if (g == 0) *reinterpret_cast<float2*>(mine_s + OFF_ML + 2 * n) = make_float2(m[nt][i], l[nt][i]);
+        float* dst = mine_s + n * C::O_STRIDE + g * (D / 8);
 #pragma unroll
         for (int j = 0; j < D / 32; ++j)
           *reinterpret_cast<float4*>(dst + 4 * j) = make_float4(o[nt][2 * j][i], o[nt][2 * j][i + 2],
                                                                 o[nt][2 * j + 1][i], o[nt][2 * j + 1][i + 2]);
       }
-    __syncthreads();
+    team_sync();
     const bool whole = unit0 == 0 && seg_end == tile_u + kts;
     auto out_row = [&](int n) -> int64_t {
       const int r = row0 + n;
       return static_cast<int64_t>(rq.qo_start + r / p.G) * p.Hq + h * p.G + r % p.G;
     };
-    const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (first_segment ? 0 : 1)) * C::ROWS;
-    for (int i = tid; i < rows * (D / 4); i += kThreads) {
+    const int64_t part = ((static_cast<int64_t>(slice) * p.g.Hkv + h) * 2 + (first_segment ? 0 : 1)) * C::ROWS;
+    for (int i = rank; i < rows * (D / 4); i += team * 32) {
       const int n = i / (D / 4), d = (i % (D / 4)) * 4;
       float top = kNone;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, m_s[w * C::ROWS + n]);
+      for (int w = 0; w < team; ++w) top = fmaxf(top, o_s[w * team_step + OFF_ML + 2 * n]);
       float sum = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float a = ex2f(m_s[w * C::ROWS + n] - top);
-        const float4 v = *reinterpret_cast<const float4*>(o_s + (w * C::ROWS + n) * C::O_STRIDE + d);
-        sum += a * l_s[w * C::ROWS + n];
+      for (int w = 0; w < team; ++w) {
+        const float2 ml = *reinterpret_cast<const float2*>(o_s + w * team_step + OFF_ML + 2 * n);
+        const float a = ex2f(ml.x - top);
+        const float4 v = *reinterpret_cast<const float4*>(o_s + w * team_step + n * C::O_STRIDE + d);
+        sum += a * ml.y;
         acc.x += a * v.x;
         acc.y += a * v.y;
         acc.z += a * v.z;
@@ -666,84 +675,47 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
       const int sa = static_cast<int>(tile_u / per_slice), sb = static_cast<int>((tile_u + kts - 1) / per_slice);
       const bool sa_first = tile_u == sa * per_slice;
       __threadfence();
-      __syncthreads();
-      if (tid == 0) {
+      team_sync();
+      if (rank == 0) {
         int32_t* count = p.counters + (sa + 1) * p.g.Hkv + h;
-        const int before_me = atomicAdd(count, 1);
-        last_s = before_me == sb - sa;
-        if (last_s) *count = 0;  // for the next run
+        const int last = atomicAdd(count, 1) == sb - sa;
+        if (last) *count = 0;  // for the next run
+        last_s[cta_head] = last;
       }
-      __syncthreads();
-      if (last_s) {
+      team_sync();
+      if (last_s[cta_head]) {
         __threadfence();
         auto part_row = [&](int sl) -> int64_t {
           const int which = (sl == sa && !sa_first) ? 1 : 0;
           return ((static_cast<int64_t>(sl) * p.g.Hkv + h) * 2 + which) * C::ROWS;
         };
-        constexpr int COLS = D / 4;                              // float4 columns of a row
-        constexpr int GROUPS = kThreads / COLS;                  // rows x part groups at a time
-        constexpr int RP = GROUPS < C::ROWS ? GROUPS : C::ROWS;  // rows at a time
-        constexpr int PG = GROUPS / RP;                          // groups that share a row's parts
-        float4* acc_s = reinterpret_cast<float4*>(o_s);          // [threads]
-        float2* ms_s = reinterpret_cast<float2*>(acc_s + kThreads);  // [threads]
-        const int col = tid % COLS, grp = tid / COLS, pg = grp / RP;
-        for (int n0 = 0; n0 < rows; n0 += RP) {
-          const int n = n0 + grp % RP;
-          const bool in = n < rows && pg < PG;
-          float top = kNone, sum = 0.f;
+        for (int i = rank; i < rows * (D / 4); i += team * 32) {
+          const int n = i / (D / 4), d = (i % (D / 4)) * 4;
+          float top = kNone;
+#pragma unroll 4
+          for (int sl = sa; sl <= sb; ++sl) top = fmaxf(top, __ldcg(p.part_lse + part_row(sl) + n));
+          float sum = 0.f;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (in) {
 #pragma unroll 4
-            for (int sl = sa + pg; sl <= sb; sl += PG) top = fmaxf(top, __ldcg(p.part_lse + part_row(sl) + n));
-#pragma unroll 4
-            for (int sl = sa + pg; sl <= sb; sl += PG) {
-              const int64_t row = part_row(sl) + n;
-              const float a = ex2f(__ldcg(p.part_lse + row) - top);
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + row * D + col * 4));
-              sum += a;
-              acc.x += a * v.x;
-              acc.y += a * v.y;
-              acc.z += a * v.z;
-              acc.w += a * v.w;
-            }
+          for (int sl = sa; sl <= sb; ++sl) {
+            const int64_t row = part_row(sl) + n;
+            const float a = ex2f(__ldcg(p.part_lse + row) - top);
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + row * D + d));
+            sum += a;
+            acc.x += a * v.x;
+            acc.y += a * v.y;
+            acc.z += a * v.z;
+            acc.w += a * v.w;
           }
-          if constexpr (PG > 1) {
-            acc_s[tid] = acc;
-            ms_s[tid] = make_float2(top, sum);
-            __syncthreads();
-            if (in && pg == 0) {
-              float all = kNone;
-#pragma unroll
-              for (int k = 0; k < PG; ++k) all = fmaxf(all, ms_s[tid + k * RP * COLS].x);
-              sum = 0.f;
-              acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-              for (int k = 0; k < PG; ++k) {
-                const int at = tid + k * RP * COLS;
-                const float2 ms = ms_s[at];
-                const float a = ex2f(ms.x - all);
-                const float4 v = acc_s[at];
-                sum += a * ms.y;
-                acc.x += a * v.x;
-                acc.y += a * v.y;
-                acc.z += a * v.z;
-                acc.w += a * v.w;
-              }
-              top = all;
-            }
-            __syncthreads();
-          }
-          if (in && pg == 0) {
-            const float inv = sum == 0.f ? 0.f : p.v_scale / sum;
-            const int64_t row = out_row(n);
-            *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + row * D + col * 4) = make_uint2(
-                Elt<T>::from_f2(acc.x * inv, acc.y * inv), Elt<T>::from_f2(acc.z * inv, acc.w * inv));
-            if (col == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2f;
-          }
+          const float inv = sum == 0.f ? 0.f : p.v_scale / sum;
+          const int64_t row = out_row(n);
+          *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + row * D + d) = make_uint2(
+              Elt<T>::from_f2(acc.x * inv, acc.y * inv), Elt<T>::from_f2(acc.z * inv, acc.w * inv));
+          if (d == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2f;
         }
       }
     }
-    __syncthreads();  // the buffers are the next row tile's
+    team_sync();  // the rings are the next row tile's
     first_segment = false;
     u = seg_end;
     if (u < u_end && rt + 1 == row_tiles(p, rq, C::ROWS)) {  // on to the next request with units
@@ -766,7 +738,7 @@ int row_groups(const Kv4Shape& s) {
 template <typename T, int D, int NT>
 cudaError_t launch_small(const Kv4Params& p, cudaStream_t stream) {
   using C = SmallCfg<D, NT>;
-  const unsigned grid = static_cast<unsigned>(p.slices) * p.g.Hkv;
+  const unsigned grid = static_cast<unsigned>(p.slices) * (p.g.Hkv / p.cta_heads);
   static std::atomic<uint64_t> set{0};
   auto* k = kv4_small_kernel<T, D, NT>;
   cudaError_t e = set_smem_once(set, reinterpret_cast<const void*>(k), C::SMEM);
@@ -802,14 +774,22 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 Kv4Layout kv4_layout(const Kv4Shape& s) {
   Kv4Layout l;
   const int nt = row_groups(s);
-  const int per_sm = s.D * nt <= 256 && s.D < 256 ? 2 : 1;  // SmallCfg::CTAS
-  const int slices = per_sm * s.num_sms / s.Hkv;
+  const int per_sm = small_ctas(s.D, nt), warps = small_warps(s.D, nt);
+  l.cta_heads = 1;
+  // (tiles of 4 row groups keep q in shared memory, one head a CTA)
+  for (int n = 2; n <= 8 && warps % n == 0 && s.Hkv % n == 0 && s.D * nt < 512; n *= 2)
+    if (int64_t(per_sm) * s.num_sms * n <= int64_t(3) * s.batch * s.Hkv / 2) l.cta_heads = n;
+  const int slices = per_sm * s.num_sms * l.cta_heads / s.Hkv;
   l.slices = slices > 0 ? slices : 1;
-  const size_t rows = size_t(l.slices) * s.Hkv * 2 * 8 * nt;
+  // partial rows of the most slices that any batch size gives (cta_heads 8),
+  // so that the size depends on the shape alone
+  const size_t most = size_t(per_sm) * s.num_sms * 8 > size_t(s.Hkv) ? size_t(per_sm) * s.num_sms * 8 : size_t(s.Hkv);
+  const size_t rows = most * 2 * 8 * nt;
   l.off_counters = 256;  // after the status word
   // the counters' place is the same for every shape: they have to stay zero
-  // between runs (more than two slices a kv head and SM there never are)
-  l.off_part_o = up256(l.off_counters + size_t(2) * s.num_sms * sizeof(int32_t));
+  // between runs (slices * Hkv, where there is more than one slice, is at most 8
+  // for each CTA of the card)
+  l.off_part_o = up256(l.off_counters + size_t(2) * s.num_sms * 8 * sizeof(int32_t));
   l.off_part_lse = up256(l.off_part_o + rows * s.D * sizeof(float));
   l.total = up256(l.off_part_lse + rows * sizeof(float));
   return l;
