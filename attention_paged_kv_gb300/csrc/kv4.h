@@ -75,6 +75,7 @@ struct Kv4Params {
   int64_t q_stride;  // elements between tokens
   Kv4Geom g;
   int32_t batch, num_tokens, num_page_indices, Hq, G, causal, slices, cta_heads;
+  int32_t num_sms, split_ctas;  // prefill: CTAs of the grid for cutting items along the keys (0: never)
   int32_t small_rows;  // requests of more packed rows are the prefill kernel's
   float scale_log2;    // log2(e) / sqrt(D) * k_scale
   float v_scale;
@@ -90,6 +91,8 @@ struct Kv4Layout {
   size_t off_counters, off_part_o, off_part_lse, total;
 };
 Kv4Layout kv4_layout(const Kv4Shape& s);
+// Rows of partial states that the prefill kernel may write.
+int64_t kv4_prefill_part_rows(const Kv4Shape& s);
 
 // Requests of more packed rows than this go to the tensor-core kernel.
 constexpr int kKv4SmallRows = 32;

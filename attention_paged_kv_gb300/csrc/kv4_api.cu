@@ -262,6 +262,11 @@ pagedattn_status pagedattn_kv4_run(const pagedattn_kv4_cache* cache, const paged
   const int64_t most = (key_units * tiles + 3) / 4;
   p.slices = most < lay.slices ? int32_t(most) : lay.slices;
   p.cta_heads = lay.cta_heads;
+  // requests of few keys are not worth cutting: the CTAs for it would only
+  // lengthen the launch (tables of 8 key tiles a request on average, or more)
+  p.num_sms = shape.num_sms;
+  p.split_ctas = int64_t(batch->num_page_indices) * cache->page_size >= int64_t(8) * 128 * batch->batch_size
+                     ? 2 * shape.num_sms : 0;
   // the bound alone decides whether the tensor-core kernel is launched; where
   // it is not, the small-query kernel takes every request
   const bool prefill = shape.max_rows > pa::kKv4SmallRows;

@@ -268,6 +268,8 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
   long long req_u = found_u;  // the request's first unit
   Req rq = req_s[0];
 
+  const DivG div_g(p.G);
+
   // ---- where a lane copies to and reads from in a stage
   const uint32_t page_bytes = static_cast<uint32_t>(p.g.ps) * p.g.Hkv * D;  // K and V codes of a page, at most 2^31
   const uint32_t slot_bytes = static_cast<uint32_t>(p.g.slot_rows) * (D / 2);
@@ -303,10 +305,13 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
     const long long seg_end = min(u_end, tile_u + kts);
     const int row0 = rt * C::ROWS;
     const int rows = min(C::ROWS, rq.qo_len * p.G - row0);
+    // packed row n of the tile: token tok0 + token_of(n), head (head0 + n) % G
+    const int tok0 = row0 / p.G, head0 = row0 - tok0 * p.G;
+    auto token_of = [&](int n) { return div_g.div(head0 + n); };
     // keys that some row of the tile sees, and those that every row sees
     const int shift = rq.kv_len - rq.qo_len + 1;
-    const int seen_end = p.causal ? max(0, shift + (row0 + rows - 1) / p.G) : rq.kv_len;
-    const int all_end = p.causal ? shift + row0 / p.G : rq.kv_len;
+    const int seen_end = p.causal ? max(0, shift + tok0 + token_of(rows - 1)) : rq.kv_len;
+    const int all_end = p.causal ? shift + tok0 : rq.kv_len;
     const int key_a = unit0 * kUnitKeys;
     const int key_b = min(static_cast<int>(seg_end - tile_u) * kUnitKeys, seen_end);
     const int steps = key_b > key_a ? (key_b - key_a + kStepKeys - 1) / kStepKeys : 0;
@@ -373,11 +378,11 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
     float fac[NT][2];
     int lim[NT][2];
     auto load_q = [&](int nt, uint32_t (&f)[D / 16][2]) -> float {  // returns the row's factor
-      const int n = nt * 8 + g, r = row0 + n;
+      const int n = nt * 8 + g, tok = token_of(n);
       float my = p.scale_log2;
       if (n < rows) {
-        const T* src = static_cast<const T*>(p.q) + static_cast<int64_t>(rq.qo_start + r / p.G) * p.q_stride +
-                       static_cast<int64_t>(h * p.G + r % p.G) * D + t * (D / 4);
+        const T* src = static_cast<const T*>(p.q) + static_cast<int64_t>(rq.qo_start + tok0 + tok) * p.q_stride +
+                       static_cast<int64_t>(h * p.G + head0 + n - tok * p.G) * D + t * (D / 4);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           const uint4 w = *(reinterpret_cast<const uint4*>(src) + c);
@@ -436,8 +441,7 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         if constexpr (!C::Q_SMEM) fac[nt][i] = __shfl_sync(0xffffffffu, my, (2 * t + i) * 4);
-        const int r2 = row0 + nt * 8 + 2 * t + i;
-        lim[nt][i] = p.causal ? min(shift + r2 / p.G, rq.kv_len) : rq.kv_len;
+        lim[nt][i] = p.causal ? min(shift + tok0 + token_of(nt * 8 + 2 * t + i), rq.kv_len) : rq.kv_len;
       }
     }
 
@@ -631,8 +635,8 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
     team_sync();
     const bool whole = unit0 == 0 && seg_end == tile_u + kts;
     auto out_row = [&](int n) -> int64_t {
-      const int r = row0 + n;
-      return static_cast<int64_t>(rq.qo_start + r / p.G) * p.Hq + h * p.G + r % p.G;
+      const int tok = token_of(n);
+      return static_cast<int64_t>(rq.qo_start + tok0 + tok) * p.Hq + h * p.G + head0 + n - tok * p.G;
     };
     const int64_t part = ((static_cast<int64_t>(slice) * p.g.Hkv + h) * 2 + (first_segment ? 0 : 1)) * C::ROWS;
     for (int i = rank; i < rows * (D / 4); i += team * 32) {
@@ -689,30 +693,7 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
           const int which = (sl == sa && !sa_first) ? 1 : 0;
           return ((static_cast<int64_t>(sl) * p.g.Hkv + h) * 2 + which) * C::ROWS;
         };
-        for (int i = rank; i < rows * (D / 4); i += team * 32) {
-          const int n = i / (D / 4), d = (i % (D / 4)) * 4;
-          float top = kNone;
-#pragma unroll 4
-          for (int sl = sa; sl <= sb; ++sl) top = fmaxf(top, __ldcg(p.part_lse + part_row(sl) + n));
-          float sum = 0.f;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (int sl = sa; sl <= sb; ++sl) {
-            const int64_t row = part_row(sl) + n;
-            const float a = ex2f(__ldcg(p.part_lse + row) - top);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + row * D + d));
-            sum += a;
-            acc.x += a * v.x;
-            acc.y += a * v.y;
-            acc.z += a * v.z;
-            acc.w += a * v.w;
-          }
-          const float inv = sum == 0.f ? 0.f : p.v_scale / sum;
-          const int64_t row = out_row(n);
-          *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + row * D + d) = make_uint2(
-              Elt<T>::from_f2(acc.x * inv, acc.y * inv), Elt<T>::from_f2(acc.z * inv, acc.w * inv));
-          if (d == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2f;
-        }
+        join_parts<T, D, 4>(p, rank, team * 32, rows, sb - sa + 1, [&](int k) { return part_row(sa + k); }, out_row);
       }
     }
     team_sync();  // the rings are the next row tile's
@@ -784,7 +765,8 @@ Kv4Layout kv4_layout(const Kv4Shape& s) {
   // partial rows of the most slices that any batch size gives (cta_heads 8),
   // so that the size depends on the shape alone
   const size_t most = size_t(per_sm) * s.num_sms * 8 > size_t(s.Hkv) ? size_t(per_sm) * s.num_sms * 8 : size_t(s.Hkv);
-  const size_t rows = most * 2 * 8 * nt;
+  const size_t pre = s.max_rows > kKv4SmallRows ? size_t(kv4_prefill_part_rows(s)) : 0;  // the two kernels take turns
+  const size_t rows = most * 2 * 8 * nt > pre ? most * 2 * 8 * nt : pre;
   l.off_counters = 256;  // after the status word
   // the counters' place is the same for every shape: they have to stay zero
   // between runs (slices * Hkv, where there is more than one slice, is at most 8

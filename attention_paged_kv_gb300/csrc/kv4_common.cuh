@@ -67,4 +67,77 @@ __device__ __forceinline__ int bf16_row_shift(uint32_t top) {
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
+// n / G and n % G for n < 512 (G <= 128): G's reciprocal in 16 bits, rounded up
+// (its error, below G / 2^16 a unit, stays below one for such n).
+struct DivG {
+  int G;
+  uint32_t m;
+  __device__ explicit DivG(int g) : G(g), m((65535u + g) / g) {}
+  __device__ __forceinline__ int div(int n) const { return static_cast<int>((static_cast<uint32_t>(n) * m) >> 16); }
+};
+
+// ---------------------------------------------------------------------------
+// partial states
+
+// Joins `parts` states of `rows` rows: o = sum_k 2^(lse_k - lse) o_k, in the
+// parts' order, by `threads` threads of which this one is `rank`.  Part k's
+// rows begin at part_row(k) of part_o / part_lse; out_row(n) is row n of out.
+// A thread has U columns in flight at a time: one by one, each would wait for
+// two dependent loads.
+template <typename T, int D, int U, typename PartRow, typename OutRow>
+__device__ __forceinline__ void join_parts(const Kv4Params& p, int rank, int threads, int rows, int parts,
+                                           PartRow part_row, OutRow out_row) {
+  constexpr int COLS = D / 4;  // float4 columns of a row
+  const int n_items = rows * COLS;
+  for (int i0 = rank; i0 < n_items; i0 += U * threads) {
+    int at[U];  // row * COLS + column, the last one again past the end
+    float top[U], sum[U];
+    float4 acc[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      at[u] = min(i0 + u * threads, n_items - 1);
+      top[u] = -3.0e38f;
+      sum[u] = 0.f;
+      acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int k = 0; k < parts; ++k) {
+      const float* lse = p.part_lse + part_row(k);
+#pragma unroll
+      for (int u = 0; u < U; ++u) top[u] = fmaxf(top[u], __ldcg(lse + at[u] / COLS));
+    }
+    for (int k = 0; k < parts; ++k) {
+      const int64_t row = part_row(k);
+      float4 v[U];
+      float a[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        v[u] = __ldcg(reinterpret_cast<const float4*>(p.part_o + row * D) + at[u]);
+        a[u] = __ldcg(p.part_lse + row + at[u] / COLS);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float w;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(a[u] - top[u]));
+        sum[u] += w;
+        acc[u].x += w * v[u].x;
+        acc[u].y += w * v[u].y;
+        acc[u].z += w * v[u].z;
+        acc[u].w += w * v[u].w;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i0 + u * threads >= n_items) break;
+      const int col = at[u] % COLS;
+      // a row that sees no key: zeros, and -inf as its lse
+      const float inv = sum[u] == 0.f ? 0.f : p.v_scale / sum[u];
+      const int64_t row = out_row(at[u] / COLS);
+      *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + row * D + col * 4) =
+          make_uint2(Elt<T>::from_f2(acc[u].x * inv, acc[u].y * inv), Elt<T>::from_f2(acc[u].z * inv, acc[u].w * inv));
+      if (col == 0 && p.lse)
+        p.lse[row] = sum[u] == 0.f ? -INFINITY : (top[u] + log2f(sum[u])) * 0.6931471805599453f;
+    }
+  }
+}
+
 }  // namespace pa

@@ -3,9 +3,10 @@
 //
 // One CTA takes NT tiles of 128 packed query rows (token major, the G heads
 // of a kv head minor; any G) of one request and one kv head, against all keys
-// that its last row sees.  The work is found on the device: every CTA sums
-// the requests' tiles and looks its own up; the grid is the host's upper
-// bound, and the CTAs behind the last tile leave at once.  Tiles are taken
+// that its last row sees, or a part of them where the items would leave most
+// of the card's last wave idle.  The work is found on the device: every CTA
+// sums the requests' tiles and looks its own up; the grid is the host's upper
+// bound, and the CTAs behind the last item leave at once.  Tiles are taken
 // from the last one down: under a causal mask the last are the longest.
 //
 // Warp roles (4 warps each; register shares after setmaxnreg):
@@ -55,7 +56,7 @@ struct PreCfg {
   static constexpr int O_COL = NT * 128;
   static constexpr uint32_t TMEM_COLS = (NT * (128 + D) <= 256) ? 256u : 512u;
   // registers: with two tiles the launch gives 512 threads 128 each, handed
-  // over as 2 x 168 (softmax) + 88 (dequantisation) + 88 (MMA) = 4 x 128;
+  // over as 2 x 168 (softmax) + 80 (dequantisation) + 96 (MMA) = 4 x 128;
   static constexpr int LAUNCH_REGS = 128;
 };
 
@@ -120,54 +121,9 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, 1) kv4_prefill_kernel(
   uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  __shared__ int warp_sums[32], found_b, found_tile;
-  pdl_wait();  // q, the cache and the tables may come from the kernel before
-
-  // ---- the item: tile from the end, kv head
-  const int h = blockIdx.x % p.g.Hkv;
-  auto tiles_of = [&](int b) -> int {
-    const Req r = load_req(p, b);
-    const int rows = r.qo_len * p.G;
-    return rows > p.small_rows ? (rows + NT * kQRows - 1) / (NT * kQRows) : 0;
-  };
-  auto sum_before = [&](int v, int* total) -> int {  // exclusive sum over the block
-    int x = v;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, d);
-      if (lane >= d) x += y;
-    }
-    if (lane == 31) warp_sums[warp] = x;
-    __syncthreads();
-    int before = x - v, all = 0;
-#pragma unroll
-    for (int w = 0; w < C::THREADS / 32; ++w) {
-      if (w < warp) before += warp_sums[w];
-      all += warp_sums[w];
-    }
-    __syncthreads();
-    *total = all;
-    return before;
-  };
-  int mine = 0;
-  for (int b = tid; b < p.batch; b += C::THREADS) mine += tiles_of(b);
-  int total;
-  int before = sum_before(mine, &total);
-  const int item = total - 1 - static_cast<int>(blockIdx.x) / p.g.Hkv;
-  if (item < 0) return;
-  for (int b0 = 0, base = 0; b0 < p.batch; b0 += C::THREADS) {
-    int v = mine, all = total;
-    if (p.batch > C::THREADS) {
-      v = b0 + tid < p.batch ? tiles_of(b0 + tid) : 0;
-      before = base + sum_before(v, &all);
-    }
-    if (v > 0 && before <= item && item < before + v) {
-      found_b = b0 + tid;
-      found_tile = item - before;
-    }
-    base += all;
-    if (item < base) break;
-  }
+  __shared__ int warp_sums[32], found_tile, last_s;
+  __shared__ long long work_s;
+  __shared__ Req found_rq;
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* full_k = bars;             // [NST] K tile written
@@ -196,35 +152,138 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, 1) kv4_prefill_kernel(
     }
     mbar_init(fin, 1);
     *abort_flag = 0;
+    work_s = 0;
     mbar_init_fence();
   }
   if (warp == C::WARP_MMA) tmem_alloc(tmem_slot, C::TMEM_COLS);
+  pdl_wait();  // q, the cache and the tables may come from the kernel before
+
+  // ---- the items: row tiles from the last one down, their kv heads adjacent
+  auto tiles_of = [&](const Req& r) -> int {
+    const int rows = r.qo_len * p.G;
+    return rows > p.small_rows ? (rows + NT * kQRows - 1) / (NT * kQRows) : 0;
+  };
+  auto sum_before = [&](int v, int* total) -> int {  // exclusive sum over the block
+    int x = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
+    }
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    int before = x - v, all = 0;
+#pragma unroll
+    for (int w = 0; w < C::THREADS / 32; ++w) {
+      if (w < warp) before += warp_sums[w];
+      all += warp_sums[w];
+    }
+    __syncthreads();
+    *total = all;
+    return before;
+  };
+  Req my_rq{0, 0, 0, 0};
+  int mine = 0;
+  long long work = 0;  // key tiles of all row tiles (as if no mask cut them)
+  for (int b = tid; b < p.batch; b += C::THREADS) {
+    my_rq = load_req(p, b);
+    const int n = tiles_of(my_rq);
+    mine += n;
+    work += static_cast<long long>(n) * ((my_rq.kv_len + kKvTile - 1) / kKvTile);
+  }
+  int total;
+  int before = sum_before(mine, &total);
+  if (p.split_ctas > 0 && work > 0) atomicAdd(reinterpret_cast<unsigned long long*>(&work_s), static_cast<unsigned long long>(work));
+  // Items are whole but for those that would not fill the last wave of one
+  // CTA an SM: they are cut along the keys into `parts` each, as many as make
+  // that wave shortest (4 key tiles stand for a part's start and join).
+  const int items = total * p.g.Hkv;
+  int whole_items = items, parts = 1;
+  if (p.split_ctas > 0) {
+    __syncthreads();
+    const int rem = items % p.num_sms;
+    if (rem > 0) {
+      const float kts = static_cast<float>(work_s) / static_cast<float>(total);
+      // lane n - 1 weighs n parts; the cheapest, the fewest among equals
+      const int n = lane + 1;
+      float cost = static_cast<float>((rem * n + p.num_sms - 1) / p.num_sms) * (kts / n + (n > 1 ? 4.f : 0.f));
+      if (n > 1 && rem * (n - 1) > p.split_ctas) cost = INFINITY;
+      float best = cost;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) best = fminf(best, __shfl_xor_sync(0xffffffffu, best, d));
+      parts = __ffs(__ballot_sync(0xffffffffu, cost == best));
+      if (parts > 1) whole_items = items - rem;
+    }
+  }
+  const int cut_item = static_cast<int>(blockIdx.x) - whole_items;  // in the cut part of the grid
+  const int item = cut_item < 0 ? static_cast<int>(blockIdx.x) : whole_items + cut_item / parts;
+  if (item >= items) {
+    __syncthreads();
+    if (warp == C::WARP_MMA) tmem_dealloc(*tmem_slot, C::TMEM_COLS);
+    return;
+  }
+  const int h = item % p.g.Hkv, tile_index = total - 1 - item / p.g.Hkv;
+  for (int b0 = 0, base = 0; b0 < p.batch; b0 += C::THREADS) {
+    int v = mine, all = total;
+    if (p.batch > C::THREADS) {
+      my_rq = Req{0, 0, 0, 0};
+      if (b0 + tid < p.batch) my_rq = load_req(p, b0 + tid);
+      v = tiles_of(my_rq);
+      before = base + sum_before(v, &all);
+    }
+    if (v > 0 && before <= tile_index && tile_index < before + v) {
+      found_rq = my_rq;
+      found_tile = tile_index - before;
+    }
+    base += all;
+    if (tile_index < base) break;
+  }
+
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  const Req rq = load_req(p, found_b);
+  const Req rq = found_rq;
   const int row0 = found_tile * NT * kQRows;  // first packed row of the item
   const int rows = min(NT * kQRows, rq.qo_len * p.G - row0);
+  const int tok0 = row0 / p.G, head0 = row0 - tok0 * p.G;
+  const DivG div_g(p.G);
+  // packed row n of the item: token qo_start + tok0 + token_of(n), and its row of out
+  auto token_of = [&](int n) { return div_g.div(head0 + n); };
+  auto out_row = [&](int n) -> int64_t {
+    const int tok = token_of(n);
+    return (static_cast<int64_t>(rq.qo_start) + tok0 + tok) * p.Hq + h * p.G + head0 + n - tok * p.G;
+  };
   const bool has_b = NT == 2 && rows > kQRows;
   const int shift = rq.kv_len - rq.qo_len + 1;
-  const int key_end = p.causal ? max(0, min(rq.kv_len, shift + (row0 + rows - 1) / p.G)) : rq.kv_len;
-  const int nkt = (key_end + kKvTile - 1) / kKvTile;
+  const int seen_end = p.causal ? max(0, min(rq.kv_len, shift + tok0 + token_of(rows - 1))) : rq.kv_len;
+  // the part's key tiles, from key 128 * kt0 on: keys below count from there
+  const int all_kts = (seen_end + kKvTile - 1) / kKvTile;
+  const int my_parts = cut_item < 0 ? 1 : max(1, min(parts, all_kts));
+  const int part = cut_item < 0 ? 0 : cut_item % parts;
+  const bool idle = part >= my_parts;
+  const int kt0 = static_cast<int>(static_cast<long long>(all_kts) * part / my_parts);
+  const int kt1 = idle ? kt0 : static_cast<int>(static_cast<long long>(all_kts) * (part + 1) / my_parts);
+  const int nkt = kt1 - kt0;
+  const int key_end = min(seen_end, kt1 * kKvTile);
+  // one row tile alone: the two softmax warpgroups take its even and its odd
+  // key tiles, as two states joined at the end
+  const bool dual = NT == 2 && !has_b && nkt > 1;
   constexpr long long kLimit = PA_WAIT_LIMIT_CYCLES;
 
   if (warp >= C::WARP_DQ && warp < C::WARP_DQ + 4) {
     // ---------------------------------------------------------------- dequantisation
-    if constexpr (NT == 2) regs_down<88>();
+    if constexpr (NT == 2) regs_down<80>();
     const int r = tid - 32 * C::WARP_DQ;  // key of the tile
     const int32_t* ids = p.pages + rq.page_start;
     const int64_t half_rows = static_cast<int64_t>(p.g.ps) * p.g.Hkv;
     auto page_of = [&](int j) -> int {
-      const int key = j * kKvTile + r;
+      const int key = (kt0 + j) * kKvTile + r;
       return key < key_end ? __ldg(ids + (key >> p.g.ps_shift)) : 0;
     };
     auto row_of = [&](int j, int pid) -> int64_t {  // the K row; V's lies half_rows behind it
-      const int key = j * kKvTile + r;
+      const int key = (kt0 + j) * kKvTile + r;
       if (static_cast<unsigned>(pid) >= static_cast<unsigned>(p.g.num_pages)) {
         atomicOr(p.status, PA_DEV_BAD_INDEX);
         pid = 0;
@@ -234,13 +293,13 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, 1) kv4_prefill_kernel(
     };
     Row4<D> k4, v4;
     int64_t at = row_of(0, page_of(0));
-    load_row4(k4, p, at, r < key_end);
-    load_row4(v4, p, at + half_rows, r < key_end);
+    load_row4(k4, p, at, kt0 * kKvTile + r < key_end);
+    load_row4(v4, p, at + half_rows, kt0 * kKvTile + r < key_end);
     int next_page = page_of(1);
     for (int j = 0; j < nkt; ++j) {
       const int st = j % NST;
       const uint32_t parity = ((j / NST) - 1) & 1;
-      const bool more = (j + 1) * kKvTile + r < key_end;
+      const bool more = (kt0 + j + 1) * kKvTile + r < key_end;
       at = row_of(j + 1, next_page);
       next_page = page_of(j + 2);
       if (j >= NST && !warp_wait(&empty_k[st], parity, abort_flag, p.status, kLimit)) break;
@@ -258,7 +317,7 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, 1) kv4_prefill_kernel(
     }
   } else if (warp >= C::WARP_MMA) {
     // ---------------------------------------------------------------- MMA issuer
-    if constexpr (NT == 2) regs_down<88>();
+    if constexpr (NT == 2) regs_down<96>();
     if (warp == C::WARP_MMA && lane == 0 && nkt > 0) {
       const uint32_t id_s = idesc_f16(0, 0, 0, 128, 128);
       const uint32_t id_o = idesc_f16(0, 0, 1, 128, D);
@@ -266,7 +325,7 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, 1) kv4_prefill_kernel(
       const uint64_t dk0 = smem_desc_sw128(sbase + C::OFF_K, 16, 1024);
       const uint64_t dv0 = smem_desc_sw128(sbase + C::OFF_V, C::BLK, 1024);
       auto issue_s = [&](int x, int st) {
-        const uint64_t qd = dq0 + uint64_t(x) * (C::TILE >> 4);
+        const uint64_t qd = dq0 + uint64_t(dual ? 0 : x) * (C::TILE >> 4);
         const uint64_t kd = dk0 + uint64_t(st) * (C::TILE >> 4);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
@@ -275,13 +334,13 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, 1) kv4_prefill_kernel(
         }
         tc_commit(&s_full[x]);
       };
-      auto issue_pv = [&](int x, int j, int st) {
+      auto issue_pv = [&](int x, bool first, bool last, int st) {
         const uint64_t vd = dv0 + uint64_t(st) * (C::TILE >> 4);
 #pragma unroll
         for (int k = 0; k < kKvTile / 16; ++k)
           tc_mma_ts(tmem + C::O_COL + x * 128, tmem + x * 128 + k * 8, vd + (k * 2048 >> 4), id_o,
-                    (j > 0 || k > 0) ? 1u : 0u);
-        if (j == nkt - 1) tc_commit(&o_done[x]);
+                    (!first || k > 0) ? 1u : 0u);
+        if (last) tc_commit(&o_done[x]);
       };
       bool ok = spin_wait(q_full, 0, abort_flag, p.status, kLimit);
       if (ok) ok = spin_wait(&full_k[0], 0, abort_flag, p.status, kLimit);
@@ -291,31 +350,59 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, 1) kv4_prefill_kernel(
         if (has_b) issue_s(1, 0);
         tc_commit(&empty_k[0]);
       }
-      for (int j = 0; ok && j < nkt; ++j) {
-        const int st = j % NST, st1 = (j + 1) % NST;
-        const bool more = j + 1 < nkt;
-        ok = spin_wait(&p_full[0], j & 1, abort_flag, p.status, kLimit);
-        if (ok) ok = spin_wait(&full_v[st], (j / NST) & 1, abort_flag, p.status, kLimit);
-        if (!ok) break;
-        tc_fence_after();
-        issue_pv(0, j, st);
-        if (more) {
-          ok = spin_wait(&full_k[st1], ((j + 1) / NST) & 1, abort_flag, p.status, kLimit);
+      if (ok && dual) {
+        ok = spin_wait(&full_k[1 % NST], 0, abort_flag, p.status, kLimit);
+        if (ok) {
+          tc_fence_after();
+          issue_s(1, 1 % NST);
+          tc_commit(&empty_k[1 % NST]);
+        }
+      }
+      if (!dual) {
+        for (int j = 0; ok && j < nkt; ++j) {  // key tile j of both row tiles
+          const int st = j % NST, st1 = (j + 1) % NST;
+          const bool more = j + 1 < nkt;
+          ok = spin_wait(&p_full[0], j & 1, abort_flag, p.status, kLimit);
+          if (ok) ok = spin_wait(&full_v[st], (j / NST) & 1, abort_flag, p.status, kLimit);
           if (!ok) break;
           tc_fence_after();
-          issue_s(0, st1);
-          if (!has_b) tc_commit(&empty_k[st1]);
+          issue_pv(0, j == 0, !more, st);
+          if (more) {
+            ok = spin_wait(&full_k[st1], ((j + 1) / NST) & 1, abort_flag, p.status, kLimit);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(0, st1);
+            if (!has_b) tc_commit(&empty_k[st1]);
+          }
+          if (has_b) {
+            ok = spin_wait(&p_full[1], j & 1, abort_flag, p.status, kLimit);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(1, j == 0, !more, st);
+          }
+          tc_commit(&empty_v[st]);
+          if (has_b && more) {
+            issue_s(1, st1);
+            tc_commit(&empty_k[st1]);
+          }
         }
-        if (has_b) {
-          ok = spin_wait(&p_full[1], j & 1, abort_flag, p.status, kLimit);
+      } else {
+        for (int j = 0; ok && j < nkt; ++j) {  // key tile j of warpgroup j & 1, whose next is j + 2
+          const int st = j % NST, x = j & 1;
+          ok = spin_wait(&p_full[x], (j >> 1) & 1, abort_flag, p.status, kLimit);
+          if (ok) ok = spin_wait(&full_v[st], (j / NST) & 1, abort_flag, p.status, kLimit);
           if (!ok) break;
           tc_fence_after();
-          issue_pv(1, j, st);
-        }
-        tc_commit(&empty_v[st]);
-        if (has_b && more) {
-          issue_s(1, st1);
-          tc_commit(&empty_k[st1]);
+          issue_pv(x, j < 2, j + 2 >= nkt, st);
+          tc_commit(&empty_v[st]);
+          if (j + 2 < nkt) {
+            const int st2 = (j + 2) % NST;
+            ok = spin_wait(&full_k[st2], ((j + 2) / NST) & 1, abort_flag, p.status, kLimit);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(x, st2);
+            tc_commit(&empty_k[st2]);
+          }
         }
       }
       tc_commit(fin);
@@ -327,22 +414,23 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, 1) kv4_prefill_kernel(
     if constexpr (NT == 2) regs_up<168>();
     const int x = warp >> 2;
     const int r = tid & 127;
-    const int pr = row0 + x * kQRows + r;  // packed row of the request
-    const bool row_valid = x * kQRows + r < rows;
-    const bool active = x == 0 || has_b;
-    const int64_t qtok = static_cast<int64_t>(rq.qo_start) + pr / p.G;
-    const int qhead = h * p.G + pr % p.G;
-    int row_end = p.causal ? shift + pr / p.G : rq.kv_len;
-    row_end = row_valid ? min(row_end, key_end) : 0;
+    const int rx = dual ? 0 : x;            // the warpgroup's row tile
+    const int pr = rx * kQRows + r;         // row of the item
+    const bool row_valid = pr < rows;
+    const bool active = x == 0 || has_b || dual;
+    const bool warp_rows = rx * kQRows + (r & ~31) < rows;  // some row of the warp is one
+    const int tok = token_of(pr);
+    int row_end = p.causal ? shift + tok0 + tok : rq.kv_len;
+    row_end = row_valid ? min(row_end, key_end) - kt0 * kKvTile : 0;
     float sl2 = p.scale_log2;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + lane_base + x * 128;
     const uint32_t o_col = tmem + lane_base + C::O_COL + x * 128;
     uint8_t* q_row = smem + x * C::TILE + r * 128;  // chunk c of block kb at kb * BLK + ((c ^ (r & 7)) << 4)
 
-    if (active) {  // the row of q as fp16
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + qtok * p.q_stride +
-                                                        static_cast<int64_t>(qhead) * D);
+    if (active) {  // the row of q as fp16 (dual: warpgroup 1 needs its factor alone)
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (static_cast<int64_t>(rq.qo_start) + tok0 + tok) * p.q_stride +
+                                                        static_cast<int64_t>(h * p.G + head0 + pr - tok * p.G) * D);
       float mul = 1.f;
       if constexpr (Elt<T>::kBf16) {
         uint32_t top = 0;
@@ -371,7 +459,7 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, 1) kv4_prefill_kernel(
           }
           w = make_uint4(ws[0], ws[1], ws[2], ws[3]);
         }
-        *reinterpret_cast<uint4*>(q_row + (i >> 3) * C::BLK + (((i & 7) ^ (r & 7)) << 4)) = w;
+        if (!dual || x == 0) *reinterpret_cast<uint4*>(q_row + (i >> 3) * C::BLK + (((i & 7) ^ (r & 7)) << 4)) = w;
       }
     }
     fence_proxy_async_smem();
@@ -380,11 +468,20 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, 1) kv4_prefill_kernel(
 
     float m_ref = -INFINITY, l_sum = 0.f;
     bool ok = active;
-    for (int j = 0; ok && j < nkt; ++j) {
-      ok = warp_wait(&s_full[x], j & 1, abort_flag, p.status, kLimit);
+    // the warpgroup's key tiles, and the row's keys that remain at each
+    const int mine_kts = dual ? (nkt + 1 - x) >> 1 : nkt;
+    int lim = row_end - (dual ? x * kKvTile : 0);
+    const int lim_step = dual ? 2 * kKvTile : kKvTile;
+    for (int i = 0; ok && i < mine_kts; ++i, lim -= lim_step) {
+      ok = warp_wait(&s_full[x], i & 1, abort_flag, p.status, kLimit);
       if (!ok) break;
       tc_fence_after();
-      const int lim = row_end - j * kKvTile;
+      if (!warp_rows) {  // rows of none: whatever stands in P reaches their O alone
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[x]);
+        continue;
+      }
       // the whole S row in registers: four loads, one wait
       uint32_t s[128];
       tmem_ld32(s_col + 0, *reinterpret_cast<uint32_t(*)[32]>(s + 0));
@@ -461,48 +558,132 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, 1) kv4_prefill_kernel(
     }
 
     // ---------------------------------------------------------------- epilogue
-    if (ok && nkt > 0) ok = warp_wait(&o_done[x], 0, abort_flag, p.status, kLimit);
-    if (ok) {
+    const bool some = nkt > 0;  // the warpgroup had a key tile (dual: two or more)
+    if (ok && some) ok = warp_wait(&o_done[x], 0, abort_flag, p.status, kLimit);
+    float other_w = 0.f;  // dual: weight of warpgroup 1's state
+    float* o_x = reinterpret_cast<float*>(smem + C::OFF_K);  // its O, [128][D + 4], where K and V were
+    float2* ml_x = reinterpret_cast<float2*>(o_x + 128 * (D + 4));
+    float scale = 1.f;
+    if (dual) {
+      if (x == 1) {
+        if (ok) ok = warp_wait(&o_done[0], 0, abort_flag, p.status, kLimit);  // nothing reads K and V any more
+        if (ok && warp_rows) {
+          tc_fence_after();
+          ml_x[r] = make_float2(m_ref, l_sum);
+#pragma unroll
+          for (int c4 = 0; c4 < D / 32; ++c4) {
+            uint32_t o[32];
+            tmem_ld32(o_col + c4 * 32, o);
+            tmem_wait_ld(o);
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+              *reinterpret_cast<uint4*>(o_x + r * (D + 4) + c4 * 32 + 4 * v) =
+                  make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+          }
+        }
+      }
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (x == 0 && warp_rows) {
+        const float2 ml = ml_x[r];
+        const float top = fmaxf(m_ref, ml.x);
+        const float ref = top == -INFINITY ? 0.f : top;
+        scale = ex2(m_ref - ref);
+        other_w = ex2(ml.x - ref);
+        l_sum = l_sum * scale + ml.y * other_w;
+        m_ref = top;
+      }
+    }
+    const bool writes = ok && (x == 0 || has_b) && !idle;
+    const bool split = my_parts > 1;
+    // a cut item's states: part i of item n at (n * parts + i) row tiles
+    const int64_t part_tile = split ? static_cast<int64_t>(cut_item / parts) * parts : 0;
+    if (writes) {
       tc_fence_after();
       const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
       // a row that sees no key: zeros, and -inf as its lse
-      const float inv = l_sum == 0.f ? 0.f : p.v_scale / l_sum;
-      if (row_valid && p.lse)
-        p.lse[qtok * p.Hq + qhead] = l_sum == 0.f ? -INFINITY : (m_use + __log2f(l_sum)) * kLn2;
-      // O scaled and rounded into the row of q's slot (free since the last S
-      // MMA); then each warp writes its 32 rows, whole rows at a time
+      const float inv = l_sum == 0.f ? 0.f : (split ? 1.f : p.v_scale) / l_sum;
+      const float lse2 = l_sum == 0.f ? -INFINITY : m_use + __log2f(l_sum);
+      const int64_t part_row = (part_tile + part) * (NT * kQRows) + x * kQRows + r;
+      if (row_valid) {
+        if (split) p.part_lse[part_row] = lse2;
+        else if (p.lse) p.lse[out_row(pr)] = lse2 * kLn2;
+      }
+      // O scaled: to the part's state, or rounded into the row of q's slot (free
+      // since the last S MMA), from where each warp writes whole rows
+      if (warp_rows) {
 #pragma unroll
-      for (int c4 = 0; c4 < D / 32; ++c4) {
-        uint32_t o[32];
-        if (nkt > 0) {
-          tmem_ld32(o_col + c4 * 32, o);
-          tmem_wait_ld(o);
-        } else {
+        for (int c4 = 0; c4 < D / 32; ++c4) {
+          uint32_t o[32];
+          float* f = reinterpret_cast<float*>(o);
+          if (some) {
+            tmem_ld32(o_col + c4 * 32, o);
+            tmem_wait_ld(o);
+          } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0;
-        }
+            for (int i = 0; i < 32; ++i) o[i] = 0;
+          }
+          if (dual) {
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const float* f = reinterpret_cast<const float*>(o) + 8 * v;
-          const int c = (c4 & 1) * 4 + v;
-          *reinterpret_cast<uint4*>(q_row + (c4 >> 1) * C::BLK + ((c ^ (r & 7)) << 4)) =
-              make_uint4(Elt<T>::from_f2(f[0] * inv, f[1] * inv), Elt<T>::from_f2(f[2] * inv, f[3] * inv),
-                         Elt<T>::from_f2(f[4] * inv, f[5] * inv), Elt<T>::from_f2(f[6] * inv, f[7] * inv));
+            for (int v = 0; v < 8; ++v) {
+              const float4 w = *reinterpret_cast<const float4*>(o_x + r * (D + 4) + c4 * 32 + 4 * v);
+              f[4 * v] = f[4 * v] * scale + w.x * other_w;
+              f[4 * v + 1] = f[4 * v + 1] * scale + w.y * other_w;
+              f[4 * v + 2] = f[4 * v + 2] * scale + w.z * other_w;
+              f[4 * v + 3] = f[4 * v + 3] * scale + w.w * other_w;
+            }
+          }
+          if (split) {
+            if (row_valid) {
+#pragma unroll
+              for (int v = 0; v < 8; ++v)
+                *reinterpret_cast<float4*>(p.part_o + part_row * D + c4 * 32 + 4 * v) =
+                    make_float4(f[4 * v] * inv, f[4 * v + 1] * inv, f[4 * v + 2] * inv, f[4 * v + 3] * inv);
+            }
+          } else {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const int c = (c4 & 1) * 4 + v;
+              const float* e = f + 8 * v;
+              *reinterpret_cast<uint4*>(q_row + (c4 >> 1) * C::BLK + ((c ^ (r & 7)) << 4)) =
+                  make_uint4(Elt<T>::from_f2(e[0] * inv, e[1] * inv), Elt<T>::from_f2(e[2] * inv, e[3] * inv),
+                             Elt<T>::from_f2(e[4] * inv, e[5] * inv), Elt<T>::from_f2(e[6] * inv, e[7] * inv));
+            }
+          }
         }
       }
-      __syncwarp();
-      constexpr int LPR = D / 8;        // lanes of a row
-      constexpr int RPI = 32 / LPR;     // rows of an access
-      const int c = lane % LPR;
+      if (!split) {
+        __syncwarp();
+        constexpr int LPR = D / 8;     // lanes of a row
+        constexpr int RPI = 32 / LPR;  // rows of an access
+        const int c = lane % LPR;
 #pragma unroll 4
-      for (int i = 0; i < 32 / RPI; ++i) {
-        const int rr = (warp & 3) * 32 + i * RPI + lane / LPR;  // row of the tile
-        if (x * kQRows + rr >= rows) break;
-        const uint4 w = *reinterpret_cast<const uint4*>(smem + x * C::TILE + (c >> 3) * C::BLK + rr * 128 +
-                                                        (((c & 7) ^ (rr & 7)) << 4));
-        const int pr2 = row0 + x * kQRows + rr;
-        const int64_t row = (static_cast<int64_t>(rq.qo_start) + pr2 / p.G) * p.Hq + h * p.G + pr2 % p.G;
-        *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + row * D + c * 8) = w;
+        for (int i = 0; i < 32 / RPI; ++i) {
+          const int rr = (warp & 3) * 32 + i * RPI + lane / LPR;  // row of the tile
+          if (x * kQRows + rr >= rows) break;
+          const uint4 w = *reinterpret_cast<const uint4*>(smem + x * C::TILE + (c >> 3) * C::BLK + rr * 128 +
+                                                          (((c & 7) ^ (rr & 7)) << 4));
+          const int64_t row = out_row(x * kQRows + rr);
+          *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + row * D + c * 8) = w;
+        }
+      }
+    }
+    if (split && !idle) {
+      // ---- the last part of an item joins them all: o = sum_s 2^(lse_s - lse)
+      // o_s, in the parts' order whichever comes last.  (A part that gave up
+      // has raised its status; it is counted all the same.)
+      __threadfence();
+      asm volatile("bar.sync 1, %0;" ::"n"(NT * 128) : "memory");
+      if (tid == 0) {
+        int32_t* count = p.counters + cut_item / parts;
+        const int last = atomicAdd(count, 1) == my_parts - 1;
+        if (last) *count = 0;  // for the next run
+        last_s = last;
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(NT * 128) : "memory");
+      if (last_s) {
+        __threadfence();
+        join_parts<T, D, 8>(p, tid, NT * 128, rows, my_parts,
+                            [&](int k) -> int64_t { return (part_tile + k) * (NT * kQRows); }, out_row);
       }
     }
   }
@@ -546,8 +727,8 @@ cudaError_t launch_d(const Kv4Params& p, cudaStream_t stream) {
   const int64_t some = rows / (p.small_rows + 1);  // requests of more rows than the small kernel takes
   const int64_t tiles = rows / tile + (some < p.batch ? some : p.batch);
   if (tiles == 0) return cudaSuccess;
-  if (tiles * p.g.Hkv > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  return launch_pdl(kernel, unsigned(tiles * p.g.Hkv), unsigned(C::THREADS), size_t(C::SMEM), stream, p);
+  if (tiles * p.g.Hkv + p.split_ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  return launch_pdl(kernel, unsigned(tiles * p.g.Hkv + p.split_ctas), unsigned(C::THREADS), size_t(C::SMEM), stream, p);
 }
 
 template <typename T>
@@ -560,6 +741,11 @@ cudaError_t launch_t(const Kv4Params& p, int D, cudaStream_t stream) {
 }
 
 }  // namespace
+
+// (parts of the cut items: fewer than the items of a wave and split_ctas)
+int64_t kv4_prefill_part_rows(const Kv4Shape& s) {
+  return int64_t(3) * s.num_sms * (s.D == 256 ? 1 : 2) * kQRows;
+}
 
 cudaError_t launch_kv4_prefill(const Kv4Params& p, const Kv4Shape& s, int dtype, cudaStream_t stream) {
   return dtype == PA_BF16 ? launch_t<__nv_bfloat16>(p, s.D, stream) : launch_t<__half>(p, s.D, stream);

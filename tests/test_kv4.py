@@ -484,6 +484,46 @@ def test_attention_splits_of_long_requests():
 
 
 @gpu
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("shape", [
+    ([8], [5000], 8, 1, 128, 16, "NHD"),           # one row tile, cut along the keys, two states a part
+    ([5, 33], [1100, 2900], 8, 2, 128, 64, "HND"),
+    ([300], [2600], 4, 1, 128, 16, "NHD"),         # a pair of row tiles and an odd one
+    ([40], [4100], 2, 1, 64, 16, "HND"),
+    ([50], [3000], 3, 1, 256, 16, "NHD"),
+    ([64, 1, 40], [64, 4000, 1300], 8, 2, 128, 16, "HND"),
+], ids=str)
+def test_attention_items_cut_along_the_keys(shape, dtype):
+    """Few items of many keys: the prefill kernel cuts them and joins the parts, run after run in one workspace."""
+    b = Batch(*shape, dtype, seed=31, pad=1)
+    for causal in (True, False):
+        a, want = b.attention(causal), b.want(causal)
+        first = None
+        for _ in range(3):
+            out, lse = a.run(b.q, b.cache, b.tables())
+            first = first or (out, lse)
+            assert torch.equal(out[:-1], first[0][:-1]) and torch.equal(lse[:-1], first[1][:-1])
+        b.check(out, lse, want)
+        assert a.device_status() == 0
+
+
+@gpu
+def test_attention_one_workspace_for_several_shapes():
+    """Runs of other shapes take turns in one workspace: each leaves its counters as it found them."""
+    bs = [Batch([1, 1], [3000, 900], 8, 1, 128, 16, "NHD", torch.float16, seed=1),
+          Batch([1] * 3, [2000, 100, 1500], 28, 7, 64, 16, "HND", torch.bfloat16, seed=2),
+          Batch([40, 1], [2100, 1900], 16, 2, 128, 16, "NHD", torch.float16, seed=3),
+          Batch([2], [1700], 6, 2, 256, 16, "NHD", torch.bfloat16, seed=4)]
+    ws = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    objs = [b.attention(workspace=ws) for b in bs]
+    want = [b.want() for b in bs]
+    for _ in range(3):
+        for b, a, w in zip(bs, objs, want):
+            out, lse = a.run(b.q, b.cache, b.tables())
+            b.check(out, lse, w)
+
+
+@gpu
 def test_attention_many_short_requests():
     rng = np.random.default_rng(1)
     kv = rng.integers(1, 90, 1300)
