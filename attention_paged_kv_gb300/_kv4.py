@@ -135,7 +135,7 @@ class BatchTables:
         self.slot_mapping = torch.full((self.max_tokens,), -1, dtype=torch.int64, device=self.device)
         self.positions = torch.zeros(self.max_tokens, **i32)
         self.free_count = torch.zeros(1, **i32)
-        self.status = torch.zeros(1, **i32)
+        self.status = torch.zeros(2, **i32)  # the second word is the library's
         self._out = _b.TablesOut(*(getattr(self, n).data_ptr() for n, t in _b.TablesOut._fields_
                                    if t is ctypes.c_void_p), self.max_tokens, self.max_pages)
 

@@ -24,13 +24,14 @@ struct TablesParams {
   int64_t* slot_mapping;                                      // [max_tokens]
   int32_t* positions;                                         // [max_tokens]
   int32_t* free_count_out;
-  int32_t* status;
+  int32_t* status;  // status word, then the ticket of the build's CTAs (0 between builds)
   int64_t table_stride;
   int32_t table_width, free_capacity, batch, ps, ps_shift, num_pages, max_tokens, max_pages;
 };
 
-// The longest list (tokens or pages) that the scan's one CTA fills itself.
-constexpr int kTablesOneLaunch = 4096;
+// The largest batch whose sums are kept in shared memory (16 bytes each, 48 KB
+// without asking for more).
+constexpr int kTablesShared = 2900;
 
 cudaError_t launch_tables(const TablesParams& p, int num_sms, cudaStream_t stream);
 
@@ -75,6 +76,7 @@ struct Kv4Params {
   int64_t q_stride;  // elements between tokens
   Kv4Geom g;
   int32_t batch, num_tokens, num_page_indices, Hq, G, causal, slices, cta_heads;
+  int32_t short_keys;  // prefill: requests of few keys, one row tile and two CTAs an SM
   int32_t num_sms, split_ctas;  // prefill: CTAs of the grid for cutting items along the keys (0: never)
   int32_t small_rows;  // requests of more packed rows are the prefill kernel's
   float scale_log2;    // log2(e) / sqrt(D) * k_scale

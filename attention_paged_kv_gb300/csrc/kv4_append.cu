@@ -6,9 +6,16 @@
 //   code = e2m1(x / (s g)), beyond 6 to 6; 0 where s is 0
 //   value read back = code * s * g
 // The divisions are correctly rounded fp32 ones: a multiplication by a
-// reciprocal would move values that lie on a border between two codes.  A
-// block with a NaN gets the NaN scale, so that it reads back as NaN; an
-// infinity saturates to the block's largest value.
+// reciprocal would move values that lie on a border between two codes.  They
+// share a block's divisor, so each is the reciprocal's product put right by one
+// residual (Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990): with r = 1/b correctly rounded and q = a r, the
+// sum q + r (a - q b), in two fused steps, is a / b correctly rounded, as long
+// as nothing over- or underflows.  It does neither here where it matters:
+// quotients are clamped to 8 (codes end at 6), and where the residual
+// underflows the quotient is far below the first border.  A block with a NaN
+// gets the NaN scale, so that it reads back as NaN; an infinity saturates to
+// the block's largest value.
 //
 // HBM-bound: 2 bytes read and 0.5625 written an element (2 more where the
 // values are wanted).  A thread takes 8 values, one 16-byte load, and its
@@ -53,6 +60,12 @@ __device__ __forceinline__ float e4m3_value(uint32_t byte) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xFFFFu)));
 }
 
+// a / b for a >= 0, given r = 1 / b rounded to nearest.
+__device__ __forceinline__ float quotient(float a, float b, float r) {
+  const float q = __fmul_rn(a, r);
+  return __fmaf_rn(__fmaf_rn(-q, b, a), r, q);
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(const Kv4AppendParams p) {
   constexpr int TPR = D / 8;  // threads of a row
@@ -92,13 +105,19 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(const Kv4App
     mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
     const float g = half ? p.v_scale : p.k_scale;
     const bool nan = mb > 0x7F800000u;
-    const uint32_t sb = nan ? 0x7Fu : e4m3(__fdiv_rn(__uint_as_float(mb), 6.f * g));
+    // (an infinite or NaN maximum would make the residual NaN)
+    const float amax = fminf(__uint_as_float(mb), 3.0e38f);
+    const uint32_t sb = nan ? 0x7Fu : e4m3(__fdiv_rn(amax, 6.f * g));
     const float per = __fmul_rn(e4m3_value(sb), g);  // value of code 1
     uint32_t codes = 0;
     if (per > 0.f) {  // false for a NaN scale as well
+      const float r = __frcp_rn(per), most = 8.f * per;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        codes |= e2m1x2(__fdiv_rn(x[2 * j], per), __fdiv_rn(x[2 * j + 1], per)) << (8 * j);
+      for (int j = 0; j < 4; ++j) {
+        const float lo = quotient(fminf(fabsf(x[2 * j]), most), per, r);
+        const float hi = quotient(fminf(fabsf(x[2 * j + 1]), most), per, r);
+        codes |= e2m1x2(copysignf(lo, x[2 * j]), copysignf(hi, x[2 * j + 1])) << (8 * j);
+      }
     }
     if (!live) continue;
     const int64_t page = slot >> p.g.ps_shift;

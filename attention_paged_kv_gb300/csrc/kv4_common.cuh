@@ -100,11 +100,13 @@ __device__ __forceinline__ void join_parts(const Kv4Params& p, int rank, int thr
       sum[u] = 0.f;
       acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
+#pragma unroll 2
     for (int k = 0; k < parts; ++k) {
       const float* lse = p.part_lse + part_row(k);
 #pragma unroll
       for (int u = 0; u < U; ++u) top[u] = fmaxf(top[u], __ldcg(lse + at[u] / COLS));
     }
+#pragma unroll 2
     for (int k = 0; k < parts; ++k) {
       const int64_t row = part_row(k);
       float4 v[U];

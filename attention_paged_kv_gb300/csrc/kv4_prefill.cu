@@ -47,7 +47,7 @@ struct PreCfg {
   static constexpr int NKB = D / 64;      // 128-byte column blocks of a row
   static constexpr int BLK = 128 * 128;   // one 128-row x 128-byte block
   static constexpr int TILE = NKB * BLK;  // 128 rows of Q, K or V
-  static constexpr int NST = D == 256 ? 1 : 2;
+  static constexpr int NST = NT == 1 ? 1 : 2;
   static constexpr int OFF_K = NT * TILE;
   static constexpr int OFF_V = OFF_K + NST * TILE;
   static constexpr int OFF_BAR = OFF_V + NST * TILE;
@@ -55,9 +55,14 @@ struct PreCfg {
   static_assert(SMEM <= 232448, "shared memory per CTA");
   static constexpr int O_COL = NT * 128;
   static constexpr uint32_t TMEM_COLS = (NT * (128 + D) <= 256) ? 256u : 512u;
-  // registers: with two tiles the launch gives 512 threads 128 each, handed
-  // over as 2 x 168 (softmax) + 80 (dequantisation) + 96 (MMA) = 4 x 128;
-  static constexpr int LAUNCH_REGS = 128;
+  // Registers: the launch's share of every thread is handed over to the
+  // warpgroups as they need it, 2 x 168 (softmax) + 80 (dequantisation) + 96
+  // (MMA) = 4 x 128 with two tiles, 160 + 48 + 32 = 3 x 80 with one, two CTAs an
+  // SM.  (At head_dim 256 the launch's own 168 do for all.)
+  static constexpr bool HANDOVER = D < 256;
+  static constexpr int CTAS = D < 256 && NT == 1 ? 2 : 1;
+  static constexpr int REGS_SOFTMAX = NT == 2 ? 168 : 160, REGS_DQ = NT == 2 ? 80 : 48, REGS_MMA = NT == 2 ? 96 : 32;
+  static constexpr int LAUNCH_REGS = NT == 2 ? 128 : 80;
 };
 
 template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -68,6 +73,10 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+constexpr int kFar = 5;  // key tiles
+
+__device__ __forceinline__ void prefetch_l2(const void* at) { asm volatile("prefetch.global.L2 [%0];" ::"l"(at)); }
 
 // A key's codes and scales of K or V.
 template <int D>
@@ -113,7 +122,7 @@ __device__ __forceinline__ void store_row4(uint8_t* dst, const Row4<D>& r, int k
 }
 
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, 1) kv4_prefill_kernel(const Kv4Params p) {
+__global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, PreCfg<D, NT>::CTAS) kv4_prefill_kernel(const Kv4Params p) {
   using C = PreCfg<D, NT>;
   constexpr int NST = C::NST;
   extern __shared__ uint8_t smem_raw[];
@@ -196,7 +205,7 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, 1) kv4_prefill_kernel(
   if (p.split_ctas > 0 && work > 0) atomicAdd(reinterpret_cast<unsigned long long*>(&work_s), static_cast<unsigned long long>(work));
   // Items are whole but for those that would not fill the last wave of one
   // CTA an SM: they are cut along the keys into `parts` each, as many as make
-  // that wave shortest (4 key tiles stand for a part's start and join).
+  // that wave shortest (8 key tiles stand for a part's start and join).
   const int items = total * p.g.Hkv;
   int whole_items = items, parts = 1;
   if (p.split_ctas > 0) {
@@ -206,7 +215,7 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, 1) kv4_prefill_kernel(
       const float kts = static_cast<float>(work_s) / static_cast<float>(total);
       // lane n - 1 weighs n parts; the cheapest, the fewest among equals
       const int n = lane + 1;
-      float cost = static_cast<float>((rem * n + p.num_sms - 1) / p.num_sms) * (kts / n + (n > 1 ? 4.f : 0.f));
+      float cost = static_cast<float>((rem * n + p.num_sms - 1) / p.num_sms) * (kts / n + (n > 1 ? 8.f : 0.f));
       if (n > 1 && rem * (n - 1) > p.split_ctas) cost = INFINITY;
       float best = cost;
 #pragma unroll
@@ -274,7 +283,7 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, 1) kv4_prefill_kernel(
 
   if (warp >= C::WARP_DQ && warp < C::WARP_DQ + 4) {
     // ---------------------------------------------------------------- dequantisation
-    if constexpr (NT == 2) regs_down<80>();
+    if constexpr (C::HANDOVER) regs_down<C::REGS_DQ>();
     const int r = tid - 32 * C::WARP_DQ;  // key of the tile
     const int32_t* ids = p.pages + rq.page_start;
     const int64_t half_rows = static_cast<int64_t>(p.g.ps) * p.g.Hkv;
@@ -291,33 +300,80 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, 1) kv4_prefill_kernel(
       return static_cast<int64_t>(pid) * 2 * half_rows + static_cast<int64_t>(key & (p.g.ps - 1)) * p.g.slot_rows +
              static_cast<int64_t>(h) * p.g.head_rows;
     };
-    Row4<D> k4, v4;
     int64_t at = row_of(0, page_of(0));
-    load_row4(k4, p, at, kt0 * kKvTile + r < key_end);
-    load_row4(v4, p, at + half_rows, kt0 * kKvTile + r < key_end);
-    int next_page = page_of(1);
-    for (int j = 0; j < nkt; ++j) {
-      const int st = j % NST;
-      const uint32_t parity = ((j / NST) - 1) & 1;
-      const bool more = (kt0 + j + 1) * kKvTile + r < key_end;
-      at = row_of(j + 1, next_page);
-      next_page = page_of(j + 2);
-      if (j >= NST && !warp_wait(&empty_k[st], parity, abort_flag, p.status, kLimit)) break;
-      store_row4<D>(smem + C::OFF_K + st * C::TILE, k4, r);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full_k[st]);
-      load_row4(k4, p, at, more);
-      if (j >= NST && !warp_wait(&empty_v[st], parity, abort_flag, p.status, kLimit)) break;
-      store_row4<D>(smem + C::OFF_V + st * C::TILE, v4, r);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full_v[st]);
-      load_row4(v4, p, at + half_rows, more);
+    if constexpr (C::CTAS == 2) {
+      // few registers: one row of codes at a time, its load's wait is the other
+      // CTA's time
+      int next_page = page_of(1);
+      for (int j = 0; j < nkt; ++j) {
+        const bool live = (kt0 + j) * kKvTile + r < key_end;
+        const int st = j % NST;
+        const uint32_t parity = ((j / NST) - 1) & 1;
+        Row4<D> row;
+        load_row4(row, p, at, live);
+        if (j >= NST && !warp_wait(&empty_k[st], parity, abort_flag, p.status, kLimit)) break;
+        store_row4<D>(smem + C::OFF_K + st * C::TILE, row, r);
+        load_row4(row, p, at + half_rows, live);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full_k[st]);
+        if (j >= NST && !warp_wait(&empty_v[st], parity, abort_flag, p.status, kLimit)) break;
+        store_row4<D>(smem + C::OFF_V + st * C::TILE, row, r);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full_v[st]);
+        at = row_of(j + 1, next_page);
+        next_page = page_of(j + 2);
+      }
+    } else {
+      Row4<D> k4, v4;
+      load_row4(k4, p, at, kt0 * kKvTile + r < key_end);
+      load_row4(v4, p, at + half_rows, kt0 * kKvTile + r < key_end);
+      // One row tile alone reads the cache as fast as memory gives it: its rows
+      // are called into L2 kFar tiles ahead (the registers hold one tile of
+      // them, far less than memory's latency wants in flight).
+      const bool far = !has_b;
+      auto call_rows = [&](int j, int pid) {
+        if ((kt0 + j) * kKvTile + r >= key_end) return;
+        const int64_t row = row_of(j, pid);
+        prefetch_l2(p.codes + row * (D / 2));
+        prefetch_l2(p.codes + (row + half_rows) * (D / 2));
+        prefetch_l2(p.scales + row * (D / 16));
+        prefetch_l2(p.scales + (row + half_rows) * (D / 16));
+      };
+      int far_page = 0;
+      if (far) {
+        for (int j = 1; j < kFar; ++j) call_rows(j, page_of(j));
+        far_page = page_of(kFar);
+      }
+      int next_page = page_of(1);
+      for (int j = 0; j < nkt; ++j) {
+        const int st = j % NST;
+        const uint32_t parity = ((j / NST) - 1) & 1;
+        if (far) {
+          call_rows(j + kFar, far_page);
+          far_page = page_of(j + kFar + 1);
+        }
+        const bool more = (kt0 + j + 1) * kKvTile + r < key_end;
+        at = row_of(j + 1, next_page);
+        next_page = page_of(j + 2);
+        if (j >= NST && !warp_wait(&empty_k[st], parity, abort_flag, p.status, kLimit)) break;
+        store_row4<D>(smem + C::OFF_K + st * C::TILE, k4, r);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full_k[st]);
+        load_row4(k4, p, at, more);
+        if (j >= NST && !warp_wait(&empty_v[st], parity, abort_flag, p.status, kLimit)) break;
+        store_row4<D>(smem + C::OFF_V + st * C::TILE, v4, r);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full_v[st]);
+        load_row4(v4, p, at + half_rows, more);
+      }
     }
   } else if (warp >= C::WARP_MMA) {
     // ---------------------------------------------------------------- MMA issuer
-    if constexpr (NT == 2) regs_down<96>();
+    if constexpr (C::HANDOVER) regs_down<C::REGS_MMA>();
     if (warp == C::WARP_MMA && lane == 0 && nkt > 0) {
       const uint32_t id_s = idesc_f16(0, 0, 0, 128, 128);
       const uint32_t id_o = idesc_f16(0, 0, 1, 128, D);
@@ -327,7 +383,7 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, 1) kv4_prefill_kernel(
       auto issue_s = [&](int x, int st) {
         const uint64_t qd = dq0 + uint64_t(dual ? 0 : x) * (C::TILE >> 4);
         const uint64_t kd = dk0 + uint64_t(st) * (C::TILE >> 4);
-#pragma unroll
+#pragma unroll(NT == 1 ? 1 : D / 16)  // one tile: few registers
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = ((k >> 2) * C::BLK + (k & 3) * 32) >> 4;
           tc_mma_ss(tmem + x * 128, qd + off, kd + off, id_s, k > 0 ? 1u : 0u);
@@ -336,7 +392,7 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, 1) kv4_prefill_kernel(
       };
       auto issue_pv = [&](int x, bool first, bool last, int st) {
         const uint64_t vd = dv0 + uint64_t(st) * (C::TILE >> 4);
-#pragma unroll
+#pragma unroll(NT == 1 ? 1 : kKvTile / 16)
         for (int k = 0; k < kKvTile / 16; ++k)
           tc_mma_ts(tmem + C::O_COL + x * 128, tmem + x * 128 + k * 8, vd + (k * 2048 >> 4), id_o,
                     (!first || k > 0) ? 1u : 0u);
@@ -411,7 +467,7 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, 1) kv4_prefill_kernel(
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- softmax warps
-    if constexpr (NT == 2) regs_up<168>();
+    if constexpr (C::HANDOVER) regs_up<C::REGS_SOFTMAX>();
     const int x = warp >> 2;
     const int r = tid & 127;
     const int rx = dual ? 0 : x;            // the warpgroup's row tile
@@ -633,12 +689,23 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, 1) kv4_prefill_kernel(
             }
           }
           if (split) {
-            if (row_valid) {
+            // through the warp's own rows of q's slot, so that a store covers
+            // 128 bytes of 4 rows and not 16 of 32
+            uint8_t* rows_s = smem + x * C::TILE + (warp & 3) * 32 * 128;
 #pragma unroll
-              for (int v = 0; v < 8; ++v)
-                *reinterpret_cast<float4*>(p.part_o + part_row * D + c4 * 32 + 4 * v) =
-                    make_float4(f[4 * v] * inv, f[4 * v + 1] * inv, f[4 * v + 2] * inv, f[4 * v + 3] * inv);
+            for (int v = 0; v < 8; ++v)
+              *reinterpret_cast<float4*>(rows_s + lane * 128 + ((v ^ (lane & 7)) << 4)) =
+                  make_float4(f[4 * v] * inv, f[4 * v + 1] * inv, f[4 * v + 2] * inv, f[4 * v + 3] * inv);
+            __syncwarp();
+            const int64_t first = part_row - lane;
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+              const int rr = v * 4 + (lane >> 3), c = lane & 7;
+              const float4 w = *reinterpret_cast<const float4*>(rows_s + rr * 128 + ((c ^ (rr & 7)) << 4));
+              if ((r & ~31) + rr + x * kQRows < rows)
+                *reinterpret_cast<float4*>(p.part_o + (first + rr) * D + c4 * 32 + c * 4) = w;
             }
+            __syncwarp();
           } else {
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
@@ -707,7 +774,7 @@ cudaError_t launch_d(const Kv4Params& p, cudaStream_t stream) {
   static std::atomic<uint64_t> attr_set{0};
   cudaError_t e = set_smem_once(attr_set, reinterpret_cast<const void*>(kernel), C::SMEM);
   if (e != cudaSuccess) return e;
-  if (NT == 2) {
+  if (C::HANDOVER) {
     // the register hand-over adds up to what the launch gives: a build that
     // gives less would wait forever
     static std::atomic<int> regs{0};
@@ -734,8 +801,8 @@ cudaError_t launch_d(const Kv4Params& p, cudaStream_t stream) {
 template <typename T>
 cudaError_t launch_t(const Kv4Params& p, int D, cudaStream_t stream) {
   switch (D) {
-    case 64: return launch_d<T, 64, 2>(p, stream);
-    case 128: return launch_d<T, 128, 2>(p, stream);
+    case 64: return p.short_keys ? launch_d<T, 64, 1>(p, stream) : launch_d<T, 64, 2>(p, stream);
+    case 128: return p.short_keys ? launch_d<T, 128, 1>(p, stream) : launch_d<T, 128, 2>(p, stream);
     default: return launch_d<T, 256, 1>(p, stream);
   }
 }

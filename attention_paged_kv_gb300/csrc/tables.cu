@@ -5,15 +5,18 @@
 // needs new_b = ceil((kv_b + qo_b) / ps); the new_b - old_b missing ones come
 // off the top of the free stack in request order.  Everything else follows
 // from exclusive sums over the batch of qo_b, new_b and new_b - old_b:
-//   scan kernel   one CTA: the sums, the checks (nothing at all is changed
-//                 when one fails), the per-request outputs;
-//   fill kernel   one thread per page-list entry and per token: a binary
-//                 search in the sums names the request, so that one request
-//                 of 10^5 tokens costs no more than 10^5 requests of one.
-// The fill reads only what the scan wrote, the held part of the block table
-// and the free stack, so kv_lens and free_count may be updated in place.
-// A batch whose lists are short is filled by the scan's own CTA, from the
-// sums that it still has in shared memory: one launch instead of two.
+//   one launch    (batches of up to kTablesShared requests) every CTA makes the
+//                 sums itself and fills its share of the lists from shared
+//                 memory; per-request outputs are the first CTA's.  Those that
+//                 may be the input arrays (kv_lens, free_count) are written by
+//                 the CTA that is the last to have read them (a ticket).
+//   two launches  (larger batches) a scan by one CTA, then the fill, which
+//                 reads only what the scan wrote, the held part of the block
+//                 table and the free stack.
+// The fill takes one thread per page-list entry and per token: a binary
+// search in the sums names the request, so that one request of 10^5 tokens
+// costs no more than 10^5 requests of one.  Nothing at all is changed when a
+// check fails.
 //
 // Latency binds both (64 requests of up to 8191 tokens move 135 KB).
 #include <climits>
@@ -104,7 +107,8 @@ __device__ __forceinline__ int page_id(const TablesParams& p, int b, int nth, in
 // Entry i of the page list (i < max_pages) and of the token lists (i <
 // max_tokens).  free_before is the count before this step's pages are taken.
 __device__ __forceinline__ void fill_entry(const TablesParams& p, const int32_t* qo_indptr, const int32_t* page_indptr,
-                                           const int32_t* fresh_indptr, int free_before, int i) {
+                                           const int32_t* fresh_indptr, const int32_t* kv_lens, int free_before,
+                                           int i) {
   if (i < p.max_pages && i < page_indptr[p.batch]) {
     const int b = request_of(page_indptr, p.batch, i);
     const int nth = i - page_indptr[b], pages = page_indptr[b + 1] - page_indptr[b];
@@ -122,7 +126,7 @@ __device__ __forceinline__ void fill_entry(const TablesParams& p, const int32_t*
       const int pages = page_indptr[b + 1] - page_indptr[b];
       const int first = fresh_indptr[b], old = pages - (fresh_indptr[b + 1] - first);
       // the request's tokens end at kv_len: position = kv_len - qo_len + nth
-      pos = p.kv_lens_out[b] - (qo_indptr[b + 1] - i);
+      pos = kv_lens[b] - (qo_indptr[b + 1] - i);
       const int id = page_id(p, b, pos >> p.ps_shift, old, first, free_before);
       if (static_cast<unsigned>(id) < static_cast<unsigned>(p.num_pages))
         slot = (static_cast<int64_t>(id) << p.ps_shift) + (pos & (p.ps - 1));
@@ -132,11 +136,13 @@ __device__ __forceinline__ void fill_entry(const TablesParams& p, const int32_t*
   }
 }
 
+// kFill: the one launch, by any number of CTAs; else the scan, by one.
 template <bool kFill>
 __global__ void __launch_bounds__(kScanThreads) tables_scan_kernel(const TablesParams p) {
   __shared__ Sums warp_sums[32];
-  __shared__ int flags_s;
-  extern __shared__ int32_t sums_s[];  // kFill: qo, page and fresh sums, batch + 1 of each
+  __shared__ int flags_s, last_s;
+  extern __shared__ int32_t sums_s[];  // kFill: qo, page and fresh sums, batch + 1 of each, then the new kv_lens
+  const bool writer = blockIdx.x == 0;
   const int tid = threadIdx.x;
   if (tid == 0) flags_s = 0;
   pdl_wait();  // the lengths may come from the kernel before
@@ -159,7 +165,7 @@ __global__ void __launch_bounds__(kScanThreads) tables_scan_kernel(const TablesP
     if (free_before < 0 || free_before > p.free_capacity) f |= PA_DEV_BAD_INDEX;
     else if (total.fresh > free_before) f |= PA_DEV_NO_PAGES;
     if (total.t > p.max_tokens || total.pages > p.max_pages) f |= PA_DEV_NO_ROOM;
-    if (f) atomicOr(p.status, f);
+    if (f && writer) atomicOr(p.status, f);
     flags_s = f;
   }
   __syncthreads();
@@ -182,39 +188,58 @@ __global__ void __launch_bounds__(kScanThreads) tables_scan_kernel(const TablesP
     if (b < p.batch) {
       const int t = fail ? 0 : static_cast<int>(before.t), pages = fail ? 0 : static_cast<int>(before.pages);
       const int fresh = fail ? 0 : static_cast<int>(before.fresh);
-      p.qo_indptr[b] = t;
-      p.kv_page_indptr[b] = pages;
-      p.new_page_indptr[b] = fresh;
-      const int kv = p.kv_lens[b];  // own element, read before it is written
+      const int kv = p.kv_lens[b];
       const int n = static_cast<int>(v.pages);
-      if (!fail) p.kv_lens_out[b] = kv + static_cast<int>(v.t);
-      else if (p.kv_lens_out != p.kv_lens) p.kv_lens_out[b] = kv;
-      p.kv_last_page_len[b] = fail || n == 0 ? 0 : kv + static_cast<int>(v.t) - ((n - 1) << p.ps_shift);
+      const int now = fail ? kv : kv + static_cast<int>(v.t);
+      if (writer) {
+        p.qo_indptr[b] = t;
+        p.kv_page_indptr[b] = pages;
+        p.new_page_indptr[b] = fresh;
+        p.kv_last_page_len[b] = fail || n == 0 ? 0 : now - ((n - 1) << p.ps_shift);
+        // (the one CTA of a scan has each element read and written by one thread)
+        if constexpr (!kFill) p.kv_lens_out[b] = now;
+      }
       if constexpr (kFill) {
         sums_s[b] = t;
         sums_s[p.batch + 1 + b] = pages;
         sums_s[2 * (p.batch + 1) + b] = fresh;
+        sums_s[3 * (p.batch + 1) + b] = now;
       }
     }
   }
   if (tid == 0) {
     const int t = fail ? 0 : static_cast<int>(total.t), pages = fail ? 0 : static_cast<int>(total.pages);
     const int fresh = fail ? 0 : static_cast<int>(total.fresh);
-    p.qo_indptr[p.batch] = t;
-    p.kv_page_indptr[p.batch] = pages;
-    p.new_page_indptr[p.batch] = fresh;
-    *p.free_count_out = free_before - fresh;
+    if (writer) {
+      p.qo_indptr[p.batch] = t;
+      p.kv_page_indptr[p.batch] = pages;
+      p.new_page_indptr[p.batch] = fresh;
+    }
     if constexpr (kFill) {
       sums_s[p.batch] = t;
       sums_s[2 * p.batch + 1] = pages;
       sums_s[3 * p.batch + 2] = fresh;
+    } else {
+      *p.free_count_out = free_before - fresh;
     }
   }
   if constexpr (kFill) {
-    __syncthreads();
+    __syncthreads();  // the sums are there, and this CTA has read what it reads of kv_lens and free_count
+    if (tid == 0) {
+      __threadfence();
+      last_s = atomicAdd(p.status + 1, 1) == static_cast<int>(gridDim.x) - 1;
+    }
     const int n = max(p.max_tokens, sums_s[2 * p.batch + 1]);
-    for (int i = tid; i < n; i += kScanThreads)
-      fill_entry(p, sums_s, sums_s + p.batch + 1, sums_s + 2 * (p.batch + 1), free_before, i);
+    for (int i = blockIdx.x * kScanThreads + tid; i < n; i += gridDim.x * kScanThreads)
+      fill_entry(p, sums_s, sums_s + p.batch + 1, sums_s + 2 * (p.batch + 1), sums_s + 3 * (p.batch + 1), free_before, i);
+    __syncthreads();
+    if (last_s) {
+      for (int b = tid; b < p.batch; b += kScanThreads) p.kv_lens_out[b] = sums_s[3 * (p.batch + 1) + b];
+      if (tid == 0) {
+        *p.free_count_out = free_before - sums_s[3 * p.batch + 2];
+        p.status[1] = 0;  // for the next build
+      }
+    }
   }
 }
 
@@ -224,15 +249,20 @@ __global__ void __launch_bounds__(kFillThreads) tables_fill_kernel(const TablesP
   const int free_before = *p.free_count_out + p.new_page_indptr[p.batch];
   const int n = max(p.max_tokens, p.kv_page_indptr[p.batch]);
   for (int i = blockIdx.x * kFillThreads + threadIdx.x; i < n; i += gridDim.x * kFillThreads)
-    fill_entry(p, p.qo_indptr, p.kv_page_indptr, p.new_page_indptr, free_before, i);
+    fill_entry(p, p.qo_indptr, p.kv_page_indptr, p.new_page_indptr, p.kv_lens_out, free_before, i);
 }
 
 }  // namespace
 
 cudaError_t launch_tables(const TablesParams& p, int num_sms, cudaStream_t stream) {
   const int longest = p.max_tokens > p.max_pages ? p.max_tokens : p.max_pages;
-  if (p.batch <= kScanThreads && longest <= kTablesOneLaunch)
-    return launch_pdl(tables_scan_kernel<true>, 1u, unsigned(kScanThreads), size_t(12) * (p.batch + 1), stream, p);
+  if (p.batch <= kTablesShared) {
+    // a thread fills up to 4 entries before another CTA is worth its scan
+    const int blocks = (longest + 4 * kScanThreads - 1) / (4 * kScanThreads);
+    const int grid = blocks < 1 ? 1 : (blocks < num_sms ? blocks : num_sms);
+    return launch_pdl(tables_scan_kernel<true>, unsigned(grid), unsigned(kScanThreads), size_t(16) * (p.batch + 1),
+                      stream, p);
+  }
   cudaError_t e = launch_pdl(tables_scan_kernel<false>, 1u, unsigned(kScanThreads), size_t(0), stream, p);
   if (e != cudaSuccess) return e;
   const int blocks = (longest + kFillThreads - 1) / kFillThreads;

@@ -390,7 +390,8 @@ typedef struct {
                                 request after request; -1 from qo_indptr[batch_size] on  */
   int32_t* positions;        /* [max_tokens] its position in its request; 0 from there on */
   int32_t* free_count;       /* [1] pages left on the stack; may be the input array      */
-  int32_t* status;           /* [1] status word                                          */
+  int32_t* status;           /* [2] status word, and a word that builds count their
+                                blocks in: zero both once                                */
   int32_t max_tokens, max_pages;
 } pagedattn_tables_out;
 
@@ -429,7 +430,7 @@ typedef struct {
   int32_t num_pages, page_size, num_kv_heads;
   int32_t head_dim;  /* 64, 128 or 256                       */
   int32_t kv_layout; /* PA_LAYOUT_NHD or PA_LAYOUT_HND       */
-  float k_scale, v_scale;  /* in [1e-30, 1e30]               */
+  float k_scale, v_scale;  /* in [1e-15, 1e15]               */
 } pagedattn_kv4_cache;
 
 /* Rows for pagedattn_kv4_append. */

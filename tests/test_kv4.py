@@ -201,7 +201,28 @@ def test_tables_advance_in_place_over_replays():
 
 
 @gpu
-@pytest.mark.parametrize("B", [6, 1500])
+@pytest.mark.parametrize("B", [2000, 3500])  # several blocks of one launch, and two launches
+def test_tables_in_place_with_many_blocks(B):
+    rng = np.random.default_rng(B)
+    page = 16
+    qo, kv = rng.choice([0, 1, 30], B).astype(np.int32), rng.integers(0, 200, B).astype(np.int32)
+    table, free, num_pages = make_tables(rng, B, page, 3 * qo, kv)
+    t = pa.BatchTables(B, int(qo.sum()) + 100, num_pages, page, num_pages)
+    t.kv_lens.copy_(torch.from_numpy(kv))
+    t.free_count.fill_(len(free))
+    qo_t, table_t, free_t = (torch.from_numpy(a).cuda() for a in (qo, table.copy(), free))
+    count = len(free)
+    for _ in range(3):
+        t.kv_page_indices.fill_(-1)
+        t.build(qo_t, t.kv_lens, table_t, free_t, t.free_count)
+        want = kv4.tables(qo, kv, table, free, count, page)
+        kv, count = want["kv_lens"].astype(np.int32), want["free_count"]
+        check_tables(t, want, table, table_t, -1)
+    assert t.device_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("B", [6, 1500, 3500])
 @pytest.mark.parametrize("fault, flag", [("pages", 4), ("tokens", 8), ("lists", 8), ("width", 8), ("qo", 2), ("kv", 2),
                                          ("sum", 2), ("count", 2)])
 def test_tables_all_or_nothing(B, fault, flag):
@@ -322,6 +343,31 @@ def test_append_equals_restated(dtype, n, h, d, page, layout, scales):
         assert (got[~live] == 7.0).all()
     np.testing.assert_array_equal(cache.scales.cpu().numpy(), want["scales"])
     np.testing.assert_array_equal(cache.codes.cpu().numpy(), want["codes"])
+
+
+@gpu
+@pytest.mark.parametrize("g", [1.0, 0.37, 1.7e-4, 913.0, 1.1e-15, 0.9e15])
+def test_append_divides_as_the_device_does(g):
+    """Millions of values of every size against the definition with the device's own fp32 divisions."""
+    n, h, d = 4096, 4, 128
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    x = torch.randn((n, h, d), generator=gen, device="cuda") * torch.exp2(
+        torch.randint(-14, 14, (n, h, d // 16, 1), generator=gen, device="cuda").float()).expand(-1, -1, -1, 16).reshape(n, h, d)
+    x = x.bfloat16() * g if g < 1e-6 or g > 1e6 else x.bfloat16()  # values in the cache's range
+    x = x.bfloat16()
+    cache = pa.Kv4Cache(n // 16, 16, h, d, "NHD", g, 1.0)
+    cache.append(x, x, torch.arange(n, device="cuda"))
+    b = x.float().unflatten(-1, (-1, 16))
+    six = torch.tensor(6.0, device="cuda") * torch.tensor(g, device="cuda", dtype=torch.float32)
+    s = (b.abs().amax(-1) / six).clamp(max=448.0).to(torch.float8_e4m3fn)
+    unit = (s.float() * torch.tensor(g, device="cuda", dtype=torch.float32))[..., None]
+    y = torch.where(unit > 0, b / unit, 0.0)
+    a = y.abs()
+    code = sum(m.int() for m in (a > 0.25, a >= 0.75, a > 1.25, a >= 1.75, a > 2.5, a >= 3.5, a > 5.0))
+    code = (code + 8 * torch.signbit(y).int()).flatten(-2)
+    want = (code[..., 0::2] | (code[..., 1::2] << 4)).to(torch.uint8)
+    assert torch.equal(cache.scales[:, 0].reshape(n, h, -1), s.view(torch.uint8))
+    assert torch.equal(cache.codes[:, 0].reshape(n, h, -1), want)
 
 
 @gpu
