@@ -137,7 +137,7 @@ __device__ __forceinline__ void fill_entry(const TablesParams& p, const int32_t*
 }
 
 // kFill: the one launch, by any number of CTAs; else the scan, by one.
-template <bool kFill>
+template <bool kFill, int kPerThread>
 __global__ void __launch_bounds__(kScanThreads) tables_scan_kernel(const TablesParams p) {
   __shared__ Sums warp_sums[32];
   __shared__ int flags_s, last_s;
@@ -149,17 +149,24 @@ __global__ void __launch_bounds__(kScanThreads) tables_scan_kernel(const TablesP
   __syncthreads();
   const int free_before = *p.free_count;
 
-  // totals and checks; the first kScanThreads requests stay in registers
+  // totals and checks; in the one launch a thread keeps its kPerThread
+  // consecutive requests in registers
+  constexpr int kKept = kFill ? kPerThread : 1;
   int flags = 0;
-  Sums mine{0, 0, 0}, all{0, 0, 0};
-  for (int b = tid; b < p.batch; b += kScanThreads) {
-    const Sums v = load_request(p, b, &flags);
-    if (b == tid) mine = v;
-    all = add(all, v);
+  Sums kept[kKept], all{0, 0, 0};
+  if constexpr (kFill) {
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) {
+      const int b = tid * kKept + i;
+      kept[i] = b < p.batch ? load_request(p, b, &flags) : Sums{0, 0, 0};
+      all = add(all, kept[i]);
+    }
+  } else {
+    for (int b = tid; b < p.batch; b += kScanThreads) all = add(all, load_request(p, b, &flags));
   }
   if (flags) atomicOr(&flags_s, flags);
   Sums total;
-  Sums before = block_scan(p.batch <= kScanThreads ? mine : all, warp_sums, &total);
+  Sums before = block_scan(all, warp_sums, &total);
   if (tid == 0) {
     int f = flags_s;
     if (free_before < 0 || free_before > p.free_capacity) f |= PA_DEV_BAD_INDEX;
@@ -173,11 +180,14 @@ __global__ void __launch_bounds__(kScanThreads) tables_scan_kernel(const TablesP
 
   // per-request outputs (of an empty batch when a check failed)
   Sums carry{0, 0, 0};
-  for (int b0 = 0; b0 < p.batch; b0 += kScanThreads) {
-    const int b = b0 + tid;
+  const int rounds = kFill ? kKept : (p.batch + kScanThreads - 1) / kScanThreads;
+#pragma unroll
+  for (int i = 0; i < rounds; ++i) {
+    const int b = kFill ? tid * kKept + i : i * kScanThreads + tid;
     Sums v{0, 0, 0};
-    if (p.batch <= kScanThreads) {
-      v = mine;
+    if constexpr (kFill) {
+      if (i > 0) before = add(before, kept[i - 1]);
+      v = kept[i];
     } else {
       int ignored = 0;
       if (b < p.batch) v = load_request(p, b, &ignored);
@@ -257,13 +267,16 @@ __global__ void __launch_bounds__(kFillThreads) tables_fill_kernel(const TablesP
 cudaError_t launch_tables(const TablesParams& p, int num_sms, cudaStream_t stream) {
   const int longest = p.max_tokens > p.max_pages ? p.max_tokens : p.max_pages;
   if (p.batch <= kTablesShared) {
-    // a thread fills up to 4 entries before another CTA is worth its scan
-    const int blocks = (longest + 4 * kScanThreads - 1) / (4 * kScanThreads);
-    const int grid = blocks < 1 ? 1 : (blocks < num_sms ? blocks : num_sms);
-    return launch_pdl(tables_scan_kernel<true>, unsigned(grid), unsigned(kScanThreads), size_t(16) * (p.batch + 1),
-                      stream, p);
+    // one entry a thread, as far as the SMs go: the entries wait for loads (the
+    // scan that every CTA repeats waits for them together)
+    const int blocks = (longest + kScanThreads - 1) / kScanThreads;
+    const unsigned grid = static_cast<unsigned>(blocks < 1 ? 1 : (blocks < num_sms ? blocks : num_sms));
+    const size_t smem = size_t(16) * (p.batch + 1);
+    if (p.batch <= kScanThreads)
+      return launch_pdl(tables_scan_kernel<true, 1>, grid, unsigned(kScanThreads), smem, stream, p);
+    return launch_pdl(tables_scan_kernel<true, 3>, grid, unsigned(kScanThreads), smem, stream, p);
   }
-  cudaError_t e = launch_pdl(tables_scan_kernel<false>, 1u, unsigned(kScanThreads), size_t(0), stream, p);
+  cudaError_t e = launch_pdl(tables_scan_kernel<false, 1>, 1u, unsigned(kScanThreads), size_t(0), stream, p);
   if (e != cudaSuccess) return e;
   const int blocks = (longest + kFillThreads - 1) / kFillThreads;
   const int most = num_sms * 8;
