@@ -47,6 +47,7 @@ namespace {
 constexpr int kUnitKeys = 64;
 constexpr int kMinUnits = 4;  // of a slice: below 256 keys a split costs more than it spreads
 constexpr int kStepKeys = 32;
+constexpr int kTries = 8;       // part sizes that are weighed
 constexpr int kKeptReqs = 128;  // requests of a slice kept in shared memory
 constexpr float kLn2f = 0.6931471805599453f;
 // A running maximum before any key: finite, so that it can be subtracted.
@@ -179,7 +180,7 @@ struct SmallCfg {
   static constexpr int O_STRIDE = D + 4;
   static_assert(ROWS * (O_STRIDE + 2) * 4 <= RING, "a warp's state fits its ring");
   static constexpr int SMEM = WARPS * RING + (Q_SMEM ? NT * (D / 16) * 256 + ROWS * 4 : 0);
-  static_assert(CTAS * (SMEM + kKeptReqs * 16 + 256 + 1024) <= 233472, "shared memory per SM");
+  static_assert(CTAS * (SMEM + kKeptReqs * 16 + 768 + 1024) <= 233472, "shared memory per SM");
 };
 
 template <typename T, int D, int NT>
@@ -189,6 +190,7 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
   constexpr int kThreads = C::THREADS, kWarps = C::WARPS;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long scratch[kWarps];
+  __shared__ int tiles_s[kWarps], longest_s[kWarps], sums_s[kWarps][kTries];
   __shared__ Req req_s[kKeptReqs];  // the slice's first requests, where its scan met them
   __shared__ long long found_u;
   __shared__ int found_b, last_s[8];
@@ -213,9 +215,23 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
   };
   Req mine{0, 0, 0, 0};
   long long units = 0;
+  int tiles = 0, longest = 0;
   for (int b = tid; b < p.batch; b += kThreads) {
     mine = load_req(p, b);
-    units += units_of(mine);
+    const int n = row_tiles(p, mine, C::ROWS), k = key_units(mine);
+    units += static_cast<long long>(n) * k;
+    tiles = min(tiles + n, 1 << 20);
+    if (n > 0) longest = max(longest, k);
+  }
+  const int my_tiles = tiles;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) {
+    tiles += __shfl_xor_sync(0xffffffffu, tiles, d);
+    longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, d));
+  }
+  if (lane == 0) {
+    tiles_s[warp] = tiles;
+    longest_s[warp] = longest;
   }
   auto sum_before = [&](long long v, long long* all) -> long long {  // exclusive sum over the block
     long long x = v;
@@ -239,8 +255,66 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
   long long total;
   long long before = sum_before(units, &total);
   const long long per_slice = max(static_cast<long long>(kMinUnits), (total + p.slices - 1) / p.slices);
+
+  // ---- Slices of one size take a share of the next request with them and leave
+  // a share of their last one to the next slice.  Where there are slices enough
+  // for every row tile, a slice may be one tile instead, or one of equal parts
+  // of at most `part_units`: no second start in a slice, and no join where the
+  // tiles stay whole.  Weighed in us: a unit's bytes at the 20 GB/s that a CTA
+  // gets when all run, 8 for the second start and the joins of equal slices,
+  // 4.5 for a join (128 requests of 1024 keys: 16.6 us in equal slices, 9.9
+  // whole).
+  int part_units = 0;  // 0: slices of equal size
+  if (p.batch <= kThreads) {
+    tiles = longest = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      tiles += tiles_s[w];
+      longest = max(longest, longest_s[w]);
+    }
+    const float unit_us = static_cast<float>(cta_heads) * D * 0.0036f;
+    const int least = static_cast<int>(min(per_slice, static_cast<long long>(longest)));
+    if (tiles > 0 && tiles <= p.slices) {
+      float best = least * unit_us + 8.f;
+      if (longest * unit_us < best) {
+        best = longest * unit_us;
+        part_units = longest;
+      }
+      if (least * unit_us + 4.5f < best) {
+        int n[kTries];
+#pragma unroll
+        for (int k = 0; k < kTries; ++k) {
+          const int size = least + (longest - least) * k / kTries;
+          n[k] = my_tiles * ((key_units(mine) + size - 1) / max(1, size));
+#pragma unroll
+          for (int d = 16; d; d >>= 1) n[k] += __shfl_xor_sync(0xffffffffu, n[k], d);
+          if (lane == 0) sums_s[warp][k] = n[k];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = kTries - 1; k >= 0; --k) {
+          const int size = least + (longest - least) * k / kTries;
+          int all = 0;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) all += sums_s[w][k];
+          if (all <= p.slices && size * unit_us + 4.5f < best) {
+            best = size * unit_us + 4.5f;
+            part_units = size;
+          }
+        }
+      }
+    }
+  }
+  const bool by_parts = part_units > 0;
+  auto parts_of = [&](const Req& r) { return (key_units(r) + part_units - 1) / part_units; };
   long long u = slice * per_slice;
-  const long long u_end = min(total, u + per_slice);
+  long long u_end = min(total, u + per_slice);
+  if (by_parts) {  // u counts parts here
+    units = static_cast<long long>(my_tiles) * parts_of(mine);
+    before = sum_before(units, &total);
+    u = slice;
+    u_end = min(total, u + 1);
+  }
   if (u >= u_end) return;
   int chunk = 0;  // first request of the threads' `mine`
   for (long long base = 0; chunk < p.batch; chunk += kThreads) {
@@ -299,10 +373,14 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
   bool first_segment = true;
   while (u < u_end) {
     const int kts = key_units(rq);
-    const int rt = static_cast<int>((u - req_u) / kts);
-    const long long tile_u = req_u + static_cast<long long>(rt) * kts;
-    const int unit0 = static_cast<int>(u - tile_u);
-    const long long seg_end = min(u_end, tile_u + kts);
+    const int n_parts = by_parts ? parts_of(rq) : kts;  // of a row tile, in what u counts
+    const int rt = static_cast<int>((u - req_u) / n_parts);
+    const long long tile_u = req_u + static_cast<long long>(rt) * n_parts;
+    const long long seg_end = min(u_end, tile_u + n_parts);
+    const int at0 = static_cast<int>(u - tile_u), at1 = static_cast<int>(seg_end - tile_u);
+    const int unit0 = by_parts ? static_cast<int>(static_cast<long long>(kts) * at0 / n_parts) : at0;
+    const int unit1 = by_parts ? static_cast<int>(static_cast<long long>(kts) * at1 / n_parts) : at1;
+    const bool whole = unit0 == 0 && unit1 == kts;
     const int row0 = rt * C::ROWS;
     const int rows = min(C::ROWS, rq.qo_len * p.G - row0);
     // packed row n of the tile: token tok0 + token_of(n), head (head0 + n) % G
@@ -313,7 +391,7 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
     const int seen_end = p.causal ? max(0, shift + tok0 + token_of(rows - 1)) : rq.kv_len;
     const int all_end = p.causal ? shift + tok0 : rq.kv_len;
     const int key_a = unit0 * kUnitKeys;
-    const int key_b = min(static_cast<int>(seg_end - tile_u) * kUnitKeys, seen_end);
+    const int key_b = min(unit1 * kUnitKeys, seen_end);
     const int steps = key_b > key_a ? (key_b - key_a + kStepKeys - 1) / kStepKeys : 0;
 
     // page of key `lane` of a step; keys that no row sees have none
@@ -633,7 +711,6 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
                                                                 o[nt][2 * j + 1][i], o[nt][2 * j + 1][i + 2]);
       }
     team_sync();
-    const bool whole = unit0 == 0 && seg_end == tile_u + kts;
     auto out_row = [&](int n) -> int64_t {
       const int tok = token_of(n);
       return static_cast<int64_t>(rq.qo_start + tok0 + tok) * p.Hq + h * p.G + head0 + n - tok * p.G;
@@ -676,11 +753,12 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
       // ---- the last slice of a cut row tile joins its parts:
       // o = sum_s 2^(lse_s - lse) o_s.  The sum's order is the slices', so
       // the result does not depend on which one comes last.
-      const int sa = static_cast<int>(tile_u / per_slice), sb = static_cast<int>((tile_u + kts - 1) / per_slice);
-      const bool sa_first = tile_u == sa * per_slice;
-      __threadfence();
+      const long long step = by_parts ? 1 : per_slice;
+      const int sa = static_cast<int>(tile_u / step), sb = static_cast<int>((tile_u + n_parts - 1) / step);
+      const bool sa_first = tile_u == sa * step;
       team_sync();
       if (rank == 0) {
+        __threadfence();
         int32_t* count = p.counters + (sa + 1) * p.g.Hkv + h;
         const int last = atomicAdd(count, 1) == sb - sa;
         if (last) *count = 0;  // for the next run
@@ -693,14 +771,16 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
           const int which = (sl == sa && !sa_first) ? 1 : 0;
           return ((static_cast<int64_t>(sl) * p.g.Hkv + h) * 2 + which) * C::ROWS;
         };
-        join_parts<T, D, 4>(p, rank, team * 32, rows, sb - sa + 1, [&](int k) { return part_row(sa + k); }, out_row);
+        auto from = [&](int k) { return part_row(sa + k); };
+        if (rows * (D / 4) <= team * 32) join_parts<T, D, 1, 8>(p, rank, team * 32, rows, sb - sa + 1, from, out_row);
+        else join_parts<T, D, 4, 2>(p, rank, team * 32, rows, sb - sa + 1, from, out_row);
       }
     }
     team_sync();  // the rings are the next row tile's
     first_segment = false;
     u = seg_end;
     if (u < u_end && rt + 1 == row_tiles(p, rq, C::ROWS)) {  // on to the next request with units
-      req_u += static_cast<long long>(row_tiles(p, rq, C::ROWS)) * kts;
+      req_u += static_cast<long long>(row_tiles(p, rq, C::ROWS)) * kts;  // (never by parts)
       do {
         if (++b >= p.batch) return;
         rq = b < kept_b ? req_s[b - first_b] : load_req(p, b);

@@ -82,9 +82,9 @@ struct DivG {
 // Joins `parts` states of `rows` rows: o = sum_k 2^(lse_k - lse) o_k, in the
 // parts' order, by `threads` threads of which this one is `rank`.  Part k's
 // rows begin at part_row(k) of part_o / part_lse; out_row(n) is row n of out.
-// A thread has U columns in flight at a time: one by one, each would wait for
-// two dependent loads.
-template <typename T, int D, int U, typename PartRow, typename OutRow>
+// A thread has K parts of U columns in flight at a time: one by one, each
+// would wait for two dependent loads.
+template <typename T, int D, int U, int K, typename PartRow, typename OutRow>
 __device__ __forceinline__ void join_parts(const Kv4Params& p, int rank, int threads, int rows, int parts,
                                            PartRow part_row, OutRow out_row) {
   constexpr int COLS = D / 4;  // float4 columns of a row
@@ -100,13 +100,13 @@ __device__ __forceinline__ void join_parts(const Kv4Params& p, int rank, int thr
       sum[u] = 0.f;
       acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-#pragma unroll 2
+#pragma unroll K
     for (int k = 0; k < parts; ++k) {
       const float* lse = p.part_lse + part_row(k);
 #pragma unroll
       for (int u = 0; u < U; ++u) top[u] = fmaxf(top[u], __ldcg(lse + at[u] / COLS));
     }
-#pragma unroll 2
+#pragma unroll K
     for (int k = 0; k < parts; ++k) {
       const int64_t row = part_row(k);
       float4 v[U];

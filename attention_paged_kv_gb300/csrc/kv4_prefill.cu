@@ -738,9 +738,9 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, PreCfg<D, NT>::CTAS) k
       // ---- the last part of an item joins them all: o = sum_s 2^(lse_s - lse)
       // o_s, in the parts' order whichever comes last.  (A part that gave up
       // has raised its status; it is counted all the same.)
-      __threadfence();
       asm volatile("bar.sync 1, %0;" ::"n"(NT * 128) : "memory");
       if (tid == 0) {
+        __threadfence();
         int32_t* count = p.counters + cut_item / parts;
         const int last = atomicAdd(count, 1) == my_parts - 1;
         if (last) *count = 0;  // for the next run
@@ -749,7 +749,7 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, PreCfg<D, NT>::CTAS) k
       asm volatile("bar.sync 1, %0;" ::"n"(NT * 128) : "memory");
       if (last_s) {
         __threadfence();
-        join_parts<T, D, 8>(p, tid, NT * 128, rows, my_parts,
+        join_parts<T, D, 8, 2>(p, tid, NT * 128, rows, my_parts,
                             [&](int k) -> int64_t { return (part_tile + k) * (NT * kQRows); }, out_row);
       }
     }
