@@ -37,6 +37,7 @@
 // shared memory.
 #include <cstring>
 #include <type_traits>
+#include <utility>
 
 #include "internal.h"
 #include "kv4_common.cuh"
@@ -94,42 +95,62 @@ __device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
+// BYTES of shared memory in registers.  (Plain loads: a constant part of the
+// address is the instruction's, where inline assembly had an addition for
+// each of a step's 24 loads.)
 template <int BYTES>
-__device__ __forceinline__ void lds(uint32_t (&r)[BYTES / 4], uint32_t at) {
+__device__ __forceinline__ void lds(uint32_t (&r)[BYTES / 4], const uint8_t* at) {
   if constexpr (BYTES == 4) {
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r[0]) : "r"(at));
+    r[0] = *reinterpret_cast<const uint32_t*>(at);
   } else if constexpr (BYTES == 8) {
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(at));
+    const uint2 v = *reinterpret_cast<const uint2*>(at);
+    r[0] = v.x;
+    r[1] = v.y;
   } else {
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(at));
+    const uint4 v = *reinterpret_cast<const uint4*>(at);
+    r[0] = v.x;
+    r[1] = v.y;
+    r[2] = v.z;
+    r[3] = v.w;
   }
 }
 // 1, 2 or 4 bytes of shared memory.
 template <int BYTES>
-__device__ __forceinline__ uint32_t lds_scales(uint32_t at) {
-  uint32_t r;
-  if constexpr (BYTES == 4) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(at));
-  else if constexpr (BYTES == 2) asm volatile("ld.shared.u16 %0, [%1];" : "=r"(r) : "r"(at));
-  else asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(at));
-  return r;
+__device__ __forceinline__ uint32_t lds_scales(const uint8_t* at) {
+  if constexpr (BYTES == 4) return *reinterpret_cast<const uint32_t*>(at);
+  if constexpr (BYTES == 2) return *reinterpret_cast<const uint16_t*>(at);
+  return *at;
 }
+// f(0), f(1), ... f(N - 1) with constants.
+template <int... I, typename F>
+__device__ __forceinline__ void each_of(std::integer_sequence<int, I...>, F&& f) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+// base + a * b in one instruction (the compiler's own choice for the same
+// expression took several).
+__device__ __forceinline__ const uint8_t* offset_by(const uint8_t* base, uint32_t a, uint32_t b) {
+  uint64_t r;
+  asm("mad.wide.u32 %0, %1, %2, %3;" : "=l"(r) : "r"(a), "r"(b), "l"(reinterpret_cast<uint64_t>(base)));
+  return reinterpret_cast<const uint8_t*>(r);
+}
+
 // cp.async of N bytes (through L2 alone where N = 16), and one that writes
 // zeros where !live.
-template <int N>
+template <int N, int OFF>
 __device__ __forceinline__ void cp_async(uint32_t dst, const uint8_t* src) {
   if constexpr (N == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0 + %2], [%1], 16;" ::"r"(dst), "l"(src), "n"(OFF) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0 + %3], [%1], %2;" ::"r"(dst), "l"(src), "n"(N), "n"(OFF) : "memory");
 }
-template <int N>
+template <int N, int OFF>
 __device__ __forceinline__ void cp_async_or_zero(uint32_t dst, const uint8_t* src, bool live) {
   if constexpr (N == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0 + %3], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0), "n"(OFF)
+                 : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(live ? N : 0), "n"(N)
+    asm volatile("cp.async.ca.shared.global [%0 + %4], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(live ? N : 0), "n"(N),
+                 "n"(OFF)
                  : "memory");
 }
 template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -350,7 +371,8 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
   const int copy_row = lane / St::LANES, copy_chunk = lane % St::LANES;
   const uint8_t* codes_h = p.codes + static_cast<int64_t>(h) * p.g.head_rows * (D / 2) + copy_chunk * 16;
   const uint8_t* scales_h = p.scales + static_cast<int64_t>(h) * p.g.head_rows * (D / 16);
-  const uint32_t ring = smem_u32(smem) + warp * C::RING;
+  const uint32_t smem_base = smem_u32(smem);
+  const uint32_t ring = smem_base + warp * C::RING;
   // states: of member w of the team at w * team_step
   float* o_s = reinterpret_cast<float*>(smem + cta_head * C::RING);  // [rows][O_STRIDE], then m and l of each row
   const int team_step = cta_heads * C::RING / 4;
@@ -403,35 +425,37 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
     // copies step s into the stage at `st`; `pids` from step_page(s)
     auto copy_rows = [&](int key, uint32_t st, int pids, auto tail) {
       constexpr bool kTail = decltype(tail)::value;  // rows of keys that no row sees are zeros
-#pragma unroll
-      for (int i = 0; i < St::LANES; ++i) {
+      const uint32_t dst0 = st + copy_to;
+      each_of(std::make_integer_sequence<int, St::LANES>{}, [&](auto which) {
+        constexpr int i = decltype(which)::value;
         constexpr int RPP = 32 / St::LANES;
         const int r = i * RPP + copy_row;
         const uint32_t pid = __shfl_sync(0xffffffffu, pids, r);
         const uint32_t slot = (key + r) & (p.g.ps - 1);
-        const uint8_t* src = codes_h + static_cast<uint64_t>(pid) * page_bytes + static_cast<uint64_t>(slot) * slot_bytes;
+        const uint8_t* src = offset_by(offset_by(codes_h, slot, slot_bytes), pid, page_bytes);
         // (the swizzle of a 4-row pass changes with bit 2 of its first row)
-        const uint32_t dst = st + ((copy_to + i * RPP * St::ROW) ^ (D == 256 ? (i & 1) << 4 : 0));
+        const uint32_t dst = D == 256 && (i & 1) ? dst0 ^ 16 : dst0;
+        constexpr int OFF = i * RPP * St::ROW;
         if constexpr (kTail) {
           const bool live = key + r < key_b;
-          cp_async_or_zero<16>(dst, src, live);
-          cp_async_or_zero<16>(dst + St::OFF_V, src + (page_bytes >> 1), live);
+          cp_async_or_zero<16, OFF>(dst, src, live);
+          cp_async_or_zero<16, OFF + St::OFF_V>(dst, src + (page_bytes >> 1), live);
         } else {
-          cp_async<16>(dst, src);
-          cp_async<16>(dst + St::OFF_V, src + (page_bytes >> 1));
+          cp_async<16, OFF>(dst, src);
+          cp_async<16, OFF + St::OFF_V>(dst, src + (page_bytes >> 1));
         }
-      }
+      });
       const uint32_t slot = (key + lane) & (p.g.ps - 1);
-      const uint8_t* src = scales_h + static_cast<uint64_t>(static_cast<uint32_t>(pids)) * (page_bytes >> 3) +
-                           static_cast<uint64_t>(slot) * (slot_bytes >> 3);
-      const uint32_t dst = st + St::OFF_KS + lane * St::SROW;
+      const uint8_t* src =
+          offset_by(offset_by(scales_h, slot, slot_bytes >> 3), static_cast<uint32_t>(pids), page_bytes >> 3);
+      const uint32_t dst = st + lane * St::SROW;
       if constexpr (kTail) {
         const bool live = key + lane < key_b;
-        cp_async_or_zero<St::SROW>(dst, src, live);
-        cp_async_or_zero<St::SROW>(dst + St::OFF_VS - St::OFF_KS, src + (page_bytes >> 4), live);
+        cp_async_or_zero<St::SROW, St::OFF_KS>(dst, src, live);
+        cp_async_or_zero<St::SROW, St::OFF_VS>(dst, src + (page_bytes >> 4), live);
       } else {
-        cp_async<St::SROW>(dst, src);
-        cp_async<St::SROW>(dst + St::OFF_VS - St::OFF_KS, src + (page_bytes >> 4));
+        cp_async<St::SROW, St::OFF_KS>(dst, src);
+        cp_async<St::SROW, St::OFF_VS>(dst, src + (page_bytes >> 4));
       }
     };
     auto copy_step = [&](int s, uint32_t st, int pids) {
@@ -546,9 +570,9 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
       __syncwarp();
       copy_step(s + (C::STAGES - 1) * team, st_write, next_pids);
       next_pids = step_page(s + C::STAGES * team);
-      const uint32_t st = st_read;
-      st_write = st;
-      st_read = st + St::BYTES == ring_end ? ring : st + St::BYTES;
+      const uint8_t* st = smem + (st_read - smem_base);
+      st_write = st_read;
+      st_read = st_read + St::BYTES == ring_end ? ring : st_read + St::BYTES;
       // ---- S^T = K q^T
       float sc[NT][2][4];
       uint32_t ks[4];
