@@ -126,14 +126,6 @@ template <int... I, typename F>
 __device__ __forceinline__ void each_of(std::integer_sequence<int, I...>, F&& f) {
   (f(std::integral_constant<int, I>{}), ...);
 }
-// base + a * b in one instruction (the compiler's own choice for the same
-// expression took several).
-__device__ __forceinline__ const uint8_t* offset_by(const uint8_t* base, uint32_t a, uint32_t b) {
-  uint64_t r;
-  asm("mad.wide.u32 %0, %1, %2, %3;" : "=l"(r) : "r"(a), "r"(b), "l"(reinterpret_cast<uint64_t>(base)));
-  return reinterpret_cast<const uint8_t*>(r);
-}
-
 // cp.async of N bytes (through L2 alone where N = 16), and one that writes
 // zeros where !live.
 template <int N, int OFF>

@@ -58,6 +58,13 @@ __device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// base + a * b in one instruction.
+__device__ __forceinline__ const uint8_t* offset_by(const uint8_t* base, uint32_t a, uint32_t b) {
+  uint64_t r;
+  asm("mad.wide.u32 %0, %1, %2, %3;" : "=l"(r) : "r"(a), "r"(b), "l"(reinterpret_cast<uint64_t>(base)));
+  return reinterpret_cast<const uint8_t*>(r);
+}
+
 // The power of two (as its exponent) that brings a bf16 row whose largest
 // magnitude has the bits `top` to [2^13, 2^14), where fp16 holds it; 0 for
 // rows of zeros, subnormals, infinities or NaN.

@@ -78,7 +78,9 @@ constexpr int kFar = 5;  // key tiles
 
 __device__ __forceinline__ void prefetch_l2(const void* at) { asm volatile("prefetch.global.L2 [%0];" ::"l"(at)); }
 
-// A key's codes and scales of K or V.
+// A key's codes and scales of K or V.  (Whole rows to an access, a lane with 16
+// bytes of every 8th key, loads better but finds four addresses where this
+// finds one: 64 drafting requests of 64 rows 247 -> 277 us.)
 template <int D>
 struct Row4 {
   uint4 codes[D / 32];
@@ -111,7 +113,7 @@ __device__ __forceinline__ void store_row4(uint8_t* dst, const Row4<D>& r, int k
     const uint32_t two = r.scales[i >> 1] >> (16 * (i & 1));
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      const uint32_t s = e4m3x2_f16(((two >> (8 * (w >> 1))) & 0xFFu) * 0x101u);
+      const uint32_t s = e4m3x2_f16(__byte_perm(two, 0, (w >> 1) * 0x1111u));
       uint32_t h[4];
       e2m1x8(words[w], h);
       const int c = (i & 1) * 4 + w;  // 16-byte chunk of the 128-byte block
@@ -133,6 +135,7 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, PreCfg<D, NT>::CTAS) k
   __shared__ int warp_sums[32], found_tile, last_s;
   __shared__ long long work_s;
   __shared__ Req found_rq;
+  __shared__ float fac_s[NT * kQRows];  // bf16: the rows' logit factors
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* full_k = bars;             // [NST] K tile written
@@ -475,8 +478,7 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, PreCfg<D, NT>::CTAS) k
     const bool row_valid = pr < rows;
     const bool active = x == 0 || has_b || dual;
     const bool warp_rows = rx * kQRows + (r & ~31) < rows;  // some row of the warp is one
-    const int tok = token_of(pr);
-    int row_end = p.causal ? shift + tok0 + tok : rq.kv_len;
+    int row_end = p.causal ? shift + tok0 + token_of(pr) : rq.kv_len;
     row_end = row_valid ? min(row_end, key_end) - kt0 * kKvTile : 0;
     float sl2 = p.scale_log2;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -484,38 +486,53 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, PreCfg<D, NT>::CTAS) k
     const uint32_t o_col = tmem + lane_base + C::O_COL + x * 128;
     uint8_t* q_row = smem + x * C::TILE + r * 128;  // chunk c of block kb at kb * BLK + ((c ^ (r & 7)) << 4)
 
-    if (active) {  // the row of q as fp16 (dual: warpgroup 1 needs its factor alone)
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (static_cast<int64_t>(rq.qo_start) + tok0 + tok) * p.q_stride +
-                                                        static_cast<int64_t>(h * p.G + head0 + pr - tok * p.G) * D);
-      float mul = 1.f;
-      if constexpr (Elt<T>::kBf16) {
-        uint32_t top = 0;
-        if (row_valid) {
-#pragma unroll 8
-          for (int i = 0; i < D / 8; ++i) {
-            const uint4 w = src[i];
-            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+    if (active && warp_rows) {
+      // the warp's 32 rows of q as fp16, whole rows at a time (a thread loading
+      // its own row took 5 us: 32 rows an access); dual: warpgroup 1 needs the
+      // factors alone
+      constexpr int LPR = D / 8;                      // lanes of a row
+      constexpr int RPI = 32 / LPR;                   // rows of an access
+      constexpr int NQ = 32 / RPI < 16 ? 32 / RPI : 16;  // accesses in flight
+#pragma unroll 1
+      for (int i0 = 0; i0 < 32 / RPI; i0 += NQ) {
+        uint4 w[NQ];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) top = max(top, max(ws[e] & 0x7FFFu, (ws[e] >> 16) & 0x7FFFu));
-          }
+        for (int i = 0; i < NQ; ++i) {
+          const int n = rx * kQRows + (warp & 3) * 32 + (i0 + i) * RPI + lane / LPR;  // row of the item
+          const int t = token_of(n);
+          w[i] = make_uint4(0, 0, 0, 0);
+          if (n < rows)
+            w[i] = __ldg(reinterpret_cast<const uint4*>(
+                static_cast<const T*>(p.q) + (static_cast<int64_t>(rq.qo_start) + tok0 + t) * p.q_stride +
+                static_cast<int64_t>(h * p.G + head0 + n - t * p.G) * D + (lane % LPR) * 8));
         }
-        const int up = bf16_row_shift(top);
-        mul = pow2(up);
-        sl2 *= pow2(-up);
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+          const int rr = (warp & 3) * 32 + (i0 + i) * RPI + lane / LPR, c = lane % LPR;
+          if constexpr (Elt<T>::kBf16) {
+            uint32_t m = __vmaxu2(__vmaxu2(w[i].x & 0x7FFF7FFFu, w[i].y & 0x7FFF7FFFu),
+                                  __vmaxu2(w[i].z & 0x7FFF7FFFu, w[i].w & 0x7FFF7FFFu));
+#pragma unroll
+            for (int d2 = 1; d2 < LPR; d2 <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, d2));
+            const int up = bf16_row_shift(max(m & 0xFFFFu, m >> 16));
+            const float mul = pow2(up);
+            if (c == 0) fac_s[x * kQRows + rr] = pow2(-up);
+            uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = Elt<T>::to_f2(ws[e]);
+              ws[e] = pack_f16x2(f.x * mul, f.y * mul);
+            }
+            w[i] = make_uint4(ws[0], ws[1], ws[2], ws[3]);
+          }
+          if (!dual || x == 0)
+            *reinterpret_cast<uint4*>(smem + x * C::TILE + (c >> 3) * C::BLK + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) =
+                w[i];
+        }
       }
-#pragma unroll 8
-      for (int i = 0; i < D / 8; ++i) {
-        uint4 w = row_valid ? src[i] : make_uint4(0, 0, 0, 0);
-        if constexpr (Elt<T>::kBf16) {
-          uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = Elt<T>::to_f2(ws[e]);
-            ws[e] = pack_f16x2(f.x * mul, f.y * mul);
-          }
-          w = make_uint4(ws[0], ws[1], ws[2], ws[3]);
-        }
-        if (!dual || x == 0) *reinterpret_cast<uint4*>(q_row + (i >> 3) * C::BLK + (((i & 7) ^ (r & 7)) << 4)) = w;
+      if constexpr (Elt<T>::kBf16) {
+        __syncwarp();
+        sl2 *= fac_s[x * kQRows + r];
       }
     }
     fence_proxy_async_smem();
