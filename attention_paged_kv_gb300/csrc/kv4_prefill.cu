@@ -56,12 +56,12 @@ struct PreCfg {
   static constexpr int O_COL = NT * 128;
   static constexpr uint32_t TMEM_COLS = (NT * (128 + D) <= 256) ? 256u : 512u;
   // Registers: the launch's share of every thread is handed over to the
-  // warpgroups as they need it, 2 x 168 (softmax) + 80 (dequantisation) + 96
+  // warpgroups as they need it, 2 x 176 (softmax) + 72 (dequantisation) + 88
   // (MMA) = 4 x 128 with two tiles, 160 + 48 + 32 = 3 x 80 with one, two CTAs an
   // SM.  (At head_dim 256 the launch's own 168 do for all.)
   static constexpr bool HANDOVER = D < 256;
   static constexpr int CTAS = D < 256 && NT == 1 ? 2 : 1;
-  static constexpr int REGS_SOFTMAX = NT == 2 ? 168 : 160, REGS_DQ = NT == 2 ? 80 : 48, REGS_MMA = NT == 2 ? 96 : 32;
+  static constexpr int REGS_SOFTMAX = NT == 2 ? 176 : 160, REGS_DQ = NT == 2 ? 72 : 48, REGS_MMA = NT == 2 ? 88 : 32;
   static constexpr int LAUNCH_REGS = NT == 2 ? 128 : 80;
 };
 
@@ -73,10 +73,6 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-
-constexpr int kFar = 5;  // key tiles
-
-__device__ __forceinline__ void prefetch_l2(const void* at) { asm volatile("prefetch.global.L2 [%0];" ::"l"(at)); }
 
 // A key's codes and scales of K or V.  (Whole rows to an access, a lane with 16
 // bytes of every 8th key, loads better but finds four addresses where this
@@ -332,31 +328,10 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, PreCfg<D, NT>::CTAS) k
       Row4<D> k4, v4;
       load_row4(k4, p, at, kt0 * kKvTile + r < key_end);
       load_row4(v4, p, at + half_rows, kt0 * kKvTile + r < key_end);
-      // One row tile alone reads the cache as fast as memory gives it: its rows
-      // are called into L2 kFar tiles ahead (the registers hold one tile of
-      // them, far less than memory's latency wants in flight).
-      const bool far = !has_b;
-      auto call_rows = [&](int j, int pid) {
-        if ((kt0 + j) * kKvTile + r >= key_end) return;
-        const int64_t row = row_of(j, pid);
-        prefetch_l2(p.codes + row * (D / 2));
-        prefetch_l2(p.codes + (row + half_rows) * (D / 2));
-        prefetch_l2(p.scales + row * (D / 16));
-        prefetch_l2(p.scales + (row + half_rows) * (D / 16));
-      };
-      int far_page = 0;
-      if (far) {
-        for (int j = 1; j < kFar; ++j) call_rows(j, page_of(j));
-        far_page = page_of(kFar);
-      }
       int next_page = page_of(1);
       for (int j = 0; j < nkt; ++j) {
         const int st = j % NST;
         const uint32_t parity = ((j / NST) - 1) & 1;
-        if (far) {
-          call_rows(j + kFar, far_page);
-          far_page = page_of(j + kFar + 1);
-        }
         const bool more = (kt0 + j + 1) * kKvTile + r < key_end;
         at = row_of(j + 1, next_page);
         next_page = page_of(j + 2);
