@@ -50,8 +50,8 @@ pagedattn_status check_heads(int32_t Hq, int32_t Hkv, int32_t D) {
 pagedattn_status check_cache(const pagedattn_kv4_cache* c, pa::Kv4Geom* g) {
   if (!c) return set_err(PA_ERR_INVALID_ARG, "cache is NULL");
   if (!c->codes || !c->scales) return set_err(PA_ERR_INVALID_ARG, "the cache's codes and scales are required");
-  if (!aligned(c->codes, 16) || !aligned(c->scales, 16))
-    return set_err(PA_ERR_INVALID_ARG, "the cache's codes and scales must be 16-byte aligned");
+  if (!aligned(c->codes, 32) || !aligned(c->scales, 32))
+    return set_err(PA_ERR_INVALID_ARG, "the cache's codes and scales must be 32-byte aligned");
   pagedattn_status s = check_heads(c->num_kv_heads, c->num_kv_heads, c->head_dim);
   if (s != PA_OK) return s;
   const int shift = page_shift(c->page_size);

@@ -74,27 +74,45 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// A key's codes and scales of K or V.  (Whole rows to an access, a lane with 16
-// bytes of every 8th key, loads better but finds four addresses where this
-// finds one: 64 drafting requests of 64 rows 247 -> 277 us.)
+// A key's codes and scales of K or V.  The 32 rows of a warp are 32 lines, and
+// the L1 cache looks up one a cycle, so a row is read in as few and as wide
+// accesses as there are (with 16 bytes an access the look-ups took 2000 cycles
+// a tile, more than the conversion).  (Whole rows to an access, a lane with 16
+// bytes of every 8th key, needs fewer still but finds four addresses where
+// this finds one: 64 drafting requests of 64 rows 247 -> 277 us.)
 template <int D>
 struct Row4 {
-  uint4 codes[D / 32];
+  uint32_t codes[D / 8];
   uint32_t scales[D / 64];
 };
 
 template <int D>
 __device__ __forceinline__ void load_row4(Row4<D>& r, const Kv4Params& p, int64_t row, bool live) {
   if (live) {
-    const uint4* c = reinterpret_cast<const uint4*>(p.codes + row * (D / 2));
+    const uint8_t* c = p.codes + row * (D / 2);
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) r.codes[i] = __ldg(c + i);
-    const uint32_t* s = reinterpret_cast<const uint32_t*>(p.scales + row * (D / 16));
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) r.scales[i] = __ldg(s + i);
+    for (int i = 0; i < D / 64; ++i)
+      asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+          : "=r"(r.codes[8 * i]), "=r"(r.codes[8 * i + 1]), "=r"(r.codes[8 * i + 2]), "=r"(r.codes[8 * i + 3]),
+            "=r"(r.codes[8 * i + 4]), "=r"(r.codes[8 * i + 5]), "=r"(r.codes[8 * i + 6]), "=r"(r.codes[8 * i + 7])
+          : "l"(c + 32 * i));
+    const uint8_t* s = p.scales + row * (D / 16);
+    if constexpr (D == 64) {
+      r.scales[0] = __ldg(reinterpret_cast<const uint32_t*>(s));
+    } else if constexpr (D == 128) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(s));
+      r.scales[0] = v.x;
+      r.scales[1] = v.y;
+    } else {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(s));
+      r.scales[0] = v.x;
+      r.scales[1] = v.y;
+      r.scales[2] = v.z;
+      r.scales[3] = v.w;
+    }
   } else {
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) r.codes[i] = make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < D / 8; ++i) r.codes[i] = 0;
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) r.scales[i] = 0;
   }
@@ -105,13 +123,12 @@ template <int D>
 __device__ __forceinline__ void store_row4(uint8_t* dst, const Row4<D>& r, int key) {
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {  // 32 dims: two scales, four 16-byte chunks
-    const uint32_t words[4] = {r.codes[i].x, r.codes[i].y, r.codes[i].z, r.codes[i].w};
     const uint32_t two = r.scales[i >> 1] >> (16 * (i & 1));
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       const uint32_t s = e4m3x2_f16(__byte_perm(two, 0, (w >> 1) * 0x1111u));
       uint32_t h[4];
-      e2m1x8(words[w], h);
+      e2m1x8(r.codes[4 * i + w], h);
       const int c = (i & 1) * 4 + w;  // 16-byte chunk of the 128-byte block
       *reinterpret_cast<uint4*>(dst + (i >> 1) * (128 * 128) + key * 128 + ((c ^ (key & 7)) << 4)) =
           make_uint4(mul_f16x2(h[0], s), mul_f16x2(h[1], s), mul_f16x2(h[2], s), mul_f16x2(h[3], s));

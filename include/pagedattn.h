@@ -421,7 +421,7 @@ PAGEDATTN_API pagedattn_status pagedattn_build_tables(const pagedattn_tables_in*
  *   NHD  codes [num_pages][2][page_size][num_kv_heads][head_dim / 2]
  *        scales[num_pages][2][page_size][num_kv_heads][head_dim / 16]
  *   HND  the same with page_size and num_kv_heads exchanged
- * Both device memory, 16-byte aligned.  Memory of slots that were never
+ * Both device memory, 32-byte aligned.  Memory of slots that were never
  * written may hold anything.
  */
 typedef struct {
