@@ -60,6 +60,13 @@ __device__ __forceinline__ float ex2f(float x) {
   return y;
 }
 
+// a / b for a >= 0, b > 0; in 32 bits where they do (a division in 64 takes a
+// hundred instructions).
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 __device__ __forceinline__ int row_tiles(const Kv4Params& p, const Req& r, int tile_rows) {
   const int rows = r.qo_len * p.G;
   return rows > p.small_rows ? 0 : (rows + tile_rows - 1) / tile_rows;
@@ -267,7 +274,7 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
   };
   long long total;
   long long before = sum_before(units, &total);
-  const long long per_slice = max(static_cast<long long>(kMinUnits), (total + p.slices - 1) / p.slices);
+  const long long per_slice = max(static_cast<long long>(kMinUnits), quotient(total + p.slices - 1, p.slices));
 
   // ---- Slices of one size take a share of the next request with them and leave
   // a share of their last one to the next slice.  Where there are slices enough
@@ -278,7 +285,7 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
   // 4.5 for a join (128 requests of 1024 keys: 16.6 us in equal slices, 9.9
   // whole).
   int part_units = 0;  // 0: slices of equal size
-  if (p.batch <= kThreads) {
+  if (p.slices > 1 && p.batch <= kThreads) {
     tiles = longest = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
@@ -388,12 +395,12 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
   while (u < u_end) {
     const int kts = key_units(rq);
     const int n_parts = by_parts ? parts_of(rq) : kts;  // of a row tile, in what u counts
-    const int rt = static_cast<int>((u - req_u) / n_parts);
+    const int rt = static_cast<int>(quotient(u - req_u, n_parts));
     const long long tile_u = req_u + static_cast<long long>(rt) * n_parts;
     const long long seg_end = min(u_end, tile_u + n_parts);
     const int at0 = static_cast<int>(u - tile_u), at1 = static_cast<int>(seg_end - tile_u);
-    const int unit0 = by_parts ? static_cast<int>(static_cast<long long>(kts) * at0 / n_parts) : at0;
-    const int unit1 = by_parts ? static_cast<int>(static_cast<long long>(kts) * at1 / n_parts) : at1;
+    const int unit0 = by_parts ? static_cast<int>(quotient(static_cast<long long>(kts) * at0, n_parts)) : at0;
+    const int unit1 = by_parts ? static_cast<int>(quotient(static_cast<long long>(kts) * at1, n_parts)) : at1;
     const bool whole = unit0 == 0 && unit1 == kts;
     const int row0 = rt * C::ROWS;
     const int rows = min(C::ROWS, rq.qo_len * p.G - row0);
@@ -471,9 +478,8 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
     uint32_t qf[C::Q_SMEM ? 1 : NT][D / 16][2];
     float fac[NT][2];
     int lim[NT][2];
-    auto load_q = [&](int nt, uint32_t (&f)[D / 16][2]) -> float {  // returns the row's factor
+    auto load_q = [&](int nt, uint32_t (&f)[D / 16][2]) {
       const int n = nt * 8 + g, tok = token_of(n);
-      float my = p.scale_log2;
       if (n < rows) {
         const T* src = static_cast<const T*>(p.q) + static_cast<int64_t>(rq.qo_start + tok0 + tok) * p.q_stride +
                        static_cast<int64_t>(h * p.G + head0 + n - tok * p.G) * D + t * (D / 4);
@@ -489,6 +495,9 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) f[j][0] = f[j][1] = 0;
       }
+    };
+    auto scale_q = [&](uint32_t (&f)[D / 16][2]) -> float {  // to fp16; returns the row's factor
+      float my = p.scale_log2;
       if constexpr (Elt<T>::kBf16) {
         uint32_t top = 0;  // the largest magnitude's bf16 bits
 #pragma unroll
@@ -513,17 +522,17 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
     if constexpr (C::Q_SMEM) {
       // warp nt makes row group nt's fragments for all (the CTA has one head)
       if (warp < NT) {
-        const float my = load_q(warp, qf[0]);
+        load_q(warp, qf[0]);
+        const float my = scale_q(qf[0]);
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) q_s[(warp * (D / 16) + j) * 32 + lane] = make_uint2(qf[0][j][0], qf[0][j][1]);
         if (t == 0) fac_s[warp * 8 + g] = my;
       }
       team_sync();
+    } else {
+      // q's loads fly while the copies wait for their page ids
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        fac[nt][0] = fac_s[nt * 8 + 2 * t];
-        fac[nt][1] = fac_s[nt * 8 + 2 * t + 1];
-      }
+      for (int nt = 0; nt < NT; ++nt) load_q(nt, qf[nt]);
     }
 #pragma unroll
     for (int i = 0; i < C::STAGES - 1; ++i) copy_step(member + i * team, ring + i * St::BYTES, pids[i]);
@@ -531,10 +540,11 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float my = 0.f;
-      if constexpr (!C::Q_SMEM) my = load_q(nt, qf[nt]);
+      if constexpr (!C::Q_SMEM) my = scale_q(qf[nt]);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        if constexpr (!C::Q_SMEM) fac[nt][i] = __shfl_sync(0xffffffffu, my, (2 * t + i) * 4);
+        if constexpr (C::Q_SMEM) fac[nt][i] = fac_s[nt * 8 + 2 * t + i];
+        else fac[nt][i] = __shfl_sync(0xffffffffu, my, (2 * t + i) * 4);
         lim[nt][i] = p.causal ? min(shift + tok0 + token_of(nt * 8 + 2 * t + i), rq.kv_len) : rq.kv_len;
       }
     }
@@ -770,7 +780,7 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
       // o = sum_s 2^(lse_s - lse) o_s.  The sum's order is the slices', so
       // the result does not depend on which one comes last.
       const long long step = by_parts ? 1 : per_slice;
-      const int sa = static_cast<int>(tile_u / step), sb = static_cast<int>((tile_u + n_parts - 1) / step);
+      const int sa = static_cast<int>(quotient(tile_u, step)), sb = static_cast<int>(quotient(tile_u + n_parts - 1, step));
       const bool sa_first = tile_u == sa * step;
       team_sync();
       if (rank == 0) {
