@@ -87,6 +87,8 @@ pagedattn_status pagedattn_build_tables(const pagedattn_tables_in* in, const pag
   if (in->batch_size < 0 || in->block_table_width < 0 || in->free_capacity < 0 || out->max_tokens < 0 ||
       out->max_pages < 0)
     return set_err(PA_ERR_INVALID_ARG, "a size is negative");
+  if (in->batch_size > (1 << 30) || out->max_tokens > (1 << 30) || out->max_pages > (1 << 30))
+    return set_err(PA_ERR_UNSUPPORTED, "batch_size, max_tokens and max_pages must be at most 2^30");
   if (in->block_table_stride < in->block_table_width)
     return set_err(PA_ERR_INVALID_ARG, "block_table_stride is below block_table_width");
   if (in->num_pages < 1) return set_err(PA_ERR_INVALID_ARG, "num_pages must be positive");
@@ -143,6 +145,7 @@ pagedattn_status pagedattn_kv4_append(const pagedattn_kv4_cache* cache, const pa
   s = check_dtype(rows->dtype);
   if (s != PA_OK) return s;
   if (rows->num_tokens < 0) return set_err(PA_ERR_INVALID_ARG, "num_tokens is negative");
+  if (rows->num_tokens > (1 << 30)) return set_err(PA_ERR_UNSUPPORTED, "num_tokens must be at most 2^30");
   if (rows->num_tokens == 0) return PA_OK;
   const int64_t width = int64_t(cache->num_kv_heads) * cache->head_dim;
   if (!rows->k || !rows->v || !rows->slot_mapping || !rows->status)

@@ -35,6 +35,7 @@
 //        fragment's (key, key + 1) pair.
 // So the cache goes from global memory to registers and into the MMA without
 // shared memory.
+#include <climits>
 #include <cstring>
 #include <type_traits>
 #include <utility>
@@ -203,7 +204,9 @@ struct SmallCfg {
   static_assert(CTAS * (SMEM + kKeptReqs * 16 + 768 + 1024) <= 233472, "shared memory per SM");
 };
 
-template <typename T, int D, int NT>
+// kScrub: rows of a tile may see different keys (several tokens under a causal
+// mask), so that a masked key's NaN has to be kept from the others.
+template <typename T, int D, int NT, bool kScrub>
 __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTAS) kv4_small_kernel(const Kv4Params p) {
   using C = SmallCfg<D, NT>;
   using St = Stage<D>;
@@ -682,6 +685,44 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
         }
       }
       // ---- O^T += V^T P^T
+      if constexpr (kEdge && kScrub) {
+        // a NaN of V would pass through P = 0 to rows that do not see its key:
+        // the rows that do get it now, and its scale becomes 0 in the stage
+        int first_nan[St::VS];  // by block of 16 dims: the step's first key with a NaN
+        bool some = false;
+#pragma unroll
+        for (int k = 0; k < St::VS; ++k) first_nan[k] = INT_MAX;
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+          const int row = 8 * (i >> 1) + (i & 1 ? v_row[1] : v_row[0]);
+          uint8_t* at = smem + (st - smem) + St::OFF_VS + row * St::SROW + g * St::VB / 8;
+#pragma unroll
+          for (int k = 0; k < St::VS; ++k)
+            if ((at[k] & 0x7F) == 0x7F) {
+              some = true;
+              first_nan[k] = min(first_nan[k], key + row);
+              at[k] = 0;
+            }
+        }
+        if (__any_sync(0xffffffffu, some)) {
+#pragma unroll
+          for (int k = 0; k < St::VS; ++k) {
+            int at = first_nan[k];  // of the block's 4 lanes
+            at = min(at, __shfl_xor_sync(0xffffffffu, at, 1));
+            at = min(at, __shfl_xor_sync(0xffffffffu, at, 2));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                if (at < lim[nt][i]) {
+#pragma unroll
+                  for (int j = 8 * k; j < (St::VS == 1 ? D / 16 : 8 * k + 8); ++j)
+                    o[nt][j][i] = o[nt][j][i + 2] = __int_as_float(0x7FFFFFFF);
+                }
+          }
+          __syncwarp();
+        }
+      }
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         uint32_t vw[4][St::VB / 4], vs[4];
@@ -822,25 +863,33 @@ int row_groups(const Kv4Shape& s) {
   return s.max_rows <= 16 ? 2 : 4;
 }
 
-template <typename T, int D, int NT>
+template <typename T, int D, int NT, bool kScrub>
 cudaError_t launch_small(const Kv4Params& p, cudaStream_t stream) {
   using C = SmallCfg<D, NT>;
   const unsigned grid = static_cast<unsigned>(p.slices) * (p.g.Hkv / p.cta_heads);
   static std::atomic<uint64_t> set{0};
-  auto* k = kv4_small_kernel<T, D, NT>;
+  auto* k = kv4_small_kernel<T, D, NT, kScrub>;
   cudaError_t e = set_smem_once(set, reinterpret_cast<const void*>(k), C::SMEM);
   return e != cudaSuccess ? e : launch_pdl(k, grid, unsigned(C::THREADS), size_t(C::SMEM), stream, p);
+}
+
+// One token a request, the commonest batch by far, does without the scrubbing
+// (256 decodes 250 us, with it 253).
+template <typename T, int D, int NT>
+cudaError_t launch_nt(const Kv4Params& p, const Kv4Shape& s, cudaStream_t stream) {
+  return p.causal && s.max_rows > s.G ? launch_small<T, D, NT, true>(p, stream)
+                                      : launch_small<T, D, NT, false>(p, stream);
 }
 
 template <typename T, int D>
 cudaError_t launch_d(const Kv4Params& p, const Kv4Shape& s, cudaStream_t stream) {
   if constexpr (D == 256) {
-    return launch_small<T, 256, 1>(p, stream);
+    return launch_nt<T, 256, 1>(p, s, stream);
   } else {
     switch (row_groups(s)) {
-      case 1: return launch_small<T, D, 1>(p, stream);
-      case 2: return launch_small<T, D, 2>(p, stream);
-      default: return launch_small<T, D, 4>(p, stream);
+      case 1: return launch_nt<T, D, 1>(p, s, stream);
+      case 2: return launch_nt<T, D, 2>(p, s, stream);
+      default: return launch_nt<T, D, 4>(p, s, stream);
     }
   }
 }

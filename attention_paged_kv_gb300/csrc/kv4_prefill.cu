@@ -30,6 +30,7 @@
 // TMEM: S_x (fp32 128 x 128) at 128 x, O_x (fp32 128 x D) after them; P_x
 // overwrites the first 64 columns of S_x.
 #include <cstring>
+#include <type_traits>
 
 #include "internal.h"
 #include "kv4_common.cuh"
@@ -118,6 +119,22 @@ __device__ __forceinline__ void load_row4(Row4<D>& r, const Kv4Params& p, int64_
   }
 }
 
+// Takes the NaN of a row of V out (its scale becomes 0) and notes its key by
+// block of 16 dims: through P = 0 it would reach rows that do not see the key.
+template <int D>
+__device__ __forceinline__ void note_nans(Row4<D>& r, int key, int* first_nan, int* any_nan) {
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+    if (__vcmpeq4(r.scales[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) == 0) continue;
+    for (int k = 0; k < 4; ++k)
+      if (((r.scales[i] >> (8 * k)) & 0x7Fu) == 0x7Fu) {
+        *any_nan = 1;
+        atomicMin(first_nan + 4 * i + k, key);
+        r.scales[i] &= ~(0xFFu << (8 * k));
+      }
+  }
+}
+
 // Row `key` of a tile at `dst` in fp16, 128-byte swizzled.
 template <int D>
 __device__ __forceinline__ void store_row4(uint8_t* dst, const Row4<D>& r, int key) {
@@ -148,6 +165,7 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, PreCfg<D, NT>::CTAS) k
   __shared__ int warp_sums[32], found_tile, last_s;
   __shared__ long long work_s;
   __shared__ Req found_rq;
+  __shared__ int any_nan, first_nan[D / 16];     // first key whose V has a NaN there, of the tiles that some row sees in part
   __shared__ float fac_s[NT * kQRows];  // bf16: the rows' logit factors
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -180,6 +198,8 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, PreCfg<D, NT>::CTAS) k
     work_s = 0;
     mbar_init_fence();
   }
+  if (tid < D / 16) first_nan[tid] = INT_MAX;
+  if (tid == 0) any_nan = 0;
   if (warp == C::WARP_MMA) tmem_alloc(tmem_slot, C::TMEM_COLS);
   pdl_wait();  // q, the cache and the tables may come from the kernel before
 
@@ -302,6 +322,7 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, PreCfg<D, NT>::CTAS) k
     if constexpr (C::HANDOVER) regs_down<C::REGS_DQ>();
     const int r = tid - 32 * C::WARP_DQ;  // key of the tile
     const int32_t* ids = p.pages + rq.page_start;
+    const int all_end = p.causal ? shift + tok0 : rq.kv_len;  // keys that every row sees
     const int64_t half_rows = static_cast<int64_t>(p.g.ps) * p.g.Hkv;
     auto page_of = [&](int j) -> int {
       const int key = (kt0 + j) * kKvTile + r;
@@ -334,6 +355,7 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, PreCfg<D, NT>::CTAS) k
         __syncwarp();
         if (lane == 0) mbar_arrive(&full_k[st]);
         if (j >= NST && !warp_wait(&empty_v[st], parity, abort_flag, p.status, kLimit)) break;
+        if ((kt0 + j + 1) * kKvTile > all_end) note_nans(row, (kt0 + j) * kKvTile + r, first_nan, &any_nan);
         store_row4<D>(smem + C::OFF_V + st * C::TILE, row, r);
         fence_proxy_async_smem();
         __syncwarp();
@@ -359,6 +381,7 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, PreCfg<D, NT>::CTAS) k
         if (lane == 0) mbar_arrive(&full_k[st]);
         load_row4(k4, p, at, more);
         if (j >= NST && !warp_wait(&empty_v[st], parity, abort_flag, p.status, kLimit)) break;
+        if ((kt0 + j + 1) * kKvTile > all_end) note_nans(v4, (kt0 + j) * kKvTile + r, first_nan, &any_nan);
         store_row4<D>(smem + C::OFF_V + st * C::TILE, v4, r);
         fence_proxy_async_smem();
         __syncwarp();
@@ -740,6 +763,19 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, PreCfg<D, NT>::CTAS) k
                                                           (((c & 7) ^ (rr & 7)) << 4));
           const int64_t row = out_row(x * kQRows + rr);
           *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + row * D + c * 8) = w;
+        }
+      }
+    }
+    if (any_nan && writes && warp_rows) {
+      // the NaN that were taken out of V, for the rows that see them
+      __syncwarp();
+      for (int k = 0; k < D / 16; ++k) {
+        if (!row_valid || first_nan[k] >= row_end + kt0 * kKvTile) continue;
+        const float nan = __int_as_float(0x7FFFFFFF);
+        const int64_t part_row = (part_tile + part) * (NT * kQRows) + x * kQRows + r;
+        for (int e = 0; e < 16; ++e) {
+          if (split) p.part_o[part_row * D + k * 16 + e] = nan;
+          else static_cast<T*>(p.out)[out_row(pr) * D + k * 16 + e] = Elt<T>::from_f(nan);
         }
       }
     }

@@ -471,7 +471,8 @@ typedef struct {
   int32_t batch_size, num_page_indices;
   int32_t num_tokens;              /* rows of q, out and lse, >= qo_indptr[batch_size]    */
   int32_t max_qo_len;              /* bound of the requests' query lengths: chooses the
-                                      kernels (a longer request is computed too, slower)  */
+                                      kernels (a longer request is computed too, slower;
+                                      see the note on NaN below)                          */
   int32_t num_qo_heads, causal;
   pagedattn_dtype dtype;           /* of q and out                                        */
 } pagedattn_kv4_batch;
@@ -484,7 +485,9 @@ PAGEDATTN_API pagedattn_status pagedattn_kv4_workspace_size(int32_t num_qo_heads
  * Attention as pagedattn_run computes it (see the top of this file), over a
  * 4-bit cache and with the batch's tables in device memory.  Any group size
  * num_qo_heads / num_kv_heads up to 128; any lengths.  A row that sees no key
- * (kv_len 0, or causal with qo_len > kv_len) gets zeros and lse = -inf.  Rows
+ * (kv_len 0, or causal with qo_len > kv_len) gets zeros and lse = -inf.  A NaN
+ * of K or V reaches the rows that see its key and no others, except that with
+ * max_qo_len <= 1 the rows of a longer request may share their NaN.  Rows
  * of q from qo_indptr[batch_size] on are not read, and rows of out and lse
  * not written.
  *

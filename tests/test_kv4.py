@@ -614,6 +614,33 @@ def test_attention_nan_rows_stay_their_own():
 
 
 @gpu
+@pytest.mark.parametrize("qo, kv, G, D", [([4, 1], [40, 200], 2, 128), ([3], [1000], 8, 64), ([3], [70], 8, 128),
+                                          ([2], [33], 4, 256), ([60], [300], 4, 128), ([300], [333], 2, 64),
+                                          ([70], [1500], 2, 128), ([50], [90], 4, 256)], ids=str)
+def test_attention_nan_behind_the_mask(qo, kv, G, D):
+    """A NaN of K or V at a key reaches the rows that see it, and no others, in the dims of its block."""
+    b = Batch(qo, kv, 2 * G, 2, D, 16, "NHD", torch.bfloat16, seed=17)
+    a = b.attention()
+    clean, clean_lse = a.run(b.q, b.cache, b.tables())
+    n, q = kv[0], qo[0]
+    for back in (0, 1, q - 1):  # the last key, and the one that all but the first rows see
+        key = n - 1 - back
+        page, slot = int(b.pages[key // 16]), key % 16
+        first_row = max(0, key - (n - q))  # rows from here on see it
+        for half in (0, 1):
+            at = (page, half, slot, 1, D // 16 - 1)
+            old = b.cache.scales[at].item()
+            b.cache.scales[at] = 0x7F
+            out, lse = a.run(b.q, b.cache, b.tables())
+            b.cache.scales[at] = old
+            hit = torch.zeros_like(clean, dtype=torch.bool)
+            hit[first_row:q, G:, (0 if half == 0 else D - 16):] = True
+            assert torch.equal(torch.isnan(out), hit), (back, half)
+            assert torch.equal(out[~hit], clean[~hit])
+            assert torch.equal(torch.isnan(lse), hit.any(-1) if half == 0 else torch.zeros_like(lse, dtype=torch.bool))
+
+
+@gpu
 def test_attention_same_for_any_page_placement_and_layout():
     ref = None
     for layout in ("NHD", "HND"):
