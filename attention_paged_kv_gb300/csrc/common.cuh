@@ -366,53 +366,6 @@ __host__ __device__ constexpr uint32_t idesc_f16(int ab_bf16, int a_mn_major, in
 }
 
 // ---------------------------------------------------------------------------
-// waits and a reduction of the tensor-core kernels
-
-// Bounded wait, made uniform across the warp (all lanes leave together).
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int32_t* abort_flag,
-                                          int32_t* status, long long limit) {
-  bool ok = mbar_wait(bar, parity, abort_flag, status, limit);
-  return __all_sync(0xffffffffu, ok);
-}
-
-// Bounded wait that polls with non-blocking probes and never suspends: the
-// MMA thread waits this way, since waking a suspended thread cost ~1.8 % of
-// the prefill (the softmax warps, which share their SM sub-partitions with the
-// other tile's softmax, wait with try_wait: spinning there cost 3.6 %, and
-// neither a suspend-time hint for them nor a back-off for the MMA thread
-// changed anything).
-__device__ __forceinline__ bool spin_wait(uint64_t* bar, uint32_t parity, volatile int32_t* abort_flag,
-                                          int32_t* status, long long limit) {
-  const uint32_t a = smem_u32(bar);
-  if (mbar_test_wait(a, parity)) return true;
-  const long long t0 = clock64();
-  while (true) {
-    if (mbar_test_wait(a, parity)) return true;
-    if (*abort_flag) return false;
-    if (clock64() - t0 > limit) {
-      *abort_flag = 1;
-      atomicOr(status, PA_DEV_TIMEOUT);
-      return false;
-    }
-  }
-}
-// Wait that ignores the abort flag (used to drain in-flight async work).
-__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
-  const uint32_t a = smem_u32(bar);
-  const long long t0 = clock64();
-  while (!mbar_try_wait(a, parity)) {
-    if (clock64() - t0 > PA_WAIT_LIMIT_CYCLES) break;
-  }
-}
-
-// Three-input maximum (one instruction on sm_100 and later).
-__device__ __forceinline__ float fmax3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
-// ---------------------------------------------------------------------------
 // element helpers
 
 template <typename T> struct Elt;

@@ -70,9 +70,10 @@ struct Kv4Params {
   const uint8_t *codes, *scales;
   const int32_t *qo_indptr, *page_indptr, *pages, *last_page_len;
   int32_t* status;
-  int32_t* counters; // [slices * Hkv]: parts written of the row tile that slice's first boundary cuts
-  float* part_o;     // [slices * Hkv * 2][rows of a tile][D], each normalised
-  float* part_lse;   // [slices * Hkv * 2][rows of a tile], base-2, v_scale not in it
+  int32_t* counters;  // parts written of each cut row tile and kv head (prefill: of each cut item); 0 between runs
+  float* part_o;      // partial states, normalised, v_scale not in them: [slices * Hkv * 2][rows of a tile][D]
+                      // (prefill: [parts of the cut items][rows of an item][D])
+  float* part_lse;    // their log-sums, base 2
   int64_t q_stride;  // elements between tokens
   Kv4Geom g;
   int32_t batch, num_tokens, num_page_indices, Hq, G, causal, slices, cta_heads;
@@ -84,7 +85,9 @@ struct Kv4Params {
 };
 
 struct Kv4Shape {  // what the launch and its workspace depend on
-  int32_t D, Hkv, G, num_sms, max_rows, batch;  // max_rows: packed rows of the longest request
+  int32_t D, Hkv, G, num_sms;
+  int32_t max_rows;  // packed rows of the longest request
+  int32_t batch;     // requests (not for the workspace's size)
 };
 
 // Bytes of a run's workspace, and where its parts lie in it.
@@ -96,7 +99,9 @@ Kv4Layout kv4_layout(const Kv4Shape& s);
 // Rows of partial states that the prefill kernel may write.
 int64_t kv4_prefill_part_rows(const Kv4Shape& s);
 
-// Requests of more packed rows than this go to the tensor-core kernel.
+// Requests of more packed rows than this go to the tensor-core kernel (64
+// drafting requests of 24 or 32 rows: 146 and 149 us here, 235 and 245 there; of
+// 64 rows 217 there).
 constexpr int kKv4SmallRows = 32;
 
 cudaError_t launch_kv4_prefill(const Kv4Params& p, const Kv4Shape& s, int dtype, cudaStream_t stream);

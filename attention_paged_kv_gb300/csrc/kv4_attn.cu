@@ -1,5 +1,5 @@
 // Attention over a paged cache held in 4 bits, through device tables
-// (pagedattn_kv4_run): the small-query kernel and the merge of its splits.
+// (pagedattn_kv4_run): the small-query kernel (decode, drafted tokens).
 //
 // Number formats.  K and V are e2m1 codes with an e4m3 scale per 16 values
 // along head_dim.  code * scale has at most 6 significant bits and lies in
@@ -14,27 +14,40 @@
 //
 // Work.  A unit is 64 keys of one row tile (8 * NT packed rows: token major,
 // the G query heads of the kv head minor) of one request.  The units of the
-// batch, in request order, are cut into equal slices, one per CTA and kv
-// head, whatever the requests' boundaries, so that one request of 10^5 keys
-// and 10^3 requests of 100 keys load the SMs alike with no plan from the
-// host: every CTA sums the units of all requests itself (one block scan) and
-// so finds where its slice begins.  CTAs of one slice and different kv heads
-// are adjacent: they read the same pages at the same time, and in the NHD
-// layout the 32-byte sectors of scales that 4 heads share come from L2.
-// A row tile that a slice boundary cuts leaves fp32 partial states.
+// batch, in request order, are cut into equal slices whatever the requests'
+// boundaries, so that one request of 10^5 keys and 10^3 requests of 100 keys
+// load the SMs alike with no plan from the host: every CTA sums the units of
+// all requests itself (one block scan) and so finds where its slice begins.
+// A row tile that a slice boundary cuts leaves fp32 partial states, which the
+// last of its slices to finish joins.  (Batches that leave a slice for every
+// row tile: see the kernel.)
+// A CTA has up to 8 kv heads, a warp or a team of warps each: the heads of a
+// page are read at the same time (in the NHD layout 4 heads share a 32-byte
+// sector of scales), and where a warp has a head alone its state is the
+// result, with nothing to join.  With fewer requests than slices it has one
+// head, whose keys the 8 warps share, so that no warp joins many parts alone.
 //
-// A warp takes 16 keys at a time and computes S^T = K q^T and O^T = V^T P^T
-// with m16n8k16, so that keys (or dims) fill the 16-row side and 8 packed
-// rows the other.  Both contractions are free in the order of their index:
-//   S^T  lane (g, t) takes dims [t D/4, (t+1) D/4) of keys g and g + 8: one
-//        16-byte load a key (head_dim 128), codes converted in the order they
-//        lie in memory; q's fragments are loaded in the same order.
-//   O^T  lane (g, t) takes dims [g D/8, (g+1) D/8) of keys 2t, 2t+1, 2t+8 and
-//        2t+9: the codes of two keys are merged nibble by nibble (two
-//        bitfield selects for 16 values) so that one conversion gives the
-//        fragment's (key, key + 1) pair.
-// So the cache goes from global memory to registers and into the MMA without
-// shared memory.
+// A warp takes 32 keys at a time.  It copies its own steps two or more ahead
+// (cp.async into a ring of its own: no warp waits for another) and computes
+// S^T = K q^T and O^T = V^T P^T with m16n8k16, so that keys (or dims) fill the
+// 16-row side and 8 packed rows the other.  Both contractions are free in the
+// order of their index:
+//   S^T  lane (g, t) takes dims [t D/4, (t+1) D/4) of its keys: 16 bytes each
+//        (head_dim 128), converted in the order they lie in memory; q's
+//        fragments are loaded in the same order.
+//   O^T  lane (g, t) takes dims [g D/8, (g+1) D/8) of 4 keys of each 16: the
+//        codes of two keys are merged nibble by nibble (two bitfield selects
+//        for 16 values) so that one conversion gives the fragment's
+//        (key, key + 1) pair.
+//
+// What bounds it: bytes and instructions alike.  256 decodes of 512 to 8192
+// keys at 64 / 8 heads (1.27 GB) take 250 us, 5.1 TB/s; the copies alone take
+// 214 to 220, the arithmetic alone 213 (635 warp instructions for 32 keys and a
+// head, of them 140 conversions, 128 scalings and 32 MMAs).  Steps on the way:
+// fragments straight from global memory 340 us; rings of cp.async 299; a CTA
+// for all heads of its keys 263; constant shared offsets and q's loads under
+// the page ids' 250.  Measured without gain: wider steps in registers (426
+// us), the conversions replaced by bit operations (2.4 times their time).
 #include <climits>
 #include <cstring>
 #include <type_traits>

@@ -58,6 +58,13 @@ __device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// Three-input maximum (one instruction).
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // base + a * b in one instruction.
 __device__ __forceinline__ const uint8_t* offset_by(const uint8_t* base, uint32_t a, uint32_t b) {
   uint64_t r;

@@ -40,6 +40,39 @@ namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
 
+// Bounded wait, made uniform across the warp (all lanes leave together).
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int32_t* abort_flag,
+                                          int32_t* status, long long limit) {
+  bool ok = mbar_wait(bar, parity, abort_flag, status, limit);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// Bounded wait of the MMA thread, which polls and never suspends (as in the
+// 16-bit prefill kernel, where waking it cost 1.8 %).
+__device__ __forceinline__ bool spin_wait(uint64_t* bar, uint32_t parity, volatile int32_t* abort_flag,
+                                          int32_t* status, long long limit) {
+  const uint32_t a = smem_u32(bar);
+  if (mbar_test_wait(a, parity)) return true;
+  const long long t0 = clock64();
+  while (true) {
+    if (mbar_test_wait(a, parity)) return true;
+    if (*abort_flag) return false;
+    if (clock64() - t0 > limit) {
+      *abort_flag = 1;
+      atomicOr(status, PA_DEV_TIMEOUT);
+      return false;
+    }
+  }
+}
+// Wait that ignores the abort flag (used to drain in-flight async work).
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
+  const uint32_t a = smem_u32(bar);
+  const long long t0 = clock64();
+  while (!mbar_try_wait(a, parity)) {
+    if (clock64() - t0 > PA_WAIT_LIMIT_CYCLES) break;
+  }
+}
+
 template <int D, int NT>
 struct PreCfg {
   static_assert(NT == 1 || (NT == 2 && D <= 128), "two tiles need 2 x (128 + D) <= 512 TMEM columns");

@@ -108,6 +108,50 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Bounded wait, made uniform across the warp (all lanes leave together).
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int32_t* abort_flag,
+                                          int32_t* status, long long limit) {
+  bool ok = mbar_wait(bar, parity, abort_flag, status, limit);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// Bounded wait that polls with non-blocking probes and never suspends: the
+// MMA thread waits this way, since waking a suspended thread cost ~1.8 % of
+// the prefill (the softmax warps, which share their SM sub-partitions with the
+// other tile's softmax, wait with try_wait: spinning there cost 3.6 %, and
+// neither a suspend-time hint for them nor a back-off for the MMA thread
+// changed anything).
+__device__ __forceinline__ bool spin_wait(uint64_t* bar, uint32_t parity, volatile int32_t* abort_flag,
+                                          int32_t* status, long long limit) {
+  const uint32_t a = smem_u32(bar);
+  if (mbar_test_wait(a, parity)) return true;
+  const long long t0 = clock64();
+  while (true) {
+    if (mbar_test_wait(a, parity)) return true;
+    if (*abort_flag) return false;
+    if (clock64() - t0 > limit) {
+      *abort_flag = 1;
+      atomicOr(status, PA_DEV_TIMEOUT);
+      return false;
+    }
+  }
+}
+// Wait that ignores the abort flag (used to drain in-flight async work).
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
+  const uint32_t a = smem_u32(bar);
+  const long long t0 = clock64();
+  while (!mbar_try_wait(a, parity)) {
+    if (clock64() - t0 > PA_WAIT_LIMIT_CYCLES) break;
+  }
+}
+
+// Three-input maximum (one instruction on sm_100 and later).
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, NT == 1 ? 2 : 1)
     prefill_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap q_map,
