@@ -579,6 +579,47 @@ def test_attention_many_short_requests():
 
 
 @gpu
+@pytest.mark.parametrize("kv_hi, D", [(40, 64), (2500, 64), (60, 256)])
+def test_attention_prompts_in_a_large_batch(kv_hi, D):
+    """More requests than a block has threads, long chunks and single tokens among them (both kernels' longer scans)."""
+    rng = np.random.default_rng(kv_hi)
+    B = 700
+    qo = np.where(rng.random(B) < 0.03, rng.integers(20, 40, B), rng.integers(0, 2, B))
+    kv = qo + np.where(rng.random(B) < 0.02, kv_hi, rng.integers(0, 30, B))
+    b = Batch(qo, kv, 4, 1, D, 16, "NHD", torch.bfloat16, seed=5)
+    a = b.attention()
+    out, lse = a.run(b.q, b.cache, b.tables())
+    assert a.device_status() == 0
+    b.check(out, lse, b.want())
+
+
+@gpu
+@pytest.mark.parametrize("qo, kv, Hq, Hkv, D", [([1, 1], [300, 40], 128, 1, 64), ([2], [90], 320, 320, 64),
+                                                ([1], [700], 400, 400, 64), ([1, 3], [200, 33], 26, 13, 128),
+                                                ([1, 1, 1], [1500, 9, 100], 12, 12, 128)], ids=str)
+def test_attention_of_many_heads(qo, kv, Hq, Hkv, D):
+    """Groups of 128, more kv heads than CTAs fit the card, odd numbers of kv heads."""
+    b = Batch(qo, kv, Hq, Hkv, D, 16, "HND", torch.float16, seed=6)
+    out, lse = b.attention().run(b.q, b.cache, b.tables())
+    b.check(out, lse, b.want())
+
+
+@gpu
+def test_empty_calls():
+    """No requests, no rows, requests without rows: nothing is written and nothing raised."""
+    cache = pa.Kv4Cache(4, 16, 2, 64)
+    z = lambda *s: torch.zeros(s, dtype=I32, device="cuda")  # noqa: E731
+    for B, T in ((0, 0), (3, 0), (0, 4), (3, 4)):
+        a = pa.Kv4Attention(B, T, 4, 2, 64, 16, torch.float16)
+        out = torch.full((T, 4, 64), 5.0, dtype=torch.float16, device="cuda")
+        got, lse = a.run(torch.zeros_like(out), cache, (z(B + 1), z(B + 1), z(0), z(B)), out=out)
+        assert (got == 5.0).all() and a.device_status() == 0
+    t = pa.BatchTables(3, 0, 0, 16, 4)
+    t.build(z(3), z(3), z(3, 1), z(0), z(1))
+    assert t.device_status() == 0 and not t.qo_indptr.any()
+
+
+@gpu
 @pytest.mark.parametrize("gain", [1e-30, 1e-5, 300.0, 1e4])
 def test_attention_bf16_queries_of_any_size(gain):
     """Queries that fp16 cannot hold as they are: rows are scaled by powers of two."""
