@@ -9,8 +9,8 @@
 // [2^13, 2^14) first (bf16's 8 significant bits fit fp16's 11; what falls
 // below fp16's range is 2^-38 of the row's largest value) and the logits by
 // its inverse.  The cache's own fp32 scales go into the logit factor (K) and
-// the epilogue (V).  P is rounded to fp16 (2^-11 relative) for the P V
-// product, whatever the type of q: a bf16 P would cost 2^-8.
+// the epilogue (V).  P is rounded to fp16 (2^-11 relative; small ones see
+// kPHead) for the P V product, whatever the type of q: a bf16 P would cost 2^-8.
 //
 // Work.  A unit is 64 keys of one row tile (8 * NT packed rows: token major,
 // the G query heads of the kv head minor) of one request.  The units of the
@@ -654,15 +654,14 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
             for (int e = 0; e < 4; ++e)
               if (key + 16 * n + k_row + 8 * (e >> 1) >= lim[nt][e & 1]) x[n][e] = -INFINITY;
         }
-        // the reference maximum moves when a logit passes it by 8 (in log2
-        // units): P stays below 2^8, which fp16 and the fp32 sums carry
+        // the reference moves when a logit passes it by kPMost (log2 units)
         const float top = fmax3(fmax3(x[0][0], x[0][1], x[0][2]), fmax3(x[0][3], x[1][0], x[1][1]),
                                 fmaxf(x[1][2], x[1][3]));
-        if (__any_sync(0xffffffffu, top > 8.f)) {
+        if (__any_sync(0xffffffffu, top > kPMost)) {
           // from the logits again: subtracting kNone has lost their bits
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float y = m[nt][i];
+            float y = kNone;
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -672,6 +671,7 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
               }
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
+            y = fmaxf(m[nt][i], y - kPHead);
             const float alpha = ex2f(m[nt][i] - y);
             m[nt][i] = y;
 #pragma unroll
@@ -814,7 +814,7 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
       }
       // a row that sees no key: zeros, and -inf as its lse
       const float inv = sum == 0.f ? 0.f : (whole ? p.v_scale : 1.f) / sum;
-      const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum);
+      const float lse2 = sum == 0.f ? -INFINITY : top + kPHead + log2f(sum * 0x1p-7f);  // (a logarithm near 0)
       acc.x *= inv;
       acc.y *= inv;
       acc.z *= inv;

@@ -91,6 +91,18 @@ struct DivG {
 };
 
 // ---------------------------------------------------------------------------
+// softmax weights
+
+// P is 2^(logit - m) with the reference m this far (in log2 units) below the
+// largest logit when it is set; it is set again when a logit passes it by
+// kPMost, so a row's largest P lies in [2^7, 2^15] and fp16 rounds P to 2^-11
+// of it down to 2^-14: 2^-21 of the row's largest weight or above.  Smaller
+// ones are off by at most 2^-25, or 2^-32 of the largest (with m the largest
+// logit itself, keys below 2^-25 of it were lost: a row with one dominant key
+// lost all others).
+constexpr float kPHead = 7.f, kPMost = 15.f;
+
+// ---------------------------------------------------------------------------
 // partial states
 
 // Joins `parts` states of `rows` rows: o = sum_k 2^(lse_k - lse) o_k, in the

@@ -23,7 +23,8 @@
 //                     their memory holds cannot pass through P = 0.
 //   warpgroup NT + 1  one thread issues the MMAs: S_x = Q_x K^T, O_x += P_x V,
 //                     all fp16 with fp32 sums in TMEM.  P is fp16 whatever q's
-//                     type (2^-11 relative), so no row needs P in two parts.
+//                     type (2^-11 relative; small ones see kPHead), so no row needs
+//                     P in two parts.
 // Per key tile j it issues PV_A(j), S_A(j+1), PV_B(j), S_B(j+1): one tile's
 // MMAs run while the other tile's rows are in their softmax.
 //
@@ -630,16 +631,16 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, PreCfg<D, NT>::CTAS) k
 #pragma unroll
       for (int u = 0; u < 5; ++u) m5[u] = fmax3(m15[3 * u], m15[3 * u + 1], m15[3 * u + 2]);
       const float mx2 = fmax3(fmax3(m5[0], m5[1], m5[2]), m5[3], m5[4]) * sl2;
-      // the reference maximum moves when it grows by more than 8 (log2 units):
-      // P stays below 2^8, which fp16 and the fp32 sums carry
+      // the reference moves when a logit passes it by kPMost (log2 units)
       float alpha = 1.f;
       bool resc = false;
-      if (mx2 > m_ref + 8.f) {
+      if (mx2 > m_ref + kPMost) {
+        const float lower = mx2 - kPHead;
         if (m_ref != -INFINITY) {
-          alpha = ex2(m_ref - mx2);
+          alpha = ex2(m_ref - lower);
           resc = true;
         }
-        m_ref = mx2;
+        m_ref = lower;
       }
       const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
       const float2 sc2 = make_float2(sl2, sl2), nm2 = make_float2(-m_use, -m_use);
@@ -723,7 +724,7 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, PreCfg<D, NT>::CTAS) k
       const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
       // a row that sees no key: zeros, and -inf as its lse
       const float inv = l_sum == 0.f ? 0.f : (split ? 1.f : p.v_scale) / l_sum;
-      const float lse2 = l_sum == 0.f ? -INFINITY : m_use + __log2f(l_sum);
+      const float lse2 = l_sum == 0.f ? -INFINITY : m_use + kPHead + __log2f(l_sum * 0x1p-7f);  // (a logarithm near 0)
       const int64_t part_row = (part_tile + part) * (NT * kQRows) + x * kQRows + r;
       if (row_valid) {
         if (split) p.part_lse[part_row] = lse2;

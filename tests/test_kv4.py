@@ -629,6 +629,42 @@ def test_attention_bf16_queries_of_any_size(gain):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("B, qo, kv, G, D", [(160, 1, 900, 1, 128), (160, 2, 900, 1, 64), (40, 4, 900, 8, 128),
+                                             (4, 40, 700, 4, 128), (4, 70, 700, 4, 64), (2, 20, 90, 4, 256)])
+def test_attention_keeps_a_long_tail(B, qo, kv, G, D, dtype):
+    """One key of 2^26 times the others' weight and values of zero: the outputs are the others' sum.
+
+    Their P is 2^7 * 2^-26 or more, which fp16 rounds by at most 2^-25: 2^-6
+    of it.  The same P stands for every key of a row's slice, so the errors
+    do not cancel; logits and weights add less than 2^-10, the output rounds
+    by half a step (v_scale keeps it a normal number of fp16).  A logit has one
+    product that is not zero, so it is off by four roundings, 2^-22 of its 18;
+    lse by three more of 2^-20: less than 2^-17 in all.
+    """
+    H = 8
+    cache = pa.Kv4Cache(B * kv, 1, H, D, v_scale=4096.0)
+    k = torch.zeros(B, kv, H, D, dtype=dtype, device="cuda")
+    v = torch.full((B, kv, H, D), 6.0 * 4096, dtype=dtype, device="cuda")
+    k[:, kv // 5, :, 0] = 6.0
+    v[:, kv // 5] = 0.0
+    cache.append(k.view(B * kv, H, D), v.view(B * kv, H, D), torch.arange(B * kv, device="cuda"))
+    q = torch.zeros(B * qo, H * G, D, dtype=dtype, device="cuda")
+    q[..., 0] = 26 * np.log(2) * D ** 0.5 / 6
+    dev = lambda a: torch.as_tensor(a, dtype=I32).cuda()  # noqa: E731
+    tables = (dev(range(0, B * qo + 1, qo)), dev(range(0, B * kv + 1, kv)), dev(range(B * kv)), dev([1] * B))
+    a = pa.Kv4Attention(B, B * qo, H * G, H, D, 1, dtype, False, qo)
+    out, lse = a.run(q, cache, tables)
+    logit = float(q[0, 0, 0]) * 6 / D ** 0.5
+    w = (kv - 1) * np.exp(-logit)
+    want, want_lse = 6 * 4096 * w / (1 + w), logit + np.log1p(w)
+    assert a.device_status() == 0
+    rel = (out.double() / want - 1).abs().max().item()
+    assert rel <= 2.0 ** -6 + 2.0 ** -10 + torch.finfo(dtype).eps / 2, rel
+    assert (lse.double() - want_lse).abs().max().item() <= 2.0 ** -17
+
+
+@gpu
 def test_attention_max_qo_len_is_a_hint():
     """A bound below the longest request costs time, not results."""
     b = Batch([40, 1, 3], [500, 77, 20], 8, 2, 128, 16, "NHD", torch.bfloat16, seed=9)
