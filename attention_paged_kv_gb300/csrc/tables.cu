@@ -278,6 +278,7 @@ cudaError_t launch_tables(const TablesParams& p, int num_sms, cudaStream_t strea
   }
   cudaError_t e = launch_pdl(tables_scan_kernel<false, 1>, 1u, unsigned(kScanThreads), size_t(0), stream, p);
   if (e != cudaSuccess) return e;
+  if (longest == 0) return cudaSuccess;  // nothing to fill
   const int blocks = (longest + kFillThreads - 1) / kFillThreads;
   const int most = num_sms * 8;
   return launch_pdl(tables_fill_kernel, unsigned(blocks < most ? blocks : most), unsigned(kFillThreads), size_t(0),

@@ -263,6 +263,20 @@ def test_tables_all_or_nothing(B, fault, flag):
 
 
 @gpu
+@pytest.mark.parametrize("B", [6, 3500])
+def test_tables_without_room_for_anything(B):
+    """Requests of no tokens and no pages need no lists; one with a token then fails the whole build."""
+    z = lambda *s: torch.zeros(s, dtype=I32, device="cuda")  # noqa: E731
+    t = pa.BatchTables(B, 0, 0, 16, 4)
+    qo = z(B)
+    t.build(qo, z(B), z(B, 1), z(0), z(1))
+    assert t.device_status() == 0 and not t.qo_indptr.any() and not t.kv_lens.any()
+    qo[3] = 1
+    t.build(qo, z(B), z(B, 1), z(0), z(1))
+    assert t.device_status() == raw.PA_DEV_NO_PAGES | raw.PA_DEV_NO_ROOM and not t.qo_indptr.any()
+
+
+@gpu
 def test_tables_bad_page_id():
     t = pa.BatchTables(2, 4, 8, 16, 10)
     dev = lambda *a: torch.tensor(a, dtype=I32).cuda()  # noqa: E731
