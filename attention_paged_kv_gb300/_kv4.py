@@ -50,12 +50,12 @@ def _rows(t, name, shape, index):
     return st[0] if n > 1 else h * d
 
 
-def _on(index, stream, tensors=()):
+def _on(index, stream, tensors=(), own=()):
     """(stream handle, context or None) for a call on device `index`.
 
     Without a stream the device's current one is used.  With another one, the
-    tensors of the call are recorded on it, so that their memory is not given
-    away before it has passed the call.  The context makes device and stream
+    tensors of the call and the objects' own are recorded on it, so that their
+    memory is not given away before it has passed the call.  The context makes device and stream
     current where they are not.
     """
     import torch
@@ -69,7 +69,7 @@ def _on(index, stream, tensors=()):
             stream = torch.cuda.ExternalStream(handle, device=index)
         if stream.device.index != index:
             _refuse(f"the stream is not one of cuda:{index}")
-        for t in tensors:
+        for t in (*tensors, *own):
             if t is not None:
                 t.record_stream(stream)
         return handle, torch.cuda.stream(stream)  # sets the device too
@@ -136,6 +136,7 @@ class BatchTables:
         self.positions = torch.zeros(self.max_tokens, **i32)
         self.free_count = torch.zeros(1, **i32)
         self.status = torch.zeros(2, **i32)  # the second word is the library's
+        self._own = tuple(t for t in vars(self).values() if isinstance(t, torch.Tensor))
         self._out = _b.TablesOut(*(getattr(self, n).data_ptr() for n, t in _b.TablesOut._fields_
                                    if t is ctypes.c_void_p), self.max_tokens, self.max_pages)
 
@@ -159,7 +160,7 @@ class BatchTables:
         width, (row, col) = block_table.shape[1], block_table.stride()
         if width > 1 and col != 1:
             _refuse("block_table: each row must be contiguous")
-        handle, guard = _on(at, stream, (qo_lens, kv_lens, block_table, free_pages, free_count))
+        handle, guard = _on(at, stream, (qo_lens, kv_lens, block_table, free_pages, free_count), self._own)
         _call(guard, self._lib.pagedattn_build_tables,
               _TABLES_IN.pack(qo_lens.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(),
                               free_count.data_ptr(), row if B > 1 else width, width, cap, B, self.page_size,
@@ -204,6 +205,7 @@ class Kv4Cache:
             setattr(self, name, given)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._status_ptr = self.status.data_ptr()
+        self._own = (self.codes, self.scales, self.status)
         self._args = _b.Kv4CacheArgs(self.codes.data_ptr(), self.scales.data_ptr(), self.num_pages, self.page_size,
                                      self.num_kv_heads, self.head_dim, self.kv_layout, self.k_scale, self.v_scale)
 
@@ -231,7 +233,7 @@ class Kv4Cache:
                               0 if v_values is None else v_values.data_ptr(), slot_mapping.data_ptr(),
                               self._status_ptr, n,
                               _b.PA_BF16 if k.dtype == torch.bfloat16 else _b.dtype_code(k.dtype))
-        handle, guard = _on(at, stream, (k, v, slot_mapping, k_values, v_values))
+        handle, guard = _on(at, stream, (k, v, slot_mapping, k_values, v_values), self._own)
         _call(guard, self._lib.pagedattn_kv4_append, ctypes.byref(self._args), rows, handle)
 
     def device_status(self, stream=None) -> int:
@@ -311,7 +313,7 @@ class Kv4Attention:
             _is(out, "out", q.dtype, shape, at)
         if lse is not None:
             _is(lse, "lse", torch.float32, shape[:2], at)
-        handle, guard = _on(at, stream, (q, out, lse, *tables))
+        handle, guard = _on(at, stream, (q, out, lse, *tables), (cache.codes, cache.scales, self.workspace))
         if guard is None:
             return self._launch(q, stride, cache, qo_indptr, page_indptr, pages, last, nnz, out, lse, return_lse, handle)
         with guard:  # the outputs are allocated on the stream that writes them

@@ -404,8 +404,8 @@ typedef struct {
  * a copy to the host) and what pagedattn_kv4_append and pagedattn_kv4_run
  * read in place.
  *
- * All or nothing: where a length is negative or their sum passes 2^31 - 1
- * (PA_DEV_BAD_INDEX), the stack is short (PA_DEV_NO_PAGES), or a row of the
+ * All or nothing: where a length is negative or their sum passes
+ * 2^31 - 1 - page_size (PA_DEV_BAD_INDEX), the stack is short (PA_DEV_NO_PAGES), or a row of the
  * block table, max_tokens or max_pages is (PA_DEV_NO_ROOM), the outputs are
  * those of an empty batch (indptr all 0, slot_mapping all -1, kv_lens and
  * free_count as they were) and the block table is left alone.  A page id
@@ -493,7 +493,8 @@ PAGEDATTN_API pagedattn_status pagedattn_kv4_workspace_size(int32_t num_qo_heads
  *
  * q         device, dtype[num_tokens][num_qo_heads][head_dim], tokens q_stride
  *           elements apart (a multiple of 8), 16-byte aligned.
- * out       device, dtype[num_tokens][num_qo_heads][head_dim], 16-byte aligned.
+ * out       device, dtype[num_tokens][num_qo_heads][head_dim], 16-byte aligned; must not
+ *           overlap q.
  * lse       device, float[num_tokens][num_qo_heads], or NULL.
  * workspace device, 256-byte aligned, pagedattn_kv4_workspace_size() bytes: zero
  *           it once, before its first run.  Its first word is the status word.
