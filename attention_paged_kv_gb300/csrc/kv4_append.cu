@@ -20,8 +20,8 @@
 // 2 bytes read and 0.5625 written an element (2 more where the values are
 // wanted); the instructions come close to the bytes' time.  A thread takes a
 // whole block of 16 values, so that the scale, its reciprocal and the row's
-// address are found once a block (with 8 values a thread the kernel took 276
-// instructions for them, 40 us for 16000 tokens of 8 heads with values).
+// address are found once a block (16000 tokens of 8 heads, 128 dims and
+// values, 150 MB: 30 us, 74 % of the copy rate; with 8 values a thread 44.9).
 #include <cstring>
 
 #include "common.cuh"

@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
   // of at most `part_units`: no second start in a slice, and no join where the
   // tiles stay whole.  Weighed in us: a unit's bytes at the 20 GB/s that a CTA
   // gets when all run, 8 for the second start and the joins of equal slices,
-  // 4.5 for a join (128 requests of 1024 keys: 16.6 us in equal slices, 9.9
+  // 4.5 for a join (128 requests of 1024 keys: 16.6 us in equal slices, 13.8
   // whole).
   int part_units = 0;  // 0: slices of equal size
   if (p.slices > 1 && p.batch <= kThreads) {

@@ -28,6 +28,12 @@
 // Per key tile j it issues PV_A(j), S_A(j+1), PV_B(j), S_B(j+1): one tile's
 // MMAs run while the other tile's rows are in their softmax.
 //
+// What bounds it: 2000 tokens behind 6000 at 64 / 8 heads take 369 us, 1244
+// TFLOP/s; the tensor pipe is busy 54 % of the time and a pair of row tiles
+// takes 1.68 us a key tile, softmax and MMAs waiting for one another.  32
+// prompts of up to 200 tokens at 32 / 8 heads take 38 us (41 a call), most of
+// it the set-up, first loads and epilogue of items with one or two key tiles.
+//
 // TMEM: S_x (fp32 128 x 128) at 128 x, O_x (fp32 128 x D) after them; P_x
 // overwrites the first 64 columns of S_x.
 #include <cstring>
