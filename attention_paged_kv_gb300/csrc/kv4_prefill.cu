@@ -239,7 +239,11 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, PreCfg<D, NT>::CTAS) k
     mbar_init_fence();
   }
   if (tid < D / 16) first_nan[tid] = INT_MAX;
-  if (tid == 0) any_nan = 0;
+  if (tid == 0) {
+    any_nan = 0;
+    found_rq = Req{0, 0, 0, 0};  // of an item that bad tables leave without a request
+    found_tile = 0;
+  }
   if (warp == C::WARP_MMA) tmem_alloc(tmem_slot, C::TMEM_COLS);
   pdl_wait();  // q, the cache and the tables may come from the kernel before
 
@@ -287,7 +291,9 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, PreCfg<D, NT>::CTAS) k
   if (p.split_ctas > 0) {
     __syncthreads();
     const int rem = items % p.num_sms;
-    if (rem > 0) {
+    // (requests that overlap, as bad tables may have them, can make more items
+    // than the grid has CTAs: a part that never runs would leave its count)
+    if (rem > 0 && items <= static_cast<int>(gridDim.x) - p.split_ctas) {
       const float kts = static_cast<float>(work_s) / static_cast<float>(total);
       // lane n - 1 weighs n parts; the cheapest, the fewest among equals
       const int n = lane + 1;

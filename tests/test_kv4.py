@@ -781,6 +781,51 @@ def test_attention_bad_tables_are_contained():
 
 
 @gpu
+@pytest.mark.parametrize("pairs", [1, 3, 5, 11])
+def test_attention_overlapping_requests_leave_the_workspace_usable(pairs):
+    """Tables whose valid requests overlap (between bad ones): flagged, and the next run joins its parts as ever."""
+    good = Batch([300], [40000], 32, 4, 64, 16, "NHD", torch.bfloat16, seed=9)
+    fresh, used = good.attention(), good.attention()
+    want = fresh.run(good.q, good.cache, good.tables())
+    qo = torch.tensor([0] + [300, 0] * pairs, dtype=I32).cuda()
+    n = int(good.page_indptr[1])
+    tables = (qo, torch.tensor([0] + [n, 0] * pairs, dtype=I32).cuda(), good.tables()[2],
+              torch.full((2 * pairs,), int(good.last[0]), dtype=I32).cuda())
+    bad = pa.Kv4Attention(2 * pairs, 300, 32, 4, 64, 16, torch.bfloat16, True, 300, workspace=used.workspace)
+    used.workspace.zero_()
+    bad.run(good.q, good.cache, tables)
+    assert bad.device_status() == raw.PA_DEV_BAD_INDEX
+    for _ in range(2):
+        out, lse = used.run(good.q, good.cache, good.tables())
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert used.device_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("qo, kv", [([1, 1], [3000, 77]), ([4, 1], [500, 300]), ([40, 9], [900, 60]), ([300], [300])])
+def test_attention_beyond_32_bit_offsets(qo, kv):
+    """Pages in the upper part of a cache of 8.7 GB of codes give what the same pages of a small one do."""
+    pages, page, H, D = 530_000, 128, 1, 128
+    rows = int(sum(-(-k // page) * page for k in kv))
+    k, v = (torch.randn(rows, H, D, device="cuda").half() for _ in range(2))
+    slots = torch.arange(rows, device="cuda")
+    first, got = torch.tensor(qo).cumsum(0), []
+    indptr = torch.tensor([0] + first.tolist(), dtype=I32).cuda()
+    counts = torch.tensor([-(-n // page) for n in kv])
+    page_indptr = torch.tensor([0] + counts.cumsum(0).tolist(), dtype=I32).cuda()
+    last = torch.tensor([(n - 1) % page + 1 for n in kv], dtype=I32).cuda()
+    q = torch.randn(sum(qo), 8, D, device="cuda").half()
+    for num, base in ((pages, pages - rows // page), (rows // page, 0)):
+        cache = pa.Kv4Cache(num, page, H, D)
+        cache.append(k, v, slots + base * page)
+        ids = torch.arange(base, base + rows // page, dtype=I32, device="cuda")
+        a = pa.Kv4Attention(len(qo), sum(qo), 8, H, D, page, torch.float16, True, max(qo))
+        got.append(a.run(q, cache, (indptr, page_indptr, ids, last)))
+        assert a.device_status() == 0 and cache.device_status() == 0
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+@gpu
 def test_attention_python_refusals():
     b = Batch([1, 1], [20, 30], 8, 2, 128, 16, "NHD", torch.float16)
     a, t = b.attention(), b.tables()
