@@ -2,6 +2,7 @@
 // the conversions of codes and scales.
 #pragma once
 
+#include <cfloat>
 #include <climits>
 
 #include "common.cuh"
@@ -80,6 +81,16 @@ __device__ __forceinline__ int bf16_row_shift(uint32_t top) {
   return (e == 0 || e == 255) ? 0 : min(140 - e, 126);
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
+// The factor from a row's scores (of q * 2^up) to its logits, kept a normal
+// number: a score is 0, or of a size in [2^-34, 2^34], or -inf where its key is
+// masked.  Below fp32's range the factor would be 0, and 0 * -inf a NaN; the
+// logits are below 2^-92 either way.  Above, it would be infinite, and a NaN
+// for scores of 0; the logits of other scores pass 2^93 either way, and the
+// largest alone counts (or passes fp32's range).
+__device__ __forceinline__ float row_factor(float scale_log2, int up) {
+  return fminf(fmaxf(scale_log2 * pow2(-up), FLT_MIN), FLT_MAX);
+}
 
 // n / G and n % G for n < 512 (G <= 128): G's reciprocal in 16 bits, rounded up
 // (its error, below G / 2^16 a unit, stays below one for such n).

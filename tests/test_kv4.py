@@ -958,3 +958,35 @@ def test_two_objects_on_two_streams():
     torch.cuda.synchronize()
     for (o, l), (wo, wl) in zip(got, want):
         assert torch.equal(o, wo) and torch.equal(l, wl)
+
+
+# ---------------------------------------------------------------- logit factors at the ends of fp32's range
+
+
+@gpu
+@pytest.mark.parametrize("k_scale, gain", [(1e-15, 1e-30), (1e-7, 2e-38), (1e-15, 1e-38)])
+@pytest.mark.parametrize("qo, kv, G, D", [([1, 40], [200, 333], 4, 128), ([300], [2600], 4, 128), ([40], [4100], 2, 64),
+                                          ([300, 33], [1500, 1500], 4, 128), ([17, 66], [90, 66], 4, 256)], ids=str)
+def test_attention_of_tiny_bf16_queries_and_scales(qo, kv, G, D, k_scale, gain):
+    """Factors below fp32's range stand for logits of zero: every key a row sees has the same weight, the others none."""
+    b = Batch(qo, kv, 2 * G, 2, D, 16, "NHD", torch.bfloat16, seed=8, k_scale=k_scale, q_gain=gain)
+    for causal in (True, False):
+        a = b.attention(causal)
+        out, lse = a.run(b.q, b.cache, b.tables())
+        b.check(out, lse, b.want(causal))
+        assert a.device_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("qo, kv, G, D", [([1, 2], [200, 33], 4, 128), ([40], [333], 4, 128), ([300], [2600], 2, 64),
+                                          ([17, 66], [90, 66], 4, 256)], ids=str)
+def test_attention_of_huge_bf16_queries_and_scales_over_zero_keys(qo, kv, G, D):
+    """Factors above fp32's range over keys of zero: the logits are zero."""
+    b = Batch(qo, kv, 2 * G, 2, D, 16, "NHD", torch.bfloat16, seed=8, k_scale=1e15, q_gain=1e30)
+    b.codes[:, 0] = 0
+    b.cache.codes[:, 0] = 0
+    for causal in (True, False):
+        a = b.attention(causal)
+        out, lse = a.run(b.q, b.cache, b.tables())
+        b.check(out, lse, b.want(causal))
+        assert a.device_status() == 0
