@@ -50,8 +50,8 @@ def _rows(t, name, shape, index):
     return st[0] if n > 1 else h * d
 
 
-def _on(index, stream, tensors=(), own=()):
-    """(stream handle, context or None) for a call on device `index`.
+def _on(index, stream, objects, tensors=(), own=()):
+    """(stream handle, context or None) for a call with these objects on device `index`.
 
     Without a stream the device's current one is used.  With another one, the
     tensors of the call and the objects' own are recorded on it, so that their
@@ -64,6 +64,9 @@ def _on(index, stream, tensors=(), own=()):
         handle = current
     else:
         handle = int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+    for o in objects:
+        if handle not in o._streams:
+            o._enter(handle)
     if handle != current:
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(handle, device=index)
@@ -96,18 +99,47 @@ def _call(guard, function, *args):
         _b.check(status)
 
 
-def _status(word, stream):
-    flags = ctypes.c_int32(0)
-    handle, guard = _on(word.get_device(), stream, (word,))
-    try:
-        _call(guard, _b.load().pagedattn_status_word, word.data_ptr(), handle, ctypes.byref(flags))
-    except PagedAttnError as e:
-        if e.status not in (_b.PA_ERR_TIMEOUT, _b.PA_ERR_DEVICE_CHECK):
-            raise
-    return int(flags.value)
+class _Object:
+    """Device memory of an object's own: initialised by the stream that is current when the object is made.
+
+    The first call on another stream makes that stream wait for it.  (A stream
+    under capture cannot: what it captures has to be replayed after the
+    initialisation, as it is where the capture began with a wait for the device.
+    The memory of an object made under capture is initialised by each replay,
+    and the object belongs to that graph.)
+    """
+
+    def _made(self):
+        import torch
+        with torch.cuda.device(self._index):
+            self._streams, self._ready = {torch._C._cuda_getCurrentRawStream(self._index)}, None
+            if not torch.cuda.is_current_stream_capturing():
+                self._ready = torch.cuda.Event()
+                self._ready.record()
+
+    def _enter(self, handle):
+        import torch
+        stream = torch.cuda.ExternalStream(handle, device=self._index)
+        with torch.cuda.stream(stream):
+            if torch.cuda.is_current_stream_capturing():
+                return
+            if self._ready is not None:
+                stream.wait_event(self._ready)
+        self._streams.add(handle)
+
+    def device_status(self, stream=None) -> int:
+        """Waits for the stream; the PA_DEV_* bits since the last read, which clears them."""
+        flags = ctypes.c_int32(0)
+        handle, guard = _on(self._index, stream, (self,), (self.status,))
+        try:
+            _call(guard, self._lib.pagedattn_status_word, self.status.data_ptr(), handle, ctypes.byref(flags))
+        except PagedAttnError as e:
+            if e.status not in (_b.PA_ERR_TIMEOUT, _b.PA_ERR_DEVICE_CHECK):
+                raise
+        return int(flags.value)
 
 
-class BatchTables:
+class BatchTables(_Object):
     """Page tables, slot maps and positions of a step, built on the device.
 
     Holds the outputs, all on the device: ``qo_indptr``, ``kv_page_indptr``,
@@ -139,6 +171,7 @@ class BatchTables:
         self._own = tuple(t for t in vars(self).values() if isinstance(t, torch.Tensor))
         self._out = _b.TablesOut(*(getattr(self, n).data_ptr() for n, t in _b.TablesOut._fields_
                                    if t is ctypes.c_void_p), self.max_tokens, self.max_pages)
+        self._made()
 
     def build(self, qo_lens, kv_lens, block_table, free_pages, free_count, stream=None):
         """Builds the tables of a step; see pagedattn_build_tables.
@@ -160,19 +193,15 @@ class BatchTables:
         width, (row, col) = block_table.shape[1], block_table.stride()
         if width > 1 and col != 1:
             _refuse("block_table: each row must be contiguous")
-        handle, guard = _on(at, stream, (qo_lens, kv_lens, block_table, free_pages, free_count), self._own)
+        handle, guard = _on(at, stream, (self,), (qo_lens, kv_lens, block_table, free_pages, free_count), self._own)
         _call(guard, self._lib.pagedattn_build_tables,
               _TABLES_IN.pack(qo_lens.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(),
                               free_count.data_ptr(), row if B > 1 else width, width, cap, B, self.page_size,
                               self.num_pages), ctypes.byref(self._out), handle)
         return self
 
-    def device_status(self, stream=None) -> int:
-        """Waits for the stream; the PA_DEV_* bits since the last read, which clears them."""
-        return _status(self.status, stream)
 
-
-class Kv4Cache:
+class Kv4Cache(_Object):
     """A paged KV cache in 4 bits: e2m1 codes with an e4m3 scale for each 16 values along head_dim.
 
     ``codes`` uint8 [num_pages, 2, page_size, num_kv_heads, head_dim / 2] and
@@ -208,6 +237,7 @@ class Kv4Cache:
         self._own = (self.codes, self.scales, self.status)
         self._args = _b.Kv4CacheArgs(self.codes.data_ptr(), self.scales.data_ptr(), self.num_pages, self.page_size,
                                      self.num_kv_heads, self.head_dim, self.kv_layout, self.k_scale, self.v_scale)
+        self._made()
 
     def append(self, k, v, slot_mapping, k_values=None, v_values=None, stream=None):
         """Quantises the rows k, v [n, num_kv_heads, head_dim] into the slots of slot_mapping (int64 [n]).
@@ -233,15 +263,11 @@ class Kv4Cache:
                               0 if v_values is None else v_values.data_ptr(), slot_mapping.data_ptr(),
                               self._status_ptr, n,
                               _b.PA_BF16 if k.dtype == torch.bfloat16 else _b.dtype_code(k.dtype))
-        handle, guard = _on(at, stream, (k, v, slot_mapping, k_values, v_values), self._own)
+        handle, guard = _on(at, stream, (self,), (k, v, slot_mapping, k_values, v_values), self._own)
         _call(guard, self._lib.pagedattn_kv4_append, ctypes.byref(self._args), rows, handle)
 
-    def device_status(self, stream=None) -> int:
-        """Waits for the stream; the PA_DEV_* bits since the last read, which clears them."""
-        return _status(self.status, stream)
 
-
-class Kv4Attention:
+class Kv4Attention(_Object):
     """Attention over a Kv4Cache, through tables in device memory.
 
     num_tokens: rows of q; max_qo_len: a bound of the requests' query lengths
@@ -281,6 +307,7 @@ class Kv4Attention:
             self._ws_ptr = workspace.data_ptr()
             self.status = workspace.view(-1).view(torch.uint8)[:4].view(torch.int32)
             workspace.zero_()
+        self._made()
 
     def run(self, q, cache, tables, out=None, lse=None, return_lse=True, stream=None):
         """out, lse of q [num_tokens, num_qo_heads, head_dim] (any token stride that is a multiple of 8).
@@ -296,7 +323,9 @@ class Kv4Attention:
         if cache._index != at or cache.num_kv_heads != self.num_kv_heads or cache.head_dim != self.head_dim or \
                 cache.page_size != self.page_size:
             _refuse("the cache's heads, head_dim, page_size or device differ from the object's")
+        objects = (self, cache)
         if isinstance(tables, BatchTables):
+            objects = (self, cache, tables)
             if tables.batch_size != B or tables.page_size != self.page_size or tables._index != at:
                 _refuse("the tables' batch, page_size or device differ from the object's")
             qo_indptr, page_indptr, pages, last = tables = (tables.qo_indptr, tables.kv_page_indptr,
@@ -313,7 +342,7 @@ class Kv4Attention:
             _is(out, "out", q.dtype, shape, at)
         if lse is not None:
             _is(lse, "lse", torch.float32, shape[:2], at)
-        handle, guard = _on(at, stream, (q, out, lse, *tables), (cache.codes, cache.scales, self.workspace))
+        handle, guard = _on(at, stream, objects, (q, out, lse, *tables), (cache.codes, cache.scales, self.workspace))
         if guard is None:
             return self._launch(q, stride, cache, qo_indptr, page_indptr, pages, last, nnz, out, lse, return_lse, handle)
         with guard:  # the outputs are allocated on the stream that writes them
@@ -335,7 +364,3 @@ class Kv4Attention:
         if status != _b.PA_OK:
             _b.check(status)
         return out, lse
-
-    def device_status(self, stream=None) -> int:
-        """Waits for the stream; the PA_DEV_* bits since the last read, which clears them."""
-        return _status(self.status, stream)

@@ -990,3 +990,52 @@ def test_attention_of_huge_bf16_queries_and_scales_over_zero_keys(qo, kv, G, D):
         out, lse = a.run(b.q, b.cache, b.tables())
         b.check(out, lse, b.want(causal))
         assert a.device_status() == 0
+
+
+# ---------------------------------------------------------------- objects made on one stream and used on another
+
+
+def garbage_for(*sizes):
+    """The allocator's next blocks of these sizes hold 0x5A."""
+    junk = [torch.full((n,), 0x5A, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(3)]
+    torch.cuda.synchronize()
+    del junk
+
+
+@gpu
+@pytest.mark.parametrize("by_hand", [True, False])
+def test_first_calls_on_another_stream_wait_for_the_objects_memory(by_hand):
+    """Objects are made while their stream is busy, so that their zeroing is still queued when another stream calls."""
+    b = Batch([1], [20_000], 8, 1, 128, 16, "NHD", torch.bfloat16, seed=3)
+    want, want_lse = b.attention().run(b.q, b.cache, b.tables())
+    rng, B, page, n = np.random.default_rng(4), 40, 16, 500
+    qo, kv = np.ones(B, np.int32), rng.integers(0, 300, B).astype(np.int32)
+    table, free, num_pages = make_tables(rng, B, page, qo, kv)
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    qo_t, kv_t, table_t, free_t, count = dev(qo), dev(kv), dev(table.copy()), dev(free), dev(np.int32([len(free)]))
+    k, slots, tables = torch.randn(n, 2, 64, device="cuda").half(), torch.arange(n, device="cuda"), b.tables()
+    out, lse = torch.zeros_like(want), torch.zeros_like(want_lse)
+    ref = pa.Kv4Cache(64, page, 2, 64)
+    ref.append(k, k, slots)
+    lists = pa.BatchTables(B, B + 7, num_pages, page, num_pages)
+    lists.build(qo_t, kv_t, table_t, free_t, count)
+    side = torch.cuda.Stream()
+    garbage_for(b.attention().workspace.numel(), ref.codes.numel(), ref.scales.numel(), 512)
+    del ref.status
+    torch.cuda.synchronize()
+    torch.cuda._sleep(400_000_000)  # a fifth of a second
+    a, cache = b.attention(), pa.Kv4Cache(64, page, 2, 64)
+    t = pa.BatchTables(B, B + 7, num_pages, page, num_pages)
+    kw = dict(stream=side) if by_hand else {}
+    with torch.cuda.stream(torch.cuda.current_stream() if by_hand else side):
+        for _ in range(2):
+            a.run(b.q, b.cache, tables, out=out, lse=lse, **kw)
+            cache.append(k, k, slots, **kw)
+            t.build(qo_t, kv_t, table_t, free_t, count, **kw)
+    assert a.device_status(side) == cache.device_status(side) == t.device_status(side) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    assert torch.equal(cache.codes, ref.codes) and torch.equal(cache.scales, ref.scales)
+    for name in ("qo_indptr", "kv_page_indptr", "new_page_indptr", "kv_page_indices", "kv_last_page_len", "kv_lens",
+                 "slot_mapping", "positions", "free_count", "status"):
+        assert torch.equal(getattr(t, name), getattr(lists, name)), name
