@@ -50,12 +50,12 @@ def _rows(t, name, shape, index):
     return st[0] if n > 1 else h * d
 
 
-def _on(index, stream, objects, tensors=(), own=()):
+def _on(index, stream, objects, tensors=()):
     """(stream handle, context or None) for a call with these objects on device `index`.
 
     Without a stream the device's current one is used.  With another one, the
-    tensors of the call and the objects' own are recorded on it, so that their
-    memory is not given away before it has passed the call.  The context makes device and stream
+    tensors of the call are recorded on it, so that their memory is not given
+    away before it has passed the call.  The context makes device and stream
     current where they are not.
     """
     import torch
@@ -72,7 +72,7 @@ def _on(index, stream, objects, tensors=(), own=()):
             stream = torch.cuda.ExternalStream(handle, device=index)
         if stream.device.index != index:
             _refuse(f"the stream is not one of cuda:{index}")
-        for t in (*tensors, *own):
+        for t in tensors:
             if t is not None:
                 t.record_stream(stream)
         return handle, torch.cuda.stream(stream)  # sets the device too
@@ -102,15 +102,18 @@ def _call(guard, function, *args):
 class _Object:
     """Device memory of an object's own: initialised by the stream that is current when the object is made.
 
-    The first call on another stream makes that stream wait for it.  (A stream
-    under capture cannot: what it captures has to be replayed after the
-    initialisation, as it is where the capture began with a wait for the device.
-    The memory of an object made under capture is initialised by each replay,
-    and the object belongs to that graph.)
+    The first call on another stream, current or given, records the memory on
+    it, so that it is not given away before it has passed the object's calls,
+    and makes it wait for the initialisation.  (A stream under capture cannot
+    wait: what it captures has to be replayed after the initialisation, as it is
+    where the capture began with a wait for the device.  The memory of an object
+    made under capture is initialised by each replay, and the object belongs to
+    that graph.)
     """
 
-    def _made(self):
+    def _made(self, *own):
         import torch
+        self._own = own
         with torch.cuda.device(self._index):
             self._streams, self._ready = {torch._C._cuda_getCurrentRawStream(self._index)}, None
             if not torch.cuda.is_current_stream_capturing():
@@ -120,6 +123,8 @@ class _Object:
     def _enter(self, handle):
         import torch
         stream = torch.cuda.ExternalStream(handle, device=self._index)
+        for t in self._own:
+            t.record_stream(stream)
         with torch.cuda.stream(stream):
             if torch.cuda.is_current_stream_capturing():
                 return
@@ -130,7 +135,7 @@ class _Object:
     def device_status(self, stream=None) -> int:
         """Waits for the stream; the PA_DEV_* bits since the last read, which clears them."""
         flags = ctypes.c_int32(0)
-        handle, guard = _on(self._index, stream, (self,), (self.status,))
+        handle, guard = _on(self._index, stream, (self,))
         try:
             _call(guard, self._lib.pagedattn_status_word, self.status.data_ptr(), handle, ctypes.byref(flags))
         except PagedAttnError as e:
@@ -168,10 +173,9 @@ class BatchTables(_Object):
         self.positions = torch.zeros(self.max_tokens, **i32)
         self.free_count = torch.zeros(1, **i32)
         self.status = torch.zeros(2, **i32)  # the second word is the library's
-        self._own = tuple(t for t in vars(self).values() if isinstance(t, torch.Tensor))
         self._out = _b.TablesOut(*(getattr(self, n).data_ptr() for n, t in _b.TablesOut._fields_
                                    if t is ctypes.c_void_p), self.max_tokens, self.max_pages)
-        self._made()
+        self._made(*(t for t in vars(self).values() if isinstance(t, torch.Tensor)))
 
     def build(self, qo_lens, kv_lens, block_table, free_pages, free_count, stream=None):
         """Builds the tables of a step; see pagedattn_build_tables.
@@ -193,7 +197,7 @@ class BatchTables(_Object):
         width, (row, col) = block_table.shape[1], block_table.stride()
         if width > 1 and col != 1:
             _refuse("block_table: each row must be contiguous")
-        handle, guard = _on(at, stream, (self,), (qo_lens, kv_lens, block_table, free_pages, free_count), self._own)
+        handle, guard = _on(at, stream, (self,), (qo_lens, kv_lens, block_table, free_pages, free_count))
         _call(guard, self._lib.pagedattn_build_tables,
               _TABLES_IN.pack(qo_lens.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(),
                               free_count.data_ptr(), row if B > 1 else width, width, cap, B, self.page_size,
@@ -234,10 +238,9 @@ class Kv4Cache(_Object):
             setattr(self, name, given)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._status_ptr = self.status.data_ptr()
-        self._own = (self.codes, self.scales, self.status)
         self._args = _b.Kv4CacheArgs(self.codes.data_ptr(), self.scales.data_ptr(), self.num_pages, self.page_size,
                                      self.num_kv_heads, self.head_dim, self.kv_layout, self.k_scale, self.v_scale)
-        self._made()
+        self._made(self.codes, self.scales, self.status)
 
     def append(self, k, v, slot_mapping, k_values=None, v_values=None, stream=None):
         """Quantises the rows k, v [n, num_kv_heads, head_dim] into the slots of slot_mapping (int64 [n]).
@@ -263,7 +266,7 @@ class Kv4Cache(_Object):
                               0 if v_values is None else v_values.data_ptr(), slot_mapping.data_ptr(),
                               self._status_ptr, n,
                               _b.PA_BF16 if k.dtype == torch.bfloat16 else _b.dtype_code(k.dtype))
-        handle, guard = _on(at, stream, (self,), (k, v, slot_mapping, k_values, v_values), self._own)
+        handle, guard = _on(at, stream, (self,), (k, v, slot_mapping, k_values, v_values))
         _call(guard, self._lib.pagedattn_kv4_append, ctypes.byref(self._args), rows, handle)
 
 
@@ -307,7 +310,7 @@ class Kv4Attention(_Object):
             self._ws_ptr = workspace.data_ptr()
             self.status = workspace.view(-1).view(torch.uint8)[:4].view(torch.int32)
             workspace.zero_()
-        self._made()
+        self._made(workspace)
 
     def run(self, q, cache, tables, out=None, lse=None, return_lse=True, stream=None):
         """out, lse of q [num_tokens, num_qo_heads, head_dim] (any token stride that is a multiple of 8).
@@ -342,7 +345,7 @@ class Kv4Attention(_Object):
             _is(out, "out", q.dtype, shape, at)
         if lse is not None:
             _is(lse, "lse", torch.float32, shape[:2], at)
-        handle, guard = _on(at, stream, objects, (q, out, lse, *tables), (cache.codes, cache.scales, self.workspace))
+        handle, guard = _on(at, stream, objects, (q, out, lse, *tables))
         if guard is None:
             return self._launch(q, stride, cache, qo_indptr, page_indptr, pages, last, nnz, out, lse, return_lse, handle)
         with guard:  # the outputs are allocated on the stream that writes them

@@ -1039,3 +1039,33 @@ def test_first_calls_on_another_stream_wait_for_the_objects_memory(by_hand):
     for name in ("qo_indptr", "kv_page_indptr", "new_page_indptr", "kv_page_indices", "kv_last_page_len", "kv_lens",
                  "slot_mapping", "positions", "free_count", "status"):
         assert torch.equal(getattr(t, name), getattr(lists, name)), name
+
+
+@gpu
+def test_memory_outlives_calls_under_another_current_stream():
+    """As test_memory_outlives_calls_on_another_stream, for the objects' own memory under torch.cuda.stream."""
+    z = lambda *s, t=I32: torch.zeros(s, dtype=t, device="cuda")  # noqa: E731
+    B, T, side = 3, 1000, torch.cuda.Stream()
+    tables, cache = pa.BatchTables(B, T, 100, 16, 100), pa.Kv4Cache(100, 16, 2, 64)
+    attention = pa.Kv4Attention(B, T, 4, 2, 64, 16, torch.float16)
+    rows, args = z(T, 2, 64, t=torch.float16), (z(B), z(B), z(B, 1), z(1), z(1))
+    slots = torch.full((T,), -1, dtype=torch.int64, device="cuda")
+    q = z(T, 4, 64, t=torch.float16)
+    held = {tables: "qo_indptr kv_page_indices slot_mapping positions kv_lens status free_count", cache:
+            "codes scales status", attention: "workspace"}
+    ptrs = {getattr(o, n).data_ptr(): getattr(o, n).numel() * getattr(o, n).element_size()
+            for o, names in held.items() for n in names.split()}
+    torch.cuda.synchronize()
+    for cycles in (0, 400_000_000):  # (first calls load kernels and may wait); then a fifth of a second
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(cycles)
+            tables.build(*args)
+            cache.append(rows, rows, slots)
+            attention.run(q, cache, tables)
+        if not cycles:
+            torch.cuda.synchronize()
+    del tables, cache, attention, held
+    again = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in ptrs.values() for _ in range(2)]
+    assert not side.query()  # (else the allocator may rightly give it away)
+    assert not ptrs.keys() & {t.data_ptr() for t in again}
+    torch.cuda.synchronize()
