@@ -276,7 +276,11 @@ class Kv4Attention(_Object):
     num_tokens: rows of q; max_qo_len: a bound of the requests' query lengths
     (default num_tokens), by which the kernels are chosen: pass 1 for decode
     steps.  Holds the workspace, so two runs that overlap on the device need
-    two objects.
+    two objects with a workspace each.
+
+    workspace: None to allocate one; another Kv4Attention, to share its
+    workspace as it stands (and its status word); or a tensor, which is cleared:
+    the constructor then waits for the device before and after.
     """
 
     def __init__(self, batch_size, num_tokens, num_qo_heads, num_kv_heads, head_dim, page_size, dtype, causal=True,
@@ -298,7 +302,11 @@ class Kv4Attention(_Object):
         with torch.cuda.device(self.device):
             _b.check(_b.load().pagedattn_kv4_workspace_size(self.num_qo_heads, self.num_kv_heads, self.head_dim,
                                                             self.max_qo_len, ctypes.byref(need)))
-            if workspace is None:
+            shared = workspace if isinstance(workspace, Kv4Attention) else None
+            given = workspace is not None
+            if shared is not None:
+                workspace = shared.workspace
+            elif not given:
                 workspace = torch.empty(need.value, dtype=torch.uint8, device=self.device)
             if workspace.device != self.device or not workspace.is_contiguous():
                 _refuse(f"workspace must be a contiguous tensor on {self.device}")
@@ -308,8 +316,17 @@ class Kv4Attention(_Object):
                 raise PagedAttnError(_b.PA_ERR_WORKSPACE_TOO_SMALL,
                                      f"workspace needs {need.value} bytes, got {self._ws_bytes}")
             self._ws_ptr = workspace.data_ptr()
-            self.status = workspace.view(-1).view(torch.uint8)[:4].view(torch.int32)
-            workspace.zero_()
+            memory = workspace.view(-1).view(torch.uint8)
+            self.status = memory[:4].view(torch.int32)
+            if shared is not None:
+                self._own, self._streams, self._ready = shared._own, shared._streams, shared._ready
+                return
+            wait = given and not torch.cuda.is_current_stream_capturing()
+            if wait:  # runs in it keep their counts there until they end
+                torch.cuda.synchronize(self.device)
+            memory[:need.value].zero_()
+            if wait:  # the next run in it may be on any stream
+                torch.cuda.current_stream(self.device).synchronize()
         self._made(workspace)
 
     def run(self, q, cache, tables, out=None, lse=None, return_lse=True, stream=None):

@@ -1069,3 +1069,53 @@ def test_memory_outlives_calls_under_another_current_stream():
     assert not side.query()  # (else the allocator may rightly give it away)
     assert not ptrs.keys() & {t.data_ptr() for t in again}
     torch.cuda.synchronize()
+
+
+@gpu
+def test_a_given_workspace_is_cleared_behind_the_runs_in_it():
+    """A run is queued on another stream when an object is made over its workspace: the clearing comes after it, and
+    before that stream's next run."""
+    b = Batch([1], [20_000], 8, 1, 128, 16, "NHD", torch.bfloat16, seed=3)
+    a, side = b.attention(), torch.cuda.Stream()
+    want, want_lse = a.run(b.q, b.cache, b.tables())
+    tables, got = b.tables(), []
+    a.run(b.q, b.cache, tables, stream=side)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+    got.append(a.run(b.q, b.cache, tables, stream=side))
+    other = b.attention(workspace=a.workspace)
+    assert side.query()  # the constructor waited
+    got.append(a.run(b.q, b.cache, tables, stream=side))
+    torch.cuda.synchronize()
+    got.append(other.run(b.q, b.cache, tables))
+    for out, lse in got:
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@gpu
+def test_objects_that_share_a_workspace():
+    """An object in place of a workspace: its memory, its status word and its counts are taken as they are."""
+    bs = [Batch([1, 1], [3000, 900], 8, 1, 128, 16, "NHD", torch.float16, seed=1),
+          Batch([40, 1], [2100, 1900], 16, 2, 128, 16, "NHD", torch.float16, seed=3),
+          Batch([2], [1700], 6, 2, 256, 16, "NHD", torch.bfloat16, seed=4)]
+    want, tables = [b.want() for b in bs], [b.tables() for b in bs]
+    first = bs[0].attention(workspace=torch.empty(256 << 20, dtype=torch.uint8, device="cuda"))
+    bad = tables[0][:3] + (torch.tensor([17, 1], dtype=I32).cuda(),)
+    first.run(bs[0].q, bs[0].cache, bad)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+    objs = [first] + [b.attention(workspace=first) for b in bs[1:]]
+    assert not side.query()  # nothing was waited for
+    assert all(o.workspace is first.workspace for o in objs)
+    assert objs[1].device_status() == pa.PA_DEV_BAD_INDEX and first.device_status() == 0
+    for _ in range(3):
+        for b, a, w, t in zip(bs, objs, want, tables):
+            out, lse = a.run(b.q, b.cache, t)
+            b.check(out, lse, w)
+    small = bs[0].attention()
+    with pytest.raises(pa.PagedAttnError) as e:
+        pa.Kv4Attention(1, 64, 128, 1, 128, 16, torch.float16, workspace=pa.Kv4Attention(1, 1, 1, 1, 64, 16, torch.float16))
+    assert e.value.status == raw.PA_ERR_WORKSPACE_TOO_SMALL and small.device_status() == 0
