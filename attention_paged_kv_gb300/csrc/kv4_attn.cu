@@ -705,18 +705,22 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
         bool some = false;
 #pragma unroll
         for (int k = 0; k < St::VS; ++k) first_nan[k] = INT_MAX;
+        auto scale_at = [&](int i) -> uint8_t* {
+          const int row = 8 * (i >> 1) + (i & 1 ? v_row[1] : v_row[0]);
+          return smem + (st - smem) + St::OFF_VS + row * St::SROW + g * St::VB / 8;
+        };
 #pragma unroll 1
         for (int i = 0; i < 8; ++i) {
-          const int row = 8 * (i >> 1) + (i & 1 ? v_row[1] : v_row[0]);
-          uint8_t* at = smem + (st - smem) + St::OFF_VS + row * St::SROW + g * St::VB / 8;
+          const uint8_t* at = scale_at(i);
 #pragma unroll
           for (int k = 0; k < St::VS; ++k)
             if ((at[k] & 0x7F) == 0x7F) {
               some = true;
-              first_nan[k] = min(first_nan[k], key + row);
-              at[k] = 0;
+              first_nan[k] = min(first_nan[k], key + 8 * (i >> 1) + (i & 1 ? v_row[1] : v_row[0]));
             }
         }
+        // (at head_dim 64 lanes g and g ^ 1 have one byte: both read it before one clears it)
+        __syncwarp();
         if (__any_sync(0xffffffffu, some)) {
 #pragma unroll
           for (int k = 0; k < St::VS; ++k) {
@@ -732,6 +736,13 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
                   for (int j = 8 * k; j < (St::VS == 1 ? D / 16 : 8 * k + 8); ++j)
                     o[nt][j][i] = o[nt][j][i + 2] = __int_as_float(0x7FFFFFFF);
                 }
+          }
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i) {
+            uint8_t* at = scale_at(i);
+#pragma unroll
+            for (int k = 0; k < St::VS; ++k)
+              if ((D > 64 || g % 2 == 0) && (at[k] & 0x7F) == 0x7F) at[k] = 0;
           }
           __syncwarp();
         }

@@ -1119,3 +1119,27 @@ def test_objects_that_share_a_workspace():
     with pytest.raises(pa.PagedAttnError) as e:
         pa.Kv4Attention(1, 64, 128, 1, 128, 16, torch.float16, workspace=pa.Kv4Attention(1, 1, 1, 1, 64, 16, torch.float16))
     assert e.value.status == raw.PA_ERR_WORKSPACE_TOO_SMALL and small.device_status() == 0
+
+
+# ---------------------------------------------------------------- a NaN of V at head_dim 64
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("qo, kv, G", [(4, 70, 2), (3, 33, 1), (5, 97, 3), (8, 64, 4)], ids=str)
+def test_attention_nan_of_v_reaches_its_whole_block_at_head_dim_64(qo, kv, G, dtype):
+    """Two lanes share a scale byte there: both halves of the block's 16 dims get the NaN, whichever key and block."""
+    b = Batch([qo], [kv], 2 * G, 2, 64, 16, "HND", dtype, seed=23)
+    a = b.attention()
+    clean, clean_lse = a.run(b.q, b.cache, b.tables())
+    for key in [kv - 1 - i for i in range(qo + 1)] + [kv - 32, 0]:
+        at = (int(b.pages[key // 16]), 1, slice(None), key % 16)
+        for block in range(4):
+            old = b.cache.scales[at][:, block].clone()
+            b.cache.scales[at][:, block] = 0xFF if block % 2 else 0x7F
+            out, lse = a.run(b.q, b.cache, b.tables())
+            b.cache.scales[at][:, block] = old
+            hit = torch.zeros_like(clean, dtype=torch.bool)
+            hit[max(0, key - (kv - qo)):, :, 16 * block: 16 * block + 16] = True
+            assert torch.equal(torch.isnan(out), hit), (key, block)
+            assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse, clean_lse)
