@@ -94,11 +94,12 @@ pagedattn_status pagedattn_build_tables(const pagedattn_tables_in* in, const pag
   if (in->num_pages < 1) return set_err(PA_ERR_INVALID_ARG, "num_pages must be positive");
   const int shift = page_shift(in->page_size);
   if (shift < 0) return set_err(PA_ERR_UNSUPPORTED, "page_size must be a power of two in [1, 128]");
-  const void* need[] = {in->qo_lens, in->kv_lens, in->block_table, out->kv_last_page_len, out->kv_lens};
+  const void* need[] = {in->qo_lens, in->kv_lens, out->kv_last_page_len, out->kv_lens};
   for (const void* p : need)
     if (in->batch_size > 0 && !p) return set_err(PA_ERR_INVALID_ARG, "a per-request array is NULL");
   if (!in->free_count || !out->free_count || !out->qo_indptr || !out->kv_page_indptr || !out->new_page_indptr ||
-      !out->status || (in->free_capacity > 0 && !in->free_pages) || (out->max_pages > 0 && !out->kv_page_indices) ||
+      !out->status || (in->batch_size > 0 && in->block_table_width > 0 && !in->block_table) ||
+      (in->free_capacity > 0 && !in->free_pages) || (out->max_pages > 0 && !out->kv_page_indices) ||
       (out->max_tokens > 0 && (!out->slot_mapping || !out->positions)))
     return set_err(PA_ERR_INVALID_ARG, "a required array is NULL");
   if (!aligned(out->slot_mapping, 8)) return set_err(PA_ERR_INVALID_ARG, "slot_mapping must be 8-byte aligned");

@@ -1143,3 +1143,16 @@ def test_attention_nan_of_v_reaches_its_whole_block_at_head_dim_64(qo, kv, G, dt
             hit[max(0, key - (kv - qo)):, :, 16 * block: 16 * block + 16] = True
             assert torch.equal(torch.isnan(out), hit), (key, block)
             assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse, clean_lse)
+
+
+@gpu
+@pytest.mark.parametrize("B", [3, 3500])
+def test_tables_of_width_zero(B):
+    """A block table without columns holds requests without pages, and no token."""
+    z = lambda *s: torch.zeros(s, dtype=I32, device="cuda")  # noqa: E731
+    t, qo = pa.BatchTables(B, 4, 8, 16, 10), z(B)
+    t.build(qo, z(B), z(B, 0), z(2), z(1))
+    assert t.device_status() == 0 and not t.kv_page_indptr.any() and (t.slot_mapping == -1).all()
+    qo[1] = 1
+    t.build(qo, z(B), z(B, 0), z(2), z(1) + 2)
+    assert t.device_status() == raw.PA_DEV_NO_ROOM and not t.qo_indptr.any()
