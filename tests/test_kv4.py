@@ -1156,3 +1156,38 @@ def test_tables_of_width_zero(B):
     qo[1] = 1
     t.build(qo, z(B), z(B, 0), z(2), z(1) + 2)
     assert t.device_status() == raw.PA_DEV_NO_ROOM and not t.qo_indptr.any()
+
+
+# ---------------------------------------------------------------- the structures' two descriptions
+
+
+@pytest.mark.parametrize("packed, struct, values", [
+    ("_TABLES_IN", "TablesIn", [11, 12, 13, 14, 15, 1 << 40, 7, 6, 5, 16, 9]),
+    ("_KV4_ROWS", "Kv4Rows", [11, 12, 1 << 40, 1 << 41, 13, 14, 15, 16, 3, 1]),
+    ("_KV4_BATCH", "Kv4Batch", [11, 12, 13, 14, 2, 8, 5, 4, 64, 1, 1])])
+def test_packed_arguments_are_the_structures(packed, struct, values):
+    """The calls pack their arguments' bytes; the binding's structures, which the refusals are tested with, hold the same."""
+    from attention_paged_kv_gb300 import _kv4
+    cls = getattr(raw, struct)
+    assert len(values) == len(cls._fields_) and getattr(_kv4, packed).size == ctypes.sizeof(cls)
+    assert getattr(_kv4, packed).pack(*values) == bytes(cls(*values))
+
+
+@pytest.mark.parametrize("struct, name", [("TablesIn", "tables_in"), ("TablesOut", "tables_out"), ("Kv4Rows", "kv4_rows"),
+                                          ("Kv4CacheArgs", "kv4_cache"), ("Kv4Batch", "kv4_batch")])
+def test_structures_are_the_headers(struct, name):
+    """Field by field, in order, with the header's types."""
+    import os
+    import re
+    path = os.path.join(os.path.dirname(os.path.dirname(pa.LIB_PATH)), "include", "pagedattn.h")
+    text = re.sub(r"/\*.*?\*/", "", open(path).read(), flags=re.S)
+    body = re.search(r"typedef struct \{([^}]*)\} pagedattn_%s;" % name, text).group(1)
+    want = []
+    for line in filter(None, (x.strip() for x in body.split(";"))):
+        kind, names = re.match(r"(?:const )?(\w+)\s*(.*)", line, re.S).groups()
+        for n in (x.strip() for x in names.split(",")):
+            ctype = ctypes.c_void_p if n.startswith("*") else {
+                "int32_t": ctypes.c_int32, "int64_t": ctypes.c_int64, "float": ctypes.c_float,
+                "pagedattn_dtype": ctypes.c_int}[kind]
+            want.append((n.lstrip("* "), ctype))
+    assert getattr(raw, struct)._fields_ == want
