@@ -283,6 +283,8 @@ pagedattn_status pagedattn_kv4_run(const pagedattn_kv4_cache* cache, const paged
   p.v_scale = cache->v_scale;
   cudaError_t e = cudaSuccess;
   if (prefill) e = pa::launch_kv4_prefill(p, shape, batch->dtype, reinterpret_cast<cudaStream_t>(stream));
+  if (e == cudaErrorLaunchOutOfResources)  // what the launcher returns where the build's registers differ
+    return cuda_err(e, "4-bit prefill launch (are the built kernel's registers those that its warps hand over?)");
   if (e != cudaSuccess) return cuda_err(e, "4-bit prefill launch");
   e = pa::launch_kv4_attention(p, shape, batch->dtype, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_err(e, "4-bit attention launch");

@@ -1191,3 +1191,23 @@ def test_structures_are_the_headers(struct, name):
                 "pagedattn_dtype": ctypes.c_int}[kind]
             want.append((n.lstrip("* "), ctype))
     assert getattr(raw, struct)._fields_ == want
+
+
+def test_built_prefill_kernels_have_the_registers_they_hand_over():
+    """The warps' shares after the hand-over add up to what the launch gives (two row tiles 128 a thread, one 80)."""
+    import os
+    import re
+    log = os.path.join(os.path.dirname(pa.LIB_PATH), "_build", "kv4_prefill.cu.o.log")
+    if not os.path.exists(log):
+        pytest.skip("the build's log is not there")
+    name, seen = None, {}
+    for line in open(log):
+        name = (re.search(r"Compiling entry function '(\S+)'", line) or [None, name])[1]
+        used = re.search(r"Used (\d+) registers", line)
+        if used and "kv4_prefill_kernel" in name:
+            D, NT = map(int, re.search(r"Li(\d+)ELi(\d)EE", name).groups())
+            seen.setdefault((D, NT), set()).add(int(used[1]))
+    assert seen.keys() == {(64, 1), (64, 2), (128, 1), (128, 2), (256, 1)}
+    for (D, NT), regs in seen.items():
+        if D < 256:
+            assert regs == {128 if NT == 2 else 80}, (D, NT)
