@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(SmallCfg<D, NT>::THREADS, SmallCfg<D, NT>::CTA
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int up = bf16_row_shift(top);
         const float mul = pow2(up);
-        my = row_factor(my, up);
+        my = row_factor(my, pow2(-up));
 #pragma unroll
         for (int j = 0; j < D / 16; ++j)
 #pragma unroll

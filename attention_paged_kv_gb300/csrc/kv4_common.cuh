@@ -88,8 +88,8 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cas
 // logits are below 2^-92 either way.  Above, it would be infinite, and a NaN
 // for scores of 0; the logits of other scores pass 2^93 either way, and the
 // largest alone counts (or passes fp32's range).
-__device__ __forceinline__ float row_factor(float scale_log2, int up) {
-  return fminf(fmaxf(scale_log2 * pow2(-up), FLT_MIN), FLT_MAX);
+__device__ __forceinline__ float row_factor(float scale_log2, float down) {  // down = 2^-up
+  return fminf(fmaxf(scale_log2 * down, FLT_MIN), FLT_MAX);
 }
 
 // n / G and n % G for n < 512 (G <= 128): G's reciprocal in 16 bits, rounded up

@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, PreCfg<D, NT>::CTAS) k
   __shared__ long long work_s;
   __shared__ Req found_rq;
   __shared__ int any_nan, first_nan[D / 16];     // first key whose V has a NaN there, of the tiles that some row sees in part
-  __shared__ float fac_s[NT * kQRows];  // bf16: the rows' logit factors
+  __shared__ float fac_s[NT * kQRows];  // bf16: the rows' powers of two, inverted
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* full_k = bars;             // [NST] K tile written
@@ -577,7 +577,7 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, PreCfg<D, NT>::CTAS) k
             for (int d2 = 1; d2 < LPR; d2 <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, d2));
             const int up = bf16_row_shift(max(m & 0xFFFFu, m >> 16));
             const float mul = pow2(up);
-            if (c == 0) fac_s[x * kQRows + rr] = row_factor(p.scale_log2, up);
+            if (c == 0) fac_s[x * kQRows + rr] = pow2(-up);
             uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(PreCfg<D, NT>::THREADS, PreCfg<D, NT>::CTAS) k
       }
       if constexpr (Elt<T>::kBf16) {
         __syncwarp();
-        sl2 = fac_s[x * kQRows + r];
+        sl2 = row_factor(sl2, fac_s[x * kQRows + r]);
       }
     }
     fence_proxy_async_smem();
