@@ -12,7 +12,8 @@ A step of a serving loop, with no length on the host:
 
 All three calls only launch kernels, so the step can be captured into a CUDA
 graph; `tables.build(qo_lens, tables.kv_lens, block_table, free_pages,
-tables.free_count)` then advances the lengths in place at each replay.
+tables.free_count)` then advances the lengths in place at each replay.  The
+objects (and the tensors of the calls) have to live as long as such a graph.
 """
 from __future__ import annotations
 
@@ -275,7 +276,8 @@ class Kv4Attention(_Object):
 
     num_tokens: rows of q; max_qo_len: a bound of the requests' query lengths
     (default num_tokens), by which the kernels are chosen: pass 1 for decode
-    steps.  Holds the workspace, so two runs that overlap on the device need
+    steps.  (A longer request is computed too, slower, but with max_qo_len <= 1
+    its rows may share a NaN of K or V that only some of them see.)  Holds the workspace, so two runs that overlap on the device need
     two objects with a workspace each.
 
     workspace: None to allocate one; another Kv4Attention, to share its
@@ -333,7 +335,10 @@ class Kv4Attention(_Object):
         """out, lse of q [num_tokens, num_qo_heads, head_dim] (any token stride that is a multiple of 8).
 
         tables: a BatchTables, or (qo_indptr, kv_page_indptr, kv_page_indices,
-        kv_last_page_len) as int32 device tensors.  See pagedattn_kv4_run.
+        kv_last_page_len) as int32 device tensors.  out must not overlap q.  The
+        size of kv_page_indices (a BatchTables' max_pages) helps to choose the
+        kernels: one far above the pages in use costs short prompts time.  See
+        pagedattn_kv4_run.
         """
         import torch
         at, B, shape = self._index, self.batch_size, self._shape

@@ -99,9 +99,14 @@ Kv4Layout kv4_layout(const Kv4Shape& s);
 // Rows of partial states that the prefill kernel may write.
 int64_t kv4_prefill_part_rows(const Kv4Shape& s);
 
-// Requests of more packed rows than this go to the tensor-core kernel (64
-// drafting requests of 24 or 32 rows: 146 and 149 us here, 235 and 245 there; of
-// 64 rows 217 there).
+// Requests of more packed rows than this go to the tensor-core kernel.  us, the
+// small-query kernel / that one, 64 requests of 512 to 8192 keys at 64 / 8 heads:
+//   rows    head_dim 64   128         256
+//   16       70 / 179     114 / 233   229 / 476
+//   24      100 / 179     149 / 233   329 / 479
+//   32      104 / 171     152 / 223   430 / 464
+// and 64 requests of 128 to 512 keys with 32 rows at head_dim 128 48 / 37, with
+// 16 rows 21 / 38: the one place where it would be the other way round.
 constexpr int kKv4SmallRows = 32;
 
 cudaError_t launch_kv4_prefill(const Kv4Params& p, const Kv4Shape& s, int dtype, cudaStream_t stream);

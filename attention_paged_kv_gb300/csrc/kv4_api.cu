@@ -266,6 +266,8 @@ pagedattn_status pagedattn_kv4_run(const pagedattn_kv4_cache* cache, const paged
   const int64_t most = (key_units * tiles + 3) / 4;
   p.slices = most < lay.slices ? int32_t(most) : lay.slices;
   p.cta_heads = lay.cta_heads;
+  // (both rules below go by the size of the page list, all that the host knows
+  // of the keys: a list far larger than the pages in use costs time, see the header)
   // requests of few keys are not worth cutting: the CTAs for it would only
   // lengthen the launch (tables of 8 key tiles a request on average, or more)
   p.num_sms = shape.num_sms;

@@ -898,7 +898,7 @@ cudaError_t launch_small(const Kv4Params& p, cudaStream_t stream) {
 }
 
 // One token a request, the commonest batch by far, does without the scrubbing
-// (256 decodes 250 us, with it 253).
+// (256 decodes 250 us, with it 253; 64 x 4 drafts 149 without, 152 with).
 template <typename T, int D, int NT>
 cudaError_t launch_nt(const Kv4Params& p, const Kv4Shape& s, cudaStream_t stream) {
   return p.causal && s.max_rows > s.G ? launch_small<T, D, NT, true>(p, stream)

@@ -28,11 +28,13 @@
 // Per key tile j it issues PV_A(j), S_A(j+1), PV_B(j), S_B(j+1): one tile's
 // MMAs run while the other tile's rows are in their softmax.
 //
-// What bounds it: 2000 tokens behind 6000 at 64 / 8 heads take 369 us, 1244
-// TFLOP/s; the tensor pipe is busy 54 % of the time and a pair of row tiles
-// takes 1.68 us a key tile, softmax and MMAs waiting for one another.  32
-// prompts of up to 200 tokens at 32 / 8 heads take 38 us (41 a call), most of
-// it the set-up, first loads and epilogue of items with one or two key tiles.
+// What bounds it: 2000 tokens behind 6000 at 64 / 8 heads take 360 to 367 us,
+// 1250 to 1275 TFLOP/s; the tensor pipe is busy 54 % of the time and a pair of row
+// tiles takes 1.68 us a key tile, softmax and MMAs waiting for one another.  32
+// prompts of up to 200 tokens at 32 / 8 heads take 38 us, most of it the set-up,
+// first loads and epilogue of items with one or two key tiles.  At head_dim 256,
+// with one K and one V stage and one row tile, the same chunk (at 32 / 4 heads)
+// takes 608 us, 755 TFLOP/s.
 //
 // TMEM: S_x (fp32 128 x 128) at 128 x, O_x (fp32 128 x D) after them; P_x
 // overwrites the first 64 columns of S_x.

@@ -468,7 +468,11 @@ typedef struct {
   const int32_t* kv_page_indptr;   /* [batch_size + 1]                                    */
   const int32_t* kv_page_indices;  /* [num_page_indices]                                  */
   const int32_t* kv_last_page_len; /* [batch_size]                                        */
-  int32_t batch_size, num_page_indices;
+  int32_t batch_size;
+  int32_t num_page_indices;        /* entries of kv_page_indices; also the host's only bound of
+                                      the batch's keys, by which the kernels are chosen: with
+                                      one far larger than the pages in use the results are as
+                                      exact, but short prompts take up to half as long again */
   int32_t num_tokens;              /* rows of q, out and lse, >= qo_indptr[batch_size]    */
   int32_t max_qo_len;              /* bound of the requests' query lengths: chooses the
                                       kernels (a longer request is computed too, slower;
@@ -487,9 +491,10 @@ PAGEDATTN_API pagedattn_status pagedattn_kv4_workspace_size(int32_t num_qo_heads
  * num_qo_heads / num_kv_heads up to 128; any lengths.  A row that sees no key
  * (kv_len 0, or causal with qo_len > kv_len) gets zeros and lse = -inf.  A NaN
  * of K or V reaches the rows that see its key and no others, except that with
- * max_qo_len <= 1 the rows of a longer request may share their NaN.  Rows
- * of q from qo_indptr[batch_size] on are not read, and rows of out and lse
- * not written.
+ * max_qo_len <= 1 the rows of a longer request may share their NaN.  Logits
+ * have to stay within fp32's range; values of a bf16 row of q are off by at most
+ * 2^-38 of the row's largest.  Rows of q from qo_indptr[batch_size] on are not
+ * read, and rows of out and lse not written.
  *
  * q         device, dtype[num_tokens][num_qo_heads][head_dim], tokens q_stride
  *           elements apart (a multiple of 8), 16-byte aligned.
