@@ -65,14 +65,15 @@ def _on(index, stream, objects, tensors=()):
         handle = current
     else:
         handle = int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
-    for o in objects:
-        if handle not in o._streams:
-            o._enter(handle)
     if handle != current:
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(handle, device=index)
         if stream.device.index != index:
             _refuse(f"the stream is not one of cuda:{index}")
+    for o in objects:
+        if handle not in o._streams:
+            o._enter(handle)
+    if handle != current:
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
@@ -109,7 +110,8 @@ class _Object:
     wait: what it captures has to be replayed after the initialisation, as it is
     where the capture began with a wait for the device.  The memory of an object
     made under capture is initialised by each replay, and the object belongs to
-    that graph.)
+    that graph.)  What a program itself does with the object's tensors on
+    another stream it has to order, as with any tensor.
     """
 
     def _made(self, *own):
@@ -277,12 +279,14 @@ class Kv4Attention(_Object):
     num_tokens: rows of q; max_qo_len: a bound of the requests' query lengths
     (default num_tokens), by which the kernels are chosen: pass 1 for decode
     steps.  (A longer request is computed too, slower, but with max_qo_len <= 1
-    its rows may share a NaN of K or V that only some of them see.)  Holds the workspace, so two runs that overlap on the device need
-    two objects with a workspace each.
+    its rows may share a NaN of K or V that only some of them see.)  Holds the
+    workspace, so two runs that overlap on the device need two objects with a
+    workspace each.
 
     workspace: None to allocate one; another Kv4Attention, to share its
     workspace as it stands (and its status word); or a tensor, which is cleared:
-    the constructor then waits for the device before and after.
+    the constructor then waits for the device before and after (under capture
+    the clearing becomes part of the graph instead).
     """
 
     def __init__(self, batch_size, num_tokens, num_qo_heads, num_kv_heads, head_dim, page_size, dtype, causal=True,

@@ -1106,7 +1106,7 @@ def test_objects_that_share_a_workspace():
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
     with torch.cuda.stream(side):
-        torch.cuda._sleep(200_000_000)
+        torch.cuda._sleep(1_000_000_000)
     objs = [first] + [b.attention(workspace=first) for b in bs[1:]]
     assert not side.query()  # nothing was waited for
     assert all(o.workspace is first.workspace for o in objs)
