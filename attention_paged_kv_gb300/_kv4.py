@@ -123,6 +123,37 @@ class _Object:
                 self._ready = torch.cuda.Event()
                 self._ready.record()
 
+    def _take_workspace(self, workspace, need, kind):
+        """``workspace``: None to allocate `need` bytes, another object of class `kind` (shared as it stands, its status
+        word too) or a tensor, which is cleared.  To be called with the object's device current."""
+        import torch
+        shared = workspace if isinstance(workspace, kind) else None
+        given = workspace is not None
+        if shared is not None:
+            workspace = shared.workspace
+        elif not given:
+            workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+        if workspace.device != self.device or not workspace.is_contiguous():
+            _refuse(f"workspace must be a contiguous tensor on {self.device}")
+        self.workspace = workspace
+        self._ws_bytes = workspace.numel() * workspace.element_size()
+        if self._ws_bytes < need:
+            raise PagedAttnError(_b.PA_ERR_WORKSPACE_TOO_SMALL,
+                                 f"workspace needs {need} bytes, got {self._ws_bytes}")
+        self._ws_ptr = workspace.data_ptr()
+        memory = workspace.view(-1).view(torch.uint8)
+        self.status = memory[:4].view(torch.int32)
+        if shared is not None:
+            self._own, self._streams, self._ready = shared._own, shared._streams, shared._ready
+            return
+        wait = given and not torch.cuda.is_current_stream_capturing()
+        if wait:  # runs in it keep their counts there until they end
+            torch.cuda.synchronize(self.device)
+        memory[:need].zero_()
+        if wait:  # the next run in it may be on any stream
+            torch.cuda.current_stream(self.device).synchronize()
+        self._made(workspace)
+
     def _enter(self, handle):
         import torch
         stream = torch.cuda.ExternalStream(handle, device=self._index)
@@ -308,32 +339,7 @@ class Kv4Attention(_Object):
         with torch.cuda.device(self.device):
             _b.check(_b.load().pagedattn_kv4_workspace_size(self.num_qo_heads, self.num_kv_heads, self.head_dim,
                                                             self.max_qo_len, ctypes.byref(need)))
-            shared = workspace if isinstance(workspace, Kv4Attention) else None
-            given = workspace is not None
-            if shared is not None:
-                workspace = shared.workspace
-            elif not given:
-                workspace = torch.empty(need.value, dtype=torch.uint8, device=self.device)
-            if workspace.device != self.device or not workspace.is_contiguous():
-                _refuse(f"workspace must be a contiguous tensor on {self.device}")
-            self.workspace = workspace
-            self._ws_bytes = workspace.numel() * workspace.element_size()
-            if self._ws_bytes < need.value:
-                raise PagedAttnError(_b.PA_ERR_WORKSPACE_TOO_SMALL,
-                                     f"workspace needs {need.value} bytes, got {self._ws_bytes}")
-            self._ws_ptr = workspace.data_ptr()
-            memory = workspace.view(-1).view(torch.uint8)
-            self.status = memory[:4].view(torch.int32)
-            if shared is not None:
-                self._own, self._streams, self._ready = shared._own, shared._streams, shared._ready
-                return
-            wait = given and not torch.cuda.is_current_stream_capturing()
-            if wait:  # runs in it keep their counts there until they end
-                torch.cuda.synchronize(self.device)
-            memory[:need.value].zero_()
-            if wait:  # the next run in it may be on any stream
-                torch.cuda.current_stream(self.device).synchronize()
-        self._made(workspace)
+            self._take_workspace(workspace, need.value, Kv4Attention)
 
     def run(self, q, cache, tables, out=None, lse=None, return_lse=True, stream=None):
         """out, lse of q [num_tokens, num_qo_heads, head_dim] (any token stride that is a multiple of 8).
