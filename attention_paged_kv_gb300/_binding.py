@@ -48,7 +48,9 @@ EXPORTED = ("pagedattn_plan", "pagedattn_workspace_size", "pagedattn_run", "page
             "pagedattn_debug_plan_dump", "pagedattn_debug_gather", "pagedattn_version",
             "pagedattn_run_decode_noalloc", "pagedattn_noalloc_device_status", "pagedattn_plan_cascade",
             "pagedattn_workspace_size_cascade", "pagedattn_build_tables", "pagedattn_kv4_append",
-            "pagedattn_kv4_workspace_size", "pagedattn_kv4_run", "pagedattn_status_word")
+            "pagedattn_kv4_workspace_size", "pagedattn_kv4_run", "pagedattn_status_word", "pagedattn_rope",
+            "pagedattn_kv_append", "pagedattn_kv_bounds", "pagedattn_blocks_workspace_size",
+            "pagedattn_select_blocks", "pagedattn_blocks_run")
 
 
 class PagedAttnError(RuntimeError):
@@ -105,6 +107,43 @@ class Kv4Batch(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("qo_indptr", "kv_page_indptr", "kv_page_indices", "kv_last_page_len")] + \
         [(n, ctypes.c_int32) for n in ("batch_size", "num_page_indices", "num_tokens", "max_qo_len", "num_qo_heads",
                                        "causal")] + [("dtype", ctypes.c_int)]
+
+
+class Rotation(ctypes.Structure):
+    """pagedattn_rotation"""
+    _fields_ = [("turns", ctypes.c_void_p), ("axes", ctypes.c_void_p)] + \
+        [(n, ctypes.c_int32) for n in ("num_axes", "rotary_dim", "interleaved")] + [("scale", ctypes.c_float)]
+
+
+class RopeRows(ctypes.Structure):
+    """pagedattn_rope_rows"""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "q_out", "k_out")] + \
+        [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "q_out_stride", "k_out_stride")] + \
+        [("positions", ctypes.c_void_p), ("position_stride", ctypes.c_int64)] + \
+        [(n, ctypes.c_int32) for n in ("num_tokens", "num_q_heads", "num_k_heads", "head_dim", "inverse")] + \
+        [("dtype", ctypes.c_int)]
+
+
+class KvCacheArgs(ctypes.Structure):
+    """pagedattn_kv_cache"""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("data", "bounds", "bound_scales")] + \
+        [(n, ctypes.c_int32) for n in ("num_pages", "page_size", "num_kv_heads", "head_dim", "kv_layout")] + \
+        [("dtype", ctypes.c_int)]
+
+
+class KvRows(ctypes.Structure):
+    """pagedattn_kv_rows"""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "q", "q_out")] + \
+        [(n, ctypes.c_int64) for n in ("k_stride", "v_stride", "q_stride", "q_out_stride")] + \
+        [("slot_mapping", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("position_stride", ctypes.c_int64),
+         ("status", ctypes.c_void_p), ("num_tokens", ctypes.c_int32), ("num_qo_heads", ctypes.c_int32)]
+
+
+class BlockBatch(ctypes.Structure):
+    """pagedattn_block_batch"""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("qo_indptr", "kv_page_indptr", "kv_page_indices", "kv_last_page_len")] + \
+        [(n, ctypes.c_int32) for n in ("batch_size", "num_page_indices", "num_tokens", "num_qo_heads", "num_blocks",
+                                       "first", "last", "max_pages")]
 
 
 class PrefixGroups(ctypes.Structure):
@@ -177,6 +216,21 @@ def load() -> ctypes.CDLL:
                                           ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                           ctypes.c_size_t, ctypes.c_void_p]
         lib.pagedattn_kv4_run.restype = ctypes.c_int
+        lib.pagedattn_rope.argtypes = [ctypes.c_void_p] * 3
+        lib.pagedattn_rope.restype = ctypes.c_int
+        lib.pagedattn_kv_append.argtypes = [ctypes.c_void_p] * 4
+        lib.pagedattn_kv_append.restype = ctypes.c_int
+        lib.pagedattn_kv_bounds.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                            ctypes.c_void_p]
+        lib.pagedattn_kv_bounds.restype = ctypes.c_int
+        lib.pagedattn_blocks_workspace_size.argtypes = [ctypes.c_int32] * 6 + [ctypes.POINTER(ctypes.c_size_t)]
+        lib.pagedattn_blocks_workspace_size.restype = ctypes.c_int
+        lib.pagedattn_select_blocks.argtypes = [ctypes.c_void_p] * 3 + [ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
+                                                                        ctypes.c_size_t, ctypes.c_void_p]
+        lib.pagedattn_select_blocks.restype = ctypes.c_int
+        lib.pagedattn_blocks_run.argtypes = [ctypes.c_void_p] * 4 + [ctypes.c_int64] + [ctypes.c_void_p] * 3 + \
+            [ctypes.c_size_t, ctypes.c_void_p]
+        lib.pagedattn_blocks_run.restype = ctypes.c_int
         lib.pagedattn_status_word.argtypes = [ctypes.c_void_p, ctypes.c_void_p, _I32P]
         lib.pagedattn_status_word.restype = ctypes.c_int
         lib.pagedattn_version.argtypes = []

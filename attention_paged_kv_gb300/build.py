@@ -19,7 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpagedattn.so")
 SOURCES = ["api.cu", "plan.cpp", "prefill.cu", "decode.cu", "noalloc.cu", "tables.cu", "kv4_api.cu", "kv4_append.cu",
-           "kv4_attn.cu", "kv4_prefill.cu"]
+           "kv4_attn.cu", "kv4_prefill.cu", "paged_api.cu", "rows.cu", "select.cu", "block_attn.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -40,7 +40,8 @@ def build(verbose: bool = False, force: bool = False) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
     nvcc = nvcc_path()
     srcs = [os.path.join(CSRC, s) for s in SOURCES]
-    deps = srcs + [os.path.join(CSRC, h) for h in ("common.cuh", "internal.h", "layout.h", "kv4.h", "kv4_common.cuh")] + \
+    deps = srcs + [os.path.join(CSRC, h) for h in ("common.cuh", "internal.h", "layout.h", "kv4.h", "kv4_common.cuh", "checks.h",
+                                                    "paged.h", "paged_common.cuh")] + \
         [os.path.join(ROOT, "include", "pagedattn.h")]
     if not force and os.path.exists(LIB):
         newest = max(os.path.getmtime(d) for d in deps)

@@ -1,0 +1,398 @@
+// Attention of each query over the pages on its list (pagedattn_blocks_run).
+//
+// Work.  An item is one query token and kv head (up to 16 of the group's heads,
+// 8 at head_dim 256): its rows share every key.  A CTA takes an item, or where
+// items are few a slice of its list; slices leave fp32 partial states that the
+// last of them joins.  The CTA's warps take every fourth tile of 16 keys each
+// and copy their own keys ahead (cp.async into a ring of their own), so that no
+// warp waits for another until their states are joined at the end.
+//
+// S^T = K q^T and O^T = V^T P^T with m16n8k16: keys (or head dims) fill the
+// 16-row side and the heads the other.  P is 2^(logit - m) with the reference m
+// set 7 below the largest logit, in log2 units, and set again when a logit
+// passes it by 15: a row's largest P lies in [2^7, 2^15], and the keys' ones
+// down to 2^-21 of it are rounded like it.  P is rounded to fp16 for fp16
+// values (2^-12 of it at most); for bf16, where that would be 2^-9, it is split
+// in two bf16 terms and multiplied twice.
+#include <climits>
+#include <cstring>
+
+#include "internal.h"
+#include "paged_common.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kTile = 16;  // keys
+constexpr float kNone = -3.0e38f;  // a maximum before any key: finite, so that it can be subtracted
+constexpr float kHead = 7.f, kMost = 15.f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int D, int NT>
+struct Cfg {
+  static constexpr int ROWS = 8 * NT;
+  static constexpr int ROW = 2 * D;                  // bytes of a key's row
+  static constexpr int STAGE = 2 * kTile * ROW;      // K, then V
+  static constexpr int STAGES = D == 64 ? 4 : 3;
+  static constexpr int RING = STAGES * STAGE;        // of a warp
+  static constexpr int CTAS = D == 64 ? 3 : (D == 128 ? 2 : 1);
+  static constexpr int SMEM = kWarps * RING;         // the list comes behind
+  static constexpr int O_STRIDE = D + 4;             // floats of a row of a warp's state, in its ring's place
+  static_assert(ROWS * (O_STRIDE + 2) * 4 <= RING, "a warp's state fits its ring");
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
+}
+template <bool kTrans>
+__device__ __forceinline__ void ldmatrix(uint32_t (&r)[4], uint32_t at) {
+  if constexpr (kTrans)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (Elt<T>::kBf16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Row `row` of a state: its four columns from `col` on as 16-bit values.
+template <typename T>
+__device__ __forceinline__ void store4(void* out, int64_t row, int D, int col, float4 v, float inv) {
+  *reinterpret_cast<uint2*>(static_cast<T*>(out) + row * D + col) =
+      make_uint2(Elt<T>::from_f2(v.x * inv, v.y * inv), Elt<T>::from_f2(v.z * inv, v.w * inv));
+}
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attend_kernel(const BlockParams p) {
+  using C = Cfg<D, NT>;
+  constexpr int CH = D / 8, RPI = 32 / CH;  // 16-byte pieces of a row; rows that a warp copies at a time
+  constexpr int KS = D / 16;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int count_s[2][kWarps];
+  __shared__ int last_s;
+  int32_t* list = reinterpret_cast<int32_t*>(smem + C::SMEM);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+  const int chunks = (p.G + C::ROWS - 1) / C::ROWS;
+  const int slice = blockIdx.x % p.slices, item = blockIdx.x / p.slices;
+  const int chunk = item % chunks, h = item / chunks % p.g.Hkv, t = item / (chunks * p.g.Hkv);
+  const int heads = min(C::ROWS, p.G - chunk * C::ROWS);
+  pdl_wait();
+
+  // ---- the list: page ids of the blocks that the query sees, its own block marked by the top bit
+  const int32_t* blocks = p.blocks + (static_cast<int64_t>(t) * p.g.Hkv + h) * p.num_blocks;
+  int e = tid < p.num_blocks ? blocks[tid] : -1;  // (in flight beside the tables)
+  const Query mine = find_query(p, t);
+  if (!mine.there) return;
+  const int64_t q_row = static_cast<int64_t>(t) * p.Hq + h * p.G + chunk * C::ROWS;  // in out and lse
+  uint32_t qf[NT][KS][2];
+  {
+    const T* q = static_cast<const T*>(p.q) + t * p.q_stride + (static_cast<int64_t>(h) * p.G + chunk * C::ROWS) * D;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const bool real = n * 8 + g < heads;
+      const uint32_t* row = reinterpret_cast<const uint32_t*>(q + (real ? n * 8 + g : 0) * D) + t4;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        qf[n][k][0] = real ? row[k * 8] : 0u;
+        qf[n][k][1] = real ? row[k * 8 + 4] : 0u;
+      }
+    }
+  }
+  const int own = mine.pos < 0 ? -1 : mine.pos >> p.g.ps_shift, limit = mine.pos & (p.g.ps - 1);
+  int count = 0;
+  for (int i0 = 0, turn = 0; i0 < p.num_blocks; i0 += kThreads, turn ^= 1) {
+    if (i0) e = i0 + tid < p.num_blocks ? blocks[i0 + tid] : -1;
+    if (e >= mine.pages) atomicOr(p.status, PA_DEV_BAD_INDEX);
+    const bool seen = e >= 0 && e <= own;
+    const int id = seen ? page_of(p, mine.page_start + e) : 0;
+    const unsigned m = __ballot_sync(0xffffffffu, seen);
+    if (lane == 0) count_s[turn][warp] = __popc(m);
+    __syncthreads();
+    int at = count + __popc(m & ((1u << lane) - 1));
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) at += count_s[turn][w];
+      count += count_s[turn][w];
+    }
+    if (seen) list[at] = id | (e == own ? INT_MIN : 0);
+  }
+  __syncthreads();
+  const int lo = static_cast<int>(static_cast<int64_t>(count) * slice / p.slices);
+  const int entries = static_cast<int>(static_cast<int64_t>(count) * (slice + 1) / p.slices) - lo;
+  list += lo;
+
+  // ---- the warp's tiles
+  const int keys = entries << p.g.ps_shift;
+  const int tiles = (keys + kTile - 1) / kTile;
+  const uint32_t ring = smem_u32(smem) + warp * C::RING;
+  const int64_t v_off = static_cast<int64_t>(p.g.ps) * p.g.Hkv * C::ROW;
+  const int64_t slot_bytes = static_cast<int64_t>(p.g.slot_rows) * C::ROW;
+  const uint8_t* data = static_cast<const uint8_t*>(p.data) + static_cast<int64_t>(h) * p.g.head_rows * C::ROW + lane % CH * 16;
+  // where key i of the slice lies, and whether the query sees it
+  auto entry_of = [&](int i) { return list[min(i >> p.g.ps_shift, entries - 1)]; };
+  auto seen = [&](int i, int word) { return i < keys && (word >= 0 || (i & (p.g.ps - 1)) <= limit); };
+  auto copy = [&](int tile, int stage) {
+    if (tile < tiles) {
+      const uint32_t dst = ring + stage * C::STAGE;
+#pragma unroll
+      for (int i = 0; i < kTile / RPI; ++i) {
+        const int r = i * RPI + lane / CH, k = tile * kTile + r;
+        const int word = entry_of(k);
+        const uint32_t bytes = seen(k, word) ? 16 : 0;
+        const uint8_t* src = data + static_cast<int64_t>(word & INT_MAX) * (2 * v_off) + (k & (p.g.ps - 1)) * slot_bytes;
+        const uint32_t at = dst + r * C::ROW + ((lane % CH) ^ (r & 7)) * 16;
+        cp_async16(at, src, bytes);
+        cp_async16(at + kTile * C::ROW, src + v_off, bytes);
+      }
+    }
+    cp_async_commit();
+  };
+  float o[NT][KS][4], m[NT][2], l[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    m[n][0] = m[n][1] = kNone;
+    l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[n][k][i] = 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < C::STAGES - 1; ++i) copy(warp + i * kWarps, i);
+  int stage = 0;
+  for (int tile = warp; tile < tiles; tile += kWarps) {
+    cp_async_wait<C::STAGES - 2>();
+    __syncwarp();
+    copy(tile + (C::STAGES - 1) * kWarps, stage == 0 ? C::STAGES - 1 : stage - 1);
+    const uint32_t at = ring + stage * C::STAGE;
+    stage = stage == C::STAGES - 1 ? 0 : stage + 1;
+    float s[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      uint32_t a[4];
+      ldmatrix<false>(a, at + (lane & 15) * C::ROW + ((2 * k + (lane >> 4)) ^ (lane & 7)) * 16);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma<T>(s[n], a, qf[n][k][0], qf[n][k][1]);
+    }
+    const int k0 = tile * kTile + g;
+    const bool see0 = seen(k0, entry_of(k0)), see1 = seen(k0 + 8, entry_of(k0 + 8));
+    bool over = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[n][i] = (i < 2 ? see0 : see1) ? s[n][i] * p.scale_log2 : -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) over = over || fmaxf(s[n][i], s[n][i + 2]) > m[n][i] + kMost;
+    }
+    if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float top = fmaxf(s[n][i], s[n][i + 2]);
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+          if (top > m[n][i] + kMost) {
+            const float f = ex2(m[n][i] - (top - kHead));
+            m[n][i] = top - kHead;
+            l[n][i] *= f;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+              o[n][k][i] *= f;
+              o[n][k][i + 2] *= f;
+            }
+          }
+        }
+      }
+    }
+    uint32_t b[NT][2], b_low[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[n][i] = ex2(s[n][i] - m[n][i & 1]);
+      l[n][0] += s[n][0] + s[n][2];
+      l[n][1] += s[n][1] + s[n][3];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t w = Elt<T>::from_f2(s[n][2 * i], s[n][2 * i + 1]);
+        b[n][i] = movmatrix(w);
+        if constexpr (Elt<T>::kBf16) {
+          const float2 r = Elt<T>::to_f2(w);
+          b_low[n][i] = movmatrix(Elt<T>::from_f2(s[n][2 * i] - r.x, s[n][2 * i + 1] - r.y));
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      uint32_t a[4];
+      const int r = (lane & 7) + (lane >> 4) * 8;
+      ldmatrix<true>(a, at + (kTile + r) * C::ROW + ((2 * k + ((lane >> 3) & 1)) ^ (lane & 7)) * 16);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        mma<T>(o[n][k], a, b[n][0], b[n][1]);
+        if constexpr (Elt<T>::kBf16) mma<T>(o[n][k], a, b_low[n][0], b_low[n][1]);
+      }
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
+
+  // ---- the warps' states, each in its ring's place
+  float* state = reinterpret_cast<float*>(smem + warp * C::RING);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], d);
+      const int row = n * 8 + 2 * t4 + i;
+      if (g == 0) {
+        state[C::ROWS * C::O_STRIDE + 2 * row] = m[n][i];
+        state[C::ROWS * C::O_STRIDE + 2 * row + 1] = l[n][i];
+      }
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        state[row * C::O_STRIDE + 16 * k + g] = o[n][k][i];
+        state[row * C::O_STRIDE + 16 * k + g + 8] = o[n][k][i + 2];
+      }
+    }
+  }
+  __syncthreads();
+  constexpr int COLS = D / 4;
+  const int64_t part = static_cast<int64_t>(blockIdx.x) * C::ROWS;  // the slice's first partial row
+  for (int i = tid; i < heads * COLS; i += kThreads) {
+    const int row = i / COLS, col = i % COLS * 4;
+    float mw[kWarps], lw[kWarps], top = kNone, sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float* st = reinterpret_cast<const float*>(smem + w * C::RING) + C::ROWS * C::O_STRIDE + 2 * row;
+      mw[w] = st[0];
+      lw[w] = st[1];
+      top = fmaxf(top, mw[w]);
+    }
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + w * C::RING) + row * C::O_STRIDE + col);
+      const float f = ex2(mw[w] - top);
+      sum += f * lw[w];
+      acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    if (p.slices == 1) {
+      store4<T>(p.out, q_row + row, D, col, acc, inv);
+      if (col == 0 && p.lse) p.lse[q_row + row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    } else {
+      *reinterpret_cast<float4*>(p.part_o + (part + row) * D + col) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+      if (col == 0) p.part_lse[part + row] = sum == 0.f ? -INFINITY : top + log2f(sum);
+    }
+  }
+  if (p.slices == 1) return;
+
+  // ---- the last slice of the item joins the parts
+  __threadfence();
+  __syncthreads();
+  if (tid == 0) {
+    last_s = atomicAdd(p.counters + item, 1) == p.slices - 1;
+    if (last_s) p.counters[item] = 0;
+  }
+  __syncthreads();
+  if (!last_s) return;
+  __threadfence();
+  const int64_t first = static_cast<int64_t>(item) * p.slices * C::ROWS;
+  for (int i = tid; i < heads * COLS; i += kThreads) {
+    const int row = i / COLS, col = i % COLS * 4;
+    float top = kNone, sum = 0.f;
+    for (int k = 0; k < p.slices; ++k) top = fmaxf(top, __ldcg(p.part_lse + first + k * C::ROWS + row));
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < p.slices; ++k) {
+      const int64_t r = first + k * C::ROWS + row;
+      const float f = ex2(__ldcg(p.part_lse + r) - top);
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + r * D + col));
+      sum += f;
+      acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
+    }
+    store4<T>(p.out, q_row + row, D, col, acc, sum == 0.f ? 0.f : 1.f / sum);
+    if (col == 0 && p.lse) p.lse[q_row + row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+  }
+}
+
+template <typename T, int D, int NT>
+cudaError_t launch_nt(const BlockParams& p, unsigned grid, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  const int most = Cfg<D, NT>::SMEM + kMaxListed * 4;
+  const cudaError_t e = set_smem_once(done, reinterpret_cast<const void*>(attend_kernel<T, D, NT>), most);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attend_kernel<T, D, NT>, grid, kThreads, Cfg<D, NT>::SMEM + p.num_blocks * 4, stream, p);
+}
+
+template <typename T>
+cudaError_t launch_t(const BlockParams& p, int D, int rows, unsigned grid, cudaStream_t stream) {
+  if (D == 256) return launch_nt<T, 256, 1>(p, grid, stream);
+  if (D == 128) return rows == 8 ? launch_nt<T, 128, 1>(p, grid, stream) : launch_nt<T, 128, 2>(p, grid, stream);
+  return rows == 8 ? launch_nt<T, 64, 1>(p, grid, stream) : launch_nt<T, 64, 2>(p, grid, stream);
+}
+
+}  // namespace
+
+constexpr int kMaxSlices = 64;
+
+AttendShape attend_shape(const BlockShape& s, int page_size) {
+  AttendShape a;
+  a.rows = s.D == 256 || s.G <= 8 ? 8 : 16;
+  a.chunks = (s.G + a.rows - 1) / a.rows;
+  const int64_t items = int64_t(s.num_tokens) * s.Hkv * a.chunks;
+  const int64_t ctas = int64_t(s.num_sms) * (s.D == 64 ? 3 : (s.D == 128 ? 2 : 1));
+  // as many slices as the card has room for CTAs, of 128 keys or more each
+  int64_t n = items > 0 ? ctas / items : 1;
+  const int64_t keys = int64_t(s.num_blocks) * page_size;
+  if (n > keys / 128) n = keys / 128;
+  if (n > s.num_blocks) n = s.num_blocks;
+  if (n > kMaxSlices) n = kMaxSlices;
+  a.slices = n < 1 ? 1 : int(n);
+  return a;
+}
+
+int64_t attend_part_rows(const BlockShape& s) {
+  return int64_t(s.num_sms) * 3 * 16;  // no more slices in all than CTAs that fit the card
+}
+
+cudaError_t launch_block_attention(BlockParams p, const BlockShape& s, int dtype, cudaStream_t stream) {
+  const AttendShape a = attend_shape(s, p.g.ps);
+  p.slices = a.slices;
+  const unsigned grid = unsigned(int64_t(s.num_tokens) * s.Hkv * a.chunks * a.slices);
+  return dtype == PA_BF16 ? launch_t<__nv_bfloat16>(p, s.D, a.rows, grid, stream)
+                          : launch_t<__half>(p, s.D, a.rows, grid, stream);
+}
+
+}  // namespace pa

@@ -1,0 +1,105 @@
+// Host-side internals of the calls over the 16-bit cache through device
+// tables: kernel parameters and launchers.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "../../include/pagedattn.h"
+#include "kv4.h"
+
+namespace pa {
+
+// ---------------------------------------------------------------------------
+// rows.cu
+
+// One run of heads of a token's row: where it is read and where it goes.
+struct RowsPart {
+  const void* in;
+  void* out;                      // nullptr: the cache
+  int64_t in_stride, out_stride;  // elements between tokens
+  int32_t heads, groups;          // groups: of heads that a thread takes one after the other
+  int32_t half;                   // of the cache: 0 K, 1 V
+  int32_t rotate;
+};
+
+struct RowsParams {
+  RowsPart part[3];
+  void* cache;
+  const int64_t* slots;
+  int32_t* status;
+  const uint64_t* turns;
+  const int32_t* axes;  // nullptr: axis 0
+  const int32_t* positions;
+  int64_t position_stride;
+  Kv4Geom g;  // of the cache; a row is head_dim values
+  int32_t n, D, pairs, num_axes, group_heads;
+  float scale, sign;  // sign -1: the inverse rotation
+};
+
+cudaError_t launch_rows(RowsParams p, int parts, bool interleaved, int dtype, int num_sms, cudaStream_t stream);
+
+struct BoundsParams {
+  const void* data;
+  int8_t* bounds;
+  float* scales;
+  const int64_t* slots;
+  int32_t* status;
+  Kv4Geom g;
+  int32_t n, warp_tokens;
+};
+
+cudaError_t launch_bounds(BoundsParams p, int D, int dtype, int num_sms, cudaStream_t stream);
+
+// ---------------------------------------------------------------------------
+// select.cu and block_attn.cu
+
+struct BlockParams {
+  const void* q;
+  const void* data;
+  const int8_t* bounds;
+  const float* bound_scales;
+  const int32_t *qo_indptr, *page_indptr, *pages, *last_page_len;
+  int32_t* blocks;  // [num_tokens][Hkv][num_blocks]: written by the selection, read by the attention
+  void* out;
+  float* lse;
+  int32_t* status;
+  int32_t* counters;  // slices done of each item; 0 between calls
+  uint32_t* keys;     // selection: order keys of the scores, [item of the launch][max_pages]
+  float* part_o;      // attention: normalised partial states, [slice][rows][D]
+  float* part_lse;    // their log-sums, base 2
+  int64_t q_stride;
+  Kv4Geom g;
+  int32_t batch, num_page_indices, num_tokens, Hq, G, num_blocks, first, last, max_pages;
+  int32_t token0, slices;  // first token of the launch; slices of an item
+  float scale_log2;
+};
+
+struct BlockShape {  // what the launches and their workspace depend on
+  int32_t D, Hkv, G, num_sms, num_tokens, num_blocks, max_pages;
+};
+
+struct BlockLayout {
+  // the scratch holds the selection's keys, or the attention's partial states
+  size_t off_counters, off_scratch, off_part_lse, total;
+  int32_t select_tokens;  // tokens of a launch of the selection
+};
+BlockLayout block_layout(const BlockShape& s);
+
+// Items are cut into slices only where they are fewer than this a SM.
+constexpr int kCutItems = 4;
+constexpr int kKeptKeys = 8192;  // of an item, in shared memory
+constexpr int kMaxListed = 4096;
+
+struct AttendShape {  // how a launch of the attention is cut
+  int32_t rows, chunks, slices;  // query heads a CTA, CTAs for a group, slices of a list
+};
+AttendShape attend_shape(const BlockShape& s, int page_size);
+// The largest slices * items and rows of a slice that attend_shape gives.
+int64_t attend_part_rows(const BlockShape& s);
+
+cudaError_t launch_select(BlockParams p, const BlockShape& s, int select_tokens, int dtype, cudaStream_t stream);
+cudaError_t launch_block_attention(BlockParams p, const BlockShape& s, int dtype, cudaStream_t stream);
+
+}  // namespace pa

@@ -1,0 +1,66 @@
+// Device helpers that the selection and the attention over selected pages share.
+#pragma once
+
+#include <climits>
+
+#include "common.cuh"
+#include "paged.h"
+
+namespace pa {
+
+// What a query token knows of its request; pos < 0: it sees no key.
+struct Query {
+  int page_start, pages, pos;
+  bool there;  // false: no request has this token (or its tables cannot be)
+};
+
+// The request of token t, found by a warp: first where a decode step has it
+// (request t), then by a search in 32 parts over qo_indptr.
+__device__ __forceinline__ Query find_query(const BlockParams& p, int t) {
+  const int lane = threadIdx.x & 31;
+  int b = t;
+  int q0 = -1, q1 = -1;
+  if (t < p.batch) {
+    q0 = p.qo_indptr[t];
+    q1 = p.qo_indptr[t + 1];
+  }
+  if (!(q0 >= 0 && q0 <= t && t < q1)) {
+    int lo = 0, hi = p.batch + 1;  // the last entry that is <= t lies in [lo, hi), if any is
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+      const bool below = lane == 0 || (at < hi && p.qo_indptr[at] <= t);
+      const unsigned m = __ballot_sync(0xffffffffu, below);
+      const int n = m == 0xffffffffu ? 31 : __ffs(~m) - 2;  // the last of the leading lanes below
+      lo += n * step;
+      hi = min(hi, lo + step);
+    }
+    b = lo;
+    if (b >= p.batch) return Query{0, 0, -1, false};
+    q0 = p.qo_indptr[b];
+    q1 = p.qo_indptr[b + 1];
+    if (q0 > t) return Query{0, 0, -1, false};
+  }
+  const int p0 = p.page_indptr[b], p1 = p.page_indptr[b + 1], last = p.last_page_len[b];
+  const long long kv = p1 > p0 ? static_cast<long long>(p1 - p0 - 1) * p.g.ps + last : 0;
+  const bool ok = q0 >= 0 && q1 > t && q1 <= p.num_tokens && p0 >= 0 && p1 >= p0 && p1 <= p.num_page_indices &&
+                  (p1 == p0 || (last >= 1 && last <= p.g.ps)) && kv <= INT_MAX - 256;
+  if (!ok) {
+    if (lane == 0) atomicOr(p.status, PA_DEV_BAD_INDEX);
+    return Query{0, 0, -1, false};
+  }
+  return Query{p0, p1 - p0, static_cast<int>(kv) - (q1 - q0) + (t - q0), true};
+}
+
+// A page id, checked.
+__device__ __forceinline__ int page_of(const BlockParams& p, int at) {
+  int id = p.pages[at];
+  if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.g.num_pages)) {
+    atomicOr(p.status, PA_DEV_BAD_INDEX);
+    id = 0;
+  }
+  return id;
+}
+
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
+}  // namespace pa

@@ -1,0 +1,337 @@
+// The pages that a query attends to (pagedattn_select_blocks).
+//
+// Score of a page for token t and kv head h, from the page's 8-bit bounds:
+//   sum over channels of (c_u * largest + c_l * smallest), times the page's scale
+// with c_u, c_l the group's summed positive and negative parts of q in 8 bits.
+// The sums are of whole numbers, so they come out alike in any order, and the
+// selection does not depend on how the work is cut.
+//
+// A CTA takes one query and kv head, or a slice of its pages where there are
+// few of them; scores go to a scratch row as unsigned keys in their order, and
+// the last slice to finish selects.  The k-th largest key is found by
+// histograms over 2048 equal parts of the keys' range, then of the part that
+// holds it, until one key (or a part taken whole) is left.
+#include <cfloat>
+#include <cstring>
+
+#include "internal.h"
+#include "paged_common.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kKept = kKeptKeys;
+constexpr uint32_t kAlways = 0xFFFFFFFFu;  // above every score's key
+
+// Scores as unsigned numbers of the same order; -0 is 0, NaN is infinity.
+__device__ __forceinline__ uint32_t order_key(float s) {
+  s = s != s ? INFINITY : s + 0.f;
+  const uint32_t b = __float_as_uint(s);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// The codes of the group's q: 2 * D bytes, c_u then c_l, made by a warp.
+template <typename T, int D>
+__device__ __forceinline__ void query_codes(const T* q, int G, int8_t* codes) {
+  constexpr int LANES = D / 8, ROWS = 32 / LANES;
+  const int lane = threadIdx.x & 31, r = lane / LANES, c = lane % LANES;
+  uint32_t top = 0;
+  for (int g = r; g < G; g += ROWS) {
+    const uint4 v = *reinterpret_cast<const uint4*>(q + g * D + c * 8);
+    top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                 __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+  }
+  top = max(top & 0xFFFFu, top >> 16);  // magnitudes have the order of their bits
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+  const float most = Elt<T>::to_f2(top).x;
+  float u[8], l[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) u[i] = l[i] = 0.f;
+  if (most > 0.f && most < INFINITY) {
+    int e;
+    frexpf(most, &e);
+    e = 15 - e;
+    const float f1 = pow2f(e / 2), f2 = pow2f(e - e / 2);  // 2^e may pass fp32's range
+    for (int g = r; g < G; g += ROWS) {
+      const uint4 v = *reinterpret_cast<const uint4*>(q + g * D + c * 8);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 x = Elt<T>::to_f2(w[i]);
+        const float a = rintf(x.x * f1 * f2), b = rintf(x.y * f1 * f2);
+        u[2 * i] += fmaxf(a, 0.f), l[2 * i] += fminf(a, 0.f);
+        u[2 * i + 1] += fmaxf(b, 0.f), l[2 * i + 1] += fminf(b, 0.f);
+      }
+    }
+  }
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+#pragma unroll
+    for (int d = LANES; d < 32; d <<= 1) {
+      u[i] += __shfl_xor_sync(0xffffffffu, u[i], d);  // whole numbers below 2^24: exact
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
+    }
+    m = fmaxf(m, fmaxf(u[i], -l[i]));
+  }
+#pragma unroll
+  for (int d = 1; d < LANES; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  const float f = m > 0.f ? 127.f * __frcp_rn(m) : 0.f;
+  if (lane < LANES) {
+    uint32_t cu[2] = {0, 0}, cl[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      cu[i >> 2] |= (static_cast<uint32_t>(static_cast<int>(rintf(u[i] * f))) & 0xFFu) << (8 * (i & 3));
+      cl[i >> 2] |= (static_cast<uint32_t>(static_cast<int>(rintf(l[i] * f))) & 0xFFu) << (8 * (i & 3));
+    }
+    *reinterpret_cast<uint2*>(codes + c * 8) = make_uint2(cu[0], cu[1]);
+    *reinterpret_cast<uint2*>(codes + D + c * 8) = make_uint2(cl[0], cl[1]);
+  }
+}
+
+struct Scan {
+  int warp_sum[kWarps];
+};
+// Exclusive sum over the CTA's threads, and the total.
+__device__ __forceinline__ int sum_before(int v, int* all, Scan& s) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) s.warp_sum[warp] = x;
+  __syncthreads();
+  int before = x - v, sum = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += s.warp_sum[w];
+    sum += s.warp_sum[w];
+  }
+  *all = sum;
+  return before;
+}
+
+// The k largest of n > k keys, of equal ones the first, as ascending indices.
+template <typename Key>
+__device__ void select_largest(Key key, int n, int k, int32_t* out, int* bins, Scan& scan, uint32_t* range) {
+  const int tid = threadIdx.x;
+  // the range of the keys that are not always taken
+  uint32_t least = 0xFFFFFFFFu, most = 0;
+  int always = 0;
+  for (int i = tid; i < n; i += kThreads) {
+    const uint32_t x = key(i);
+    if (x == kAlways) {
+      ++always;
+    } else {
+      least = min(least, x);
+      most = max(most, x);
+    }
+  }
+  least = __reduce_min_sync(0xffffffffu, least);
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (tid == 0) {
+    range[0] = 0xFFFFFFFFu;
+    range[1] = 0;
+  }
+  int forced;
+  sum_before(always, &forced, scan);
+  if ((tid & 31) == 0) {
+    atomicMin(range, least);
+    atomicMax(range + 1, most);
+  }
+  __syncthreads();
+  uint32_t base = range[0];
+  int need = k - forced;  // of the keys at or above `base` and below `top`; all above are taken
+  uint64_t top = static_cast<uint64_t>(range[1]) + 1;
+  while (need > 0 && top - base > 1) {
+    // parts of 2^shift keys each
+    const uint32_t span = static_cast<uint32_t>(top - 1 - base);
+    const int shift = max(0, 32 - __clz(span) - 11);
+    for (int i = tid; i < kBins; i += kThreads) bins[i] = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += kThreads) {
+      const uint32_t x = key(i);
+      if (x >= base && x < top) atomicAdd(bins + ((x - base) >> shift), 1);
+    }
+    __syncthreads();
+    // the part that holds the need-th largest, seen from above
+    int mine[kBins / kThreads], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kBins / kThreads; ++i) {
+      mine[i] = bins[kBins - 1 - (tid * (kBins / kThreads) + i)];
+      sum += mine[i];
+    }
+    int all, above = sum_before(sum, &all, scan);
+#pragma unroll
+    for (int i = 0; i < kBins / kThreads; ++i) {
+      if (above < need && above + mine[i] >= need) {
+        range[0] = kBins - 1 - (tid * (kBins / kThreads) + i);
+        range[1] = need - above;  // still to take from this part
+        range[2] = mine[i];
+      }
+      above += mine[i];
+    }
+    __syncthreads();
+    const uint32_t part = range[0];
+    need = range[1];
+    const bool whole = need == static_cast<int>(range[2]);
+    const uint64_t end = static_cast<uint64_t>(base) + ((static_cast<uint64_t>(part) + 1) << shift);
+    base += part << shift;
+    top = min(top, end);
+    if (whole) {  // all of the part: everything from `base` on is taken
+      top = base;
+      need = 0;
+    }
+    __syncthreads();
+  }
+  // Now: keys >= top are taken, and of those equal to base (if top > base) the
+  // first `need`.
+  const int run = ((n + kThreads - 1) / kThreads) | 1;  // odd: no two threads' keys in one bank
+  const int from = min(tid * run, n), to = min(from + run, n);
+  int equal = 0, over = 0;
+  for (int i = from; i < to; ++i) {
+    const uint32_t x = key(i);
+    if (x >= top) ++over;
+    else if (x == base) ++equal;
+  }
+  int all;
+  int equal_before = sum_before(equal, &all, scan);
+  int taken = over + max(0, min(equal, need - equal_before));
+  int at = sum_before(taken, &all, scan);
+  for (int i = from; i < to; ++i) {
+    const uint32_t x = key(i);
+    bool take = x >= top;
+    if (!take && x == base) take = equal_before++ < need;
+    if (take) out[at++] = i;
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) select_kernel(const BlockParams p) {
+  constexpr int LPR = D / 32, RPW = 32 / LPR;  // lanes of a page's bounds, 64 bytes each; pages of a warp
+  constexpr int U = 2;
+  extern __shared__ __align__(16) uint32_t kept[];  // keys
+  __shared__ __align__(16) int8_t codes[kWarps][2 * D];
+  __shared__ int bins[kBins];
+  __shared__ Scan scan;
+  __shared__ uint32_t range[3];
+  __shared__ int last_s;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int item = blockIdx.x / p.slices, slice = blockIdx.x % p.slices;
+  const int t = p.token0 + item / p.g.Hkv, h = item % p.g.Hkv;
+  pdl_wait();
+  const Query mine = find_query(p, t);
+  if (!mine.there) return;
+  const int n = mine.pos < 0 ? 0 : mine.pos / p.g.ps + 1;
+  int32_t* out = p.blocks + (static_cast<int64_t>(t) * p.g.Hkv + h) * p.num_blocks;
+  if (n <= p.num_blocks || n > p.max_pages) {
+    if (slice == 0)
+      for (int i = tid; i < p.num_blocks; i += kThreads) out[i] = i < n && n <= p.num_blocks ? i : -1;
+    if (n > p.num_blocks && tid == 0) atomicOr(p.status, PA_DEV_NO_ROOM);
+    return;
+  }
+  query_codes<T, D>(static_cast<const T*>(p.q) + t * p.q_stride + static_cast<int64_t>(h) * p.G * D, p.G, codes[warp]);
+  __syncwarp();
+  int c[16];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int4 v = *reinterpret_cast<const int4*>(codes[warp] + (i * LPR + lane % LPR) * 16);
+    c[4 * i] = v.x, c[4 * i + 1] = v.y, c[4 * i + 2] = v.z, c[4 * i + 3] = v.w;
+  }
+  const int lo = static_cast<int>(static_cast<int64_t>(n) * slice / p.slices);
+  const int hi = static_cast<int>(static_cast<int64_t>(n) * (slice + 1) / p.slices);
+  uint32_t* row = p.keys + static_cast<int64_t>(item) * p.max_pages;
+  const bool own = p.slices == 1 && n <= kKept;  // the keys need not leave the CTA
+  for (int b0 = lo + warp * RPW; b0 < hi; b0 += kWarps * RPW * U) {
+    int4 v[U][4];
+    float scale[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int b = min(b0 + u * kWarps * RPW + lane / LPR, hi - 1);
+      const int64_t at = static_cast<int64_t>(page_of(p, mine.page_start + b)) * p.g.Hkv + h;
+      const int4* src = reinterpret_cast<const int4*>(p.bounds + at * (2 * D)) + lane % LPR;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[u][i] = __ldg(src + i * LPR);
+      scale[u] = __ldg(p.bound_scales + at);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      int sum = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sum = __dp4a(v[u][i].x, c[4 * i], sum);
+        sum = __dp4a(v[u][i].y, c[4 * i + 1], sum);
+        sum = __dp4a(v[u][i].z, c[4 * i + 2], sum);
+        sum = __dp4a(v[u][i].w, c[4 * i + 3], sum);
+      }
+#pragma unroll
+      for (int d = 1; d < LPR; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      const int b = b0 + u * kWarps * RPW + lane / LPR;
+      if (lane % LPR == 0 && b < hi) {
+        const uint32_t x = b < p.first || b >= n - p.last ? kAlways : order_key(__fmul_rn(static_cast<float>(sum), scale[u]));
+        if (own) kept[b] = x;
+        else row[b] = x;
+      }
+    }
+  }
+  if (p.slices > 1) {
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+      int32_t* counter = p.counters + item;
+      last_s = atomicAdd(counter, 1) == p.slices - 1;
+      if (last_s) *counter = 0;
+    }
+    __syncthreads();
+    if (!last_s) return;
+    __threadfence();
+  } else {
+    __syncthreads();
+  }
+  if (own) {
+    select_largest([&](int i) { return kept[i]; }, n, p.num_blocks, out, bins, scan, range);
+  } else if (n <= kKept) {
+    for (int i = tid; i < n; i += kThreads) kept[i] = __ldcg(row + i);
+    __syncthreads();
+    select_largest([&](int i) { return kept[i]; }, n, p.num_blocks, out, bins, scan, range);
+  } else {
+    select_largest([&](int i) { return __ldcg(row + i); }, n, p.num_blocks, out, bins, scan, range);
+  }
+}
+
+template <typename T>
+cudaError_t launch_t(const BlockParams& p, int D, unsigned grid, size_t smem, cudaStream_t stream) {
+  switch (D) {
+    case 64: return launch_pdl(select_kernel<T, 64>, grid, kThreads, smem, stream, p);
+    case 128: return launch_pdl(select_kernel<T, 128>, grid, kThreads, smem, stream, p);
+    default: return launch_pdl(select_kernel<T, 256>, grid, kThreads, smem, stream, p);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_select(BlockParams p, const BlockShape& s, int select_tokens, int dtype, cudaStream_t stream) {
+  const int tokens = select_tokens;
+  const size_t smem = sizeof(uint32_t) * (s.max_pages < kKept ? s.max_pages : kKept);
+  for (int t = 0; t < s.num_tokens; t += tokens) {
+    const int n = s.num_tokens - t < tokens ? s.num_tokens - t : tokens;
+    const int items = n * s.Hkv;
+    // slices of 256 pages or more, until the card has two CTAs an SM
+    int slices = 1;
+    while (slices < 64 && items * slices < 2 * s.num_sms && s.max_pages > 512 * slices) slices *= 2;
+    p.token0 = t;
+    p.slices = slices;
+    const cudaError_t e = dtype == PA_BF16 ? launch_t<__nv_bfloat16>(p, s.D, unsigned(items * slices), smem, stream)
+                                           : launch_t<__half>(p, s.D, unsigned(items * slices), smem, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace pa

@@ -515,6 +515,178 @@ PAGEDATTN_API pagedattn_status pagedattn_kv4_run(const pagedattn_kv4_cache* cach
                                    const void* q, int64_t q_stride, void* out, float* lse, void* workspace,
                                    size_t workspace_bytes, pagedattn_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * A step over the 16-bit cache without the host: rotary positions, rows
+ * appended with the rotation on the way, bounds of each page's keys, the
+ * pages that a query attends to, and the attention over them.  As for the
+ * entries above: asynchronous on `stream`, nothing allocated or kept, tables
+ * in device memory, PA_DEV_* bits in a status word, and two calls may overlap
+ * on the device unless one writes what the other uses.
+ */
+
+/*
+ * A rotation by position.  The first rotary_dim values of a head are pairs:
+ * value i and value i + rotary_dim / 2, or with `interleaved` values 2 i and
+ * 2 i + 1.  Pair i = (a, b) at position x becomes
+ *   (a cos - b sin, b cos + a sin) * scale,  angle = 2 pi * x * turns[i] / 2^64
+ * in fp32, rounded once; values behind the pairs stay as they are.  turns[i] is
+ * the pair's turns a position modulo 1, as a 64-bit fraction, so that the
+ * angle of any position is exact to 2^-33 turns before its cosine is taken.
+ */
+typedef struct {
+  const uint64_t* turns; /* device, [rotary_dim / 2], 8-byte aligned                             */
+  const int32_t* axes;   /* device, [rotary_dim / 2]: the axis whose position turns the pair, in
+                            [0, num_axes); or NULL, axis 0 for all                              */
+  int32_t num_axes;      /* positions a token: 1, or one for each of time, height, width ...    */
+  int32_t rotary_dim;    /* a multiple of 16, at most head_dim                                  */
+  int32_t interleaved;
+  float scale;
+} pagedattn_rotation;
+
+/* Rows for pagedattn_rope.  Tokens are strides elements apart (multiples of 8). */
+typedef struct {
+  const void* q; /* device, dtype[num_tokens][num_q_heads][head_dim], 16-byte aligned            */
+  const void* k; /* likewise with num_k_heads, or NULL with num_k_heads 0                        */
+  void* q_out;   /* may be q (with its stride), otherwise must not overlap it; likewise k_out    */
+  void* k_out;
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+  const int32_t* positions; /* device, [num_axes][num_tokens], axes position_stride entries apart
+                               (0: one row for all axes)                                      */
+  int64_t position_stride;
+  int32_t num_tokens, num_q_heads, num_k_heads;
+  int32_t head_dim; /* a multiple of 16, at most 256                                             */
+  int32_t inverse;  /* rotate by the negative angle: the gradient of the rotation                */
+  pagedattn_dtype dtype;
+} pagedattn_rope_rows;
+
+/* Rotate the rows of q and k by their positions. */
+PAGEDATTN_API pagedattn_status pagedattn_rope(const pagedattn_rotation* rotation, const pagedattn_rope_rows* rows,
+                                pagedattn_stream_t stream);
+
+/*
+ * A paged cache of 16-bit keys and values, laid out as pagedattn_run reads it,
+ * with the bounds of its keys where pages are to be selected:
+ *   bounds        [num_pages][num_kv_heads][2][head_dim] codes of the largest (0) and
+ *                 the smallest (1) value of each channel over the page's keys
+ *   bound_scales  [num_pages][num_kv_heads] what code 1 stands for
+ * With a the largest magnitude over the page's keys and channels, and f = 127 * (1 / a):
+ * the scale is a * (1 / 127) and the codes min(127, ceil(x * f)) of the largest x and
+ * max(-127, floor(x * f)) of the smallest, each step rounded to fp32: they
+ * enclose the keys.  (a below 2^-100 counts as 0: scale and codes 0.  Where a
+ * key is NaN or infinite the scale is infinite and the codes 127 and -127.)
+ */
+typedef struct {
+  void* data;          /* device, 16-byte aligned                                  */
+  int8_t* bounds;      /* device, 16-byte aligned, or NULL: no bounds are kept     */
+  float* bound_scales; /* device, or NULL with bounds                              */
+  int32_t num_pages, page_size, num_kv_heads;
+  int32_t head_dim;    /* 64, 128 or 256                                           */
+  int32_t kv_layout;   /* PA_LAYOUT_NHD or PA_LAYOUT_HND                           */
+  pagedattn_dtype dtype;
+} pagedattn_kv_cache;
+
+/* Rows for pagedattn_kv_append.  Tokens are strides elements apart (multiples of 8). */
+typedef struct {
+  const void* k; /* device, dtype[num_tokens][num_kv_heads][head_dim], 16-byte aligned          */
+  const void* v;
+  const void* q; /* device, dtype[num_tokens][num_qo_heads][head_dim] to be rotated too, or NULL */
+  void* q_out;   /* may be q (with its stride), otherwise must not overlap it                    */
+  int64_t k_stride, v_stride, q_stride, q_out_stride;
+  const int64_t* slot_mapping; /* device, [num_tokens] page * page_size + slot; a row with a
+                                  negative slot is skipped (its q is rotated all the same)      */
+  const int32_t* positions;    /* device, [num_axes][num_tokens]; not used without a rotation    */
+  int64_t position_stride;
+  int32_t* status;             /* device, status word                                           */
+  int32_t num_tokens, num_qo_heads;
+} pagedattn_kv_rows;
+
+/*
+ * Append rows to the cache: k rotated where a rotation is given (NULL: as it
+ * is), v as it is; and q rotated into q_out.  Slots at num_pages * page_size or
+ * beyond are skipped and raise PA_DEV_BAD_INDEX.  The non-negative slots of
+ * one call must be distinct: two rows for one slot may leave a mixture of both
+ * there.  Where the cache has bounds, those of the pages written to are made
+ * anew, as by pagedattn_kv_bounds.
+ */
+PAGEDATTN_API pagedattn_status pagedattn_kv_append(const pagedattn_kv_cache* cache, const pagedattn_rotation* rotation,
+                                     const pagedattn_kv_rows* rows, pagedattn_stream_t stream);
+
+/*
+ * The bounds of the pages that the slots name, each over its slots from 0 to
+ * the one named last.  The slots of one page have to stand one behind the other
+ * in ascending order, as pagedattn_build_tables lays them out.  Negative ones
+ * are skipped, those beyond the cache too, which raises PA_DEV_BAD_INDEX.
+ */
+PAGEDATTN_API pagedattn_status pagedattn_kv_bounds(const pagedattn_kv_cache* cache, const int64_t* slot_mapping,
+                                     int32_t num_tokens, int32_t* status, pagedattn_stream_t stream);
+
+/* The batch of pagedattn_select_blocks and pagedattn_blocks_run; a block is a page's worth of
+ * a request's keys, counted from 0.  Arrays are device memory. */
+typedef struct {
+  const int32_t* qo_indptr;        /* [batch_size + 1]                                    */
+  const int32_t* kv_page_indptr;   /* [batch_size + 1]                                    */
+  const int32_t* kv_page_indices;  /* [num_page_indices]                                  */
+  const int32_t* kv_last_page_len; /* [batch_size]                                        */
+  int32_t batch_size, num_page_indices;
+  int32_t num_tokens;              /* rows of q, blocks, out and lse, >= qo_indptr[batch_size] */
+  int32_t num_qo_heads;
+  int32_t num_blocks;              /* entries of a list, in [1, 4096]                     */
+  int32_t first, last;             /* blocks that are always selected: the first ones, and the
+                                      last ones up to the query's own; first >= 0, last >= 1,
+                                      first + last <= num_blocks                          */
+  int32_t max_pages;               /* most pages of a request                             */
+} pagedattn_block_batch;
+
+/* Bytes of workspace that the two calls below need on the current device. */
+PAGEDATTN_API pagedattn_status pagedattn_blocks_workspace_size(int32_t num_qo_heads, int32_t num_kv_heads,
+                                                 int32_t head_dim, int32_t num_tokens, int32_t num_blocks,
+                                                 int32_t max_pages, size_t* bytes);
+
+/*
+ * The blocks that each query attends to: for token t and kv head h the list
+ * blocks[t][h][num_blocks], ascending, -1 behind its end.  A query at position x
+ * (aligned as in pagedattn_run with causal = 1) has the blocks 0 .. x / page_size.
+ * With no more than num_blocks of them all are listed; otherwise the first and
+ * the last ones, and of the others those of the largest scores, of equal ones the
+ * lowest.  The score bounds the sum over the group's query heads of q . key
+ * for every key of the block from above, up to the rounding of q:
+ *   x = rint(q * 2^e) for the group's heads, e such that their largest magnitude
+ *       lies in [2^14, 2^15); u, l = the sums over the heads of max(x, 0) and min(x, 0)
+ *   codes c = rint((u, l) * (127 * (1 / max(|u|, |l|))))      (each step in fp32; 0 where all are 0)
+ *   score = scale of the block * sum over channels of (c_u * largest + c_l * smallest)
+ * The sums are of whole numbers, so a score has the same bits in any batch.
+ * A NaN of the product (0 times an infinite scale) counts as infinity; a group
+ * with a NaN or infinity in q has codes of 0.
+ *
+ * Rows of queries that have more than max_pages blocks get -1 throughout, and
+ * PA_DEV_NO_ROOM is raised; table entries that cannot be leave their rows
+ * unwritten, a page id outside [0, num_pages) is read as page 0, and both raise
+ * PA_DEV_BAD_INDEX.  Rows from qo_indptr[batch_size] on are not written.
+ *
+ * q         device, the cache's dtype[num_tokens][num_qo_heads][head_dim], tokens q_stride
+ *           elements apart (a multiple of 8), 16-byte aligned.
+ * workspace device, 256-byte aligned, pagedattn_blocks_workspace_size() bytes: zero it once.
+ *           Its first word is the status word.  Calls that overlap on the device need
+ *           different workspaces; one after the other they may share one.
+ */
+PAGEDATTN_API pagedattn_status pagedattn_select_blocks(const pagedattn_kv_cache* cache, const pagedattn_block_batch* batch,
+                                         const void* q, int64_t q_stride, int32_t* blocks, void* workspace,
+                                         size_t workspace_bytes, pagedattn_stream_t stream);
+
+/*
+ * Attention of each query over the keys of its listed blocks up to its own
+ * position; softmax, out and lse as for pagedattn_run.  The lists are those of
+ * pagedattn_select_blocks or the caller's own, in any order: negative entries and
+ * blocks behind the query's own are skipped, a block listed twice counts
+ * twice.  A query that sees no key gets zeros and lse = -inf.  Entries beyond
+ * the request's pages are skipped and raise PA_DEV_BAD_INDEX, and so are
+ * tables and page ids as above.  Rows from qo_indptr[batch_size] on are neither
+ * read nor written.  out must not overlap q.
+ */
+PAGEDATTN_API pagedattn_status pagedattn_blocks_run(const pagedattn_kv_cache* cache, const pagedattn_block_batch* batch,
+                                      const int32_t* blocks, const void* q, int64_t q_stride, void* out, float* lse,
+                                      void* workspace, size_t workspace_bytes, pagedattn_stream_t stream);
+
 /*
  * Wait for `stream`, read the status word *word (device memory) into *flags
  * and clear it.  Returns PA_ERR_TIMEOUT / PA_ERR_DEVICE_CHECK when a bit is
