@@ -143,7 +143,7 @@ class BlockBatch(ctypes.Structure):
     """pagedattn_block_batch"""
     _fields_ = [(n, ctypes.c_void_p) for n in ("qo_indptr", "kv_page_indptr", "kv_page_indices", "kv_last_page_len")] + \
         [(n, ctypes.c_int32) for n in ("batch_size", "num_page_indices", "num_tokens", "num_qo_heads", "num_blocks",
-                                       "first", "last", "max_pages")]
+                                       "first", "last", "max_pages", "max_qo_len")]
 
 
 class PrefixGroups(ctypes.Structure):
@@ -223,7 +223,8 @@ def load() -> ctypes.CDLL:
         lib.pagedattn_kv_bounds.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
                                             ctypes.c_void_p]
         lib.pagedattn_kv_bounds.restype = ctypes.c_int
-        lib.pagedattn_blocks_workspace_size.argtypes = [ctypes.c_int32] * 6 + [ctypes.POINTER(ctypes.c_size_t)]
+        lib.pagedattn_blocks_workspace_size.argtypes = [ctypes.c_int32] * 3 + [ctypes.c_void_p,
+                                                                               ctypes.POINTER(ctypes.c_size_t)]
         lib.pagedattn_blocks_workspace_size.restype = ctypes.c_int
         lib.pagedattn_select_blocks.argtypes = [ctypes.c_void_p] * 3 + [ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
                                                                         ctypes.c_size_t, ctypes.c_void_p]

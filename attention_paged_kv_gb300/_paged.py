@@ -28,7 +28,7 @@ from ._kv4 import BatchTables, _call, _device, _is, _Object, _on, _refuse, _rows
 # The arguments' structures (include/pagedattn.h) packed directly.
 _ROPE_ROWS = struct.Struct("@4P4qPq6i0P")
 _KV_ROWS = struct.Struct("@4P4q2PqP2i0P")
-_BLOCK_BATCH = struct.Struct("@4P8i0P")
+_BLOCK_BATCH = struct.Struct("@4P9i0P")
 
 _TWO_PI = 2 * Fraction("3.14159265358979323846264338327950288419716939937510582")
 
@@ -260,12 +260,15 @@ class BlockAttention(_Object):
     num_tokens: rows of q.  num_blocks: pages of a query's list (of each kv
     head), at most 4096.  max_kv_len: most keys of a request.  first, last: pages
     that are always selected, from the start of the request and back from the
-    query's own.  Holds the workspace, so two calls that overlap on the device
+    query's own.  max_qo_len: a bound of the requests' query lengths, by which the
+    kernels are chosen (a longer request is computed too, slower); by default 1
+    where there are as many tokens as requests, else num_tokens: pass 1 for a
+    decode step with rows to spare.  Holds the workspace, so two calls that overlap on the device
     need two objects with a workspace each; workspace: as for Kv4Attention.
     """
 
     def __init__(self, batch_size, num_tokens, num_qo_heads, num_kv_heads, head_dim, page_size, dtype, num_blocks,
-                 max_kv_len, first=1, last=1, workspace=None, device=None):
+                 max_kv_len, first=1, last=1, max_qo_len=None, workspace=None, device=None):
         import torch
         if isinstance(workspace, _Object) and not isinstance(workspace, BlockAttention):
             _refuse("the workspace of an object of another class cannot be shared")
@@ -278,6 +281,9 @@ class BlockAttention(_Object):
         self.max_pages = -(-int(max_kv_len) // self.page_size)
         if self.first < 0 or self.last < 1 or self.first + self.last > self.num_blocks:
             _refuse("first must not be negative, last positive, and both fit num_blocks")
+        if max_qo_len is None:
+            max_qo_len = 1 if self.num_tokens == self.batch_size else self.num_tokens
+        self.max_qo_len = int(max_qo_len)
         self._dtype = (torch.float16, torch.bfloat16)[_b.dtype_code(dtype)]
         self._shape = (self.num_tokens, self.num_qo_heads, self.head_dim)
         self._lists = (self.num_tokens, self.num_kv_heads, self.num_blocks)
@@ -288,10 +294,15 @@ class BlockAttention(_Object):
         self._index = self.device.index
         need = ctypes.c_size_t(0)
         with torch.cuda.device(self.device):
-            _b.check(self._lib.pagedattn_blocks_workspace_size(self.num_qo_heads, self.num_kv_heads, self.head_dim,
-                                                               self.num_tokens, self.num_blocks, self.max_pages,
+            sizes = self._sizes(0, 0, 0, 0, 0)
+            _b.check(self._lib.pagedattn_blocks_workspace_size(self.num_kv_heads, self.head_dim, self.page_size, sizes,
                                                                ctypes.byref(need)))
             self._take_workspace(workspace, need.value, BlockAttention)
+
+    def _sizes(self, qo_indptr, page_indptr, pages, last, nnz):
+        return _BLOCK_BATCH.pack(qo_indptr, page_indptr, pages, last, self.batch_size, nnz, self.num_tokens,
+                                 self.num_qo_heads, self.num_blocks, self.first, self.last, self.max_pages,
+                                 self.max_qo_len)
 
     def _batch(self, q, cache, tables):
         """(q's stride, packed batch, the objects and the tensors of a call), checked."""
@@ -317,8 +328,7 @@ class BlockAttention(_Object):
             _is(page_indptr, "kv_page_indptr", i32, (B + 1,), at)
             _is(pages, "kv_page_indices", i32, (nnz,), at)
             _is(last, "kv_last_page_len", i32, (B,), at)
-        batch = _BLOCK_BATCH.pack(*(t.data_ptr() for t in tables), B, nnz, self.num_tokens, self.num_qo_heads,
-                                  self.num_blocks, self.first, self.last, self.max_pages)
+        batch = self._sizes(*(t.data_ptr() for t in tables), nnz)
         return stride, batch, objects, tables
 
     def select(self, q, cache, tables, out=None, stream=None):
@@ -351,8 +361,8 @@ class BlockAttention(_Object):
     def run(self, q, cache, tables, blocks, out=None, lse=None, return_lse=True, stream=None):
         """out, lse of q over the listed blocks (of select, or any int32 lists of that shape).
 
-        Entries below 0 or behind a query's own block are skipped; one listed
-        twice counts twice.  out must not overlap q.  See pagedattn_blocks_run.
+        Lists ascend, with negative entries behind them; blocks behind a query's
+        own are skipped.  out must not overlap q.  See pagedattn_blocks_run.
         """
         import torch
         at = self._index

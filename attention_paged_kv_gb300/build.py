@@ -19,7 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpagedattn.so")
 SOURCES = ["api.cu", "plan.cpp", "prefill.cu", "decode.cu", "noalloc.cu", "tables.cu", "kv4_api.cu", "kv4_append.cu",
-           "kv4_attn.cu", "kv4_prefill.cu", "paged_api.cu", "rows.cu", "select.cu", "block_attn.cu"]
+           "kv4_attn.cu", "kv4_prefill.cu", "paged_api.cu", "rows.cu", "select.cu", "block_attn.cu",
+           "block_prefill.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -81,11 +81,13 @@ pagedattn_status encode_kv_map(CUtensorMap* m, const pa::HostPlan& hp, const voi
 
 // 3-D view of q: (D, Hq, T), innermost first; box {64, G, 128 / G}: one
 // 128-row tile of packed (token, head) rows of one kv head, 128-byte swizzle.
-pagedattn_status encode_q_map(CUtensorMap* m, const pa::HostPlan& hp, const void* q, uint32_t box_rows) {
+pagedattn_status encode_q_map(CUtensorMap* m, const pa::HostPlan& hp, const void* q, uint32_t box_rows,
+                              int64_t token_stride) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return set_err(PA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   const cuuint64_t dims[3] = {cuuint64_t(hp.D), cuuint64_t(hp.Hq), cuuint64_t(hp.T)};
-  const cuuint64_t strides[2] = {cuuint64_t(hp.D) * 2, cuuint64_t(hp.Hq) * hp.D * 2};
+  const cuuint64_t strides[2] = {cuuint64_t(hp.D) * 2,
+                                 (token_stride ? cuuint64_t(token_stride) : cuuint64_t(hp.Hq) * hp.D) * 2};
   const cuuint32_t box[3] = {64, cuuint32_t(hp.G), cuuint32_t(box_rows / hp.G)};
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUtensorMapDataType dt =

@@ -12,7 +12,7 @@
 // set 7 below the largest logit, in log2 units, and set again when a logit
 // passes it by 15: a row's largest P lies in [2^7, 2^15], and the keys' ones
 // down to 2^-21 of it are rounded like it.  P is rounded to fp16 for fp16
-// values (2^-12 of it at most); for bf16, where that would be 2^-9, it is split
+// values (by 2^-11 of it at most); for bf16, where that would be 2^-8, it is split
 // in two bf16 terms and multiplied twice.
 #include <climits>
 #include <cstring>
@@ -95,19 +95,29 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attend_kernel(cons
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int count_s[2][kWarps];
   __shared__ int last_s;
-  int32_t* list = reinterpret_cast<int32_t*>(smem + C::SMEM);
+  int32_t* const list0 = reinterpret_cast<int32_t*>(smem + C::SMEM);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
   const int chunks = (p.G + C::ROWS - 1) / C::ROWS;
-  const int slice = blockIdx.x % p.slices, item = blockIdx.x / p.slices;
-  const int chunk = item % chunks, h = item / chunks % p.g.Hkv, t = item / (chunks * p.g.Hkv);
-  const int heads = min(C::ROWS, p.G - chunk * C::ROWS);
   pdl_wait();
+  // an item for each token, kv head and chunk of heads, or (listed) for those of the tokens that small_indptr counts
+  const unsigned works = p.listed ? unsigned(p.small_indptr[p.batch]) * p.g.Hkv * chunks : gridDim.x;
+  for (unsigned work = blockIdx.x; work < works; work += gridDim.x) {
+  const int slice = work % p.slices, item = work / p.slices;
+  const int chunk = item % chunks, h = item / chunks % p.g.Hkv;
+  int t = item / (chunks * p.g.Hkv), guess = t;
+  if (p.listed) {
+    guess = last_below(p.small_indptr, p.batch + 1, t);
+    t = p.qo_indptr[guess] + t - p.small_indptr[guess];
+  }
+  const int heads = min(C::ROWS, p.G - chunk * C::ROWS);
+  int32_t* list = list0;
 
   // ---- the list: page ids of the blocks that the query sees, its own block marked by the top bit
   const int32_t* blocks = p.blocks + (static_cast<int64_t>(t) * p.g.Hkv + h) * p.num_blocks;
   int e = tid < p.num_blocks ? blocks[tid] : -1;  // (in flight beside the tables)
-  const Query mine = find_query(p, t);
-  if (!mine.there) return;
+  int before = tid > 0 && tid < p.num_blocks ? blocks[tid - 1] : e - 1;
+  const Query mine = find_query(p, t, guess);
+  if (!mine.there) continue;
   const int64_t q_row = static_cast<int64_t>(t) * p.Hq + h * p.G + chunk * C::ROWS;  // in out and lse
   uint32_t qf[NT][KS][2];
   {
@@ -125,8 +135,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attend_kernel(cons
   }
   const int own = mine.pos < 0 ? -1 : mine.pos >> p.g.ps_shift, limit = mine.pos & (p.g.ps - 1);
   int count = 0;
+  bool sound = true;
   for (int i0 = 0, turn = 0; i0 < p.num_blocks; i0 += kThreads, turn ^= 1) {
-    if (i0) e = i0 + tid < p.num_blocks ? blocks[i0 + tid] : -1;
+    if (i0) {
+      e = i0 + tid < p.num_blocks ? blocks[i0 + tid] : -1;
+      before = i0 + tid < p.num_blocks ? blocks[i0 + tid - 1] : -1;
+    }
+    if (e >= 0 && (e <= before || (before < 0 && i0 + tid > 0))) sound = false;
     if (e >= mine.pages) atomicOr(p.status, PA_DEV_BAD_INDEX);
     const bool seen = e >= 0 && e <= own;
     const int id = seen ? page_of(p, mine.page_start + e) : 0;
@@ -141,7 +156,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attend_kernel(cons
     }
     if (seen) list[at] = id | (e == own ? INT_MIN : 0);
   }
-  __syncthreads();
+  // a list out of order, or a request longer than it may be: as an empty list
+  if (__syncthreads_or(!sound || own >= p.max_pages)) {
+    if (tid == 0) atomicOr(p.status, own >= p.max_pages ? PA_DEV_NO_ROOM : PA_DEV_BAD_INDEX);
+    count = 0;
+  }
   const int lo = static_cast<int>(static_cast<int64_t>(count) * slice / p.slices);
   const int entries = static_cast<int>(static_cast<int64_t>(count) * (slice + 1) / p.slices) - lo;
   list += lo;
@@ -288,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attend_kernel(cons
   }
   __syncthreads();
   constexpr int COLS = D / 4;
-  const int64_t part = static_cast<int64_t>(blockIdx.x) * C::ROWS;  // the slice's first partial row
+  const int64_t part = static_cast<int64_t>(work) * C::ROWS;  // the slice's first partial row
   for (int i = tid; i < heads * COLS; i += kThreads) {
     const int row = i / COLS, col = i % COLS * 4;
     float mw[kWarps], lw[kWarps], top = kNone, sum = 0.f;
@@ -316,7 +335,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attend_kernel(cons
       if (col == 0) p.part_lse[part + row] = sum == 0.f ? -INFINITY : top + log2f(sum);
     }
   }
-  if (p.slices == 1) return;
+  if (p.slices == 1) {
+    __syncthreads();  // the list and the states have been read
+    continue;
+  }
 
   // ---- the last slice of the item joins the parts
   __threadfence();
@@ -326,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attend_kernel(cons
     if (last_s) p.counters[item] = 0;
   }
   __syncthreads();
-  if (!last_s) return;
+  if (!last_s) continue;
   __threadfence();
   const int64_t first = static_cast<int64_t>(item) * p.slices * C::ROWS;
   for (int i = tid; i < heads * COLS; i += kThreads) {
@@ -344,6 +366,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attend_kernel(cons
     }
     store4<T>(p.out, q_row + row, D, col, acc, sum == 0.f ? 0.f : 1.f / sum);
     if (col == 0 && p.lse) p.lse[q_row + row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+  }
   }
 }
 
@@ -367,7 +390,7 @@ cudaError_t launch_t(const BlockParams& p, int D, int rows, unsigned grid, cudaS
 
 constexpr int kMaxSlices = 64;
 
-AttendShape attend_shape(const BlockShape& s, int page_size) {
+AttendShape attend_shape(const BlockShape& s) {
   AttendShape a;
   a.rows = s.D == 256 || s.G <= 8 ? 8 : 16;
   a.chunks = (s.G + a.rows - 1) / a.rows;
@@ -375,7 +398,7 @@ AttendShape attend_shape(const BlockShape& s, int page_size) {
   const int64_t ctas = int64_t(s.num_sms) * (s.D == 64 ? 3 : (s.D == 128 ? 2 : 1));
   // as many slices as the card has room for CTAs, of 128 keys or more each
   int64_t n = items > 0 ? ctas / items : 1;
-  const int64_t keys = int64_t(s.num_blocks) * page_size;
+  const int64_t keys = int64_t(s.num_blocks) * s.page_size;
   if (n > keys / 128) n = keys / 128;
   if (n > s.num_blocks) n = s.num_blocks;
   if (n > kMaxSlices) n = kMaxSlices;
@@ -388,9 +411,12 @@ int64_t attend_part_rows(const BlockShape& s) {
 }
 
 cudaError_t launch_block_attention(BlockParams p, const BlockShape& s, int dtype, cudaStream_t stream) {
-  const AttendShape a = attend_shape(s, p.g.ps);
-  p.slices = a.slices;
-  const unsigned grid = unsigned(int64_t(s.num_tokens) * s.Hkv * a.chunks * a.slices);
+  const AttendShape a = attend_shape(s);
+  p.slices = p.listed ? 1 : a.slices;
+  int64_t items = int64_t(s.num_tokens) * s.Hkv * a.chunks;
+  // how many tokens are listed the host does not know: CTAs for a full card, item after item
+  if (p.listed && items > int64_t(s.num_sms) * 6) items = int64_t(s.num_sms) * 6;
+  const unsigned grid = unsigned(items * p.slices);
   return dtype == PA_BF16 ? launch_t<__nv_bfloat16>(p, s.D, a.rows, grid, stream)
                           : launch_t<__half>(p, s.D, a.rows, grid, stream);
 }

@@ -117,8 +117,10 @@ pagedattn_status cuda_err(cudaError_t e, const char* what);
 pagedattn_status encode_kv_map(CUtensorMap* m, const HostPlan& hp, const void* kv, uint32_t box0, uint32_t box2,
                                CUtensorMapSwizzle sw);
 // Tensor map over q, or over out (same shape), viewed as (D, Hq, T), box
-// {64, G, 128 / G}: one 128-row query tile of 64 columns (api.cu).
-pagedattn_status encode_q_map(CUtensorMap* m, const HostPlan& hp, const void* q, uint32_t box_rows = 128);
+// {64, G, 128 / G}: one 128-row query tile of 64 columns (api.cu).  Tokens are
+// token_stride elements apart (0: contiguous).
+pagedattn_status encode_q_map(CUtensorMap* m, const HostPlan& hp, const void* q, uint32_t box_rows = 128,
+                              int64_t token_stride = 0);
 
 }  // namespace pa
 

@@ -4,6 +4,7 @@
 
 #include <cstdint>
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "../../include/pagedattn.h"
@@ -55,6 +56,15 @@ cudaError_t launch_bounds(BoundsParams p, int D, int dtype, int num_sms, cudaStr
 // ---------------------------------------------------------------------------
 // select.cu and block_attn.cu
 
+// The tokens of two row tiles of a long request, for one kv head.
+struct BlockItem {
+  int32_t token, tokens;   // first one in q, how many
+  int32_t entries;         // of the union of their lists
+  int32_t diag;            // first step of 128 keys with a block that some token sees in part
+  int32_t pos, kv_len;     // position of the first token, keys of the request
+  int32_t unused[2];
+};
+
 struct BlockParams {
   const void* q;
   const void* data;
@@ -69,20 +79,27 @@ struct BlockParams {
   uint32_t* keys;     // selection: order keys of the scores, [item of the launch][max_pages]
   float* part_o;      // attention: normalised partial states, [slice][rows][D]
   float* part_lse;    // their log-sums, base 2
+  // chunks (block_prefill.cu)
+  int32_t *tile_indptr, *small_indptr;  // [batch + 1]: row-tile pairs of the requests before, tokens of the short ones
+  BlockItem* items;                     // [max_tiles][Hkv]
+  int2* entries;                        // of each item, [max_entries]: page id, block
+  uint16_t* masks;                      // of each item, [step of 128 keys][tile_tokens]: a bit for 8 keys
   int64_t q_stride;
   Kv4Geom g;
+  int32_t max_entries, max_tiles, tile_tokens, long_tokens, hnd;
+  int32_t listed;  // attention: the tokens that small_indptr counts, not all
   int32_t batch, num_page_indices, num_tokens, Hq, G, num_blocks, first, last, max_pages;
   int32_t token0, slices;  // first token of the launch; slices of an item
   float scale_log2;
 };
 
 struct BlockShape {  // what the launches and their workspace depend on
-  int32_t D, Hkv, G, num_sms, num_tokens, num_blocks, max_pages;
+  int32_t D, Hkv, G, num_sms, num_tokens, num_blocks, max_pages, batch, page_size, max_qo_len;
 };
 
 struct BlockLayout {
   // the scratch holds the selection's keys, or the attention's partial states
-  size_t off_counters, off_scratch, off_part_lse, total;
+  size_t off_counters, off_scratch, off_part_lse, off_indptr, off_items, off_entries, off_masks, total;
   int32_t select_tokens;  // tokens of a launch of the selection
 };
 BlockLayout block_layout(const BlockShape& s);
@@ -95,11 +112,21 @@ constexpr int kMaxListed = 4096;
 struct AttendShape {  // how a launch of the attention is cut
   int32_t rows, chunks, slices;  // query heads a CTA, CTAs for a group, slices of a list
 };
-AttendShape attend_shape(const BlockShape& s, int page_size);
+AttendShape attend_shape(const BlockShape& s);
 // The largest slices * items and rows of a slice that attend_shape gives.
 int64_t attend_part_rows(const BlockShape& s);
 
 cudaError_t launch_select(BlockParams p, const BlockShape& s, int select_tokens, int dtype, cudaStream_t stream);
+// Chunks: which requests go to the tensor-core kernel, and what it keeps in the workspace.
+struct TileShape {
+  bool use;
+  int32_t tokens, long_tokens;     // of an item; the fewest of a request that goes there
+  int32_t max_tiles, max_entries;
+  int64_t union_smem;
+};
+TileShape tile_shape(const BlockShape& s);
+cudaError_t launch_block_tiles(BlockParams p, const BlockShape& s, const TileShape& t, const CUtensorMap& kv_map,
+                               const CUtensorMap& q_map, int dtype, cudaStream_t stream);
 cudaError_t launch_block_attention(BlockParams p, const BlockShape& s, int dtype, cudaStream_t stream);
 
 }  // namespace pa

@@ -81,32 +81,43 @@ void set_rotation(pa::RowsParams* p, const pagedattn_rotation* r, const int32_t*
   p->sign = inverse ? -1.f : 1.f;
 }
 
-// What the selection and the attention both check.
-pagedattn_status check_batch(const pagedattn_kv_cache* cache, const pagedattn_block_batch* b, const int32_t* blocks,
-                             const void* q, int64_t q_stride, void* workspace, size_t workspace_bytes,
-                             pa::BlockParams* p, pa::BlockShape* shape, pa::BlockLayout* lay, bool* empty) {
-  pagedattn_status s = check_cache(cache, &p->g);
-  if (s != PA_OK) return s;
+pagedattn_status check_shape(int32_t Hkv, int32_t D, int32_t page_size, const pagedattn_block_batch* b,
+                             pa::BlockShape* shape) {
   if (!b) return set_err(PA_ERR_INVALID_ARG, "batch is NULL");
-  s = check_heads(b->num_qo_heads, cache->num_kv_heads, cache->head_dim);
+  pagedattn_status s = check_heads(b->num_qo_heads, Hkv, D);
   if (s != PA_OK) return s;
-  if (b->batch_size < 0 || b->num_tokens < 0 || b->num_page_indices < 0 || b->max_pages < 0)
+  if (page_shift(page_size) < 0) return set_err(PA_ERR_UNSUPPORTED, "page_size must be a power of two in [1, 128]");
+  if (b->batch_size < 0 || b->num_tokens < 0 || b->num_page_indices < 0 || b->max_pages < 0 || b->max_qo_len < 0)
     return set_err(PA_ERR_INVALID_ARG, "a size is negative");
   if (b->batch_size > (1 << 30)) return set_err(PA_ERR_UNSUPPORTED, "batch_size must be at most 2^30");
   if (int64_t(b->num_tokens) * b->num_qo_heads > 0x3FFFFFFF)
     return set_err(PA_ERR_UNSUPPORTED, "num_tokens * num_qo_heads must be below 2^30");
   if (b->num_blocks < 1 || b->num_blocks > pa::kMaxListed)
     return set_err(PA_ERR_UNSUPPORTED, "num_blocks must lie in [1, " + std::to_string(pa::kMaxListed) + "]");
-  if (!workspace || !aligned(workspace, 256))
-    return set_err(PA_ERR_INVALID_ARG, "a 256-byte aligned workspace is required");
   s = device_sms(&shape->num_sms);
   if (s != PA_OK) return s;
-  shape->D = cache->head_dim;
-  shape->Hkv = cache->num_kv_heads;
-  shape->G = b->num_qo_heads / cache->num_kv_heads;
+  shape->D = D;
+  shape->Hkv = Hkv;
+  shape->G = b->num_qo_heads / Hkv;
   shape->num_tokens = b->num_tokens;
   shape->num_blocks = b->num_blocks;
   shape->max_pages = b->max_pages;
+  shape->batch = b->batch_size;
+  shape->page_size = page_size;
+  shape->max_qo_len = b->max_qo_len;
+  return PA_OK;
+}
+
+// What the selection and the attention both check.
+pagedattn_status check_batch(const pagedattn_kv_cache* cache, const pagedattn_block_batch* b, const int32_t* blocks,
+                             const void* q, int64_t q_stride, void* workspace, size_t workspace_bytes,
+                             pa::BlockParams* p, pa::BlockShape* shape, pa::BlockLayout* lay, bool* empty) {
+  pagedattn_status s = check_cache(cache, &p->g);
+  if (s != PA_OK) return s;
+  if (!workspace || !aligned(workspace, 256))
+    return set_err(PA_ERR_INVALID_ARG, "a 256-byte aligned workspace is required");
+  s = check_shape(cache->num_kv_heads, cache->head_dim, cache->page_size, b, shape);
+  if (s != PA_OK) return s;
   *lay = pa::block_layout(*shape);
   if (workspace_bytes < lay->total)
     return set_err(PA_ERR_WORKSPACE_TOO_SMALL, "workspace needs " + std::to_string(lay->total) + " bytes, got " +
@@ -134,6 +145,12 @@ pagedattn_status check_batch(const pagedattn_kv_cache* cache, const pagedattn_bl
   p->keys = reinterpret_cast<uint32_t*>(ws + lay->off_scratch);
   p->part_o = reinterpret_cast<float*>(ws + lay->off_scratch);
   p->part_lse = reinterpret_cast<float*>(ws + lay->off_part_lse);
+  p->tile_indptr = reinterpret_cast<int32_t*>(ws + lay->off_indptr);
+  p->small_indptr = p->tile_indptr + b->batch_size + 1;
+  p->items = reinterpret_cast<pa::BlockItem*>(ws + lay->off_items);
+  p->entries = reinterpret_cast<int2*>(ws + lay->off_entries);
+  p->masks = reinterpret_cast<uint16_t*>(ws + lay->off_masks);
+  p->hnd = cache->kv_layout == PA_LAYOUT_HND;
   p->q_stride = q_stride;
   p->batch = b->batch_size;
   p->num_page_indices = b->num_page_indices;
@@ -172,7 +189,15 @@ BlockLayout block_layout(const BlockShape& s) {
   const size_t keys = size_t(rows) * s.max_pages * 4, states = size_t(parts) * s.D * 4;
   l.off_part_lse = l.off_scratch + up(states);
   const size_t attend_end = l.off_part_lse + up(size_t(parts) * 4);
-  l.total = l.off_scratch + up(keys) > attend_end ? l.off_scratch + up(keys) : attend_end;
+  size_t end = l.off_scratch + up(keys) > attend_end ? l.off_scratch + up(keys) : attend_end;
+  // chunks: the requests' sums, and the unions of the lists with their masks
+  const TileShape t = tile_shape(s);
+  const size_t items = size_t(t.max_tiles) * s.Hkv;
+  l.off_indptr = end;
+  l.off_items = l.off_indptr + (t.use ? up((size_t(s.batch) + 1) * 8) : 0);
+  l.off_entries = l.off_items + up(items * sizeof(BlockItem));
+  l.off_masks = l.off_entries + up(items * t.max_entries * sizeof(int2));
+  l.total = l.off_masks + up(items * (t.use ? t.max_entries / (128 / s.page_size) : 0) * t.tokens * 2);
   return l;
 }
 
@@ -301,24 +326,12 @@ pagedattn_status pagedattn_kv_bounds(const pagedattn_kv_cache* cache, const int6
   return PA_OK;
 }
 
-pagedattn_status pagedattn_blocks_workspace_size(int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim,
-                                                 int32_t num_tokens, int32_t num_blocks, int32_t max_pages,
-                                                 size_t* bytes) {
+pagedattn_status pagedattn_blocks_workspace_size(int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
+                                                 const pagedattn_block_batch* batch, size_t* bytes) {
   if (!bytes) return set_err(PA_ERR_INVALID_ARG, "bytes is NULL");
-  pagedattn_status s = check_heads(num_qo_heads, num_kv_heads, head_dim);
-  if (s != PA_OK) return s;
-  if (num_tokens < 0 || max_pages < 0) return set_err(PA_ERR_INVALID_ARG, "a size is negative");
-  if (num_blocks < 1 || num_blocks > pa::kMaxListed)
-    return set_err(PA_ERR_UNSUPPORTED, "num_blocks must lie in [1, " + std::to_string(pa::kMaxListed) + "]");
   pa::BlockShape shape;
-  s = device_sms(&shape.num_sms);
+  const pagedattn_status s = check_shape(num_kv_heads, head_dim, page_size, batch, &shape);
   if (s != PA_OK) return s;
-  shape.D = head_dim;
-  shape.Hkv = num_kv_heads;
-  shape.G = num_qo_heads / num_kv_heads;
-  shape.num_tokens = num_tokens;
-  shape.num_blocks = num_blocks;
-  shape.max_pages = max_pages;
   *bytes = pa::block_layout(shape).total;
   return PA_OK;
 }
@@ -357,7 +370,34 @@ pagedattn_status pagedattn_blocks_run(const pagedattn_kv_cache* cache, const pag
   if (!aligned(lse, 4)) return set_err(PA_ERR_INVALID_ARG, "lse must be 4-byte aligned");
   p.out = out;
   p.lse = lse;
-  const cudaError_t e = pa::launch_block_attention(p, shape, cache->dtype, reinterpret_cast<cudaStream_t>(stream));
+  const pa::TileShape tiles = pa::tile_shape(shape);
+  cudaError_t e = cudaSuccess;
+  if (tiles.use) {
+    // tensor maps over the cache, and over q in boxes of a row tile's tokens
+    pa::HostPlan view;
+    view.D = shape.D;
+    view.Hkv = shape.Hkv;
+    view.Hq = batch->num_qo_heads;
+    view.G = shape.G;
+    view.ps = cache->page_size;
+    view.num_pages = cache->num_pages;
+    view.hnd = p.hnd;
+    view.dtype = cache->dtype;
+    view.T = batch->num_tokens;
+    CUtensorMap kv_map, q_map;
+    s = pa::encode_kv_map(&kv_map, view, cache->data, 64, uint32_t(cache->page_size), CU_TENSOR_MAP_SWIZZLE_128B);
+    if (s != PA_OK) return s;
+    s = pa::encode_q_map(&q_map, view, q, 128, batch->num_tokens > 1 ? q_stride : 0);
+    if (s != PA_OK) return s;
+    p.max_entries = tiles.max_entries;
+    p.max_tiles = tiles.max_tiles;
+    p.tile_tokens = tiles.tokens;
+    p.long_tokens = tiles.long_tokens;
+    e = pa::launch_block_tiles(p, shape, tiles, kv_map, q_map, cache->dtype, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_err(e, "chunk attention launch");
+    p.listed = 1;
+  }
+  e = pa::launch_block_attention(p, shape, cache->dtype, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_err(e, "attention launch");
   return PA_OK;
 }

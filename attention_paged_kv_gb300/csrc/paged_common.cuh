@@ -14,27 +14,33 @@ struct Query {
   bool there;  // false: no request has this token (or its tables cannot be)
 };
 
-// The request of token t, found by a warp: first where a decode step has it
-// (request t), then by a search in 32 parts over qo_indptr.
-__device__ __forceinline__ Query find_query(const BlockParams& p, int t) {
+// A warp's search in 32 parts: the last index in [0, n) with indptr[index] <= x, 0 if there is none.
+__device__ __forceinline__ int last_below(const int32_t* indptr, int n, int x) {
   const int lane = threadIdx.x & 31;
-  int b = t;
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const bool below = lane == 0 || (at < hi && indptr[at] <= x);
+    const unsigned m = __ballot_sync(0xffffffffu, below);
+    const int k = m == 0xffffffffu ? 31 : __ffs(~m) - 2;  // the last of the leading lanes below
+    lo += k * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+// The request of token t, found by a warp: first where the caller guesses it
+// (request t, in a decode step), then by a search over qo_indptr.
+__device__ __forceinline__ Query find_query(const BlockParams& p, int t, int guess) {
+  const int lane = threadIdx.x & 31;
+  int b = guess;
   int q0 = -1, q1 = -1;
-  if (t < p.batch) {
-    q0 = p.qo_indptr[t];
-    q1 = p.qo_indptr[t + 1];
+  if (b < p.batch) {
+    q0 = p.qo_indptr[b];
+    q1 = p.qo_indptr[b + 1];
   }
   if (!(q0 >= 0 && q0 <= t && t < q1)) {
-    int lo = 0, hi = p.batch + 1;  // the last entry that is <= t lies in [lo, hi), if any is
-    while (hi - lo > 1) {
-      const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-      const bool below = lane == 0 || (at < hi && p.qo_indptr[at] <= t);
-      const unsigned m = __ballot_sync(0xffffffffu, below);
-      const int n = m == 0xffffffffu ? 31 : __ffs(~m) - 2;  // the last of the leading lanes below
-      lo += n * step;
-      hi = min(hi, lo + step);
-    }
-    b = lo;
+    b = last_below(p.qo_indptr, p.batch + 1, t);
     if (b >= p.batch) return Query{0, 0, -1, false};
     q0 = p.qo_indptr[b];
     q1 = p.qo_indptr[b + 1];

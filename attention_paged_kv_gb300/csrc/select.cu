@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const BlockParams p) {
   const int item = blockIdx.x / p.slices, slice = blockIdx.x % p.slices;
   const int t = p.token0 + item / p.g.Hkv, h = item % p.g.Hkv;
   pdl_wait();
-  const Query mine = find_query(p, t);
+  const Query mine = find_query(p, t, t);
   if (!mine.there) return;
   const int n = mine.pos < 0 ? 0 : mine.pos / p.g.ps + 1;
   int32_t* out = p.blocks + (static_cast<int64_t>(t) * p.g.Hkv + h) * p.num_blocks;

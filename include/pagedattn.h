@@ -635,12 +635,14 @@ typedef struct {
                                       last ones up to the query's own; first >= 0, last >= 1,
                                       first + last <= num_blocks                          */
   int32_t max_pages;               /* most pages of a request                             */
+  int32_t max_qo_len;              /* bound of the requests' query lengths, by which the kernels
+                                      are chosen (a longer request is computed too, slower) */
 } pagedattn_block_batch;
 
-/* Bytes of workspace that the two calls below need on the current device. */
-PAGEDATTN_API pagedattn_status pagedattn_blocks_workspace_size(int32_t num_qo_heads, int32_t num_kv_heads,
-                                                 int32_t head_dim, int32_t num_tokens, int32_t num_blocks,
-                                                 int32_t max_pages, size_t* bytes);
+/* Bytes of workspace that the two calls below need on the current device, by the batch's sizes alone. */
+PAGEDATTN_API pagedattn_status pagedattn_blocks_workspace_size(int32_t num_kv_heads, int32_t head_dim,
+                                                 int32_t page_size, const pagedattn_block_batch* batch,
+                                                 size_t* bytes);
 
 /*
  * The blocks that each query attends to: for token t and kv head h the list
@@ -676,12 +678,19 @@ PAGEDATTN_API pagedattn_status pagedattn_select_blocks(const pagedattn_kv_cache*
 /*
  * Attention of each query over the keys of its listed blocks up to its own
  * position; softmax, out and lse as for pagedattn_run.  The lists are those of
- * pagedattn_select_blocks or the caller's own, in any order: negative entries and
- * blocks behind the query's own are skipped, a block listed twice counts
- * twice.  A query that sees no key gets zeros and lse = -inf.  Entries beyond
- * the request's pages are skipped and raise PA_DEV_BAD_INDEX, and so are
- * tables and page ids as above.  Rows from qo_indptr[batch_size] on are neither
- * read nor written.  out must not overlap q.
+ * pagedattn_select_blocks or the caller's own: ascending, negative entries behind
+ * them; blocks behind the query's own are skipped.  A query that sees no key gets
+ * zeros and lse = -inf.  So does one whose list is not ascending or names a
+ * block twice (PA_DEV_BAD_INDEX is raised), or who has more than max_pages blocks
+ * (PA_DEV_NO_ROOM).  Entries beyond the request's pages are skipped and raise
+ * PA_DEV_BAD_INDEX, as do tables and page ids as above.  Rows from
+ * qo_indptr[batch_size] on are neither read nor written.  out must not overlap q.
+ *
+ * Requests of few tokens (up to 32 packed rows) read the keys of each token by
+ * itself; longer ones, where max_qo_len allows for them and pages have 8 slots or
+ * more, those of many tokens together.  There a NaN or an infinity of K or V may reach
+ * other tokens of its request and kv head, and weights are rounded to the values' type
+ * (of bf16 values by up to 2^-8).
  */
 PAGEDATTN_API pagedattn_status pagedattn_blocks_run(const pagedattn_kv_cache* cache, const pagedattn_block_batch* batch,
                                       const int32_t* blocks, const void* q, int64_t q_stride, void* out, float* lse,

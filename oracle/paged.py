@@ -102,7 +102,11 @@ def attention(q, data, lists, qo_indptr, page_indptr, pages, last, page_size, hn
     av, sv, sabs, seen = np.zeros((T, Hq, D)), np.zeros((T, Hq, D)), np.zeros((T, Hq)), np.zeros((T, Hq), int)
     for i, (_, start, n, pos) in enumerate(queries(qo_indptr, page_indptr, last, page_size)):
         for h in range(Hkv):
-            mine = [int(e) for e in lists[i, h] if 0 <= e < n and e * page_size <= pos]
+            listed = [int(e) for e in lists[i, h]]
+            end = next((j for j, e in enumerate(listed) if e < 0), len(listed))
+            if any(e >= 0 for e in listed[end:]) or any(a >= b for a, b in zip(listed[:end], listed[1:end])):
+                continue  # out of order: as an empty list
+            mine = [e for e in listed[:end] if e < n and e * page_size <= pos]
             if not mine:
                 continue
             ids = np.asarray(pages)[start + np.array(mine)]

@@ -108,6 +108,7 @@ def test_bounds_refusals(cache, n, slots, status, text):
 BAD_BATCH = [
     (dict(num_qo_heads=3), {}, INVALID, "num_qo_heads"), (dict(num_qo_heads=2 * 129), {}, UNSUPPORTED, "128"),
     (dict(batch_size=-1), {}, INVALID, "negative"), (dict(max_pages=-1), {}, INVALID, "negative"),
+    (dict(max_qo_len=-1), {}, INVALID, "negative"),
     (dict(num_tokens=1 << 29), {}, UNSUPPORTED, "2^30"), (dict(num_blocks=0), {}, UNSUPPORTED, "num_blocks"),
     (dict(num_blocks=4097), {}, UNSUPPORTED, "num_blocks"), ({}, dict(workspace=None), INVALID, "workspace"),
     ({}, dict(workspace=FAKE + 128), INVALID, "workspace")]
@@ -119,7 +120,7 @@ BAD_BATCH = [
 def test_block_refusals(which, cache, batch, more, status, text):
     c = raw.KvCacheArgs(**{**CACHE, **cache})
     d = dict(qo_indptr=FAKE, kv_page_indptr=FAKE, kv_page_indices=FAKE, kv_last_page_len=FAKE, batch_size=2,
-             num_page_indices=8, num_tokens=2, num_qo_heads=8, num_blocks=4, first=1, last=1, max_pages=100)
+             num_page_indices=8, num_tokens=2, num_qo_heads=8, num_blocks=4, first=1, last=1, max_pages=100, max_qo_len=1)
     b = raw.BlockBatch(**{**d, **batch})
     m = {**dict(q=FAKE, blocks=FAKE, out=FAKE, workspace=FAKE), **more}
     lib = pa.load()
@@ -135,7 +136,7 @@ def test_block_refusals(which, cache, batch, more, status, text):
 @pytest.mark.parametrize("packed, struct, values", [
     ("_ROPE_ROWS", "RopeRows", [11, 12, 13, 14, 1 << 40, 1 << 41, 15, 16, 17, 1 << 42, 3, 4, 5, 6, 1, 1]),
     ("_KV_ROWS", "KvRows", [11, 12, 13, 14, 1 << 40, 1 << 41, 15, 16, 17, 18, 1 << 42, 19, 3, 4]),
-    ("_BLOCK_BATCH", "BlockBatch", [11, 12, 13, 14, 1, 2, 3, 4, 5, 6, 7, 8])])
+    ("_BLOCK_BATCH", "BlockBatch", [11, 12, 13, 14, 1, 2, 3, 4, 5, 6, 7, 8, 9])])
 def test_packed_arguments_are_the_structures(packed, struct, values):
     from attention_paged_kv_gb300 import _paged
     cls = getattr(raw, struct)
@@ -498,7 +499,8 @@ class Batch:
 
         logits  fp32 sums of exact products in D/16 steps, truncated at worst: ds = 2^-22 (D/16 + 2) sum |q k| scale
         p       exp2 and its argument: 2^-21, and ds; both in numerator and normaliser, hence twice
-        P       fp16: 2^-11 of each p, and 2^-25 of the largest where p is a subnormal; bf16: two terms, 2^-16
+        P       fp16: 2^-11 of each p, and 2^-25 of the largest where p is a subnormal; bf16: two terms, 2^-16; in
+                requests of more than 32 packed rows half a step of either type
         sums    fp32 products of P V over n / 16 steps: 2^-23 (n / 16 + 8) of sum p |v|
         out     half a step of its type
         lse     ds, 2^-20, the fp32 sum of n terms and the last roundings
@@ -507,7 +509,8 @@ class Batch:
         ref, ref_lse, sp = want
         eps = torch.finfo(self.dtype).eps / 2
         ds = 2.0 ** -22 * (self.D / 16 + 2) * sp["s"]
-        rel = 2 * (ds + 2.0 ** -21) + (2.0 ** -11 if self.dtype == torch.float16 else 2.0 ** -16) + \
+        long = np.repeat([q * (self.Hq // self.Hkv) > 32 and q > 1 and self.page >= 8 for q in self.qo], self.qo)[:, None]
+        rel = 2 * (ds + 2.0 ** -21) + np.where(long, eps, 2.0 ** -11 if self.dtype == torch.float16 else 2.0 ** -16) + \
             2.0 ** -23 * (sp["n"] / 16 + 8)
         bound = (rel[..., None] * sp["av"] + 2.0 ** -25 * sp["v"]) * (1 + eps) + eps * np.abs(ref) + 2.0 ** -25
         err = np.abs(host(out[:n]) - ref)
@@ -655,23 +658,79 @@ def test_no_room_for_the_pages():
 @gpu
 @pytest.mark.parametrize("dtype", TYPES)
 def test_attention_over_the_callers_lists(dtype):
-    """Lists in any order, with gaps, repeated, empty, of blocks that the query does not see, and of none that exist."""
-    b = Batch([1, 7, 1], [300, 130, 40], 8, 2, 128, 16, "NHD", dtype, seed=9)
+    """Lists without the query's own block, empty, of blocks that the query does not see, of none that exist, out of
+    order and with repetitions: for single tokens, and for chunks."""
+    b = Batch([1, 40, 1, 3], [300, 130, 40, 100], 8, 2, 128, 16, "NHD", dtype, seed=9)
     rng = np.random.default_rng(1)
-    lists = rng.integers(-3, 19, (9, 2, 12)).astype(np.int32)
-    pages = np.array([19] + [9] * 7 + [3])[:, None, None]
-    lists[lists >= pages] = -1
-    lists[0, 0] = [18, 3, 3, -1, 0, 18, -7, 3, 5, -1, 1, 2]
+    pages = np.repeat([19, 9, 3, 7], b.qo)
+    lists = np.full((b.T, 2, 12), -1, np.int32)
+    for i in range(b.T):
+        for h in range(2):
+            mine = np.sort(rng.permutation(pages[i])[: rng.integers(0, min(12, pages[i]) + 1)])
+            lists[i, h, : len(mine)] = mine
     lists[2, 1] = -1
-    lists[8] = [[2] * 12, [0] + [-1] * 11]
     a = b.attention(12)
     out, lse = a.run(b.q, b.cache, b.tables(), dev(lists))
     b.check(out, lse, b.want(lists))
     assert a.device_status() == 0 and torch.isneginf(lse[2, 4:]).all() and not out[2, 4:].any()
-    lists[4, 0, 3] = 9  # beyond its request's pages
-    out2, lse2 = a.run(b.q, b.cache, b.tables(), dev(lists))
-    assert a.device_status() == pa.PA_DEV_BAD_INDEX
-    b.check(out2, lse2, b.want(lists))
+    bad = lists.copy()
+    bad[0, 0, :3] = [4, 4, 5]
+    bad[7, 1, :4] = [0, 3, 2, 5]
+    bad[20, 0, :3] = [-1, 2, 3]
+    bad[1, 0] = [0, 1, 2, 1] + [-1] * 8  # the first token of a chunk
+    bad[41] = [[2, 2] + [-1] * 10, [0, -1, 1] + [-1] * 9]
+    for wrong in (bad, lists.copy()):
+        wrong[12, 0] = [0, 2, 9, 70] + [-1] * 8  # beyond its request's pages
+        wrong[-1, 1] = [0, 7] + [-1] * 10
+        out, lse = a.run(b.q, b.cache, b.tables(), dev(wrong))
+        assert a.device_status() == pa.PA_DEV_BAD_INDEX
+        b.check(out, lse, b.want(wrong))
+
+
+@gpu
+def test_requests_longer_than_they_may_be():
+    b = Batch([1, 20, 1], [200, 700, 100], 4, 2, 64, 16, "NHD", torch.float16, seed=6)
+    lists = b.attention(5).select(b.q, b.cache, b.tables())
+    want = b.attention(5).run(b.q, b.cache, b.tables(), lists)
+    a = b.attention(5, max_kv=208)
+    out, lse = a.run(b.q, b.cache, b.tables(), lists)
+    assert a.device_status() == raw.PA_DEV_NO_ROOM and not out[1:21].any() and torch.isneginf(lse[1:21]).all()
+    for r in (0, 21):
+        assert torch.equal(out[r], want[0][r]) and torch.equal(lse[r], want[1][r])
+
+
+CHUNKS = [
+    # qo, kv, Hq, Hkv, D, page, layout, blocks
+    ([300], [300], 8, 1, 128, 16, "NHD", 4), ([129, 64, 1, 5], [700, 64, 900, 40], 8, 2, 128, 16, "HND", 9),
+    ([200, 33], [1111, 2000], 16, 2, 64, 32, "NHD", 12), ([100], [450], 8, 1, 256, 64, "HND", 3),
+    ([70, 90], [500, 95], 20, 4, 128, 8, "NHD", 10), ([260], [700], 3, 3, 64, 128, "NHD", 2),
+    ([300], [901], 2, 1, 128, 16, "HND", 11), ([30, 17], [600, 300], 48, 1, 64, 16, "NHD", 8),
+    ([9], [1000], 128, 1, 128, 16, "NHD", 20), ([65], [200], 7, 1, 256, 8, "HND", 6),
+    ([40] * 30 + [1] * 50, [300] * 40 + [77] * 40, 8, 1, 64, 16, "NHD", 5), ([256], [20_000], 8, 1, 128, 16, "NHD", 30),
+    ([64, 0, 2, 64], [10, 5, 2, 100], 4, 1, 128, 16, "HND", 3)]
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("shape", CHUNKS, ids=lambda s: "%s-%d.%d.%d-p%d%s" % ("_".join(map(str, s[0][:4])), *s[2:7]))
+def test_chunks_equal_restated(shape, dtype):
+    """Long requests through row tiles, beside short ones; the same lists through single tokens agree within both bounds."""
+    *base, blocks = shape
+    b = Batch(*base, dtype, seed=len(shape[0]) + shape[4], pad=2)
+    a = b.attention(blocks, 1, 1)
+    lists = a.select(b.q, b.cache, b.tables())
+    np.testing.assert_array_equal(lists.cpu().numpy()[:-2], b.lists(blocks, 1, 1)[:-2])
+    want = b.want(lists.cpu().numpy())
+    out = torch.full((b.T, b.Hq, b.D), 9.0, dtype=dtype, device="cuda")
+    lse = torch.full((b.T, b.Hq), 9.0, device="cuda")
+    for _ in range(2):
+        a.run(b.q, b.cache, b.tables(), lists, out=out, lse=lse)
+        assert a.device_status() == 0
+        b.check(out, lse, want)
+        assert (out[-2:] == 9.0).all() and (lse[-2:] == 9.0).all()
+    one = b.attention(blocks, 1, 1, max_qo_len=1)  # a bound that does not hold costs time, not results
+    out, lse = one.run(b.q, b.cache, b.tables(), lists)
+    b.check(out, lse, want)
 
 
 @gpu
@@ -871,6 +930,7 @@ def test_captured_step_grows_requests(layout, dtype):
         want_q, size = paged.rope(host(q[:B]), (kv - 1)[None], w, None, True)
         check_rotated(turned[:B], want_q, size, dtype)
         b = Batch.__new__(Batch)
+        b.qo = [1] * B
         b.qo_indptr, b.page_indptr = np.arange(B + 1), tables.kv_page_indptr.cpu().numpy()
         b.pages, b.last = tables.kv_page_indices.cpu().numpy(), tables.kv_last_page_len.cpu().numpy()
         b.q, b.cache, b.page, b.Hq, b.Hkv, b.D, b.T, b.pad, b.hnd, b.dtype = turned, cache, page, Hq, Hkv, D, B + 2, 2, \
