@@ -8,8 +8,8 @@
 // lists, and masks each row to its own list: whatever the lists share is read
 // and multiplied once, and what they do not share costs less than by itself.
 //
-//   order_requests  cumulative counts of row tiles and of the tokens that are
-//                   left to the small-query kernel, over the requests
+//   order_requests  (select.cu) cumulative counts of row-tile pairs and of the tokens
+//                   that are left to the small-query kernel, over the requests
 //   union_lists     per row-tile pair and kv head: the union of the lists, in
 //                   ascending order, and for each 128 of its keys and each token
 //                   a mask of 16 bits, one for 8 keys
@@ -33,65 +33,6 @@ namespace {
 
 constexpr float kLn2f = 0.6931471805599453f;
 constexpr int kUnionThreads = 256;
-
-// ---------------------------------------------------------------------------
-// requests
-
-struct Span {  // a request, checked; qo_len 0 where its tables cannot be
-  int qo_start, qo_len, page_start, pages, kv_len;
-};
-__device__ __forceinline__ Span load_span(const BlockParams& p, int b, bool report) {
-  const int q0 = p.qo_indptr[b], q1 = p.qo_indptr[b + 1];
-  const int p0 = p.page_indptr[b], p1 = p.page_indptr[b + 1], last = p.last_page_len[b];
-  const long long kv = p1 > p0 ? static_cast<long long>(p1 - p0 - 1) * p.g.ps + last : 0;
-  const bool ok = q0 >= 0 && q1 >= q0 && q1 <= p.num_tokens && p0 >= 0 && p1 >= p0 && p1 <= p.num_page_indices &&
-                  (p1 == p0 || (last >= 1 && last <= p.g.ps)) && kv <= INT_MAX - 256;
-  if (!ok) {
-    if (report) atomicOr(p.status, PA_DEV_BAD_INDEX);
-    return Span{0, 0, 0, 0, 0};
-  }
-  return Span{q0, q1 - q0, p0, p1 - p0, static_cast<int>(kv)};
-}
-
-// One CTA: tile_indptr and small_indptr, [batch + 1] each.
-__global__ void __launch_bounds__(1024) order_requests_kernel(const BlockParams p) {
-  __shared__ int sums[2][32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  pdl_wait();
-  int base_t = 0, base_s = 0;
-  if (tid == 0) p.tile_indptr[0] = p.small_indptr[0] = 0;
-  for (int b0 = 0; b0 < p.batch; b0 += 1024) {
-    const int b = b0 + tid;
-    int tiles = 0, small = 0;
-    if (b < p.batch) {
-      const Span r = load_span(p, b, true);
-      if (r.qo_len >= p.long_tokens) tiles = min((r.qo_len + p.tile_tokens - 1) / p.tile_tokens, p.max_tiles);
-      else small = r.qo_len;
-    }
-    int t = tiles, s = small;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int a = __shfl_up_sync(0xffffffffu, t, d), c = __shfl_up_sync(0xffffffffu, s, d);
-      if (lane >= d) t += a, s += c;
-    }
-    __syncthreads();
-    if (lane == 31) sums[0][warp] = t, sums[1][warp] = s;
-    __syncthreads();
-    int all_t = 0, all_s = 0;
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) t += sums[0][w], s += sums[1][w];
-      all_t += sums[0][w], all_s += sums[1][w];
-    }
-    // (requests that overlap, in tables that cannot be, may have more tiles than
-    // there is room for: what is past it is left out)
-    if (b < p.batch) {
-      p.tile_indptr[b + 1] = min(base_t + t, p.max_tiles);
-      p.small_indptr[b + 1] = min(base_s + s, p.num_tokens);
-    }
-    base_t = min(base_t + all_t, p.max_tiles);
-    base_s = min(base_s + all_s, p.num_tokens);
-  }
-}
 
 // ---------------------------------------------------------------------------
 // unions
@@ -620,7 +561,7 @@ TileShape tile_shape(const BlockShape& s) {
 cudaError_t launch_block_tiles(BlockParams p, const BlockShape& s, const TileShape& t, const CUtensorMap& kv_map,
                                const CUtensorMap& q_map, int dtype, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = launch_pdl(order_requests_kernel, 1u, 1024u, size_t(0), stream, p);
+  cudaError_t e = launch_order_requests(p, stream);
   if (e != cudaSuccess) return e;
   e = set_smem_once(done, reinterpret_cast<const void*>(union_lists_kernel), 200 * 1024);
   if (e != cudaSuccess) return e;

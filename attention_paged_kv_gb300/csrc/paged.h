@@ -102,6 +102,12 @@ struct BlockLayout {
   size_t off_counters, off_scratch, off_part_lse, off_indptr, off_items, off_entries, off_masks, total;
   int32_t select_tokens;  // tokens of a launch of the selection
 };
+
+// Selection: tokens that a CTA takes together (0: each by itself), and the fewest of a request that goes there.
+struct SelectShape {
+  int32_t tokens, long_tokens, max_tiles, row;  // row: keys of a token in shared memory
+};
+SelectShape select_shape(const BlockShape& s);
 BlockLayout block_layout(const BlockShape& s);
 
 // Items are cut into slices only where they are fewer than this a SM.
@@ -116,6 +122,8 @@ AttendShape attend_shape(const BlockShape& s);
 // The largest slices * items and rows of a slice that attend_shape gives.
 int64_t attend_part_rows(const BlockShape& s);
 
+// tile_indptr and small_indptr: the requests of long_tokens or more in tiles of tile_tokens, and the others' tokens.
+cudaError_t launch_order_requests(const BlockParams& p, cudaStream_t stream);
 cudaError_t launch_select(BlockParams p, const BlockShape& s, int select_tokens, int dtype, cudaStream_t stream);
 // Chunks: which requests go to the tensor-core kernel, and what it keeps in the workspace.
 struct TileShape {

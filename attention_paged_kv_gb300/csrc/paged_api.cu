@@ -194,7 +194,7 @@ BlockLayout block_layout(const BlockShape& s) {
   const TileShape t = tile_shape(s);
   const size_t items = size_t(t.max_tiles) * s.Hkv;
   l.off_indptr = end;
-  l.off_items = l.off_indptr + (t.use ? up((size_t(s.batch) + 1) * 8) : 0);
+  l.off_items = l.off_indptr + (t.use || select_shape(s).tokens ? up((size_t(s.batch) + 1) * 8) : 0);
   l.off_entries = l.off_items + up(items * sizeof(BlockItem));
   l.off_masks = l.off_entries + up(items * t.max_entries * sizeof(int2));
   l.total = l.off_masks + up(items * (t.use ? t.max_entries / (128 / s.page_size) : 0) * t.tokens * 2);

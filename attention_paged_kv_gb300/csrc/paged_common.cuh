@@ -57,6 +57,22 @@ __device__ __forceinline__ Query find_query(const BlockParams& p, int t, int gue
   return Query{p0, p1 - p0, static_cast<int>(kv) - (q1 - q0) + (t - q0), true};
 }
 
+struct Span {  // a request, checked; qo_len 0 where its tables cannot be
+  int qo_start, qo_len, page_start, pages, kv_len;
+};
+__device__ __forceinline__ Span load_span(const BlockParams& p, int b, bool report) {
+  const int q0 = p.qo_indptr[b], q1 = p.qo_indptr[b + 1];
+  const int p0 = p.page_indptr[b], p1 = p.page_indptr[b + 1], last = p.last_page_len[b];
+  const long long kv = p1 > p0 ? static_cast<long long>(p1 - p0 - 1) * p.g.ps + last : 0;
+  const bool ok = q0 >= 0 && q1 >= q0 && q1 <= p.num_tokens && p0 >= 0 && p1 >= p0 && p1 <= p.num_page_indices &&
+                  (p1 == p0 || (last >= 1 && last <= p.g.ps)) && kv <= INT_MAX - 256;
+  if (!ok) {
+    if (report) atomicOr(p.status, PA_DEV_BAD_INDEX);
+    return Span{0, 0, 0, 0, 0};
+  }
+  return Span{q0, q1 - q0, p0, p1 - p0, static_cast<int>(kv)};
+}
+
 // A page id, checked.
 __device__ __forceinline__ int page_of(const BlockParams& p, int at) {
   int id = p.pages[at];

@@ -6,11 +6,16 @@
 // The sums are of whole numbers, so they come out alike in any order, and the
 // selection does not depend on how the work is cut.
 //
-// A CTA takes one query and kv head, or a slice of its pages where there are
-// few of them; scores go to a scratch row as unsigned keys in their order, and
-// the last slice to finish selects.  The k-th largest key is found by
+// Single tokens: a CTA takes one query and kv head, or a slice of its pages where
+// there are few of them; scores go to a scratch row as unsigned keys in their
+// order, and the last slice to finish selects.  The k-th largest key is found by
 // histograms over 2048 equal parts of the keys' range, then of the part that
 // holds it, until one key (or a part taken whole) is left.
+//
+// Chunks: a CTA takes up to 16 tokens of a request, whose scores for 8 pages at a
+// time are one m16n8k32 product of 8-bit integers: the bounds are read once for
+// all.  The keys stay in shared memory, and each warp selects for two of the
+// tokens by itself, with histograms over 256 parts.
 #include <cfloat>
 #include <cstring>
 
@@ -23,6 +28,7 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kKept = kKeptKeys;
+constexpr int kTileSmem = 192 * 1024;  // of a chunk's keys
 constexpr uint32_t kAlways = 0xFFFFFFFFu;  // above every score's key
 
 // Scores as unsigned numbers of the same order; -0 is 0, NaN is infinity.
@@ -212,6 +218,46 @@ __device__ void select_largest(Key key, int n, int k, int32_t* out, int* bins, S
   }
 }
 
+// One CTA: tile_indptr and small_indptr, [batch + 1] each.
+__global__ void __launch_bounds__(1024) order_requests_kernel(const BlockParams p) {
+  __shared__ int sums[2][32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  int base_t = 0, base_s = 0;
+  if (tid == 0) p.tile_indptr[0] = p.small_indptr[0] = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += 1024) {
+    const int b = b0 + tid;
+    int tiles = 0, small = 0;
+    if (b < p.batch) {
+      const Span r = load_span(p, b, true);
+      if (r.qo_len >= p.long_tokens) tiles = min((r.qo_len + p.tile_tokens - 1) / p.tile_tokens, p.max_tiles);
+      else small = r.qo_len;
+    }
+    int t = tiles, s = small;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, t, d), c = __shfl_up_sync(0xffffffffu, s, d);
+      if (lane >= d) t += a, s += c;
+    }
+    __syncthreads();
+    if (lane == 31) sums[0][warp] = t, sums[1][warp] = s;
+    __syncthreads();
+    int all_t = 0, all_s = 0;
+    for (int w = 0; w < 32; ++w) {
+      if (w < warp) t += sums[0][w], s += sums[1][w];
+      all_t += sums[0][w], all_s += sums[1][w];
+    }
+    // (requests that overlap, in tables that cannot be, may have more tiles than
+    // there is room for: what is past it is left out)
+    if (b < p.batch) {
+      p.tile_indptr[b + 1] = min(base_t + t, p.max_tiles);
+      p.small_indptr[b + 1] = min(base_s + s, p.num_tokens);
+    }
+    base_t = min(base_t + all_t, p.max_tiles);
+    base_s = min(base_s + all_s, p.num_tokens);
+  }
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) select_kernel(const BlockParams p) {
   constexpr int LPR = D / 32, RPW = 32 / LPR;  // lanes of a page's bounds, 64 bytes each; pages of a warp
@@ -223,18 +269,27 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const BlockParams p) {
   __shared__ uint32_t range[3];
   __shared__ int last_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int item = blockIdx.x / p.slices, slice = blockIdx.x % p.slices;
-  const int t = p.token0 + item / p.g.Hkv, h = item % p.g.Hkv;
   pdl_wait();
-  const Query mine = find_query(p, t, t);
-  if (!mine.there) return;
+  // an item for each token and kv head, or (listed) for those of the tokens that small_indptr counts
+  const unsigned works = p.listed ? unsigned(p.small_indptr[p.batch]) * p.g.Hkv : gridDim.x;
+  for (unsigned work = blockIdx.x; work < works; work += gridDim.x) {
+  __syncthreads();  // (shared memory of the item before)
+  const int item = work / p.slices, slice = work % p.slices;
+  const int h = item % p.g.Hkv;
+  int t = p.token0 + item / p.g.Hkv, guess = t;
+  if (p.listed) {
+    guess = last_below(p.small_indptr, p.batch + 1, t);
+    t = p.qo_indptr[guess] + t - p.small_indptr[guess];
+  }
+  const Query mine = find_query(p, t, guess);
+  if (!mine.there) continue;
   const int n = mine.pos < 0 ? 0 : mine.pos / p.g.ps + 1;
   int32_t* out = p.blocks + (static_cast<int64_t>(t) * p.g.Hkv + h) * p.num_blocks;
   if (n <= p.num_blocks || n > p.max_pages) {
     if (slice == 0)
       for (int i = tid; i < p.num_blocks; i += kThreads) out[i] = i < n && n <= p.num_blocks ? i : -1;
     if (n > p.num_blocks && tid == 0) atomicOr(p.status, PA_DEV_NO_ROOM);
-    return;
+    continue;
   }
   query_codes<T, D>(static_cast<const T*>(p.q) + t * p.q_stride + static_cast<int64_t>(h) * p.G * D, p.G, codes[warp]);
   __syncwarp();
@@ -289,7 +344,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const BlockParams p) {
       if (last_s) *counter = 0;
     }
     __syncthreads();
-    if (!last_s) return;
+    if (!last_s) continue;
     __threadfence();
   } else {
     __syncthreads();
@@ -303,6 +358,161 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const BlockParams p) {
   } else {
     select_largest([&](int i) { return __ldcg(row + i); }, n, p.num_blocks, out, bins, scan, range);
   }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// chunks
+
+constexpr int kTileRows = 16, kWarpBins = 256;
+
+__device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// As select_largest, by one warp: the first and last ones of n > k keys, and the
+// largest of the others.
+__device__ __forceinline__ void warp_select(const uint32_t* key, int n, int k, int first, int last, int32_t* out, int* bins) {
+  const int lane = threadIdx.x & 31;
+  const int lo = first, hi = n - last;
+  int need = k - first - last;
+  uint32_t least = 0xFFFFFFFFu, most = 0;
+  for (int i = lo + lane; i < hi; i += 32) {
+    const uint32_t x = key[i];
+    least = min(least, x);
+    most = max(most, x);
+  }
+  uint32_t base = __reduce_min_sync(0xffffffffu, least), top = __reduce_max_sync(0xffffffffu, most) + 1;
+  while (need > 0 && top - base > 1) {
+    const int shift = max(0, 32 - __clz(top - 1 - base) - 8);
+#pragma unroll
+    for (int i = 0; i < kWarpBins / 32; ++i) bins[i * 32 + lane] = 0;
+    __syncwarp();
+    for (int i = lo + lane; i < hi; i += 32) {
+      const uint32_t x = key[i];
+      if (x >= base && x < top) atomicAdd(bins + ((x - base) >> shift), 1);
+    }
+    __syncwarp();
+    int mine[kWarpBins / 32], sum = 0;  // lane l: the parts 255 - 8 l and down
+    const int4 p0 = *reinterpret_cast<const int4*>(bins + 248 - 8 * lane), p1 = *reinterpret_cast<const int4*>(bins + 252 - 8 * lane);
+    mine[0] = p1.w, mine[1] = p1.z, mine[2] = p1.y, mine[3] = p1.x, mine[4] = p0.w, mine[5] = p0.z, mine[6] = p0.y, mine[7] = p0.x;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += mine[i];
+    int above = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, above, d);
+      if (lane >= d) above += y;
+    }
+    above -= sum;
+    int part = -1, still = 0, count = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (above < need && above + mine[i] >= need) part = 255 - 8 * lane - i, still = need - above, count = mine[i];
+      above += mine[i];
+    }
+    const int src = __ffs(__ballot_sync(0xffffffffu, part >= 0)) - 1;
+    part = __shfl_sync(0xffffffffu, part, src);
+    need = __shfl_sync(0xffffffffu, still, src);
+    count = __shfl_sync(0xffffffffu, count, src);
+    const uint64_t end = static_cast<uint64_t>(base) + ((static_cast<uint64_t>(part) + 1) << shift);
+    base += static_cast<uint32_t>(part) << shift;
+    if (end < top) top = static_cast<uint32_t>(end);
+    if (need == count) {  // the part whole
+      top = base;
+      need = 0;
+    }
+    __syncwarp();
+  }
+  int at = 0;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const int i = i0 + lane;
+    const bool other = i >= lo && i < hi;
+    const uint32_t x = other ? key[i] : 0u;
+    const bool equal = other && x < top && x == base;
+    const unsigned equals = __ballot_sync(0xffffffffu, equal);
+    const bool take = i < n && (!other || x >= top || (equal && __popc(equals & ((1u << lane) - 1)) < need));
+    const unsigned taken = __ballot_sync(0xffffffffu, take);
+    if (take) out[at + __popc(taken & ((1u << lane) - 1))] = i;
+    at += __popc(taken);
+    need = max(0, need - __popc(equals));
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) select_tiles_kernel(const BlockParams p, const int row) {
+  constexpr int PIECE = D / 2;  // bytes of a page's bounds that a lane takes: a quarter
+  constexpr int STEPS = 2 * D / 32;
+  extern __shared__ __align__(16) uint32_t kept[];  // [token][row]
+  __shared__ __align__(16) int8_t codes[kTileRows][2 * D];
+  __shared__ __align__(16) int bins[kWarps][kWarpBins];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+  const int tile = blockIdx.x / p.g.Hkv, h = blockIdx.x % p.g.Hkv;
+  pdl_wait();
+  if (tile >= p.tile_indptr[p.batch]) return;
+  const int b = last_below(p.tile_indptr, p.batch + 1, tile);
+  const Span r = load_span(p, b, false);
+  const int q0 = (tile - p.tile_indptr[b]) * p.tile_tokens;
+  const int tokens = min(p.tile_tokens, r.qo_len - q0), token = r.qo_start + q0;
+  const int pos0 = r.kv_len - r.qo_len + q0;
+  // pages that the last token sees (of tokens that see more than there is room for none is selected)
+  const int end = pos0 + tokens - 1;
+  const int pages = end < 0 ? 0 : min((end >> p.g.ps_shift) + 1, p.max_pages);
+  if (pages > p.num_blocks) {
+    for (int i = warp; i < kTileRows; i += kWarps) {
+      if (i < tokens) {
+        query_codes<T, D>(static_cast<const T*>(p.q) + (token + i) * p.q_stride + static_cast<int64_t>(h) * p.G * D, p.G, codes[i]);
+      } else {
+        for (int c = lane; c < D / 2; c += 32) reinterpret_cast<uint32_t*>(codes[i])[c] = 0;
+      }
+    }
+    __syncthreads();
+    // k-step s takes bytes [8 s, 8 s + 8) of each lane's quarter of a row: the
+    // order of the sum is free
+    uint2 a[2][STEPS];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) a[i][s] = *reinterpret_cast<const uint2*>(codes[g + 8 * i] + t4 * PIECE + 8 * s);
+    for (int b0 = warp * 8; b0 < pages; b0 += kWarps * 8) {
+      const int mine = min(b0 + g, pages - 1);
+      const int64_t at = static_cast<int64_t>(page_of(p, r.page_start + mine)) * p.g.Hkv + h;
+      const uint4* src = reinterpret_cast<const uint4*>(p.bounds + at * (2 * D) + t4 * PIECE);
+      uint4 v[STEPS / 2];
+#pragma unroll
+      for (int i = 0; i < STEPS / 2; ++i) v[i] = __ldg(src + i);
+      const float scale = __ldg(p.bound_scales + at);
+      int c[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < STEPS / 2; ++i) {
+        mma_s8(c, a[0][2 * i].x, a[1][2 * i].x, a[0][2 * i].y, a[1][2 * i].y, v[i].x, v[i].y);
+        mma_s8(c, a[0][2 * i + 1].x, a[1][2 * i + 1].x, a[0][2 * i + 1].y, a[1][2 * i + 1].y, v[i].z, v[i].w);
+      }
+      // c: tokens g and g + 8, pages 2 t4 and the next
+      const float s0 = __shfl_sync(0xffffffffu, scale, 8 * t4), s1 = __shfl_sync(0xffffffffu, scale, 8 * t4 + 4);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (g + 8 * i < tokens)
+          *reinterpret_cast<uint2*>(kept + (g + 8 * i) * row + b0 + 2 * t4) =
+              make_uint2(order_key(__fmul_rn(static_cast<float>(c[2 * i]), s0)),
+                         order_key(__fmul_rn(static_cast<float>(c[2 * i + 1]), s1)));
+    }
+  }
+  __syncthreads();
+  for (int i = warp; i < tokens; i += kWarps) {
+    const int pos = pos0 + i, n = pos < 0 ? 0 : (pos >> p.g.ps_shift) + 1;
+    int32_t* out = p.blocks + (static_cast<int64_t>(token + i) * p.g.Hkv + h) * p.num_blocks;
+    if (n <= p.num_blocks || n > p.max_pages) {
+      for (int c = lane; c < p.num_blocks; c += 32) out[c] = c < n && n <= p.num_blocks ? c : -1;
+      if (n > p.num_blocks && lane == 0) atomicOr(p.status, PA_DEV_NO_ROOM);
+    } else {
+      warp_select(kept + i * row, n, p.num_blocks, p.first, p.last, out, bins[warp]);
+    }
+    __syncwarp();
+  }
 }
 
 template <typename T>
@@ -314,11 +524,68 @@ cudaError_t launch_t(const BlockParams& p, int D, unsigned grid, size_t smem, cu
   }
 }
 
+template <typename T, int D>
+cudaError_t launch_tiles_d(const BlockParams& p, const SelectShape& t, unsigned grid, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = set_smem_once(done, reinterpret_cast<const void*>(select_tiles_kernel<T, D>), kTileSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(select_tiles_kernel<T, D>, grid, kThreads, size_t(t.tokens) * t.row * 4, stream, p, t.row);
+}
+template <typename T>
+cudaError_t launch_tiles(const BlockParams& p, const SelectShape& t, int D, unsigned grid, cudaStream_t stream) {
+  switch (D) {
+    case 64: return launch_tiles_d<T, 64>(p, t, grid, stream);
+    case 128: return launch_tiles_d<T, 128>(p, t, grid, stream);
+    default: return launch_tiles_d<T, 256>(p, t, grid, stream);
+  }
+}
+
 }  // namespace
+
+SelectShape select_shape(const BlockShape& s) {
+  SelectShape t;
+  t.row = (s.max_pages + 31) / 32 * 32 + 8;  // (rows 8 banks apart)
+  t.tokens = kTileRows;
+  while (t.tokens >= 4 && int64_t(t.tokens) * t.row * 4 > kTileSmem) t.tokens /= 2;
+  t.long_tokens = 4;
+  if (t.tokens < 4 || s.max_qo_len < t.long_tokens || s.max_pages <= s.num_blocks || s.max_pages > kKeptKeys) t.tokens = 0;
+  const int64_t longs = s.num_tokens / t.long_tokens < s.batch ? s.num_tokens / t.long_tokens : s.batch;
+  t.max_tiles = t.tokens ? int32_t(s.num_tokens / t.tokens + longs) : 0;
+  return t;
+}
+
+cudaError_t launch_order_requests(const BlockParams& p, cudaStream_t stream) {
+  return launch_pdl(order_requests_kernel, 1u, 1024u, size_t(0), stream, p);
+}
 
 cudaError_t launch_select(BlockParams p, const BlockShape& s, int select_tokens, int dtype, cudaStream_t stream) {
   const int tokens = select_tokens;
+  const SelectShape chunk = select_shape(s);
+  if (chunk.tokens) {
+    p.tile_tokens = chunk.tokens;
+    p.long_tokens = chunk.long_tokens;
+    p.max_tiles = chunk.max_tiles;
+    cudaError_t e = launch_order_requests(p, stream);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = unsigned(chunk.max_tiles) * unsigned(s.Hkv);
+    if (grid > 0) {
+      e = dtype == PA_BF16 ? launch_tiles<__nv_bfloat16>(p, chunk, s.D, grid, stream)
+                           : launch_tiles<__half>(p, chunk, s.D, grid, stream);
+      if (e != cudaSuccess) return e;
+    }
+    p.listed = 1;
+  }
   const size_t smem = sizeof(uint32_t) * (s.max_pages < kKept ? s.max_pages : kKept);
+  if (p.listed) {
+    // how many tokens are listed the host does not know: CTAs for a full card, item after item
+    // (max_pages is at most kKept here: no keys go to the scratch)
+    const int64_t items = int64_t(s.num_tokens) * s.Hkv, most = int64_t(s.num_sms) * 4;
+    const unsigned grid = unsigned(items < most ? items : most);
+    p.token0 = 0;
+    p.slices = 1;
+    return dtype == PA_BF16 ? launch_t<__nv_bfloat16>(p, s.D, grid, smem, stream)
+                            : launch_t<__half>(p, s.D, grid, smem, stream);
+  }
   for (int t = 0; t < s.num_tokens; t += tokens) {
     const int n = s.num_tokens - t < tokens ? s.num_tokens - t : tokens;
     const int items = n * s.Hkv;

@@ -621,7 +621,8 @@ def test_selection_of_unusual_queries(kind):
 @gpu
 @pytest.mark.parametrize("qo, kv, Hkv, page, blocks", [
     ([1], [150_000], 1, 16, 128), ([1, 1], [30_000, 9000], 3, 1, 700), ([1], [20_000], 1, 1, 4096),
-    ([40, 2], [20_000, 12_000], 2, 1, 300), ([1] * 300, [2000] * 300, 2, 16, 20)], ids=str)
+    ([40, 2], [20_000, 12_000], 2, 1, 300), ([40, 2, 4], [5000, 300, 3900], 2, 1, 60), ([33, 1], [8000, 7000], 1, 1, 100),
+    ([100], [2900], 3, 1, 5), ([1] * 300, [2000] * 300, 2, 16, 20)], ids=str)
 def test_selection_of_many_pages(qo, kv, Hkv, page, blocks):
     """Items cut into slices; more keys than shared memory keeps; several launches of one call."""
     b = Batch(qo, kv, 2 * Hkv, Hkv, 64, page, "NHD", torch.float16, seed=8)
