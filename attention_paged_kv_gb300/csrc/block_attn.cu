@@ -26,7 +26,7 @@ namespace {
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kTile = 16;  // keys
 constexpr float kNone = -3.0e38f;  // a maximum before any key: finite, so that it can be subtracted
-constexpr float kHead = 7.f, kMost = 15.f;
+constexpr float kHead = 7.f, kRise = 8.f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 template <int D, int NT>
@@ -100,9 +100,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attend_kernel(cons
   const int chunks = (p.G + C::ROWS - 1) / C::ROWS;
   pdl_wait();
   // an item for each token, kv head and chunk of heads, or (listed) for those of the tokens that small_indptr counts
-  const unsigned works = p.listed ? unsigned(p.small_indptr[p.batch]) * p.g.Hkv * chunks : gridDim.x;
+  unsigned works = gridDim.x;
+  int slices = p.slices;
+  if (p.listed) {
+    const int items = p.small_indptr[p.batch] * p.g.Hkv * chunks;
+    slices = items > 0 ? max(1, min(p.slices, p.ctas / items)) : 1;
+    works = unsigned(items) * slices;
+  }
   for (unsigned work = blockIdx.x; work < works; work += gridDim.x) {
-  const int slice = work % p.slices, item = work / p.slices;
+  const int slice = work % slices, item = work / slices;
   const int chunk = item % chunks, h = item / chunks % p.g.Hkv;
   int t = item / (chunks * p.g.Hkv), guess = t;
   if (p.listed) {
@@ -161,8 +167,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attend_kernel(cons
     if (tid == 0) atomicOr(p.status, own >= p.max_pages ? PA_DEV_NO_ROOM : PA_DEV_BAD_INDEX);
     count = 0;
   }
-  const int lo = static_cast<int>(static_cast<int64_t>(count) * slice / p.slices);
-  const int entries = static_cast<int>(static_cast<int64_t>(count) * (slice + 1) / p.slices) - lo;
+  const int lo = static_cast<int>(static_cast<int64_t>(count) * slice / slices);
+  const int entries = static_cast<int>(static_cast<int64_t>(count) * (slice + 1) / slices) - lo;
   list += lo;
 
   // ---- the warp's tiles
@@ -171,30 +177,59 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attend_kernel(cons
   const uint32_t ring = smem_u32(smem) + warp * C::RING;
   const int64_t v_off = static_cast<int64_t>(p.g.ps) * p.g.Hkv * C::ROW;
   const int64_t slot_bytes = static_cast<int64_t>(p.g.slot_rows) * C::ROW;
+  const int row0 = lane / CH;  // of the rows that the lane copies, every RPI-th
   const uint8_t* data = static_cast<const uint8_t*>(p.data) + static_cast<int64_t>(h) * p.g.head_rows * C::ROW + lane % CH * 16;
-  // where key i of the slice lies, and whether the query sees it
+  const bool whole = p.g.ps_shift >= 4;  // a tile lies in one page
+  // Key i of the slice: the list's entry, and whether the query sees it.
   auto entry_of = [&](int i) { return list[min(i >> p.g.ps_shift, entries - 1)]; };
   auto seen = [&](int i, int word) { return i < keys && (word >= 0 || (i & (p.g.ps - 1)) <= limit); };
+  // Rows of a tile that lies in one page which the query sees: the first `live`.
+  auto live_of = [&](int tile, int word) { return word >= 0 ? kTile : limit + 1 - ((tile * kTile) & (p.g.ps - 1)); };
   auto copy = [&](int tile, int stage) {
     if (tile < tiles) {
-      const uint32_t dst = ring + stage * C::STAGE;
+      const uint32_t dst = ring + stage * C::STAGE + row0 * C::ROW;
+      const uint32_t piece = (lane % CH) ^ row0;
+      if (whole) {
+        const int word = list[tile >> (p.g.ps_shift - 4)], slot0 = (tile * kTile) & (p.g.ps - 1);
+        const int live = live_of(tile, word);
+        const uint8_t* k = data + static_cast<int64_t>(word & INT_MAX) * (2 * v_off) + (slot0 + row0) * slot_bytes;
+        const uint8_t* v = k + v_off;
+        if (live >= kTile) {
 #pragma unroll
-      for (int i = 0; i < kTile / RPI; ++i) {
-        const int r = i * RPI + lane / CH, k = tile * kTile + r;
-        const int word = entry_of(k);
-        const uint32_t bytes = seen(k, word) ? 16 : 0;
-        const uint8_t* src = data + static_cast<int64_t>(word & INT_MAX) * (2 * v_off) + (k & (p.g.ps - 1)) * slot_bytes;
-        const uint32_t at = dst + r * C::ROW + ((lane % CH) ^ (r & 7)) * 16;
-        cp_async16(at, src, bytes);
-        cp_async16(at + kTile * C::ROW, src + v_off, bytes);
+          for (int i = 0; i < kTile / RPI; ++i) {
+            const uint32_t at = dst + i * RPI * C::ROW + (piece ^ (i * RPI & 7)) * 16;
+            cp_async16(at, k + i * RPI * slot_bytes, 16);
+            cp_async16(at + kTile * C::ROW, v + i * RPI * slot_bytes, 16);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kTile / RPI; ++i) {
+            const uint32_t at = dst + i * RPI * C::ROW + (piece ^ (i * RPI & 7)) * 16;
+            const uint32_t bytes = i * RPI + row0 < live ? 16 : 0;
+            cp_async16(at, k + i * RPI * slot_bytes, bytes);
+            cp_async16(at + kTile * C::ROW, v + i * RPI * slot_bytes, bytes);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kTile / RPI; ++i) {
+          const int key = tile * kTile + i * RPI + row0;
+          const int word = entry_of(key);
+          const uint32_t bytes = seen(key, word) ? 16 : 0;
+          const uint8_t* src = data + static_cast<int64_t>(word & INT_MAX) * (2 * v_off) + (key & (p.g.ps - 1)) * slot_bytes;
+          const uint32_t at = dst + i * RPI * C::ROW + (piece ^ (i * RPI & 7)) * 16;
+          cp_async16(at, src, bytes);
+          cp_async16(at + kTile * C::ROW, src + v_off, bytes);
+        }
       }
     }
     cp_async_commit();
   };
-  float o[NT][KS][4], m[NT][2], l[NT][2];
+  // Running reference m, and the score above which it is set again.
+  float o[NT][KS][4], m[NT][2], l[NT][2], above[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    m[n][0] = m[n][1] = kNone;
+    m[n][0] = m[n][1] = above[n][0] = above[n][1] = kNone;
     l[n][0] = l[n][1] = 0.f;
 #pragma unroll
     for (int k = 0; k < KS; ++k)
@@ -222,16 +257,30 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attend_kernel(cons
 #pragma unroll
       for (int n = 0; n < NT; ++n) mma<T>(s[n], a, qf[n][k][0], qf[n][k][1]);
     }
-    const int k0 = tile * kTile + g;
-    const bool see0 = seen(k0, entry_of(k0)), see1 = seen(k0 + 8, entry_of(k0 + 8));
+    bool see0 = true, see1 = true, masked = false;
+    if (whole) {
+      const int word = list[tile >> (p.g.ps_shift - 4)];
+      if (word < 0) {
+        const int live = live_of(tile, word);
+        masked = live < kTile;
+        see0 = g < live, see1 = g + 8 < live;
+      }
+    } else {
+      const int k0 = tile * kTile + g;
+      masked = true;
+      see0 = seen(k0, entry_of(k0)), see1 = seen(k0 + 8, entry_of(k0 + 8));
+    }
+    if (masked) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[n][i] = (i < 2 ? see0 : see1) ? s[n][i] : -INFINITY;
+    }
     bool over = false;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[n][i] = (i < 2 ? see0 : see1) ? s[n][i] * p.scale_log2 : -INFINITY;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) over = over || fmaxf(s[n][i], s[n][i + 2]) > m[n][i] + kMost;
-    }
+      for (int i = 0; i < 2; ++i) over = over || fmaxf(s[n][i], s[n][i + 2]) > above[n][i];
     if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -240,9 +289,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attend_kernel(cons
           float top = fmaxf(s[n][i], s[n][i + 2]);
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-          if (top > m[n][i] + kMost) {
-            const float f = ex2(m[n][i] - (top - kHead));
-            m[n][i] = top - kHead;
+          if (top > above[n][i]) {
+            const float next = top * p.scale_log2 - kHead, f = ex2(m[n][i] - next);
+            above[n][i] = top + kRise / p.scale_log2;
+            m[n][i] = next;
             l[n][i] *= f;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
@@ -257,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attend_kernel(cons
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[n][i] = ex2(s[n][i] - m[n][i & 1]);
+      for (int i = 0; i < 4; ++i) s[n][i] = ex2(fmaf(s[n][i], p.scale_log2, -m[n][i & 1]));
       l[n][0] += s[n][0] + s[n][2];
       l[n][1] += s[n][1] + s[n][3];
 #pragma unroll
@@ -327,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attend_kernel(cons
       acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    if (p.slices == 1) {
+    if (slices == 1) {
       store4<T>(p.out, q_row + row, D, col, acc, inv);
       if (col == 0 && p.lse) p.lse[q_row + row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
     } else {
@@ -335,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attend_kernel(cons
       if (col == 0) p.part_lse[part + row] = sum == 0.f ? -INFINITY : top + log2f(sum);
     }
   }
-  if (p.slices == 1) {
+  if (slices == 1) {
     __syncthreads();  // the list and the states have been read
     continue;
   }
@@ -344,20 +394,20 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attend_kernel(cons
   __threadfence();
   __syncthreads();
   if (tid == 0) {
-    last_s = atomicAdd(p.counters + item, 1) == p.slices - 1;
+    last_s = atomicAdd(p.counters + item, 1) == slices - 1;
     if (last_s) p.counters[item] = 0;
   }
   __syncthreads();
   if (!last_s) continue;
   __threadfence();
-  const int64_t first = static_cast<int64_t>(item) * p.slices * C::ROWS;
+  const int64_t first = static_cast<int64_t>(item) * slices * C::ROWS;
   for (int i = tid; i < heads * COLS; i += kThreads) {
     const int row = i / COLS, col = i % COLS * 4;
     float top = kNone, sum = 0.f;
-    for (int k = 0; k < p.slices; ++k) top = fmaxf(top, __ldcg(p.part_lse + first + k * C::ROWS + row));
+    for (int k = 0; k < slices; ++k) top = fmaxf(top, __ldcg(p.part_lse + first + k * C::ROWS + row));
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int k = 0; k < p.slices; ++k) {
+    for (int k = 0; k < slices; ++k) {
       const int64_t r = first + k * C::ROWS + row;
       const float f = ex2(__ldcg(p.part_lse + r) - top);
       const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + r * D + col));
@@ -394,12 +444,9 @@ AttendShape attend_shape(const BlockShape& s) {
   AttendShape a;
   a.rows = s.D == 256 || s.G <= 8 ? 8 : 16;
   a.chunks = (s.G + a.rows - 1) / a.rows;
-  const int64_t items = int64_t(s.num_tokens) * s.Hkv * a.chunks;
-  const int64_t ctas = int64_t(s.num_sms) * (s.D == 64 ? 3 : (s.D == 128 ? 2 : 1));
-  // as many slices as the card has room for CTAs, of 128 keys or more each
-  int64_t n = items > 0 ? ctas / items : 1;
-  const int64_t keys = int64_t(s.num_blocks) * s.page_size;
-  if (n > keys / 128) n = keys / 128;
+  a.ctas = s.num_sms * (s.D == 64 ? 3 : (s.D == 128 ? 2 : 1));
+  // slices of 128 keys or more
+  int64_t n = int64_t(s.num_blocks) * s.page_size / 128;
   if (n > s.num_blocks) n = s.num_blocks;
   if (n > kMaxSlices) n = kMaxSlices;
   a.slices = n < 1 ? 1 : int(n);
@@ -412,13 +459,22 @@ int64_t attend_part_rows(const BlockShape& s) {
 
 cudaError_t launch_block_attention(BlockParams p, const BlockShape& s, int dtype, cudaStream_t stream) {
   const AttendShape a = attend_shape(s);
-  p.slices = p.listed ? 1 : a.slices;
-  int64_t items = int64_t(s.num_tokens) * s.Hkv * a.chunks;
-  // how many tokens are listed the host does not know: CTAs for a full card, item after item
-  if (p.listed && items > int64_t(s.num_sms) * 6) items = int64_t(s.num_sms) * 6;
-  const unsigned grid = unsigned(items * p.slices);
-  return dtype == PA_BF16 ? launch_t<__nv_bfloat16>(p, s.D, a.rows, grid, stream)
-                          : launch_t<__half>(p, s.D, a.rows, grid, stream);
+  const int64_t items = int64_t(s.num_tokens) * s.Hkv * a.chunks;
+  p.slices = a.slices;
+  p.ctas = a.ctas;
+  int64_t grid;
+  if (p.listed) {
+    // how many tokens are listed the host does not know: CTAs for a full card or
+    // two, slice after slice (which the kernel cuts by the number that it finds)
+    grid = items * a.slices < 2 * a.ctas ? items * a.slices : 2 * a.ctas;
+  } else {
+    // as many slices as the card has room for CTAs
+    const int64_t fit = a.ctas / items;
+    p.slices = fit < 1 ? 1 : (fit < a.slices ? int(fit) : a.slices);
+    grid = items * p.slices;
+  }
+  return dtype == PA_BF16 ? launch_t<__nv_bfloat16>(p, s.D, a.rows, unsigned(grid), stream)
+                          : launch_t<__half>(p, s.D, a.rows, unsigned(grid), stream);
 }
 
 }  // namespace pa

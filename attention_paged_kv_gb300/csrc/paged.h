@@ -89,7 +89,8 @@ struct BlockParams {
   int32_t max_entries, max_tiles, tile_tokens, long_tokens, hnd;
   int32_t listed;  // attention: the tokens that small_indptr counts, not all
   int32_t batch, num_page_indices, num_tokens, Hq, G, num_blocks, first, last, max_pages;
-  int32_t token0, slices;  // first token of the launch; slices of an item
+  int32_t token0, slices;  // first token of the launch; slices of an item (listed attention: the most)
+  int32_t ctas;            // listed attention: CTAs of a full card
   float scale_log2;
 };
 
@@ -116,7 +117,7 @@ constexpr int kKeptKeys = 8192;  // of an item, in shared memory
 constexpr int kMaxListed = 4096;
 
 struct AttendShape {  // how a launch of the attention is cut
-  int32_t rows, chunks, slices;  // query heads a CTA, CTAs for a group, slices of a list
+  int32_t rows, chunks, slices, ctas;  // query heads a CTA, CTAs for a group, most slices of a list, CTAs of a full card
 };
 AttendShape attend_shape(const BlockShape& s);
 // The largest slices * items and rows of a slice that attend_shape gives.

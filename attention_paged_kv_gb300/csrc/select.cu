@@ -303,36 +303,42 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const BlockParams p) {
   const int hi = static_cast<int>(static_cast<int64_t>(n) * (slice + 1) / p.slices);
   uint32_t* row = p.keys + static_cast<int64_t>(item) * p.max_pages;
   const bool own = p.slices == 1 && n <= kKept;  // the keys need not leave the CTA
-  for (int b0 = lo + warp * RPW; b0 < hi; b0 += kWarps * RPW * U) {
-    int4 v[U][4];
-    float scale[U];
+  // 32 pages at a time: their ids in one load, a page's lanes then get theirs
+  for (int b0 = lo + warp * 32; b0 < hi; b0 += kWarps * 32) {
+    const int id = page_of(p, mine.page_start + min(b0 + lane, hi - 1));
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int b = min(b0 + u * kWarps * RPW + lane / LPR, hi - 1);
-      const int64_t at = static_cast<int64_t>(page_of(p, mine.page_start + b)) * p.g.Hkv + h;
-      const int4* src = reinterpret_cast<const int4*>(p.bounds + at * (2 * D)) + lane % LPR;
+    for (int w = 0; w < 32; w += U * RPW) {
+      int4 v[U][4];
+      float scale[U];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[u][i] = __ldg(src + i * LPR);
-      scale[u] = __ldg(p.bound_scales + at);
-    }
+      for (int u = 0; u < U; ++u) {
+        const int64_t at = static_cast<int64_t>(__shfl_sync(0xffffffffu, id, w + u * RPW + lane / LPR)) * p.g.Hkv + h;
+        const int4* src = reinterpret_cast<const int4*>(p.bounds + at * (2 * D)) + lane % LPR;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      int sum = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        sum = __dp4a(v[u][i].x, c[4 * i], sum);
-        sum = __dp4a(v[u][i].y, c[4 * i + 1], sum);
-        sum = __dp4a(v[u][i].z, c[4 * i + 2], sum);
-        sum = __dp4a(v[u][i].w, c[4 * i + 3], sum);
+        for (int i = 0; i < 4; ++i) v[u][i] = __ldg(src + i * LPR);
+        scale[u] = __ldg(p.bound_scales + at);
       }
 #pragma unroll
-      for (int d = 1; d < LPR; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      const int b = b0 + u * kWarps * RPW + lane / LPR;
-      if (lane % LPR == 0 && b < hi) {
-        const uint32_t x = b < p.first || b >= n - p.last ? kAlways : order_key(__fmul_rn(static_cast<float>(sum), scale[u]));
-        if (own) kept[b] = x;
-        else row[b] = x;
+      for (int u = 0; u < U; ++u) {
+        int sum = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sum = __dp4a(v[u][i].x, c[4 * i], sum);
+          sum = __dp4a(v[u][i].y, c[4 * i + 1], sum);
+          sum = __dp4a(v[u][i].z, c[4 * i + 2], sum);
+          sum = __dp4a(v[u][i].w, c[4 * i + 3], sum);
+        }
+#pragma unroll
+        for (int d = 1; d < LPR; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        const int b = b0 + w + u * RPW + lane / LPR;
+        if (lane % LPR == 0 && b < hi) {
+          const uint32_t x =
+              b < p.first || b >= n - p.last ? kAlways : order_key(__fmul_rn(static_cast<float>(sum), scale[u]));
+          if (own) kept[b] = x;
+          else row[b] = x;
+        }
       }
+      if (b0 + w + U * RPW >= hi) break;
     }
   }
   if (p.slices > 1) {
@@ -374,27 +380,44 @@ __device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, ui
 }
 
 // As select_largest, by one warp: the first and last ones of n > k keys, and the
-// largest of the others.
+// largest of the others.  kRegs: of up to 32 * kRegs keys, held in registers; 0: of
+// any number.
+template <int kRegs>
 __device__ __forceinline__ void warp_select(const uint32_t* key, int n, int k, int first, int last, int32_t* out, int* bins) {
+  constexpr int STRIPS = kRegs ? kRegs : 1;
   const int lane = threadIdx.x & 31;
   const int lo = first, hi = n - last;
   int need = k - first - last;
-  uint32_t least = 0xFFFFFFFFu, most = 0;
-  for (int i = lo + lane; i < hi; i += 32) {
-    const uint32_t x = key[i];
-    least = min(least, x);
-    most = max(most, x);
+  uint32_t held[STRIPS];  // 0, below every score's key, where there is none to choose
+  auto load = [&](int i) { return i >= lo && i < hi ? key[i] : 0u; };
+  if constexpr (kRegs > 0) {
+#pragma unroll
+    for (int s = 0; s < kRegs; ++s) held[s] = load(32 * s + lane);
   }
-  uint32_t base = __reduce_min_sync(0xffffffffu, least), top = __reduce_max_sync(0xffffffffu, most) + 1;
+  // f(strip's first index, the lane's key of the strip)
+  auto each = [&](auto&& f) {
+    if constexpr (kRegs > 0) {
+#pragma unroll
+      for (int s = 0; s < kRegs; ++s)
+        if (32 * s < n) f(32 * s, held[s]);
+    } else {
+      for (int i = 0; i < n; i += 32) f(i, load(i + lane));
+    }
+  };
+  uint32_t least = 0xFFFFFFFFu, most = 0;
+  each([&](int, uint32_t x) {
+    least = min(least, x - 1);  // 0 is no key
+    most = max(most, x);
+  });
+  uint32_t base = __reduce_min_sync(0xffffffffu, least) + 1, top = __reduce_max_sync(0xffffffffu, most) + 1;
   while (need > 0 && top - base > 1) {
     const int shift = max(0, 32 - __clz(top - 1 - base) - 8);
 #pragma unroll
     for (int i = 0; i < kWarpBins / 32; ++i) bins[i * 32 + lane] = 0;
     __syncwarp();
-    for (int i = lo + lane; i < hi; i += 32) {
-      const uint32_t x = key[i];
+    each([&](int, uint32_t x) {
       if (x >= base && x < top) atomicAdd(bins + ((x - base) >> shift), 1);
-    }
+    });
     __syncwarp();
     int mine[kWarpBins / 32], sum = 0;  // lane l: the parts 255 - 8 l and down
     const int4 p0 = *reinterpret_cast<const int4*>(bins + 248 - 8 * lane), p1 = *reinterpret_cast<const int4*>(bins + 252 - 8 * lane);
@@ -428,18 +451,19 @@ __device__ __forceinline__ void warp_select(const uint32_t* key, int n, int k, i
     __syncwarp();
   }
   int at = 0;
-  for (int i0 = 0; i0 < n; i0 += 32) {
+  const unsigned before = (1u << lane) - 1;
+  each([&](int i0, uint32_t x) {
     const int i = i0 + lane;
-    const bool other = i >= lo && i < hi;
-    const uint32_t x = other ? key[i] : 0u;
-    const bool equal = other && x < top && x == base;
-    const unsigned equals = __ballot_sync(0xffffffffu, equal);
-    const bool take = i < n && (!other || x >= top || (equal && __popc(equals & ((1u << lane) - 1)) < need));
+    bool take = x >= top || (i < n && (i < lo || i >= hi));
+    if (need > 0) {
+      const unsigned equals = __ballot_sync(0xffffffffu, x < top && x == base);
+      take = take || (x < top && x == base && __popc(equals & before) < need);
+      need = max(0, need - __popc(equals));
+    }
     const unsigned taken = __ballot_sync(0xffffffffu, take);
-    if (take) out[at + __popc(taken & ((1u << lane) - 1))] = i;
+    if (take) out[at + __popc(taken & before)] = i;
     at += __popc(taken);
-    need = max(0, need - __popc(equals));
-  }
+  });
 }
 
 template <typename T, int D>
@@ -509,7 +533,10 @@ __global__ void __launch_bounds__(kThreads) select_tiles_kernel(const BlockParam
       for (int c = lane; c < p.num_blocks; c += 32) out[c] = c < n && n <= p.num_blocks ? c : -1;
       if (n > p.num_blocks && lane == 0) atomicOr(p.status, PA_DEV_NO_ROOM);
     } else {
-      warp_select(kept + i * row, n, p.num_blocks, p.first, p.last, out, bins[warp]);
+      // (a strip of 32 keys past n costs little, so few sizes do)
+      if (n <= 256) warp_select<8>(kept + i * row, n, p.num_blocks, p.first, p.last, out, bins[warp]);
+      else if (n <= 640) warp_select<20>(kept + i * row, n, p.num_blocks, p.first, p.last, out, bins[warp]);
+      else warp_select<0>(kept + i * row, n, p.num_blocks, p.first, p.last, out, bins[warp]);
     }
     __syncwarp();
   }
