@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(kUnionThreads) union_lists_kernel(const BlockP
     if (any) entries[at] = make_int2(page_of(p, r.page_start + e), e);
   }
   __syncthreads();  // (entries are read again below, by the CTA that wrote them)
+  pdl_launch();
   // masks, and the first 128-key step with a block that some token sees in part
   const int per = 128 / p.g.ps, bits = p.g.ps / 8;
   const int steps = (count + per - 1) / per;
@@ -206,16 +207,20 @@ __global__ void __launch_bounds__(TileCfg<D, NT>::THREADS, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
   // the longest tiles of a chunk, its last ones, first
-  const int tiles = p.tile_indptr[p.batch];
-  const int tile = tiles - 1 - static_cast<int>(blockIdx.x) / p.g.Hkv, h = blockIdx.x % p.g.Hkv;
+  const int tiles = p.tile_indptr[p.batch], parts = p.small_indptr[p.batch + 1];
+  const int place = static_cast<int>(blockIdx.x) / parts, part = static_cast<int>(blockIdx.x) - place * parts;
+  const int tile = tiles - 1 - place / p.g.Hkv, h = place % p.g.Hkv;
   if (tile < 0) return;
   const int64_t item = static_cast<int64_t>(tile) * p.g.Hkv + h;
   const BlockItem it = p.items[item];
   const int G = p.G, TQ = 128 / G;  // tokens of a row tile
   const bool has_b = NT == 2 && it.tokens > TQ;
   const int per = 128 >> p.g.ps_shift;  // pages of a step
-  const int steps = (it.entries + per - 1) / per;
-  const int2* entries = p.entries + item * p.max_entries;
+  // the part's steps of 128 keys, and what they hold of the union
+  const int all_steps = (it.entries + per - 1) / per;
+  const int step0 = all_steps * part / parts, steps = all_steps * (part + 1) / parts - step0;
+  const int count = min(it.entries - step0 * per, steps * per), diag = it.diag - step0;
+  const int2* entries = p.entries + item * p.max_entries + step0 * per;
 
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
@@ -247,7 +252,7 @@ __global__ void __launch_bounds__(TileCfg<D, NT>::THREADS, 1)
     uint64_t* empty = half ? empty_v : empty_k;
     const uint32_t ring = sbase + (half ? C::OFF_V : C::OFF_K);
     // the page of lane l of a step, read two steps ahead
-    auto page = [&](int j) { return lane < per && j * per + lane < it.entries ? entries[j * per + lane].x : 0; };
+    auto page = [&](int j) { return lane < per && j * per + lane < count ? entries[j * per + lane].x : 0; };
     if (!half && lane == 0 && steps > 0) {
       mbar_arrive_expect_tx(q_full, uint32_t((has_b ? 2 : 1) * NKB * TQ * G * 128));
 #pragma unroll
@@ -267,7 +272,7 @@ __global__ void __launch_bounds__(TileCfg<D, NT>::THREADS, 1)
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
       }
-      const int n = min(per, it.entries - j * per);
+      const int n = min(per, count - j * per);
       if (lane == 0) mbar_arrive_expect_tx(&full[st], uint32_t(n * p.g.ps * 128 * NKB));
       __syncwarp();
       if (lane < n) {
@@ -353,7 +358,7 @@ __global__ void __launch_bounds__(TileCfg<D, NT>::THREADS, 1)
     const int t_local = r / G, g = r - t_local * G, t = x * TQ + t_local;  // token of the item
     const bool real = t_local < TQ && t < it.tokens;
     const int pos = it.pos + t;
-    const uint16_t* masks = p.masks + item * (p.max_entries / per) * p.tile_tokens + (real ? t : 0);
+    const uint16_t* masks = p.masks + (item * (p.max_entries / per) + step0) * p.tile_tokens + (real ? t : 0);
     const float sl2 = p.scale_log2;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + lane_base + x * 128, o_col = tmem + lane_base + C::O_COL + x * 128;
@@ -373,13 +378,13 @@ __global__ void __launch_bounds__(TileCfg<D, NT>::THREADS, 1)
       tmem_wait_ld();
 #pragma unroll
       for (int i = 0; i < 128; ++i) asm volatile("" : "+r"(s[i]));
-      if (j >= it.diag || j == steps - 1) {
+      if (j >= diag || j == steps - 1) {
         // keys behind the row's position, and what no page of the step holds
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
           const int e = j * per + (c * 8 >> p.g.ps_shift);
-          const bool there = e < it.entries && (mask >> c & 1);
-          const int limit = there ? pos + 1 - (entries[min(e, it.entries - 1)].y * p.g.ps + (c * 8 & (p.g.ps - 1))) : 0;
+          const bool there = e < count && (mask >> c & 1);
+          const int limit = there ? pos + 1 - (entries[min(e, count - 1)].y * p.g.ps + (c * 8 & (p.g.ps - 1))) : 0;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             if (i >= limit) s[8 * c + i] = __float_as_uint(-INFINITY);
@@ -441,8 +446,8 @@ __global__ void __launch_bounds__(TileCfg<D, NT>::THREADS, 1)
       }
       // V rows of the last step that hold no key (0 * NaN would reach O)
       if (x == 0 && j == steps - 1) {
-        const int last = it.entries - 1 - j * per;
-        const int valid = last * p.g.ps + min(p.g.ps, it.kv_len - entries[it.entries - 1].y * p.g.ps);
+        const int last = count - 1 - j * per;
+        const int valid = last * p.g.ps + min(p.g.ps, it.kv_len - entries[count - 1].y * p.g.ps);
         if (valid < 128) {
           const int st = j % NST;
           ok = warp_wait(&full_v[st], (j / NST) & 1, abort_flag, p.status);
@@ -470,14 +475,7 @@ __global__ void __launch_bounds__(TileCfg<D, NT>::THREADS, 1)
       tc_fence_after();
       const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
       const int64_t row0 = static_cast<int64_t>(it.token) * p.Hq + static_cast<int64_t>(h) * G;
-      if (real && p.lse)
-        p.lse[row0 + static_cast<int64_t>(t) * p.Hq + g] =
-            l_sum == 0.f ? -INFINITY : ((m_ref == -INFINITY ? 0.f : m_ref) + log2f(l_sum)) * kLn2f;
-      // through the row tile's Q memory (free by now), whole rows at a time
-      uint8_t* own = smem + x * C::TILE + r * 128;
-#pragma unroll
-      for (int c4 = 0; c4 < D / 32; ++c4) {
-        uint32_t o[32];
+      auto column = [&](int c4, uint32_t(&o)[32]) {  // 32 of the row's values
         if (steps > 0) {
           tmem_ld32(o_col + c4 * 32, o);
           tmem_wait_ld(o);
@@ -485,25 +483,52 @@ __global__ void __launch_bounds__(TileCfg<D, NT>::THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0;
         }
+      };
+      if (parts > 1) {  // a part's state: normalised, in fp32, with its log-sum in base 2
+        const int64_t row = (static_cast<int64_t>(place) * parts + part) * (NT * 128) + x * 128 + r;
+        if (real) p.part_lse[row] = l_sum == 0.f ? -INFINITY : m_ref + log2f(l_sum);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int c = (c4 & 1) * 4 + v;
-          auto f = [&](int i) { return __uint_as_float(o[8 * v + i]) * inv; };
-          *reinterpret_cast<uint4*>(own + (c4 >> 1) * C::BLK + ((c ^ (r & 7)) << 4)) =
-              l_sum == 0.f ? make_uint4(0, 0, 0, 0)
-                           : make_uint4(Elt<T>::from_f2(f(0), f(1)), Elt<T>::from_f2(f(2), f(3)), Elt<T>::from_f2(f(4), f(5)),
-                                        Elt<T>::from_f2(f(6), f(7)));
+        for (int c4 = 0; c4 < D / 32; ++c4) {
+          uint32_t o[32];
+          column(c4, o);
+          if (real) {
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+              auto f = [&](int i) { return l_sum == 0.f ? 0.f : __uint_as_float(o[4 * v + i]) * inv; };
+              *reinterpret_cast<float4*>(p.part_o + row * D + c4 * 32 + v * 4) = make_float4(f(0), f(1), f(2), f(3));
+            }
+          }
         }
-      }
-      __syncwarp();
-      constexpr int LANES = D / 8;  // of a row
+      } else {
+        if (real && p.lse)
+          p.lse[row0 + static_cast<int64_t>(t) * p.Hq + g] =
+              l_sum == 0.f ? -INFINITY : ((m_ref == -INFINITY ? 0.f : m_ref) + log2f(l_sum)) * kLn2f;
+        // through the row tile's Q memory (free by now), whole rows at a time
+        uint8_t* own = smem + x * C::TILE + r * 128;
+#pragma unroll
+        for (int c4 = 0; c4 < D / 32; ++c4) {
+          uint32_t o[32];
+          column(c4, o);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const int c = (c4 & 1) * 4 + v;
+            auto f = [&](int i) { return __uint_as_float(o[8 * v + i]) * inv; };
+            *reinterpret_cast<uint4*>(own + (c4 >> 1) * C::BLK + ((c ^ (r & 7)) << 4)) =
+                l_sum == 0.f ? make_uint4(0, 0, 0, 0)
+                             : make_uint4(Elt<T>::from_f2(f(0), f(1)), Elt<T>::from_f2(f(2), f(3)), Elt<T>::from_f2(f(4), f(5)),
+                                          Elt<T>::from_f2(f(6), f(7)));
+          }
+        }
+        __syncwarp();
+        constexpr int LANES = D / 8;  // of a row
 #pragma unroll 4
-      for (int i = lane / LANES; i < 32; i += 32 / LANES) {
-        const int rr = (warp & 3) * 32 + i, tl = rr / G, c = lane % LANES;
-        if (tl < TQ && x * TQ + tl < it.tokens) {
-          const uint4 w = *reinterpret_cast<const uint4*>(smem + x * C::TILE + (c >> 3) * C::BLK + rr * 128 + (((c & 7) ^ (rr & 7)) << 4));
-          const int64_t row = row0 + static_cast<int64_t>(x * TQ + tl) * p.Hq + (rr - tl * G);
-          *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + row * D + c * 8) = w;
+        for (int i = lane / LANES; i < 32; i += 32 / LANES) {
+          const int rr = (warp & 3) * 32 + i, tl = rr / G, c = lane % LANES;
+          if (tl < TQ && x * TQ + tl < it.tokens) {
+            const uint4 w = *reinterpret_cast<const uint4*>(smem + x * C::TILE + (c >> 3) * C::BLK + rr * 128 + (((c & 7) ^ (rr & 7)) << 4));
+            const int64_t row = row0 + static_cast<int64_t>(x * TQ + tl) * p.Hq + (rr - tl * G);
+            *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + row * D + c * 8) = w;
+          }
         }
       }
     }
@@ -515,6 +540,38 @@ __global__ void __launch_bounds__(TileCfg<D, NT>::THREADS, 1)
   if (warp == C::WARP_MMA) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+  if (parts == 1) return;
+
+  // ---------------------------------------------------------------- the item's last part joins all
+  __shared__ int last_s;
+  __threadfence();
+  __syncthreads();
+  if (tid == 0) {
+    last_s = atomicAdd(p.counters + place, 1) == parts - 1;
+    if (last_s) p.counters[place] = 0;
+  }
+  __syncthreads();
+  if (!last_s) return;
+  __threadfence();
+  const int64_t first = static_cast<int64_t>(place) * parts * (NT * 128);
+  for (int i = tid; i < it.tokens * G * (D / 4); i += C::THREADS) {
+    const int rr = i / (D / 4), col = i % (D / 4) * 4, t = rr / G, g = rr - t * G;  // rr: without the rows that a tile leaves free
+    const int64_t row = first + t / TQ * 128 + t % TQ * G + g;
+    float top = -3.0e38f, sum = 0.f;
+    for (int k = 0; k < parts; ++k) top = fmaxf(top, __ldcg(p.part_lse + row + k * (NT * 128)));
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < parts; ++k) {
+      const float w = ex2(__ldcg(p.part_lse + row + k * (NT * 128)) - top);
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + (row + k * (NT * 128)) * D + col));
+      sum += w;
+      acc.x += w * v.x, acc.y += w * v.y, acc.z += w * v.z, acc.w += w * v.w;
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int64_t to = (static_cast<int64_t>(it.token) + t) * p.Hq + static_cast<int64_t>(h) * G + g;
+    *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + to * D + col) =
+        make_uint2(Elt<T>::from_f2(acc.x * inv, acc.y * inv), Elt<T>::from_f2(acc.z * inv, acc.w * inv));
+    if (col == 0 && p.lse) p.lse[to] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2f;
   }
 }
 
@@ -541,6 +598,10 @@ TileShape tile_shape(const BlockShape& s) {
   TileShape t;
   t.tokens = (s.D == 256 ? 1 : 2) * (128 / s.G);
   t.long_tokens = 32 / s.G + 1 > 2 ? 32 / s.G + 1 : 2;
+  t.rows = (s.D == 256 ? 1 : 2) * 128;
+  // below half a million keys of single tokens and kv heads (30 us there) the few
+  // tiles would take longer
+  t.least_long = int32_t((1 << 19) / (int64_t(s.Hkv) * s.num_blocks * s.page_size) + 1);
   const int words = (t.tokens + 31) / 32;
   t.union_smem = int64_t(s.max_pages) * words * 4;
   // pages of 8 slots or more (a TMA copy's rows keep the swizzle's period of 8),
@@ -569,8 +630,10 @@ cudaError_t launch_block_tiles(BlockParams p, const BlockShape& s, const TileSha
   if (grid == 0) return cudaSuccess;
   e = launch_pdl(union_lists_kernel, grid, unsigned(kUnionThreads), size_t(t.union_smem), stream, p);
   if (e != cudaSuccess) return e;
-  return dtype == PA_BF16 ? launch_t<__nv_bfloat16>(kv_map, q_map, p, s.D, grid, stream)
-                          : launch_t<__half>(kv_map, q_map, p, s.D, grid, stream);
+  // where items are few, up to two CTAs an SM for their parts
+  const unsigned ctas = grid > 2u * s.num_sms ? grid : 2u * s.num_sms;
+  return dtype == PA_BF16 ? launch_t<__nv_bfloat16>(kv_map, q_map, p, s.D, ctas, stream)
+                          : launch_t<__half>(kv_map, q_map, p, s.D, ctas, stream);
 }
 
 }  // namespace pa

@@ -80,14 +80,17 @@ struct BlockParams {
   float* part_o;      // attention: normalised partial states, [slice][rows][D]
   float* part_lse;    // their log-sums, base 2
   // chunks (block_prefill.cu)
-  int32_t *tile_indptr, *small_indptr;  // [batch + 1]: row-tile pairs of the requests before, tokens of the short ones
+  // [batch + 1]: row-tile pairs of the requests before, tokens of the short ones; behind these the parts of an item
+  int32_t *tile_indptr, *small_indptr;
   BlockItem* items;                     // [max_tiles][Hkv]
   int2* entries;                        // of each item, [max_entries]: page id, block
   uint16_t* masks;                      // of each item, [step of 128 keys][tile_tokens]: a bit for 8 keys
   int64_t q_stride;
   Kv4Geom g;
   int32_t max_entries, max_tiles, tile_tokens, long_tokens, hnd;
-  int32_t listed;  // attention: the tokens that small_indptr counts, not all
+  int32_t listed;      // the tokens that small_indptr counts, not all
+  int32_t least_long;  // tokens of long requests for which these are worth their own kernels
+  int32_t num_sms;
   int32_t batch, num_page_indices, num_tokens, Hq, G, num_blocks, first, last, max_pages;
   int32_t token0, slices;  // first token of the launch; slices of an item (listed attention: the most)
   int32_t ctas;            // listed attention: CTAs of a full card
@@ -114,6 +117,7 @@ BlockLayout block_layout(const BlockShape& s);
 // Items are cut into slices only where they are fewer than this a SM.
 constexpr int kCutItems = 4;
 constexpr int kKeptKeys = 8192;  // of an item, in shared memory
+constexpr int kMaxParts = 16;    // of a chunk's item, along its keys
 constexpr int kMaxListed = 4096;
 
 struct AttendShape {  // how a launch of the attention is cut
@@ -130,6 +134,7 @@ cudaError_t launch_select(BlockParams p, const BlockShape& s, int select_tokens,
 struct TileShape {
   bool use;
   int32_t tokens, long_tokens;     // of an item; the fewest of a request that goes there
+  int32_t rows, least_long;        // packed rows of an item; the fewest tokens of such requests in all
   int32_t max_tiles, max_entries;
   int64_t union_smem;
 };

@@ -151,6 +151,7 @@ pagedattn_status check_batch(const pagedattn_kv_cache* cache, const pagedattn_bl
   p->entries = reinterpret_cast<int2*>(ws + lay->off_entries);
   p->masks = reinterpret_cast<uint16_t*>(ws + lay->off_masks);
   p->hnd = cache->kv_layout == PA_LAYOUT_HND;
+  p->num_sms = shape->num_sms;
   p->q_stride = q_stride;
   p->batch = b->batch_size;
   p->num_page_indices = b->num_page_indices;
@@ -185,16 +186,17 @@ BlockLayout block_layout(const BlockShape& s) {
     rows = int64_t(kCutItems) * s.num_sms;
   }
   l.select_tokens = int32_t(tokens > 0 ? tokens : 1);
-  const int64_t parts = attend_part_rows(s);
+  const TileShape t = tile_shape(s);
+  const int64_t cut_rows = t.use ? int64_t(2) * s.num_sms * t.rows : 0;
+  const int64_t parts = attend_part_rows(s) > cut_rows ? attend_part_rows(s) : cut_rows;
   const size_t keys = size_t(rows) * s.max_pages * 4, states = size_t(parts) * s.D * 4;
   l.off_part_lse = l.off_scratch + up(states);
   const size_t attend_end = l.off_part_lse + up(size_t(parts) * 4);
   size_t end = l.off_scratch + up(keys) > attend_end ? l.off_scratch + up(keys) : attend_end;
   // chunks: the requests' sums, and the unions of the lists with their masks
-  const TileShape t = tile_shape(s);
   const size_t items = size_t(t.max_tiles) * s.Hkv;
   l.off_indptr = end;
-  l.off_items = l.off_indptr + (t.use || select_shape(s).tokens ? up((size_t(s.batch) + 1) * 8) : 0);
+  l.off_items = l.off_indptr + (t.use || select_shape(s).tokens ? up((size_t(s.batch) + 2) * 8) : 0);
   l.off_entries = l.off_items + up(items * sizeof(BlockItem));
   l.off_masks = l.off_entries + up(items * t.max_entries * sizeof(int2));
   l.total = l.off_masks + up(items * (t.use ? t.max_entries / (128 / s.page_size) : 0) * t.tokens * 2);
@@ -393,6 +395,7 @@ pagedattn_status pagedattn_blocks_run(const pagedattn_kv_cache* cache, const pag
     p.max_tiles = tiles.max_tiles;
     p.tile_tokens = tiles.tokens;
     p.long_tokens = tiles.long_tokens;
+    p.least_long = tiles.least_long;
     e = pa::launch_block_tiles(p, shape, tiles, kv_map, q_map, cache->dtype, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_err(e, "chunk attention launch");
     p.listed = 1;

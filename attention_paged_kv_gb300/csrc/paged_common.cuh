@@ -34,19 +34,18 @@ __device__ __forceinline__ int last_below(const int32_t* indptr, int n, int x) {
 __device__ __forceinline__ Query find_query(const BlockParams& p, int t, int guess) {
   const int lane = threadIdx.x & 31;
   int b = guess;
-  int q0 = -1, q1 = -1;
-  if (b < p.batch) {
-    q0 = p.qo_indptr[b];
-    q1 = p.qo_indptr[b + 1];
+  int q0 = -1, q1 = -1, p0 = 0, p1 = 0, last = 0;
+  if (b < p.batch) {  // all that is needed of it at once
+    q0 = p.qo_indptr[b], q1 = p.qo_indptr[b + 1];
+    p0 = p.page_indptr[b], p1 = p.page_indptr[b + 1], last = p.last_page_len[b];
   }
   if (!(q0 >= 0 && q0 <= t && t < q1)) {
     b = last_below(p.qo_indptr, p.batch + 1, t);
     if (b >= p.batch) return Query{0, 0, -1, false};
-    q0 = p.qo_indptr[b];
-    q1 = p.qo_indptr[b + 1];
+    q0 = p.qo_indptr[b], q1 = p.qo_indptr[b + 1];
+    p0 = p.page_indptr[b], p1 = p.page_indptr[b + 1], last = p.last_page_len[b];
     if (q0 > t) return Query{0, 0, -1, false};
   }
-  const int p0 = p.page_indptr[b], p1 = p.page_indptr[b + 1], last = p.last_page_len[b];
   const long long kv = p1 > p0 ? static_cast<long long>(p1 - p0 - 1) * p.g.ps + last : 0;
   const bool ok = q0 >= 0 && q1 > t && q1 <= p.num_tokens && p0 >= 0 && p1 >= p0 && p1 <= p.num_page_indices &&
                   (p1 == p0 || (last >= 1 && last <= p.g.ps)) && kv <= INT_MAX - 256;

@@ -21,7 +21,7 @@
 namespace pa {
 namespace {
 
-constexpr int kRowsThreads = 256;
+constexpr int kRowsThreads = 128;
 
 // cos and sin of x * turn / 2^64 turns.
 __device__ __forceinline__ float2 turned(int32_t x, uint64_t turn) {
@@ -261,7 +261,7 @@ cudaError_t launch_rows(RowsParams p, int parts, bool interleaved, int dtype, in
   for (int i = 0; i < parts; ++i) heads += p.part[i].heads;
   // the angles are made once a group: large ones where the card is full without
   // more, small ones for few tokens
-  p.group_heads = blocks * heads >= int64_t(num_sms) * 64 ? 16 : 4;
+  p.group_heads = blocks * heads >= int64_t(num_sms) * 128 ? 8 : 4;
   unsigned groups = 0;
   for (int i = 0; i < 3; ++i) {
     p.part[i].groups = i < parts ? (p.part[i].heads + p.group_heads - 1) / p.group_heads : 0;
@@ -276,9 +276,9 @@ cudaError_t launch_rows(RowsParams p, int parts, bool interleaved, int dtype, in
 }
 
 cudaError_t launch_bounds(BoundsParams p, int D, int dtype, int num_sms, cudaStream_t stream) {
-  // a warp a token where there are few (each may end a page), 32 where most do not
+  // a warp a token where there are few (each may end a page), up to 32 where most do not
   p.warp_tokens = 1;
-  while (p.warp_tokens < 32 && int64_t(p.n) * p.g.Hkv > int64_t(num_sms) * 64 * p.warp_tokens) p.warp_tokens *= 2;
+  while (p.warp_tokens < 32 && int64_t(p.n) * p.g.Hkv > int64_t(num_sms) * 32 * p.warp_tokens) p.warp_tokens *= 2;
   const int64_t per_block = int64_t(p.warp_tokens) * kBoundsWarps;
   const dim3 grid(static_cast<unsigned>((p.n + per_block - 1) / per_block), p.g.Hkv);
   const unsigned block = 32 * kBoundsWarps;

@@ -42,49 +42,63 @@ __device__ __forceinline__ uint32_t order_key(float s) {
 template <typename T, int D>
 __device__ __forceinline__ void query_codes(const T* q, int G, int8_t* codes) {
   constexpr int LANES = D / 8, ROWS = 32 / LANES;
+  constexpr int HELD = 4;  // rows of a lane that are kept between the two passes
   const int lane = threadIdx.x & 31, r = lane / LANES, c = lane % LANES;
+  auto row = [&](int g) { return __ldg(reinterpret_cast<const uint4*>(q + g * D + c * 8)); };
+  uint4 held[HELD];
+#pragma unroll
+  for (int i = 0; i < HELD; ++i) held[i] = r + i * ROWS < G ? row(r + i * ROWS) : make_uint4(0, 0, 0, 0);
   uint32_t top = 0;
-  for (int g = r; g < G; g += ROWS) {
-    const uint4 v = *reinterpret_cast<const uint4*>(q + g * D + c * 8);
+  auto look = [&](const uint4& v) {
     top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
                                  __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
-  }
-  top = max(top & 0xFFFFu, top >> 16);  // magnitudes have the order of their bits
+  };
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+  for (int i = 0; i < HELD; ++i) look(held[i]);
+  for (int g = r + HELD * ROWS; g < G; g += ROWS) look(row(g));
+  // magnitudes have the order of their bits
+  top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
   const float most = Elt<T>::to_f2(top).x;
-  float u[8], l[8];
+  // sums of the values and of their magnitudes: u = (size + sum) / 2, l = (sum - size) / 2
+  float sum[8], size[8], u[8], l[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) u[i] = l[i] = 0.f;
+  for (int i = 0; i < 8; ++i) sum[i] = size[i] = 0.f;
   if (most > 0.f && most < INFINITY) {
     int e;
     frexpf(most, &e);
     e = 15 - e;
-    const float f1 = pow2f(e / 2), f2 = pow2f(e - e / 2);  // 2^e may pass fp32's range
-    for (int g = r; g < G; g += ROWS) {
-      const uint4 v = *reinterpret_cast<const uint4*>(q + g * D + c * 8);
+    // x * 2^e rounded to a whole number (to even): its size is at most 2^15, so
+    // 3 * 2^22 added and taken away again does it.  2^e may pass fp32's range: in two steps.
+    const float f1 = pow2f(e / 2), f2 = pow2f(e - e / 2);
+    auto whole = [&](float x) { return fmaf(x * f1, f2, 12582912.f) - 12582912.f; };
+    auto add = [&](const uint4& v) {
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 x = Elt<T>::to_f2(w[i]);
-        const float a = rintf(x.x * f1 * f2), b = rintf(x.y * f1 * f2);
-        u[2 * i] += fmaxf(a, 0.f), l[2 * i] += fminf(a, 0.f);
-        u[2 * i + 1] += fmaxf(b, 0.f), l[2 * i + 1] += fminf(b, 0.f);
+        const float a = whole(x.x), b = whole(x.y);
+        sum[2 * i] += a, size[2 * i] += fabsf(a);
+        sum[2 * i + 1] += b, size[2 * i + 1] += fabsf(b);
       }
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < HELD; ++i)
+      if (i * ROWS < G) add(held[i]);
+    for (int g = r + HELD * ROWS; g < G; g += ROWS) add(row(g));
   }
   float m = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
 #pragma unroll
     for (int d = LANES; d < 32; d <<= 1) {
-      u[i] += __shfl_xor_sync(0xffffffffu, u[i], d);  // whole numbers below 2^24: exact
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
+      sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], d);  // whole numbers up to 2^22: exact
+      size[i] += __shfl_xor_sync(0xffffffffu, size[i], d);
     }
+    u[i] = 0.5f * (size[i] + sum[i]);
+    l[i] = 0.5f * (sum[i] - size[i]);
     m = fmaxf(m, fmaxf(u[i], -l[i]));
   }
-#pragma unroll
-  for (int d = 1; d < LANES; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));  // (not negative: in the order of its bits)
   const float f = m > 0.f ? 127.f * __frcp_rn(m) : 0.f;
   if (lane < LANES) {
     uint32_t cu[2] = {0, 0}, cl[2] = {0, 0};
@@ -218,20 +232,36 @@ __device__ void select_largest(Key key, int n, int k, int32_t* out, int* bins, S
   }
 }
 
-// One CTA: tile_indptr and small_indptr, [batch + 1] each.
+// One CTA: tile_indptr and small_indptr, [batch + 1] each, and the parts that
+// an item's keys are cut into.  Where the long requests have fewer than
+// least_long tokens in all, they are left to the kernel of single tokens.
 __global__ void __launch_bounds__(1024) order_requests_kernel(const BlockParams p) {
   __shared__ int sums[2][32];
+  __shared__ long long long_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) long_s = 0;
+  __syncthreads();
+  pdl_launch();  // (the next kernel's CTAs may take their places)
   pdl_wait();
+  int mine = 0;
+  for (int b = tid; b < p.batch; b += 1024) {
+    const int n = load_span(p, b, true).qo_len;
+    if (n >= p.long_tokens) mine = min(mine + n, 1 << 30);
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) mine = min(mine + __shfl_xor_sync(0xffffffffu, mine, d), 1 << 30);
+  if (lane == 0 && mine) atomicAdd(reinterpret_cast<unsigned long long*>(&long_s), static_cast<unsigned long long>(mine));
+  __syncthreads();
+  const int long_tokens = long_s < p.least_long ? INT_MAX : p.long_tokens;
   int base_t = 0, base_s = 0;
   if (tid == 0) p.tile_indptr[0] = p.small_indptr[0] = 0;
   for (int b0 = 0; b0 < p.batch; b0 += 1024) {
     const int b = b0 + tid;
     int tiles = 0, small = 0;
     if (b < p.batch) {
-      const Span r = load_span(p, b, true);
-      if (r.qo_len >= p.long_tokens) tiles = min((r.qo_len + p.tile_tokens - 1) / p.tile_tokens, p.max_tiles);
-      else small = r.qo_len;
+      const int n = load_span(p, b, false).qo_len;
+      if (n >= long_tokens) tiles = min((n + p.tile_tokens - 1) / p.tile_tokens, p.max_tiles);
+      else small = n;
     }
     int t = tiles, s = small;
 #pragma unroll
@@ -256,6 +286,18 @@ __global__ void __launch_bounds__(1024) order_requests_kernel(const BlockParams 
     base_t = min(base_t + all_t, p.max_tiles);
     base_s = min(base_s + all_s, p.num_tokens);
   }
+  if (tid == 0) {
+    // parts of an item: the number that gives the shortest run of whole waves, a
+    // part's start and end weighed as 1/16 of an item (5 us of 80)
+    const int items = base_t * p.g.Hkv;
+    int parts = 1;
+    float best = 3.0e38f;
+    for (int n = 1; n <= kMaxParts && (n == 1 || items * n <= 2 * p.num_sms); ++n) {
+      const float cost = static_cast<float>((items * n + p.num_sms - 1) / p.num_sms) * (1.f / n + 0.0625f);
+      if (cost < best) best = cost, parts = n;
+    }
+    p.small_indptr[p.batch + 1] = parts;
+  }
 }
 
 template <typename T, int D>
@@ -271,10 +313,16 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const BlockParams p) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
   // an item for each token and kv head, or (listed) for those of the tokens that small_indptr counts
-  const unsigned works = p.listed ? unsigned(p.small_indptr[p.batch]) * p.g.Hkv : gridDim.x;
+  unsigned works = gridDim.x;
+  int slices = p.slices;
+  if (p.listed) {
+    const int items = p.small_indptr[p.batch] * p.g.Hkv;
+    slices = items > 0 ? max(1, min(p.slices, 2 * p.num_sms / items)) : 1;
+    works = unsigned(items) * slices;
+  }
   for (unsigned work = blockIdx.x; work < works; work += gridDim.x) {
   __syncthreads();  // (shared memory of the item before)
-  const int item = work / p.slices, slice = work % p.slices;
+  const int item = work / slices, slice = work % slices;
   const int h = item % p.g.Hkv;
   int t = p.token0 + item / p.g.Hkv, guess = t;
   if (p.listed) {
@@ -291,6 +339,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const BlockParams p) {
     if (n > p.num_blocks && tid == 0) atomicOr(p.status, PA_DEV_NO_ROOM);
     continue;
   }
+  const int lo = static_cast<int>(static_cast<int64_t>(n) * slice / slices);
+  const int hi = static_cast<int>(static_cast<int64_t>(n) * (slice + 1) / slices);
   query_codes<T, D>(static_cast<const T*>(p.q) + t * p.q_stride + static_cast<int64_t>(h) * p.G * D, p.G, codes[warp]);
   __syncwarp();
   int c[16];
@@ -299,10 +349,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const BlockParams p) {
     const int4 v = *reinterpret_cast<const int4*>(codes[warp] + (i * LPR + lane % LPR) * 16);
     c[4 * i] = v.x, c[4 * i + 1] = v.y, c[4 * i + 2] = v.z, c[4 * i + 3] = v.w;
   }
-  const int lo = static_cast<int>(static_cast<int64_t>(n) * slice / p.slices);
-  const int hi = static_cast<int>(static_cast<int64_t>(n) * (slice + 1) / p.slices);
   uint32_t* row = p.keys + static_cast<int64_t>(item) * p.max_pages;
-  const bool own = p.slices == 1 && n <= kKept;  // the keys need not leave the CTA
+  const bool own = slices == 1 && n <= kKept;  // the keys need not leave the CTA
   // 32 pages at a time: their ids in one load, a page's lanes then get theirs
   for (int b0 = lo + warp * 32; b0 < hi; b0 += kWarps * 32) {
     const int id = page_of(p, mine.page_start + min(b0 + lane, hi - 1));
@@ -341,12 +389,12 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const BlockParams p) {
       if (b0 + w + U * RPW >= hi) break;
     }
   }
-  if (p.slices > 1) {
+  if (slices > 1) {
     __threadfence();
     __syncthreads();
     if (tid == 0) {
       int32_t* counter = p.counters + item;
-      last_s = atomicAdd(counter, 1) == p.slices - 1;
+      last_s = atomicAdd(counter, 1) == slices - 1;
       if (last_s) *counter = 0;
     }
     __syncthreads();
@@ -409,6 +457,7 @@ __device__ __forceinline__ void warp_select(const uint32_t* key, int n, int k, i
     least = min(least, x - 1);  // 0 is no key
     most = max(most, x);
   });
+  const unsigned before = (1u << lane) - 1;
   uint32_t base = __reduce_min_sync(0xffffffffu, least) + 1, top = __reduce_max_sync(0xffffffffu, most) + 1;
   while (need > 0 && top - base > 1) {
     const int shift = max(0, 32 - __clz(top - 1 - base) - 8);
@@ -444,14 +493,34 @@ __device__ __forceinline__ void warp_select(const uint32_t* key, int n, int k, i
     const uint64_t end = static_cast<uint64_t>(base) + ((static_cast<uint64_t>(part) + 1) << shift);
     base += static_cast<uint32_t>(part) << shift;
     if (end < top) top = static_cast<uint32_t>(end);
+    __syncwarp();
     if (need == count) {  // the part whole
       top = base;
       need = 0;
+    } else if (count <= 32) {  // a lane for each of its keys: the one with need - 1 larger ones is the border
+      int at = 0;
+      each([&](int, uint32_t x) {
+        const bool in = x >= base && x < top;
+        const unsigned some = __ballot_sync(0xffffffffu, in);
+        if (in) bins[at + __popc(some & before)] = static_cast<int>(x);
+        at += __popc(some);
+      });
+      __syncwarp();
+      const uint32_t x = lane < count ? static_cast<uint32_t>(bins[lane]) : 0u;
+      int larger = 0, equal = 0;
+      for (int i = 0; i < count; ++i) {
+        const uint32_t y = __shfl_sync(0xffffffffu, x, i);
+        larger += y > x;
+        equal += y == x;
+      }
+      const int border = __ffs(__ballot_sync(0xffffffffu, lane < count && larger < need && larger + equal >= need)) - 1;
+      base = __shfl_sync(0xffffffffu, x, border);
+      need -= __shfl_sync(0xffffffffu, larger, border);
+      top = base + 1;
+      __syncwarp();
     }
-    __syncwarp();
   }
   int at = 0;
-  const unsigned before = (1u << lane) - 1;
   each([&](int i0, uint32_t x) {
     const int i = i0 + lane;
     bool take = x >= top || (i < n && (i < lo || i >= hi));
@@ -467,8 +536,7 @@ __device__ __forceinline__ void warp_select(const uint32_t* key, int n, int k, i
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) select_tiles_kernel(const BlockParams p, const int row) {
-  constexpr int PIECE = D / 2;  // bytes of a page's bounds that a lane takes: a quarter
+__global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 4) select_tiles_kernel(const BlockParams p, const int row) {
   constexpr int STEPS = 2 * D / 32;
   extern __shared__ __align__(16) uint32_t kept[];  // [token][row]
   __shared__ __align__(16) int8_t codes[kTileRows][2 * D];
@@ -494,38 +562,45 @@ __global__ void __launch_bounds__(kThreads) select_tiles_kernel(const BlockParam
       }
     }
     __syncthreads();
-    // k-step s takes bytes [8 s, 8 s + 8) of each lane's quarter of a row: the
-    // order of the sum is free
+    // a lane takes every fourth piece of 16 bytes of a row, k-step s the half
+    // s % 2 of piece s / 2: the order of the sum is free
     uint2 a[2][STEPS];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int s = 0; s < STEPS; ++s) a[i][s] = *reinterpret_cast<const uint2*>(codes[g + 8 * i] + t4 * PIECE + 8 * s);
-    for (int b0 = warp * 8; b0 < pages; b0 += kWarps * 8) {
-      const int mine = min(b0 + g, pages - 1);
-      const int64_t at = static_cast<int64_t>(page_of(p, r.page_start + mine)) * p.g.Hkv + h;
-      const uint4* src = reinterpret_cast<const uint4*>(p.bounds + at * (2 * D) + t4 * PIECE);
-      uint4 v[STEPS / 2];
+      for (int s = 0; s < STEPS; ++s) a[i][s] = *reinterpret_cast<const uint2*>(codes[g + 8 * i] + ((s >> 1) * 4 + t4) * 16 + 8 * (s & 1));
+    // four steps of 8 pages at a time: their ids in one load
+    for (int c0 = warp; c0 * 8 < pages; c0 += 4 * kWarps) {
+      const int mine = (c0 + (lane >> 3) * kWarps) * 8 + (lane & 7);
+      const int id = page_of(p, r.page_start + min(mine, pages - 1));
+      for (int k = 0; k < 4; ++k) {
+        const int b0 = (c0 + k * kWarps) * 8;
+        if (b0 >= pages) break;
+        const int64_t at = static_cast<int64_t>(__shfl_sync(0xffffffffu, id, k * 8 + g)) * p.g.Hkv + h;
+        const uint4* src = reinterpret_cast<const uint4*>(p.bounds + at * (2 * D)) + t4;
+        uint4 v[STEPS / 2];
 #pragma unroll
-      for (int i = 0; i < STEPS / 2; ++i) v[i] = __ldg(src + i);
-      const float scale = __ldg(p.bound_scales + at);
-      int c[4] = {0, 0, 0, 0};
+        for (int i = 0; i < STEPS / 2; ++i) v[i] = __ldg(src + 4 * i);
+        const float scale = __ldg(p.bound_scales + at);
+        int c[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int i = 0; i < STEPS / 2; ++i) {
-        mma_s8(c, a[0][2 * i].x, a[1][2 * i].x, a[0][2 * i].y, a[1][2 * i].y, v[i].x, v[i].y);
-        mma_s8(c, a[0][2 * i + 1].x, a[1][2 * i + 1].x, a[0][2 * i + 1].y, a[1][2 * i + 1].y, v[i].z, v[i].w);
+        for (int i = 0; i < STEPS / 2; ++i) {
+          mma_s8(c, a[0][2 * i].x, a[1][2 * i].x, a[0][2 * i].y, a[1][2 * i].y, v[i].x, v[i].y);
+          mma_s8(c, a[0][2 * i + 1].x, a[1][2 * i + 1].x, a[0][2 * i + 1].y, a[1][2 * i + 1].y, v[i].z, v[i].w);
+        }
+        // c: tokens g and g + 8, pages 2 t4 and the next
+        const float s0 = __shfl_sync(0xffffffffu, scale, 8 * t4), s1 = __shfl_sync(0xffffffffu, scale, 8 * t4 + 4);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (g + 8 * i < tokens)
+            *reinterpret_cast<uint2*>(kept + (g + 8 * i) * row + b0 + 2 * t4) =
+                make_uint2(order_key(__fmul_rn(static_cast<float>(c[2 * i]), s0)),
+                           order_key(__fmul_rn(static_cast<float>(c[2 * i + 1]), s1)));
       }
-      // c: tokens g and g + 8, pages 2 t4 and the next
-      const float s0 = __shfl_sync(0xffffffffu, scale, 8 * t4), s1 = __shfl_sync(0xffffffffu, scale, 8 * t4 + 4);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (g + 8 * i < tokens)
-          *reinterpret_cast<uint2*>(kept + (g + 8 * i) * row + b0 + 2 * t4) =
-              make_uint2(order_key(__fmul_rn(static_cast<float>(c[2 * i]), s0)),
-                         order_key(__fmul_rn(static_cast<float>(c[2 * i + 1]), s1)));
     }
   }
   __syncthreads();
+  pdl_launch();
   for (int i = warp; i < tokens; i += kWarps) {
     const int pos = pos0 + i, n = pos < 0 ? 0 : (pos >> p.g.ps_shift) + 1;
     int32_t* out = p.blocks + (static_cast<int64_t>(token + i) * p.g.Hkv + h) * p.num_blocks;
@@ -535,7 +610,7 @@ __global__ void __launch_bounds__(kThreads) select_tiles_kernel(const BlockParam
     } else {
       // (a strip of 32 keys past n costs little, so few sizes do)
       if (n <= 256) warp_select<8>(kept + i * row, n, p.num_blocks, p.first, p.last, out, bins[warp]);
-      else if (n <= 640) warp_select<20>(kept + i * row, n, p.num_blocks, p.first, p.last, out, bins[warp]);
+      else if (n <= 512) warp_select<16>(kept + i * row, n, p.num_blocks, p.first, p.last, out, bins[warp]);
       else warp_select<0>(kept + i * row, n, p.num_blocks, p.first, p.last, out, bins[warp]);
     }
     __syncwarp();
@@ -588,10 +663,13 @@ cudaError_t launch_order_requests(const BlockParams& p, cudaStream_t stream) {
 cudaError_t launch_select(BlockParams p, const BlockShape& s, int select_tokens, int dtype, cudaStream_t stream) {
   const int tokens = select_tokens;
   const SelectShape chunk = select_shape(s);
+  p.num_sms = s.num_sms;
   if (chunk.tokens) {
     p.tile_tokens = chunk.tokens;
     p.long_tokens = chunk.long_tokens;
     p.max_tiles = chunk.max_tiles;
+    // fewer than the single tokens' CTAs of a full card are quicker there
+    p.least_long = 4 * s.num_sms / s.Hkv;
     cudaError_t e = launch_order_requests(p, stream);
     if (e != cudaSuccess) return e;
     const unsigned grid = unsigned(chunk.max_tiles) * unsigned(s.Hkv);
@@ -603,22 +681,24 @@ cudaError_t launch_select(BlockParams p, const BlockShape& s, int select_tokens,
     p.listed = 1;
   }
   const size_t smem = sizeof(uint32_t) * (s.max_pages < kKept ? s.max_pages : kKept);
+  // slices of 256 pages or more
+  int most = 1;
+  while (most < 64 && s.max_pages > 512 * most) most *= 2;
   if (p.listed) {
-    // how many tokens are listed the host does not know: CTAs for a full card, item after item
-    // (max_pages is at most kKept here: no keys go to the scratch)
-    const int64_t items = int64_t(s.num_tokens) * s.Hkv, most = int64_t(s.num_sms) * 4;
-    const unsigned grid = unsigned(items < most ? items : most);
+    // how many tokens are listed the host does not know: CTAs for a full card, slice after slice
+    const int64_t works = int64_t(s.num_tokens) * s.Hkv * most, full = int64_t(s.num_sms) * 4;
+    const unsigned grid = unsigned(works < full ? works : full);
     p.token0 = 0;
-    p.slices = 1;
+    p.slices = most;
     return dtype == PA_BF16 ? launch_t<__nv_bfloat16>(p, s.D, grid, smem, stream)
                             : launch_t<__half>(p, s.D, grid, smem, stream);
   }
   for (int t = 0; t < s.num_tokens; t += tokens) {
     const int n = s.num_tokens - t < tokens ? s.num_tokens - t : tokens;
     const int items = n * s.Hkv;
-    // slices of 256 pages or more, until the card has two CTAs an SM
+    // until the card has two CTAs an SM
     int slices = 1;
-    while (slices < 64 && items * slices < 2 * s.num_sms && s.max_pages > 512 * slices) slices *= 2;
+    while (slices < most && items * slices < 2 * s.num_sms) slices *= 2;
     p.token0 = t;
     p.slices = slices;
     const cudaError_t e = dtype == PA_BF16 ? launch_t<__nv_bfloat16>(p, s.D, unsigned(items * slices), smem, stream)

@@ -621,8 +621,8 @@ def test_selection_of_unusual_queries(kind):
 @gpu
 @pytest.mark.parametrize("qo, kv, Hkv, page, blocks", [
     ([1], [150_000], 1, 16, 128), ([1, 1], [30_000, 9000], 3, 1, 700), ([1], [20_000], 1, 1, 4096),
-    ([40, 2], [20_000, 12_000], 2, 1, 300), ([40, 2, 4], [5000, 300, 3900], 2, 1, 60), ([33, 1], [8000, 7000], 1, 1, 100),
-    ([100], [2900], 3, 1, 5), ([1] * 300, [2000] * 300, 2, 16, 20)], ids=str)
+    ([40, 2], [20_000, 12_000], 2, 1, 300), ([320, 2, 4], [5000, 300, 3900], 2, 1, 60),
+    ([310, 300, 1], [8000, 7000, 30], 1, 1, 100), ([210, 1], [2900, 8000], 3, 1, 5), ([1] * 300, [2000] * 300, 2, 16, 20)], ids=str)
 def test_selection_of_many_pages(qo, kv, Hkv, page, blocks):
     """Items cut into slices; more keys than shared memory keeps; several launches of one call."""
     b = Batch(qo, kv, 2 * Hkv, Hkv, 64, page, "NHD", torch.float16, seed=8)
@@ -658,19 +658,20 @@ def test_no_room_for_the_pages():
 
 @gpu
 @pytest.mark.parametrize("dtype", TYPES)
-def test_attention_over_the_callers_lists(dtype):
+@pytest.mark.parametrize("chunk, kv, blocks", [(40, 130, 12), (400, 1300, 64)])
+def test_attention_over_the_callers_lists(chunk, kv, blocks, dtype):
     """Lists without the query's own block, empty, of blocks that the query does not see, of none that exist, out of
     order and with repetitions: for single tokens, and for chunks."""
-    b = Batch([1, 40, 1, 3], [300, 130, 40, 100], 8, 2, 128, 16, "NHD", dtype, seed=9)
+    b = Batch([1, chunk, 1, 3], [300, kv, 40, 100], 8, 2, 128, 16, "NHD", dtype, seed=9)
     rng = np.random.default_rng(1)
-    pages = np.repeat([19, 9, 3, 7], b.qo)
-    lists = np.full((b.T, 2, 12), -1, np.int32)
+    pages = np.repeat([19, -(-kv // 16), 3, 7], b.qo)
+    lists = np.full((b.T, 2, blocks), -1, np.int32)
     for i in range(b.T):
         for h in range(2):
-            mine = np.sort(rng.permutation(pages[i])[: rng.integers(0, min(12, pages[i]) + 1)])
+            mine = np.sort(rng.permutation(pages[i])[: rng.integers(0, min(blocks, pages[i]) + 1)])
             lists[i, h, : len(mine)] = mine
     lists[2, 1] = -1
-    a = b.attention(12)
+    a = b.attention(blocks)
     out, lse = a.run(b.q, b.cache, b.tables(), dev(lists))
     b.check(out, lse, b.want(lists))
     assert a.device_status() == 0 and torch.isneginf(lse[2, 4:]).all() and not out[2, 4:].any()
@@ -678,37 +679,43 @@ def test_attention_over_the_callers_lists(dtype):
     bad[0, 0, :3] = [4, 4, 5]
     bad[7, 1, :4] = [0, 3, 2, 5]
     bad[20, 0, :3] = [-1, 2, 3]
-    bad[1, 0] = [0, 1, 2, 1] + [-1] * 8  # the first token of a chunk
-    bad[41] = [[2, 2] + [-1] * 10, [0, -1, 1] + [-1] * 9]
+    bad[1, 0, :5] = [0, 1, 2, 1, -1]  # the first token of a chunk
+    bad[chunk + 1, 0, :3] = [2, 2, -1]
+    bad[chunk + 1, 1, :4] = [0, -1, 1, -1]
     for wrong in (bad, lists.copy()):
-        wrong[12, 0] = [0, 2, 9, 70] + [-1] * 8  # beyond its request's pages
-        wrong[-1, 1] = [0, 7] + [-1] * 10
+        wrong[12, 0, :5] = [0, 2, pages[12], pages[12] + 70, -1]  # beyond its request's pages
+        wrong[12, 0, 5:] = -1
+        wrong[-1, 1, :3] = [0, 7, -1]
+        wrong[-1, 1, 3:] = -1
         out, lse = a.run(b.q, b.cache, b.tables(), dev(wrong))
         assert a.device_status() == pa.PA_DEV_BAD_INDEX
         b.check(out, lse, b.want(wrong))
 
 
 @gpu
-def test_requests_longer_than_they_may_be():
-    b = Batch([1, 20, 1], [200, 700, 100], 4, 2, 64, 16, "NHD", torch.float16, seed=6)
-    lists = b.attention(5).select(b.q, b.cache, b.tables())
-    want = b.attention(5).run(b.q, b.cache, b.tables(), lists)
-    a = b.attention(5, max_kv=208)
+@pytest.mark.parametrize("n, blocks", [(20, 5), (600, 60)])
+def test_requests_longer_than_they_may_be(n, blocks):
+    b = Batch([1, n, 1], [200, 700 + n, 100], 4, 2, 64, 16, "NHD", torch.float16, seed=6)
+    lists = b.attention(blocks).select(b.q, b.cache, b.tables())
+    want = b.attention(blocks).run(b.q, b.cache, b.tables(), lists)
+    a = b.attention(blocks, max_kv=208)
     out, lse = a.run(b.q, b.cache, b.tables(), lists)
-    assert a.device_status() == raw.PA_DEV_NO_ROOM and not out[1:21].any() and torch.isneginf(lse[1:21]).all()
-    for r in (0, 21):
+    assert a.device_status() == raw.PA_DEV_NO_ROOM and not out[1: n + 1].any() and torch.isneginf(lse[1: n + 1]).all()
+    for r in (0, n + 1):
         assert torch.equal(out[r], want[0][r]) and torch.equal(lse[r], want[1][r])
 
 
 CHUNKS = [
-    # qo, kv, Hq, Hkv, D, page, layout, blocks
-    ([300], [300], 8, 1, 128, 16, "NHD", 4), ([129, 64, 1, 5], [700, 64, 900, 40], 8, 2, 128, 16, "HND", 9),
-    ([200, 33], [1111, 2000], 16, 2, 64, 32, "NHD", 12), ([100], [450], 8, 1, 256, 64, "HND", 3),
-    ([70, 90], [500, 95], 20, 4, 128, 8, "NHD", 10), ([260], [700], 3, 3, 64, 128, "NHD", 2),
-    ([300], [901], 2, 1, 128, 16, "HND", 11), ([30, 17], [600, 300], 48, 1, 64, 16, "NHD", 8),
-    ([9], [1000], 128, 1, 128, 16, "NHD", 20), ([65], [200], 7, 1, 256, 8, "HND", 6),
-    ([40] * 30 + [1] * 50, [300] * 40 + [77] * 40, 8, 1, 64, 16, "NHD", 5), ([256], [20_000], 8, 1, 128, 16, "NHD", 30),
-    ([64, 0, 2, 64], [10, 5, 2, 100], 4, 1, 128, 16, "HND", 3)]
+    # qo, kv, Hq, Hkv, D, page, layout, blocks: long requests of half a million keys of single tokens or more
+    ([300], [900], 8, 1, 128, 16, "NHD", 128), ([129, 64, 1, 5], [3000, 64, 900, 40], 8, 2, 128, 16, "HND", 100),
+    ([200, 33], [1111, 2000], 16, 2, 64, 32, "NHD", 40), ([260], [6000], 8, 1, 256, 64, "HND", 40),
+    ([70, 90], [900, 95], 20, 4, 128, 8, "NHD", 110), ([260], [2500], 3, 3, 64, 128, "NHD", 6),
+    ([300], [2901], 2, 1, 128, 16, "HND", 120), ([150, 17], [1600, 300], 48, 1, 64, 16, "NHD", 200),
+    ([65], [1500], 72, 1, 64, 64, "NHD", 130), ([65], [700], 7, 1, 256, 8, "HND", 1100),
+    ([40] * 30 + [1] * 50, [300] * 40 + [77] * 40, 8, 1, 64, 16, "NHD", 30), ([256], [20_000], 8, 1, 128, 16, "NHD", 130),
+    ([64, 0, 2, 64], [10, 5, 2, 100], 4, 1, 128, 16, "HND", 4096), ([700], [4000], 8, 1, 128, 16, "NHD", 100),
+    ([300, 20], [3000, 500], 16, 2, 64, 16, "HND", 120), ([150], [5000], 4, 1, 256, 64, "NHD", 60),
+    ([300, 90, 4], [2000, 90, 900], 5, 1, 128, 32, "NHD", 60), ([40, 3], [700, 90], 8, 1, 128, 16, "NHD", 30)]
 
 
 @gpu
@@ -729,6 +736,8 @@ def test_chunks_equal_restated(shape, dtype):
         assert a.device_status() == 0
         b.check(out, lse, want)
         assert (out[-2:] == 9.0).all() and (lse[-2:] == 9.0).all()
+    long = sum(n for n in b.qo if n > 1 and n * (b.Hq // b.Hkv) > 32)
+    assert long * b.Hkv * blocks * b.page >= 1 << 19 or b.qo == [40, 3]
     one = b.attention(blocks, 1, 1, max_qo_len=1)  # a bound that does not hold costs time, not results
     out, lse = one.run(b.q, b.cache, b.tables(), lists)
     b.check(out, lse, want)
