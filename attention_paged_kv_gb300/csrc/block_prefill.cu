@@ -606,7 +606,7 @@ TileShape tile_shape(const BlockShape& s) {
   t.union_smem = int64_t(s.max_pages) * words * 4;
   // pages of 8 slots or more (a TMA copy's rows keep the swizzle's period of 8),
   // and unions that shared memory holds
-  t.use = s.max_qo_len >= t.long_tokens && s.page_size >= 8 && t.union_smem <= 200 * 1024;
+  t.use = s.max_qo_len >= t.long_tokens && s.num_tokens >= t.least_long && s.page_size >= 8 && t.union_smem <= 200 * 1024;
   if (!t.use) {
     t.max_tiles = t.max_entries = 0;
     return t;

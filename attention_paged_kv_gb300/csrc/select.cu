@@ -539,7 +539,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 4) select_tiles_kernel(const BlockParams p, const int row) {
   constexpr int STEPS = 2 * D / 32;
   extern __shared__ __align__(16) uint32_t kept[];  // [token][row]
-  __shared__ __align__(16) int8_t codes[kTileRows][2 * D];
+  __shared__ __align__(16) int8_t codes[kTileRows][2 * D + 64];  // (rows 64 bytes apart in the banks)
   __shared__ __align__(16) int bins[kWarps][kWarpBins];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
   const int tile = blockIdx.x / p.g.Hkv, h = blockIdx.x % p.g.Hkv;
@@ -562,13 +562,13 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 4) select_tiles_kerne
       }
     }
     __syncthreads();
-    // a lane takes every fourth piece of 16 bytes of a row, k-step s the half
-    // s % 2 of piece s / 2: the order of the sum is free
-    uint2 a[2][STEPS];
+    // a lane takes every fourth piece of 16 bytes of a row, half a piece a k-step:
+    // the order of the sum is free
+    uint4 a[2][STEPS / 2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int s = 0; s < STEPS; ++s) a[i][s] = *reinterpret_cast<const uint2*>(codes[g + 8 * i] + ((s >> 1) * 4 + t4) * 16 + 8 * (s & 1));
+      for (int s = 0; s < STEPS / 2; ++s) a[i][s] = *reinterpret_cast<const uint4*>(codes[g + 8 * i] + (s * 4 + t4) * 16);
     // four steps of 8 pages at a time: their ids in one load
     for (int c0 = warp; c0 * 8 < pages; c0 += 4 * kWarps) {
       const int mine = (c0 + (lane >> 3) * kWarps) * 8 + (lane & 7);
@@ -585,8 +585,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 4) select_tiles_kerne
         int c[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < STEPS / 2; ++i) {
-          mma_s8(c, a[0][2 * i].x, a[1][2 * i].x, a[0][2 * i].y, a[1][2 * i].y, v[i].x, v[i].y);
-          mma_s8(c, a[0][2 * i + 1].x, a[1][2 * i + 1].x, a[0][2 * i + 1].y, a[1][2 * i + 1].y, v[i].z, v[i].w);
+          mma_s8(c, a[0][i].x, a[1][i].x, a[0][i].y, a[1][i].y, v[i].x, v[i].y);
+          mma_s8(c, a[0][i].z, a[1][i].z, a[0][i].w, a[1][i].w, v[i].z, v[i].w);
         }
         // c: tokens g and g + 8, pages 2 t4 and the next
         const float s0 = __shfl_sync(0xffffffffu, scale, 8 * t4), s1 = __shfl_sync(0xffffffffu, scale, 8 * t4 + 4);
@@ -650,7 +650,11 @@ SelectShape select_shape(const BlockShape& s) {
   t.tokens = kTileRows;
   while (t.tokens >= 4 && int64_t(t.tokens) * t.row * 4 > kTileSmem) t.tokens /= 2;
   t.long_tokens = 4;
-  if (t.tokens < 4 || s.max_qo_len < t.long_tokens || s.max_pages <= s.num_blocks || s.max_pages > kKeptKeys) t.tokens = 0;
+  // fewer than the single tokens' CTAs of a full card are quicker there
+  t.least_long = 4 * s.num_sms / s.Hkv;
+  if (t.tokens < 4 || s.max_qo_len < t.long_tokens || s.num_tokens < t.least_long || s.max_pages <= s.num_blocks ||
+      s.max_pages > kKeptKeys)
+    t.tokens = 0;
   const int64_t longs = s.num_tokens / t.long_tokens < s.batch ? s.num_tokens / t.long_tokens : s.batch;
   t.max_tiles = t.tokens ? int32_t(s.num_tokens / t.tokens + longs) : 0;
   return t;
@@ -668,8 +672,7 @@ cudaError_t launch_select(BlockParams p, const BlockShape& s, int select_tokens,
     p.tile_tokens = chunk.tokens;
     p.long_tokens = chunk.long_tokens;
     p.max_tiles = chunk.max_tiles;
-    // fewer than the single tokens' CTAs of a full card are quicker there
-    p.least_long = 4 * s.num_sms / s.Hkv;
+    p.least_long = chunk.least_long;
     cudaError_t e = launch_order_requests(p, stream);
     if (e != cudaSuccess) return e;
     const unsigned grid = unsigned(chunk.max_tiles) * unsigned(s.Hkv);
