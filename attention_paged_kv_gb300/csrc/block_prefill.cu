@@ -51,6 +51,7 @@ __global__ void __launch_bounds__(kUnionThreads) union_lists_kernel(const BlockP
   const int q0 = (tile - p.tile_indptr[b]) * p.tile_tokens;
   const int tokens = min(p.tile_tokens, r.qo_len - q0);
   const int W = (p.tile_tokens + 31) / 32;
+  int32_t* listed = reinterpret_cast<int32_t*>(words + p.max_pages * W);  // the union's blocks
   const int pos0 = r.kv_len - r.qo_len + q0;  // of the first token
   const int end = pos0 + tokens - 1;
   const int blocks = end < 0 ? 0 : min(end / p.g.ps + 1, p.max_pages);
@@ -58,21 +59,35 @@ __global__ void __launch_bounds__(kUnionThreads) union_lists_kernel(const BlockP
   for (int i = tid; i < blocks * W; i += kUnionThreads) words[i] = 0;
   if (tid < 8) bad[tid] = 0;
   __syncthreads();
-  for (int t = warp; t < tokens; t += kUnionThreads / 32) {
-    const int32_t* list = p.blocks + (static_cast<int64_t>(r.qo_start + q0 + t) * p.g.Hkv + h) * p.num_blocks;
-    const int pos = pos0 + t, own = pos < 0 ? -1 : pos / p.g.ps;
-    bool sound = own < p.max_pages;
-    for (int i = lane; i < p.num_blocks; i += 32) {
-      const int e = list[i], before = i ? list[i - 1] : e - 1;
-      if (e < 0) continue;
-      if (before < 0 && i) sound = false;
-      if (e <= before) sound = false;
-      if (e >= r.pages) atomicOr(p.status, PA_DEV_BAD_INDEX);
-      if (e <= own && e < blocks) atomicOr(words + e * W + (t >> 5), 1u << (t & 31));
+  // 32 entries of a list at a time, kBatch such strips of a warp's lists in flight
+  constexpr int kUnionWarps = kUnionThreads / 32, kBatch = 8;
+  const int strips = (p.num_blocks + 31) / 32, mine = (tokens - warp + kUnionWarps - 1) / kUnionWarps * strips;
+  for (int j0 = 0; j0 < mine; j0 += kBatch) {
+    int e[kBatch], before[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int j = j0 + k, t = warp + j / strips * kUnionWarps, i = j % strips * 32 + lane;
+      const int32_t* list = p.blocks + (static_cast<int64_t>(r.qo_start + q0 + t) * p.g.Hkv + h) * p.num_blocks;
+      const bool there = j < mine && i < p.num_blocks;
+      e[k] = there ? list[i] : -1;
+      before[k] = there && lane == 0 && i > 0 ? list[i - 1] : -1;
     }
-    if (!__all_sync(0xffffffffu, sound) && lane == 0) {
-      atomicOr(bad + (t >> 5), 1u << (t & 31));
-      if (own < p.max_pages) atomicOr(p.status, PA_DEV_BAD_INDEX);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int j = j0 + k, t = warp + j / strips * kUnionWarps, i = j % strips * 32 + lane;
+      if (j >= mine) break;
+      const int pos = pos0 + t, own = pos < 0 ? -1 : pos / p.g.ps;
+      const int up = __shfl_up_sync(0xffffffffu, e[k], 1), last = lane ? up : before[k];
+      bool sound = own < p.max_pages;
+      if (e[k] >= 0) {
+        if (i > 0 && (last < 0 || e[k] <= last)) sound = false;
+        if (e[k] >= r.pages) atomicOr(p.status, PA_DEV_BAD_INDEX);
+        if (e[k] <= own && e[k] < blocks) atomicOr(words + e[k] * W + (t >> 5), 1u << (t & 31));
+      }
+      if (!__all_sync(0xffffffffu, sound) && lane == 0) {
+        atomicOr(bad + (t >> 5), 1u << (t & 31));
+        if (own < p.max_pages) atomicOr(p.status, PA_DEV_BAD_INDEX);
+      }
     }
   }
   __syncthreads();
@@ -94,9 +109,12 @@ __global__ void __launch_bounds__(kUnionThreads) union_lists_kernel(const BlockP
       if (w < warp) at += warp_count[turn][w];
       count += warp_count[turn][w];
     }
-    if (any) entries[at] = make_int2(page_of(p, r.page_start + e), e);
+    if (any) {
+      entries[at] = make_int2(page_of(p, r.page_start + e), e);
+      listed[at] = e;
+    }
   }
-  __syncthreads();  // (entries are read again below, by the CTA that wrote them)
+  __syncthreads();
   pdl_launch();
   // masks, and the first 128-key step with a block that some token sees in part
   const int per = 128 / p.g.ps, bits = p.g.ps / 8;
@@ -108,7 +126,7 @@ __global__ void __launch_bounds__(kUnionThreads) union_lists_kernel(const BlockP
     uint32_t m = 0;
     if (t < tokens && !(bad[t >> 5] >> (t & 31) & 1)) {
       for (int k = 0; k < per && s * per + k < count; ++k) {
-        const int e = entries[s * per + k].y;
+        const int e = listed[s * per + k];
         if (words[e * W + (t >> 5)] >> (t & 31) & 1) m |= ((1u << bits) - 1) << (k * bits);
         if (t == 0 && e >= first_own) diag = min(diag, s);
       }
@@ -603,7 +621,7 @@ TileShape tile_shape(const BlockShape& s) {
   // tiles would take longer
   t.least_long = int32_t((1 << 19) / (int64_t(s.Hkv) * s.num_blocks * s.page_size) + 1);
   const int words = (t.tokens + 31) / 32;
-  t.union_smem = int64_t(s.max_pages) * words * 4;
+  t.union_smem = int64_t(s.max_pages) * (words + 1) * 4;
   // pages of 8 slots or more (a TMA copy's rows keep the swizzle's period of 8),
   // and unions that shared memory holds
   t.use = s.max_qo_len >= t.long_tokens && s.num_tokens >= t.least_long && s.page_size >= 8 && t.union_smem <= 200 * 1024;

@@ -465,7 +465,8 @@ __device__ __forceinline__ void warp_select(const uint32_t* key, int n, int k, i
     for (int i = 0; i < kWarpBins / 32; ++i) bins[i * 32 + lane] = 0;
     __syncwarp();
     each([&](int, uint32_t x) {
-      if (x >= base && x < top) atomicAdd(bins + ((x - base) >> shift), 1);
+      const uint32_t y = x - base;  // (of a key below base, and of 0, above all)
+      if (y < top - base) atomicAdd(bins + (y >> shift), 1);
     });
     __syncwarp();
     int mine[kWarpBins / 32], sum = 0;  // lane l: the parts 255 - 8 l and down
@@ -500,10 +501,12 @@ __device__ __forceinline__ void warp_select(const uint32_t* key, int n, int k, i
     } else if (count <= 32) {  // a lane for each of its keys: the one with need - 1 larger ones is the border
       int at = 0;
       each([&](int, uint32_t x) {
-        const bool in = x >= base && x < top;
+        const bool in = x - base < top - base;
         const unsigned some = __ballot_sync(0xffffffffu, in);
-        if (in) bins[at + __popc(some & before)] = static_cast<int>(x);
-        at += __popc(some);
+        if (some) {
+          if (in) bins[at + __popc(some & before)] = static_cast<int>(x);
+          at += __popc(some);
+        }
       });
       __syncwarp();
       const uint32_t x = lane < count ? static_cast<uint32_t>(bins[lane]) : 0u;
