@@ -85,8 +85,9 @@ class Rope(_Object):
 
         q, k [n, heads, head_dim] (k may be None): any token stride that is a
         multiple of 8; head_dim a multiple of 16 up to 256.  q_out and k_out
-        (allocated where not given) may be q and k themselves.  inverse: the
-        rotation back, by which gradients pass through it.  See pagedattn_rope.
+        (allocated where not given) may be q and k themselves.  inverse: by the
+        negative angle, as gradients pass through the rotation (with scale 1, the
+        rotation back).  See pagedattn_rope.
         """
         import torch
         at = self._index

@@ -121,7 +121,8 @@ typedef struct {
 #define PA_DEV_TIMEOUT 1
 #define PA_DEV_BAD_INDEX 2
 #define PA_DEV_NO_PAGES 4 /* build_tables: the free stack holds too few pages            */
-#define PA_DEV_NO_ROOM 8  /* build_tables: block_table_width, max_tokens or max_pages     */
+#define PA_DEV_NO_ROOM 8  /* build_tables: block_table_width, max_tokens or max_pages;
+                             blocks: max_pages                                         */
 
 /*
  * Build the work partition for one batch ("auxiliary data structures" that
@@ -555,7 +556,8 @@ typedef struct {
   int64_t position_stride;
   int32_t num_tokens, num_q_heads, num_k_heads;
   int32_t head_dim; /* a multiple of 16, at most 256                                             */
-  int32_t inverse;  /* rotate by the negative angle: the gradient of the rotation                */
+  int32_t inverse;  /* rotate by the negative angle: the gradient of the rotation (and, with scale
+                       1, the rotation back)                                               */
   pagedattn_dtype dtype;
 } pagedattn_rope_rows;
 

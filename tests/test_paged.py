@@ -992,6 +992,36 @@ def test_calls_on_another_stream():
 
 
 @gpu
+@pytest.mark.parametrize("qo, kv, Hkv, blocks", [([1] * 3, [3000, 700, 9000], 1, 200), ([300], [3000], 2, 60)], ids=str)
+def test_two_objects_on_two_streams_and_a_replayed_graph(qo, kv, Hkv, blocks):
+    """Runs that overlap, each in its own workspace; a captured one replayed between them, over queries that change."""
+    bs = [Batch(qo, kv, 8 * Hkv, Hkv, 128, 16, "NHD", torch.bfloat16, seed=s) for s in (1, 2, 3)]
+    objs, tables = [b.attention(blocks, 1, 1) for b in bs], [b.tables() for b in bs]
+    both = lambda i: (lists := objs[i].select(bs[i].q, bs[i].cache, tables[i]),  # noqa: E731
+                      *objs[i].run(bs[i].q, bs[i].cache, tables[i], lists))
+    want = [both(i) for i in range(3)]
+    queries = [bs[2].q.clone(), -bs[2].q]
+    bs[2].q.copy_(queries[1])
+    other = both(2)
+    graph, streams = torch.cuda.CUDAGraph(), [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        captured = both(2)
+    torch.cuda.synchronize()
+    for n in range(20):
+        got = []
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append(both(i))
+        bs[2].q.copy_(queries[n % 2])
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip((*got, captured), (*want[:2], (want[2], other)[n % 2])):
+            assert all(torch.equal(a, b) for a, b in zip(x, y))
+    assert all(a.device_status() == 0 for a in objs)
+
+
+@gpu
 def test_objects_that_share_a_workspace():
     bs = [Batch([1, 1], [3000, 900], 8, 1, 128, 16, "NHD", torch.float16, seed=1),
           Batch([40, 1], [2100, 1900], 16, 2, 64, 16, "NHD", torch.bfloat16, seed=3),
