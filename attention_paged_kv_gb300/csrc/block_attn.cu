@@ -87,6 +87,70 @@ __device__ __forceinline__ void store4(void* out, int64_t row, int D, int col, f
       make_uint2(Elt<T>::from_f2(v.x * inv, v.y * inv), Elt<T>::from_f2(v.z * inv, v.w * inv));
 }
 
+// Chunks whose items were cut along their keys (block_prefill.cu): the parts'
+// states of each row joined, a row a warp, four rows in flight.
+template <typename T, int D>
+__device__ __forceinline__ void join_tiles(const BlockParams& p, int parts) {
+  constexpr int V = D / 32, U = 4;  // columns of a lane
+  const int TQ = 128 / p.G, lane = threadIdx.x & 31;
+  const int per_item = p.tile_tokens * p.G, rows = p.tile_indptr[p.batch] * p.g.Hkv * per_item;
+  const int tiles = p.tile_indptr[p.batch];
+  for (int r0 = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * U; r0 < rows; r0 += gridDim.x * kWarps * U) {
+    const float *lse[U], *o[U];
+    int64_t out[U];  // rows of out, -1: none
+    float top[U], sum[U], acc[U][V];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = min(r0 + u, rows - 1), place = r / per_item, rr = r - place * per_item, t = rr / p.G, g = rr - t * p.G;
+      const int h = place % p.g.Hkv;
+      const BlockItem* it = p.items + static_cast<int64_t>(tiles - 1 - place / p.g.Hkv) * p.g.Hkv + h;
+      out[u] = r0 + u < rows && t < it->tokens ? (static_cast<int64_t>(it->token) + t) * p.Hq + h * p.G + g : -1;
+      const int64_t row = static_cast<int64_t>(place) * parts * p.tile_rows + (out[u] < 0 ? 0 : t / TQ * 128 + t % TQ * p.G + g);
+      lse[u] = p.part_lse + row;
+      o[u] = p.part_o + row * D + lane * V;
+      top[u] = kNone;
+      sum[u] = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[u][i] = 0.f;
+    }
+    for (int k = 0; k < parts; ++k)
+#pragma unroll
+      for (int u = 0; u < U; ++u) top[u] = fmaxf(top[u], __ldcg(lse[u] + k * p.tile_rows));
+#pragma unroll 2
+    for (int k = 0; k < parts; ++k) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float w = ex2(__ldcg(lse[u] + k * p.tile_rows) - top[u]);
+        const float* src = o[u] + static_cast<int64_t>(k) * p.tile_rows * D;
+        float v[V];
+        if constexpr (V == 2) {
+          const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+          v[0] = x.x, v[1] = x.y;
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; i += 4) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(src + i));
+            v[i] = x.x, v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
+          }
+        }
+        sum[u] += w;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[u][i] += w * v[i];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (out[u] < 0) continue;
+      const float inv = sum[u] == 0.f ? 0.f : 1.f / sum[u];
+#pragma unroll
+      for (int i = 0; i < V; i += 2)
+        *reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + out[u] * D + lane * V + i) =
+            Elt<T>::from_f2(acc[u][i] * inv, acc[u][i + 1] * inv);
+      if (lane == 0 && p.lse) p.lse[out[u]] = sum[u] == 0.f ? -INFINITY : (top[u] + log2f(sum[u])) * kLn2;
+    }
+  }
+}
+
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attend_kernel(const BlockParams p) {
   using C = Cfg<D, NT>;
@@ -103,6 +167,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attend_kernel(cons
   unsigned works = gridDim.x;
   int slices = p.slices;
   if (p.listed) {
+    const int parts = p.small_indptr[p.batch + 1];
+    if (parts > 1) join_tiles<T, D>(p, parts);
     const int items = p.small_indptr[p.batch] * p.g.Hkv * chunks;
     slices = items > 0 ? max(1, min(p.slices, p.ctas / items)) : 1;
     works = unsigned(items) * slices;
@@ -357,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attend_kernel(cons
   }
   __syncthreads();
   constexpr int COLS = D / 4;
-  const int64_t part = static_cast<int64_t>(work) * C::ROWS;  // the slice's first partial row
+  const int64_t part = p.part_base + static_cast<int64_t>(work) * C::ROWS;  // the slice's first partial row
   for (int i = tid; i < heads * COLS; i += kThreads) {
     const int row = i / COLS, col = i % COLS * 4;
     float mw[kWarps], lw[kWarps], top = kNone, sum = 0.f;
@@ -400,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attend_kernel(cons
   __syncthreads();
   if (!last_s) continue;
   __threadfence();
-  const int64_t first = static_cast<int64_t>(item) * slices * C::ROWS;
+  const int64_t first = p.part_base + static_cast<int64_t>(item) * slices * C::ROWS;
   for (int i = tid; i < heads * COLS; i += kThreads) {
     const int row = i / COLS, col = i % COLS * 4;
     float top = kNone, sum = 0.f;

@@ -505,17 +505,30 @@ __global__ void __launch_bounds__(TileCfg<D, NT>::THREADS, 1)
       if (parts > 1) {  // a part's state: normalised, in fp32, with its log-sum in base 2
         const int64_t row = (static_cast<int64_t>(place) * parts + part) * (NT * 128) + x * 128 + r;
         if (real) p.part_lse[row] = l_sum == 0.f ? -INFINITY : m_ref + log2f(l_sum);
+        // 64 columns at a time (32 at head_dim 64) through the warp's Q rows, free by
+        // now, to leave in whole rows
+        constexpr int TURN = D == 64 ? 32 : 64, BYTES = TURN * 4, LANES = TURN / 4;
+        static_assert(4 * 32 * BYTES <= C::TILE, "four warps' rows fit a Q tile");
+        uint8_t* own = smem + x * C::TILE + (warp & 3) * 32 * BYTES;
 #pragma unroll
-        for (int c4 = 0; c4 < D / 32; ++c4) {
-          uint32_t o[32];
-          column(c4, o);
-          if (real) {
+        for (int turn = 0; turn < D / TURN; ++turn) {
+#pragma unroll
+          for (int c4 = 0; c4 < TURN / 32; ++c4) {
+            uint32_t o[32];
+            column(turn * (TURN / 32) + c4, o);
 #pragma unroll
             for (int v = 0; v < 8; ++v) {
               auto f = [&](int i) { return l_sum == 0.f ? 0.f : __uint_as_float(o[4 * v + i]) * inv; };
-              *reinterpret_cast<float4*>(p.part_o + row * D + c4 * 32 + v * 4) = make_float4(f(0), f(1), f(2), f(3));
+              *reinterpret_cast<float4*>(own + lane * BYTES + (((c4 * 8 + v) ^ (lane & 7)) << 4)) = make_float4(f(0), f(1), f(2), f(3));
             }
           }
+          __syncwarp();
+          const int c = lane % LANES;
+#pragma unroll 4
+          for (int i = lane / LANES; i < 32; i += 32 / LANES)
+            *reinterpret_cast<float4*>(p.part_o + (row - lane + i) * D + turn * TURN + c * 4) =
+                *reinterpret_cast<const float4*>(own + i * BYTES + ((c ^ (i & 7)) << 4));
+          __syncwarp();
         }
       } else {
         if (real && p.lse)
@@ -559,38 +572,6 @@ __global__ void __launch_bounds__(TileCfg<D, NT>::THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
-  if (parts == 1) return;
-
-  // ---------------------------------------------------------------- the item's last part joins all
-  __shared__ int last_s;
-  __threadfence();
-  __syncthreads();
-  if (tid == 0) {
-    last_s = atomicAdd(p.counters + place, 1) == parts - 1;
-    if (last_s) p.counters[place] = 0;
-  }
-  __syncthreads();
-  if (!last_s) return;
-  __threadfence();
-  const int64_t first = static_cast<int64_t>(place) * parts * (NT * 128);
-  for (int i = tid; i < it.tokens * G * (D / 4); i += C::THREADS) {
-    const int rr = i / (D / 4), col = i % (D / 4) * 4, t = rr / G, g = rr - t * G;  // rr: without the rows that a tile leaves free
-    const int64_t row = first + t / TQ * 128 + t % TQ * G + g;
-    float top = -3.0e38f, sum = 0.f;
-    for (int k = 0; k < parts; ++k) top = fmaxf(top, __ldcg(p.part_lse + row + k * (NT * 128)));
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < parts; ++k) {
-      const float w = ex2(__ldcg(p.part_lse + row + k * (NT * 128)) - top);
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + (row + k * (NT * 128)) * D + col));
-      sum += w;
-      acc.x += w * v.x, acc.y += w * v.y, acc.z += w * v.z, acc.w += w * v.w;
-    }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int64_t to = (static_cast<int64_t>(it.token) + t) * p.Hq + static_cast<int64_t>(h) * G + g;
-    *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + to * D + col) =
-        make_uint2(Elt<T>::from_f2(acc.x * inv, acc.y * inv), Elt<T>::from_f2(acc.z * inv, acc.w * inv));
-    if (col == 0 && p.lse) p.lse[to] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2f;
-  }
 }
 
 template <typename T, int D, int NT>
@@ -617,9 +598,10 @@ TileShape tile_shape(const BlockShape& s) {
   t.tokens = (s.D == 256 ? 1 : 2) * (128 / s.G);
   t.long_tokens = 32 / s.G + 1 > 2 ? 32 / s.G + 1 : 2;
   t.rows = (s.D == 256 ? 1 : 2) * 128;
-  // below half a million keys of single tokens and kv heads (30 us there) the few
-  // tiles would take longer
-  t.least_long = int32_t((1 << 19) / (int64_t(s.Hkv) * s.num_blocks * s.page_size) + 1);
+  // A million keys of single tokens and kv heads: 64 tokens of 2048 keys at 8 kv
+  // heads take 47 us in tiles (32 where their lists are alike) and 46 by
+  // themselves, 32 tokens 43 (32) and 24, 128 tokens 63 (37) and 91.
+  t.least_long = int32_t((1 << 20) / (int64_t(s.Hkv) * s.num_blocks * s.page_size) + 1);
   const int words = (t.tokens + 31) / 32;
   t.union_smem = int64_t(s.max_pages) * (words + 1) * 4;
   // pages of 8 slots or more (a TMA copy's rows keep the swizzle's period of 8),

@@ -79,6 +79,7 @@ struct BlockParams {
   uint32_t* keys;     // selection: order keys of the scores, [item of the launch][max_pages]
   float* part_o;      // attention: normalised partial states, [slice][rows][D]
   float* part_lse;    // their log-sums, base 2
+  int64_t part_base;  // first row of the single tokens' states, behind those of chunks
   // chunks (block_prefill.cu)
   // [batch + 1]: row-tile pairs of the requests before, tokens of the short ones; behind these the parts of an item
   int32_t *tile_indptr, *small_indptr;
@@ -87,7 +88,7 @@ struct BlockParams {
   uint16_t* masks;                      // of each item, [step of 128 keys][tile_tokens]: a bit for 8 keys
   int64_t q_stride;
   Kv4Geom g;
-  int32_t max_entries, max_tiles, tile_tokens, long_tokens, hnd;
+  int32_t max_entries, max_tiles, tile_tokens, tile_rows, long_tokens, hnd;
   int32_t listed;      // the tokens that small_indptr counts, not all
   int32_t least_long;  // tokens of long requests for which these are worth their own kernels
   int32_t num_sms;
@@ -139,6 +140,8 @@ struct TileShape {
   int64_t union_smem;
 };
 TileShape tile_shape(const BlockShape& s);
+// Rows of partial states of the items that are cut: of two parts an SM.
+inline int64_t tile_part_rows(const BlockShape& s, const TileShape& t) { return t.use ? int64_t(2) * s.num_sms * t.rows : 0; }
 cudaError_t launch_block_tiles(BlockParams p, const BlockShape& s, const TileShape& t, const CUtensorMap& kv_map,
                                const CUtensorMap& q_map, int dtype, cudaStream_t stream);
 cudaError_t launch_block_attention(BlockParams p, const BlockShape& s, int dtype, cudaStream_t stream);

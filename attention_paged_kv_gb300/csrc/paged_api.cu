@@ -187,8 +187,7 @@ BlockLayout block_layout(const BlockShape& s) {
   }
   l.select_tokens = int32_t(tokens > 0 ? tokens : 1);
   const TileShape t = tile_shape(s);
-  const int64_t cut_rows = t.use ? int64_t(2) * s.num_sms * t.rows : 0;
-  const int64_t parts = attend_part_rows(s) > cut_rows ? attend_part_rows(s) : cut_rows;
+  const int64_t parts = attend_part_rows(s) + tile_part_rows(s, t);
   const size_t keys = size_t(rows) * s.max_pages * 4, states = size_t(parts) * s.D * 4;
   l.off_part_lse = l.off_scratch + up(states);
   const size_t attend_end = l.off_part_lse + up(size_t(parts) * 4);
@@ -394,11 +393,13 @@ pagedattn_status pagedattn_blocks_run(const pagedattn_kv_cache* cache, const pag
     p.max_entries = tiles.max_entries;
     p.max_tiles = tiles.max_tiles;
     p.tile_tokens = tiles.tokens;
+    p.tile_rows = tiles.rows;
     p.long_tokens = tiles.long_tokens;
     p.least_long = tiles.least_long;
     e = pa::launch_block_tiles(p, shape, tiles, kv_map, q_map, cache->dtype, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_err(e, "chunk attention launch");
     p.listed = 1;
+    p.part_base = pa::tile_part_rows(shape, tiles);
   }
   e = pa::launch_block_attention(p, shape, cache->dtype, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_err(e, "attention launch");

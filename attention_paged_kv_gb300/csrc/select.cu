@@ -287,13 +287,17 @@ __global__ void __launch_bounds__(1024) order_requests_kernel(const BlockParams 
     base_s = min(base_s + all_s, p.num_tokens);
   }
   if (tid == 0) {
-    // parts of an item: the number that gives the shortest run of whole waves, a
-    // part's start and end weighed as 1/16 of an item (5 us of 80)
+    // Parts of an item: the number that gives the shortest run.  In units of an item
+    // (85 us for 8000 keys): whole waves of parts, a part's start and end, and
+    // the join of all parts' states.  1000 tokens behind 7000, us: 1 kv head (32 items)
+    // whole 127, in 2 parts 85, 4 60, 8 (two waves) 69; 2 kv heads 130, 92, 97 (4);
+    // 800 at 4 kv heads (100 items) 129, 148, 123 (3).
     const int items = base_t * p.g.Hkv;
     int parts = 1;
     float best = 3.0e38f;
     for (int n = 1; n <= kMaxParts && (n == 1 || items * n <= 2 * p.num_sms); ++n) {
-      const float cost = static_cast<float>((items * n + p.num_sms - 1) / p.num_sms) * (1.f / n + 0.0625f);
+      const float cost = static_cast<float>((items * n + p.num_sms - 1) / p.num_sms) * (1.f / n + 0.07f) +
+                         (n > 1 ? static_cast<float>(items * n) * 0.0006f : 0.f);
       if (cost < best) best = cost, parts = n;
     }
     p.small_indptr[p.batch + 1] = parts;
@@ -653,7 +657,9 @@ SelectShape select_shape(const BlockShape& s) {
   t.tokens = kTileRows;
   while (t.tokens >= 4 && int64_t(t.tokens) * t.row * 4 > kTileSmem) t.tokens /= 2;
   t.long_tokens = 4;
-  // fewer than the single tokens' CTAs of a full card are quicker there
+  // Fewer than the single tokens' CTAs of a full card are quicker there: of 500 pages
+  // at 8 kv heads 32 tokens take 24 us in tiles and 11 by themselves, 64 24 and
+  // 21, 128 24 and 30.
   t.least_long = 4 * s.num_sms / s.Hkv;
   if (t.tokens < 4 || s.max_qo_len < t.long_tokens || s.num_tokens < t.least_long || s.max_pages <= s.num_blocks ||
       s.max_pages > kKeptKeys)
