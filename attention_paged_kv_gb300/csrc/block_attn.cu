@@ -14,6 +14,12 @@
 // down to 2^-21 of it are rounded like it.  P is rounded to fp16 for fp16
 // values (by 2^-11 of it at most); for bf16, where that would be 2^-8, it is split
 // in two bf16 terms and multiplied twice.
+//
+// What bounds it: HBM.  64 decodes of 2048 keys at 64 / 8 heads (464 MB) take 75
+// us, 6.2 TB/s, 91 % of the copy rate; 3 requests of 4096 of up to 131071 keys (50 MB)
+// 16.5, of them about 7 the copies, the rest tables, list, page ids and the first
+// keys one after the other, and the join.  Steps on the way (us): a look-up of
+// list and page for each row that is copied 89; whole pages 75.
 #include <climits>
 #include <cstring>
 
@@ -511,7 +517,7 @@ AttendShape attend_shape(const BlockShape& s) {
   a.rows = s.D == 256 || s.G <= 8 ? 8 : 16;
   a.chunks = (s.G + a.rows - 1) / a.rows;
   a.ctas = s.num_sms * (s.D == 64 ? 3 : (s.D == 128 ? 2 : 1));
-  // slices of 128 keys or more
+  // slices of 128 keys or more (3 requests of 4096 keys 16.4 us, in one slice each 34.5)
   int64_t n = int64_t(s.num_blocks) * s.page_size / 128;
   if (n > s.num_blocks) n = s.num_blocks;
   if (n > kMaxSlices) n = kMaxSlices;

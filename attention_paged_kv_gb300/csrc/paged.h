@@ -110,7 +110,8 @@ struct BlockLayout {
 
 // Selection: tokens that a CTA takes together (0: each by itself), and the fewest of a request that goes there.
 struct SelectShape {
-  int32_t tokens, long_tokens, least_long, max_tiles, row;  // row: keys of a token in shared memory
+  int32_t tokens, long_tokens, least_long, max_tiles;
+  int32_t row, ctas;  // keys kept of a token; CTAs with keys in global memory (0: in shared memory)
 };
 SelectShape select_shape(const BlockShape& s);
 BlockLayout block_layout(const BlockShape& s);

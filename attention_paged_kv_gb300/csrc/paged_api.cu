@@ -188,14 +188,17 @@ BlockLayout block_layout(const BlockShape& s) {
   l.select_tokens = int32_t(tokens > 0 ? tokens : 1);
   const TileShape t = tile_shape(s);
   const int64_t parts = attend_part_rows(s) + tile_part_rows(s, t);
-  const size_t keys = size_t(rows) * s.max_pages * 4, states = size_t(parts) * s.D * 4;
+  const SelectShape chunk = select_shape(s);
+  size_t keys = size_t(rows) * s.max_pages * 4;
+  const size_t states = size_t(parts) * s.D * 4, tile_keys = chunk.tokens ? size_t(chunk.ctas) * 16 * chunk.row * 4 : 0;
+  if (tile_keys > keys) keys = tile_keys;
   l.off_part_lse = l.off_scratch + up(states);
   const size_t attend_end = l.off_part_lse + up(size_t(parts) * 4);
   size_t end = l.off_scratch + up(keys) > attend_end ? l.off_scratch + up(keys) : attend_end;
   // chunks: the requests' sums, and the unions of the lists with their masks
   const size_t items = size_t(t.max_tiles) * s.Hkv;
   l.off_indptr = end;
-  l.off_items = l.off_indptr + (t.use || select_shape(s).tokens ? up((size_t(s.batch) + 2) * 8) : 0);
+  l.off_items = l.off_indptr + (t.use || chunk.tokens ? up((size_t(s.batch) + 2) * 8) : 0);
   l.off_entries = l.off_items + up(items * sizeof(BlockItem));
   l.off_masks = l.off_entries + up(items * t.max_entries * sizeof(int2));
   l.total = l.off_masks + up(items * (t.use ? t.max_entries / (128 / s.page_size) : 0) * t.tokens * 2);

@@ -12,10 +12,19 @@
 // histograms over 2048 equal parts of the keys' range, then of the part that
 // holds it, until one key (or a part taken whole) is left.
 //
-// Chunks: a CTA takes up to 16 tokens of a request, whose scores for 8 pages at a
-// time are one m16n8k32 product of 8-bit integers: the bounds are read once for
-// all.  The keys stay in shared memory, and each warp selects for two of the
-// tokens by itself, with histograms over 256 parts.
+// Chunks: a CTA takes 16 tokens of a request, whose scores for 8 pages at a time
+// are m16n8k32 products of 8-bit integers: the bounds are read once for all.
+// Each warp then selects for tokens by itself, from keys in shared memory: a
+// histogram over 256 parts, and the ranks of the keys of the part that holds the border.
+//
+// What bounds them.  64 decodes of 512 to 8192 keys (pages of 16, 8 kv heads, 34
+// MB): 13.6 us, 5 at the copy rate; the rest is one dependent load after the
+// other (tables, page ids, bounds) and the CTA's barriers.  A chunk of 2000
+// tokens over 500 pages: 57 us, in two rounds of CTAs; in each, codes of q 3.6
+// us, scores 10.4 (8-bit products: 36 cycles of a sub-partition each), the
+// selection 8.6 (its instructions).  Measured without gain there: products in
+// fp16 (bounds converted, 62), bounds loaded a step ahead (registers for two CTAs
+// an SM: 79), keys of the selection in more registers, thresholds by bisection.
 #include <cfloat>
 #include <cstring>
 
@@ -28,7 +37,7 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kKept = kKeptKeys;
-constexpr int kTileSmem = 192 * 1024;  // of a chunk's keys
+constexpr int kTileSmem = 100 * 1024;  // of a chunk's keys: two CTAs an SM
 constexpr uint32_t kAlways = 0xFFFFFFFFu;  // above every score's key
 
 // Scores as unsigned numbers of the same order; -0 is 0, NaN is infinity.
@@ -453,6 +462,7 @@ __device__ __forceinline__ void warp_select(const uint32_t* key, int n, int k, i
       for (int s = 0; s < kRegs; ++s)
         if (32 * s < n) f(32 * s, held[s]);
     } else {
+#pragma unroll 4
       for (int i = 0; i < n; i += 32) f(i, load(i + lane));
     }
   };
@@ -542,16 +552,21 @@ __device__ __forceinline__ void warp_select(const uint32_t* key, int n, int k, i
   });
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 4) select_tiles_kernel(const BlockParams p, const int row) {
-  constexpr int STEPS = 2 * D / 32;
-  extern __shared__ __align__(16) uint32_t kept[];  // [token][row]
+// kGlobal: the keys in global memory, a piece for each of the CTAs, which take
+// tile after tile.
+template <typename T, int D, bool kGlobal>
+__global__ void __launch_bounds__(kGlobal ? 512 : kThreads, D == 256 ? (kGlobal ? 1 : 2) : (kGlobal ? 2 : 4))
+    select_tiles_kernel(const BlockParams p, const int row) {
+  constexpr int STEPS = 2 * D / 32, kWarps = kGlobal ? 16 : kThreads / 32;
+  extern __shared__ __align__(16) uint32_t kept_s[];  // [token][row]
   __shared__ __align__(16) int8_t codes[kTileRows][2 * D + 64];  // (rows 64 bytes apart in the banks)
   __shared__ __align__(16) int bins[kWarps][kWarpBins];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
-  const int tile = blockIdx.x / p.g.Hkv, h = blockIdx.x % p.g.Hkv;
+  uint32_t* const kept = kGlobal ? p.keys + static_cast<int64_t>(blockIdx.x) * kTileRows * row : kept_s;
   pdl_wait();
-  if (tile >= p.tile_indptr[p.batch]) return;
+  const int works = p.tile_indptr[p.batch] * p.g.Hkv;
+  for (int work = blockIdx.x; work < works; work += gridDim.x) {
+  const int tile = work / p.g.Hkv, h = work % p.g.Hkv;
   const int b = last_below(p.tile_indptr, p.batch + 1, tile);
   const Span r = load_span(p, b, false);
   const int q0 = (tile - p.tile_indptr[b]) * p.tile_tokens;
@@ -607,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 4) select_tiles_kerne
     }
   }
   __syncthreads();
-  pdl_launch();
+  if constexpr (!kGlobal) pdl_launch();
   for (int i = warp; i < tokens; i += kWarps) {
     const int pos = pos0 + i, n = pos < 0 ? 0 : (pos >> p.g.ps_shift) + 1;
     int32_t* out = p.blocks + (static_cast<int64_t>(token + i) * p.g.Hkv + h) * p.num_blocks;
@@ -622,6 +637,9 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 4) select_tiles_kerne
     }
     __syncwarp();
   }
+  if constexpr (!kGlobal) return;  // (the grid has a CTA for each tile)
+  __syncthreads();
+  }
 }
 
 template <typename T>
@@ -635,10 +653,11 @@ cudaError_t launch_t(const BlockParams& p, int D, unsigned grid, size_t smem, cu
 
 template <typename T, int D>
 cudaError_t launch_tiles_d(const BlockParams& p, const SelectShape& t, unsigned grid, cudaStream_t stream) {
+  if (t.ctas) return launch_pdl(select_tiles_kernel<T, D, true>, grid < unsigned(t.ctas) ? grid : unsigned(t.ctas), 512u, size_t(0), stream, p, t.row);
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = set_smem_once(done, reinterpret_cast<const void*>(select_tiles_kernel<T, D>), kTileSmem);
+  const cudaError_t e = set_smem_once(done, reinterpret_cast<const void*>(select_tiles_kernel<T, D, false>), kTileSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(select_tiles_kernel<T, D>, grid, kThreads, size_t(t.tokens) * t.row * 4, stream, p, t.row);
+  return launch_pdl(select_tiles_kernel<T, D, false>, grid, kThreads, size_t(kTileRows) * t.row * 4, stream, p, t.row);
 }
 template <typename T>
 cudaError_t launch_tiles(const BlockParams& p, const SelectShape& t, int D, unsigned grid, cudaStream_t stream) {
@@ -655,13 +674,16 @@ SelectShape select_shape(const BlockShape& s) {
   SelectShape t;
   t.row = (s.max_pages + 31) / 32 * 32 + 8;  // (rows 8 banks apart)
   t.tokens = kTileRows;
-  while (t.tokens >= 4 && int64_t(t.tokens) * t.row * 4 > kTileSmem) t.tokens /= 2;
+  // More keys than two CTAs an SM keep go to global memory, that is, to L2: 2000 tokens
+  // at 8 kv heads take 199 us for 1500 pages with keys in shared memory and 210 so,
+  // for 2000 pages (one CTA an SM) 396 and 275.
+  t.ctas = int64_t(kTileRows) * t.row * 4 > kTileSmem ? s.num_sms * (s.D == 256 ? 1 : 2) : 0;
   t.long_tokens = 4;
   // Fewer than the single tokens' CTAs of a full card are quicker there: of 500 pages
   // at 8 kv heads 32 tokens take 24 us in tiles and 11 by themselves, 64 24 and
   // 21, 128 24 and 30.
   t.least_long = 4 * s.num_sms / s.Hkv;
-  if (t.tokens < 4 || s.max_qo_len < t.long_tokens || s.num_tokens < t.least_long || s.max_pages <= s.num_blocks ||
+  if (s.max_qo_len < t.long_tokens || s.num_tokens < t.least_long || s.max_pages <= s.num_blocks ||
       s.max_pages > kKeptKeys)
     t.tokens = 0;
   const int64_t longs = s.num_tokens / t.long_tokens < s.batch ? s.num_tokens / t.long_tokens : s.batch;
