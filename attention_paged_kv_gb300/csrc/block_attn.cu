@@ -157,29 +157,16 @@ __device__ __forceinline__ void join_tiles(const BlockParams& p, int parts) {
   }
 }
 
+// One slice of one item: an item for each token, kv head and chunk of heads, or (listed) for those of the
+// tokens that small_indptr counts.
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attend_kernel(const BlockParams p) {
+__device__ __forceinline__ void attend_item(const BlockParams& p, unsigned work, int slices, uint8_t* smem,
+                                            int (&count_s)[2][kWarps], int* last_s) {
   using C = Cfg<D, NT>;
   constexpr int CH = D / 8, RPI = 32 / CH;  // 16-byte pieces of a row; rows that a warp copies at a time
   constexpr int KS = D / 16;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int count_s[2][kWarps];
-  __shared__ int last_s;
-  int32_t* const list0 = reinterpret_cast<int32_t*>(smem + C::SMEM);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
   const int chunks = (p.G + C::ROWS - 1) / C::ROWS;
-  pdl_wait();
-  // an item for each token, kv head and chunk of heads, or (listed) for those of the tokens that small_indptr counts
-  unsigned works = gridDim.x;
-  int slices = p.slices;
-  if (p.listed) {
-    const int parts = p.small_indptr[p.batch + 1];
-    if (parts > 1) join_tiles<T, D>(p, parts);
-    const int items = p.small_indptr[p.batch] * p.g.Hkv * chunks;
-    slices = items > 0 ? max(1, min(p.slices, p.ctas / items)) : 1;
-    works = unsigned(items) * slices;
-  }
-  for (unsigned work = blockIdx.x; work < works; work += gridDim.x) {
   const int slice = work % slices, item = work / slices;
   const int chunk = item % chunks, h = item / chunks % p.g.Hkv;
   int t = item / (chunks * p.g.Hkv), guess = t;
@@ -188,14 +175,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attend_kernel(cons
     t = p.qo_indptr[guess] + t - p.small_indptr[guess];
   }
   const int heads = min(C::ROWS, p.G - chunk * C::ROWS);
-  int32_t* list = list0;
+  int32_t* list = reinterpret_cast<int32_t*>(smem + C::SMEM);
 
   // ---- the list: page ids of the blocks that the query sees, its own block marked by the top bit
   const int32_t* blocks = p.blocks + (static_cast<int64_t>(t) * p.g.Hkv + h) * p.num_blocks;
   int e = tid < p.num_blocks ? blocks[tid] : -1;  // (in flight beside the tables)
   int before = tid > 0 && tid < p.num_blocks ? blocks[tid - 1] : e - 1;
   const Query mine = find_query(p, t, guess);
-  if (!mine.there) continue;
+  if (!mine.there) return;
   const int64_t q_row = static_cast<int64_t>(t) * p.Hq + h * p.G + chunk * C::ROWS;  // in out and lse
   uint32_t qf[NT][KS][2];
   {
@@ -459,18 +446,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attend_kernel(cons
   }
   if (slices == 1) {
     __syncthreads();  // the list and the states have been read
-    continue;
+    return;
   }
 
   // ---- the last slice of the item joins the parts
   __threadfence();
   __syncthreads();
   if (tid == 0) {
-    last_s = atomicAdd(p.counters + item, 1) == slices - 1;
-    if (last_s) p.counters[item] = 0;
+    *last_s = atomicAdd(p.counters + item, 1) == slices - 1;
+    if (*last_s) p.counters[item] = 0;
   }
   __syncthreads();
-  if (!last_s) continue;
+  if (!*last_s) return;
   __threadfence();
   const int64_t first = p.part_base + static_cast<int64_t>(item) * slices * C::ROWS;
   for (int i = tid; i < heads * COLS; i += kThreads) {
@@ -489,7 +476,25 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attend_kernel(cons
     store4<T>(p.out, q_row + row, D, col, acc, sum == 0.f ? 0.f : 1.f / sum);
     if (col == 0 && p.lse) p.lse[q_row + row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
   }
+}
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::CTAS) attend_kernel(const BlockParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int count_s[2][kWarps];
+  __shared__ int last_s;
+  pdl_wait();
+  unsigned works = gridDim.x;
+  int slices = p.slices;
+  if (p.listed) {
+    const int parts = p.small_indptr[p.batch + 1], rows = Cfg<D, NT>::ROWS;
+    if (parts > 1) join_tiles<T, D>(p, parts);
+    const int items = p.small_indptr[p.batch] * p.g.Hkv * ((p.G + rows - 1) / rows);
+    slices = items > 0 ? max(1, min(p.slices, p.ctas / items)) : 1;
+    works = unsigned(items) * slices;
   }
+  for (unsigned work = blockIdx.x; work < works; work += gridDim.x)
+    attend_item<T, D, NT>(p, work, slices, smem, count_s, &last_s);
 }
 
 template <typename T, int D, int NT>

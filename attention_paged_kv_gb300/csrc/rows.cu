@@ -99,19 +99,27 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsParams p) 
   const int lo = halves ? 8 * j : 16 * j, hi = halves ? p.pairs + 8 * j : 16 * j + 8;
   float c[8], s[8];
   if (turns) {
-    const int32_t x0 = p.axes ? 0 : p.positions[tok];
+    int32_t x[8];
+    if (p.axes) {
+      int axis[8];
+      bool sound = true;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) axis[i] = p.axes[8 * j + i];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool in = static_cast<unsigned>(axis[i]) < static_cast<unsigned>(p.num_axes);
+        sound = sound && in;
+        x[i] = p.positions[(in ? axis[i] : 0) * p.position_stride + tok];
+      }
+      if (!sound && p.status) atomicOr(p.status, PA_DEV_BAD_INDEX);
+    } else {
+      x[0] = p.positions[tok];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) x[i] = x[0];
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      int32_t x = x0;
-      if (p.axes) {
-        const int axis = p.axes[8 * j + i];
-        if (static_cast<unsigned>(axis) < static_cast<unsigned>(p.num_axes)) {
-          x = p.positions[axis * p.position_stride + tok];
-        } else if (p.status) {
-          atomicOr(p.status, PA_DEV_BAD_INDEX);
-        }
-      }
-      const float2 cs = turned(x, p.turns[8 * j + i]);
+      const float2 cs = turned(x[i], p.turns[8 * j + i]);
       c[i] = cs.x * p.scale;
       s[i] = cs.y * (p.scale * p.sign);
     }

@@ -313,28 +313,23 @@ __global__ void __launch_bounds__(1024) order_requests_kernel(const BlockParams 
   }
 }
 
+template <int D>
+struct SelectShared {
+  __align__(16) int8_t codes[kWarps][2 * D];
+  int bins[kBins];
+  Scan scan;
+  uint32_t range[3];
+  int last;
+};
+
+// One slice of one item: an item for each token and kv head, or (listed) for those of the tokens that
+// small_indptr counts.  kept: the item's keys.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) select_kernel(const BlockParams p) {
+__device__ __forceinline__ void select_item(const BlockParams& p, unsigned work, int slices, uint32_t* kept,
+                                            SelectShared<D>& sh) {
   constexpr int LPR = D / 32, RPW = 32 / LPR;  // lanes of a page's bounds, 64 bytes each; pages of a warp
   constexpr int U = 2;
-  extern __shared__ __align__(16) uint32_t kept[];  // keys
-  __shared__ __align__(16) int8_t codes[kWarps][2 * D];
-  __shared__ int bins[kBins];
-  __shared__ Scan scan;
-  __shared__ uint32_t range[3];
-  __shared__ int last_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_wait();
-  // an item for each token and kv head, or (listed) for those of the tokens that small_indptr counts
-  unsigned works = gridDim.x;
-  int slices = p.slices;
-  if (p.listed) {
-    const int items = p.small_indptr[p.batch] * p.g.Hkv;
-    slices = items > 0 ? max(1, min(p.slices, 2 * p.num_sms / items)) : 1;
-    works = unsigned(items) * slices;
-  }
-  for (unsigned work = blockIdx.x; work < works; work += gridDim.x) {
-  __syncthreads();  // (shared memory of the item before)
   const int item = work / slices, slice = work % slices;
   const int h = item % p.g.Hkv;
   int t = p.token0 + item / p.g.Hkv, guess = t;
@@ -343,23 +338,23 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const BlockParams p) {
     t = p.qo_indptr[guess] + t - p.small_indptr[guess];
   }
   const Query mine = find_query(p, t, guess);
-  if (!mine.there) continue;
+  if (!mine.there) return;
   const int n = mine.pos < 0 ? 0 : mine.pos / p.g.ps + 1;
   int32_t* out = p.blocks + (static_cast<int64_t>(t) * p.g.Hkv + h) * p.num_blocks;
   if (n <= p.num_blocks || n > p.max_pages) {
     if (slice == 0)
       for (int i = tid; i < p.num_blocks; i += kThreads) out[i] = i < n && n <= p.num_blocks ? i : -1;
     if (n > p.num_blocks && tid == 0) atomicOr(p.status, PA_DEV_NO_ROOM);
-    continue;
+    return;
   }
   const int lo = static_cast<int>(static_cast<int64_t>(n) * slice / slices);
   const int hi = static_cast<int>(static_cast<int64_t>(n) * (slice + 1) / slices);
-  query_codes<T, D>(static_cast<const T*>(p.q) + t * p.q_stride + static_cast<int64_t>(h) * p.G * D, p.G, codes[warp]);
+  query_codes<T, D>(static_cast<const T*>(p.q) + t * p.q_stride + static_cast<int64_t>(h) * p.G * D, p.G, sh.codes[warp]);
   __syncwarp();
   int c[16];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int4 v = *reinterpret_cast<const int4*>(codes[warp] + (i * LPR + lane % LPR) * 16);
+    const int4 v = *reinterpret_cast<const int4*>(sh.codes[warp] + (i * LPR + lane % LPR) * 16);
     c[4 * i] = v.x, c[4 * i + 1] = v.y, c[4 * i + 2] = v.z, c[4 * i + 3] = v.w;
   }
   uint32_t* row = p.keys + static_cast<int64_t>(item) * p.max_pages;
@@ -407,24 +402,41 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const BlockParams p) {
     __syncthreads();
     if (tid == 0) {
       int32_t* counter = p.counters + item;
-      last_s = atomicAdd(counter, 1) == slices - 1;
-      if (last_s) *counter = 0;
+      sh.last = atomicAdd(counter, 1) == slices - 1;
+      if (sh.last) *counter = 0;
     }
     __syncthreads();
-    if (!last_s) continue;
+    if (!sh.last) return;
     __threadfence();
   } else {
     __syncthreads();
   }
   if (own) {
-    select_largest([&](int i) { return kept[i]; }, n, p.num_blocks, out, bins, scan, range);
+    select_largest([&](int i) { return kept[i]; }, n, p.num_blocks, out, sh.bins, sh.scan, sh.range);
   } else if (n <= kKept) {
     for (int i = tid; i < n; i += kThreads) kept[i] = __ldcg(row + i);
     __syncthreads();
-    select_largest([&](int i) { return kept[i]; }, n, p.num_blocks, out, bins, scan, range);
+    select_largest([&](int i) { return kept[i]; }, n, p.num_blocks, out, sh.bins, sh.scan, sh.range);
   } else {
-    select_largest([&](int i) { return __ldcg(row + i); }, n, p.num_blocks, out, bins, scan, range);
+    select_largest([&](int i) { return __ldcg(row + i); }, n, p.num_blocks, out, sh.bins, sh.scan, sh.range);
   }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) select_kernel(const BlockParams p) {
+  extern __shared__ __align__(16) uint32_t kept[];
+  __shared__ SelectShared<D> shared;
+  pdl_wait();
+  unsigned works = gridDim.x;
+  int slices = p.slices;
+  if (p.listed) {
+    const int items = p.small_indptr[p.batch] * p.g.Hkv;
+    slices = items > 0 ? max(1, min(p.slices, 2 * p.num_sms / items)) : 1;
+    works = unsigned(items) * slices;
+  }
+  for (unsigned work = blockIdx.x; work < works; work += gridDim.x) {
+    __syncthreads();  // (shared memory of the item before)
+    select_item<T, D>(p, work, slices, kept, shared);
   }
 }
 
@@ -552,20 +564,18 @@ __device__ __forceinline__ void warp_select(const uint32_t* key, int n, int k, i
   });
 }
 
-// kGlobal: the keys in global memory, a piece for each of the CTAs, which take
-// tile after tile.
-template <typename T, int D, bool kGlobal>
-__global__ void __launch_bounds__(kGlobal ? 512 : kThreads, D == 256 ? (kGlobal ? 1 : 2) : (kGlobal ? 2 : 4))
-    select_tiles_kernel(const BlockParams p, const int row) {
-  constexpr int STEPS = 2 * D / 32, kWarps = kGlobal ? 16 : kThreads / 32;
-  extern __shared__ __align__(16) uint32_t kept_s[];  // [token][row]
-  __shared__ __align__(16) int8_t codes[kTileRows][2 * D + 64];  // (rows 64 bytes apart in the banks)
-  __shared__ __align__(16) int bins[kWarps][kWarpBins];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
-  uint32_t* const kept = kGlobal ? p.keys + static_cast<int64_t>(blockIdx.x) * kTileRows * row : kept_s;
-  pdl_wait();
-  const int works = p.tile_indptr[p.batch] * p.g.Hkv;
-  for (int work = blockIdx.x; work < works; work += gridDim.x) {
+template <int D, int kWarps>
+struct TilesShared {
+  __align__(16) int8_t codes[kTileRows][2 * D + 64];  // (rows 64 bytes apart in the banks)
+  __align__(16) int bins[kWarps][kWarpBins];
+};
+
+// One tile of a request's tokens and one kv head.  kept: keys, [token][row].
+template <typename T, int D, bool kGlobal, int kWarps>
+__device__ __forceinline__ void select_tile(const BlockParams& p, int work, uint32_t* kept, int row,
+                                            TilesShared<D, kWarps>& sh) {
+  constexpr int STEPS = 2 * D / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
   const int tile = work / p.g.Hkv, h = work % p.g.Hkv;
   const int b = last_below(p.tile_indptr, p.batch + 1, tile);
   const Span r = load_span(p, b, false);
@@ -578,9 +588,9 @@ __global__ void __launch_bounds__(kGlobal ? 512 : kThreads, D == 256 ? (kGlobal 
   if (pages > p.num_blocks) {
     for (int i = warp; i < kTileRows; i += kWarps) {
       if (i < tokens) {
-        query_codes<T, D>(static_cast<const T*>(p.q) + (token + i) * p.q_stride + static_cast<int64_t>(h) * p.G * D, p.G, codes[i]);
+        query_codes<T, D>(static_cast<const T*>(p.q) + (token + i) * p.q_stride + static_cast<int64_t>(h) * p.G * D, p.G, sh.codes[i]);
       } else {
-        for (int c = lane; c < D / 2; c += 32) reinterpret_cast<uint32_t*>(codes[i])[c] = 0;
+        for (int c = lane; c < D / 2; c += 32) reinterpret_cast<uint32_t*>(sh.codes[i])[c] = 0;
       }
     }
     __syncthreads();
@@ -590,7 +600,7 @@ __global__ void __launch_bounds__(kGlobal ? 512 : kThreads, D == 256 ? (kGlobal 
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int s = 0; s < STEPS / 2; ++s) a[i][s] = *reinterpret_cast<const uint4*>(codes[g + 8 * i] + (s * 4 + t4) * 16);
+      for (int s = 0; s < STEPS / 2; ++s) a[i][s] = *reinterpret_cast<const uint4*>(sh.codes[g + 8 * i] + (s * 4 + t4) * 16);
     // four steps of 8 pages at a time: their ids in one load
     for (int c0 = warp; c0 * 8 < pages; c0 += 4 * kWarps) {
       const int mine = (c0 + (lane >> 3) * kWarps) * 8 + (lane & 7);
@@ -631,14 +641,32 @@ __global__ void __launch_bounds__(kGlobal ? 512 : kThreads, D == 256 ? (kGlobal 
       if (n > p.num_blocks && lane == 0) atomicOr(p.status, PA_DEV_NO_ROOM);
     } else {
       // (a strip of 32 keys past n costs little, so few sizes do)
-      if (n <= 256) warp_select<8>(kept + i * row, n, p.num_blocks, p.first, p.last, out, bins[warp]);
-      else if (n <= 512) warp_select<16>(kept + i * row, n, p.num_blocks, p.first, p.last, out, bins[warp]);
-      else warp_select<0>(kept + i * row, n, p.num_blocks, p.first, p.last, out, bins[warp]);
+      if (n <= 256) warp_select<8>(kept + i * row, n, p.num_blocks, p.first, p.last, out, sh.bins[warp]);
+      else if (n <= 512) warp_select<16>(kept + i * row, n, p.num_blocks, p.first, p.last, out, sh.bins[warp]);
+      else warp_select<0>(kept + i * row, n, p.num_blocks, p.first, p.last, out, sh.bins[warp]);
     }
     __syncwarp();
   }
-  if constexpr (!kGlobal) return;  // (the grid has a CTA for each tile)
-  __syncthreads();
+}
+
+// kGlobal: the keys in global memory, a piece for each of the CTAs, which take
+// tile after tile; otherwise the grid has a CTA for each tile.
+template <typename T, int D, bool kGlobal>
+__global__ void __launch_bounds__(kGlobal ? 512 : kThreads, D == 256 ? (kGlobal ? 1 : 2) : (kGlobal ? 2 : 4))
+    select_tiles_kernel(const BlockParams p, const int row) {
+  constexpr int kWarps = kGlobal ? 16 : kThreads / 32;
+  extern __shared__ __align__(16) uint32_t kept[];
+  __shared__ TilesShared<D, kWarps> shared;
+  pdl_wait();
+  const int works = p.tile_indptr[p.batch] * p.g.Hkv;
+  if constexpr (kGlobal) {
+    uint32_t* piece = p.keys + static_cast<int64_t>(blockIdx.x) * kTileRows * row;
+    for (int work = blockIdx.x; work < works; work += gridDim.x) {
+      select_tile<T, D, true, kWarps>(p, work, piece, row, shared);
+      __syncthreads();
+    }
+  } else if (static_cast<int>(blockIdx.x) < works) {
+    select_tile<T, D, false, kWarps>(p, blockIdx.x, kept, row, shared);
   }
 }
 

@@ -537,7 +537,7 @@ PAGEDATTN_API pagedattn_status pagedattn_kv4_run(const pagedattn_kv4_cache* cach
 typedef struct {
   const uint64_t* turns; /* device, [rotary_dim / 2], 8-byte aligned                             */
   const int32_t* axes;   /* device, [rotary_dim / 2]: the axis whose position turns the pair, in
-                            [0, num_axes); or NULL, axis 0 for all                              */
+                            [0, num_axes) (others count as 0); or NULL, axis 0 for all          */
   int32_t num_axes;      /* positions a token: 1, or one for each of time, height, width ...    */
   int32_t rotary_dim;    /* a multiple of 16, at most head_dim                                  */
   int32_t interleaved;
