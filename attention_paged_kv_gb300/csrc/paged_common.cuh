@@ -73,14 +73,14 @@ __device__ __forceinline__ Span load_span(const BlockParams& p, int b, bool repo
 }
 
 // A page id, checked.
-__device__ __forceinline__ int page_of(const BlockParams& p, int at) {
-  int id = p.pages[at];
+__device__ __forceinline__ int checked_page(const BlockParams& p, int id) {
   if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.g.num_pages)) {
     atomicOr(p.status, PA_DEV_BAD_INDEX);
     id = 0;
   }
   return id;
 }
+__device__ __forceinline__ int page_of(const BlockParams& p, int at) { return checked_page(p, p.pages[at]); }
 
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 

@@ -328,7 +328,7 @@ template <typename T, int D>
 __device__ __forceinline__ void select_item(const BlockParams& p, unsigned work, int slices, uint32_t* kept,
                                             SelectShared<D>& sh) {
   constexpr int LPR = D / 32, RPW = 32 / LPR;  // lanes of a page's bounds, 64 bytes each; pages of a warp
-  constexpr int U = 2;
+  constexpr int U = D == 256 ? 4 : 2;  // 16 pages or more of a warp in flight
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int item = work / slices, slice = work % slices;
   const int h = item % p.g.Hkv;
@@ -349,6 +349,10 @@ __device__ __forceinline__ void select_item(const BlockParams& p, unsigned work,
   }
   const int lo = static_cast<int>(static_cast<int64_t>(n) * slice / slices);
   const int hi = static_cast<int>(static_cast<int64_t>(n) * (slice + 1) / slices);
+  // 32 pages of a warp at a time: their ids in one load, a page's lanes then get
+  // theirs (the first ones are on their way while q's codes are made)
+  auto ids = [&](int b0) { return b0 < hi ? p.pages[mine.page_start + min(b0 + lane, hi - 1)] : 0; };
+  int next = ids(lo + warp * 32);
   query_codes<T, D>(static_cast<const T*>(p.q) + t * p.q_stride + static_cast<int64_t>(h) * p.G * D, p.G, sh.codes[warp]);
   __syncwarp();
   int c[16];
@@ -359,9 +363,9 @@ __device__ __forceinline__ void select_item(const BlockParams& p, unsigned work,
   }
   uint32_t* row = p.keys + static_cast<int64_t>(item) * p.max_pages;
   const bool own = slices == 1 && n <= kKept;  // the keys need not leave the CTA
-  // 32 pages at a time: their ids in one load, a page's lanes then get theirs
   for (int b0 = lo + warp * 32; b0 < hi; b0 += kWarps * 32) {
-    const int id = page_of(p, mine.page_start + min(b0 + lane, hi - 1));
+    const int id = checked_page(p, next);
+    next = ids(b0 + kWarps * 32);
 #pragma unroll
     for (int w = 0; w < 32; w += U * RPW) {
       int4 v[U][4];
