@@ -20,7 +20,6 @@ from __future__ import annotations
 
 import ctypes
 import struct
-from fractions import Fraction
 
 from . import _binding as _b
 from ._kv4 import BatchTables, _call, _device, _is, _Object, _on, _refuse, _rows
@@ -30,7 +29,16 @@ _ROPE_ROWS = struct.Struct("@4P4qPq6i0P")
 _KV_ROWS = struct.Struct("@4P4q2PqP2i0P")
 _BLOCK_BATCH = struct.Struct("@4P9i0P")
 
-_TWO_PI = 2 * Fraction("3.14159265358979323846264338327950288419716939937510582")
+# 2 pi as a ratio of whole numbers, good to 50 digits
+_TWO_PI = (2 * 314159265358979323846264338327950288419716939937510582, 10 ** 53)
+
+
+def _turns(w):
+    """w radians in turns modulo 1, as the nearest multiple of 2^-64 (its numerator, signed: torch has no unsigned)."""
+    n, d = w.as_integer_ratio()
+    a, b = n * (_TWO_PI[1] << 64), d * _TWO_PI[0]
+    t = (2 * a + b) // (2 * b) & ((1 << 64) - 1)
+    return t - (1 << 64) if t >> 63 else t
 
 
 class Rope(_Object):
@@ -61,9 +69,7 @@ class Rope(_Object):
         self._lib = _b.load()
         self.device = _device(device)
         self._index = self.device.index
-        # turns a position modulo 1, in 64 bits (as signed ones: torch has no arithmetic on unsigned)
-        turns = [round(Fraction(w) / _TWO_PI * (1 << 64)) % (1 << 64) for w in freq]
-        self.turns = torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns], dtype=torch.int64, device=self.device)
+        self.turns = torch.tensor([_turns(w) for w in freq], dtype=torch.int64, device=self.device)
         self.axes = None if axes is None else torch.tensor(axes, dtype=torch.int32, device=self.device)
         self._args = _b.Rotation(self.turns.data_ptr(), None if axes is None else self.axes.data_ptr(), self.num_axes,
                                  self.rotary_dim, self.interleaved, self.scale)

@@ -1060,3 +1060,16 @@ def test_offsets_beyond_32_bits():
         assert a.device_status() == c.device_status() == 0
     for x, y in zip(*got):
         assert torch.equal(x, y)
+
+
+def test_turns_are_the_nearest_fractions():
+    """w / 2 pi modulo 1 in units of 2^-64, to the unit, for frequencies of either sign and any size."""
+    from fractions import Fraction
+    from attention_paged_kv_gb300 import _paged
+    two_pi = 2 * Fraction("3.14159265358979323846264338327950288419716939937510582")
+    rng = np.random.default_rng(0)
+    for w in [0.0, 1.0, -2.5, 6.283185307179586, 5e-324, 1e-9, 123.456, *rng.uniform(-3, 3, 50), *10.0 ** rng.uniform(-12, 6, 50)]:
+        exact = Fraction(float(w)) / two_pi * (1 << 64)
+        got = _paged._turns(float(w))
+        assert -(1 << 63) <= got < 1 << 63
+        assert abs((exact - got + (1 << 63)) % (1 << 64) - (1 << 63)) <= Fraction(1, 2) + Fraction(1, 1 << 40) * max(1, abs(exact) / (1 << 64))
