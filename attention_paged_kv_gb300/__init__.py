@@ -6,7 +6,8 @@ a tcgen05/TMEM tensor-core prefill kernel, a warp-MMA small-query kernel
 merge kernel and a C++ planner; and, for steps whose lengths stay on the
 device, page tables built there, a cache held in 4 bits and the attention
 over it, and over the 16-bit cache rotary positions, appending, the selection
-of pages and the attention over them.  This package is the thin ctypes binding with the same names.  Build the library with
+of pages and the attention over them.  This package is the thin ctypes binding
+with the same names.  Build the library with
 ``python -m attention_paged_kv_gb300.build``.
 """
 from ._binding import (DEFAULT_WORKSPACE_BYTES, EXPORTED, PA_BF16, PA_DEV_BAD_INDEX, PA_DEV_TIMEOUT,
@@ -19,6 +20,6 @@ from ._binding import (DEFAULT_WORKSPACE_BYTES, EXPORTED, PA_BF16, PA_DEV_BAD_IN
 from ._kv4 import BatchTables, Kv4Attention, Kv4Cache
 from ._paged import BlockAttention, KvCache, Rope
 
-__all__ = ["Plan", "BatchTables", "Kv4Cache", "Kv4Attention", "Rope", "KvCache", "BlockAttention",
-            "PagedAttnError", "workspace_size", "load", "version", "last_error", "check", "Options",
-           "EXPORTED", "LIB_PATH", "DEFAULT_WORKSPACE_BYTES"]
+__all__ = ["Plan", "BatchTables", "Kv4Cache", "Kv4Attention", "Rope", "KvCache", "BlockAttention", "PagedAttnError",
+           "workspace_size", "load", "version", "last_error", "check", "Options", "EXPORTED", "LIB_PATH",
+           "DEFAULT_WORKSPACE_BYTES"]

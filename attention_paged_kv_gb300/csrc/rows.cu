@@ -13,7 +13,7 @@
 // token, two 16-byte pieces of a head, and goes through the heads of a group
 // with the same 8 cosines and sines.  16000 tokens of 64 / 8 heads of 128 with V
 // (656 MB): 102 us, 6.4 TB/s; 12001 tokens of 32 / 8 heads, three axes, pairs side
-// by side (246 MB): 41 us, 6.0 TB/s; 64 tokens 2.3 to 2.5 us, a launch's time.  In
+// by side (246 MB): 41 us, 6.0 TB/s; 64 tokens 2.4 to 2.6 us, a launch's time.  In
 // CTAs of 256 threads 104, 42.2 and 2.8.
 //
 // Bounds: a page's keys are read once, D / 8 lanes a row.  8 prompts of 1001 to

@@ -18,9 +18,9 @@
 // histogram over 256 parts, and the ranks of the keys of the part that holds the border.
 //
 // What bounds them.  64 decodes of 512 to 8192 keys (pages of 16, 8 kv heads, 34
-// MB): 14.3 us, 5 at the copy rate; the rest is one dependent load after the
+// MB): 13.7 us, 5 at the copy rate; the rest is one dependent load after the
 // other (tables, page ids, bounds) and the CTA's barriers.  A chunk of 2000
-// tokens over 500 pages: 57 us, in two rounds of CTAs; in each, codes of q 3.6
+// tokens over 500 pages: 58 us, in two rounds of CTAs; in each, codes of q 3.6
 // us, scores 10.4 (8-bit products: 36 cycles of a sub-partition each), the
 // selection 8.6 (its instructions).  Measured without gain there: products in
 // fp16 (bounds converted, 62), bounds loaded a step ahead (registers for two CTAs
