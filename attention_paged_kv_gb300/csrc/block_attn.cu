@@ -3,9 +3,9 @@
 // Work.  An item is one query token and kv head (up to 16 of the group's heads,
 // 8 at head_dim 256): its rows share every key.  A CTA takes an item, or where
 // items are few a slice of its list; slices leave fp32 partial states that the
-// last of them joins.  The CTA's warps take every fourth tile of 16 keys each
-// and copy their own keys ahead (cp.async into a ring of their own), so that no
-// warp waits for another until their states are joined at the end.
+// last of them joins.  The CTA's warps take every fourth tile of 16 keys (32 at
+// head_dim 64) and copy their own keys ahead (cp.async into a ring of their own),
+// so that no warp waits for another until their states are joined at the end.
 //
 // S^T = K q^T and O^T = V^T P^T with m16n8k16: keys (or head dims) fill the
 // 16-row side and the heads the other.  P is 2^(logit - m) with the reference m
@@ -30,7 +30,6 @@ namespace pa {
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kTile = 16;  // keys
 constexpr float kNone = -3.0e38f;  // a maximum before any key: finite, so that it can be subtracted
 constexpr float kHead = 7.f, kRise = 8.f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -39,10 +38,14 @@ template <int D, int NT>
 struct Cfg {
   static constexpr int ROWS = 8 * NT;
   static constexpr int ROW = 2 * D;                  // bytes of a key's row
-  static constexpr int STAGE = 2 * kTile * ROW;      // K, then V
-  static constexpr int STAGES = D == 64 ? 4 : 3;
+  // A tile: two pieces of 16 keys at head_dim 64, else one.  64 decodes of 2048 keys
+  // at 64 / 8 heads of 64 take 44.0 us so and 45.3 with one piece (and three CTAs an
+  // SM), 3 requests of 4096 keys 9.7 and 11.4.
+  static constexpr int PIECES = D == 64 ? 2 : 1, TILE = 16 * PIECES;
+  static constexpr int STAGE = 2 * TILE * ROW;       // K, then V
+  static constexpr int STAGES = 3;
   static constexpr int RING = STAGES * STAGE;        // of a warp
-  static constexpr int CTAS = D == 64 ? 3 : (D == 128 ? 2 : 1);
+  static constexpr int CTAS = D == 256 ? 1 : 2;
   static constexpr int SMEM = kWarps * RING;         // the list comes behind
   static constexpr int O_STRIDE = D + 4;             // floats of a row of a warp's state, in its ring's place
   static_assert(ROWS * (O_STRIDE + 2) * 4 <= RING, "a warp's state fits its ring");
@@ -232,53 +235,59 @@ __device__ __forceinline__ void attend_item(const BlockParams& p, unsigned work,
 
   // ---- the warp's tiles
   const int keys = entries << p.g.ps_shift;
-  const int tiles = (keys + kTile - 1) / kTile;
+  const int pieces = (keys + 15) / 16, tiles = (pieces + C::PIECES - 1) / C::PIECES;
   const uint32_t ring = smem_u32(smem) + warp * C::RING;
   const int64_t v_off = static_cast<int64_t>(p.g.ps) * p.g.Hkv * C::ROW;
   const int64_t slot_bytes = static_cast<int64_t>(p.g.slot_rows) * C::ROW;
   const int row0 = lane / CH;  // of the rows that the lane copies, every RPI-th
   const uint8_t* data = static_cast<const uint8_t*>(p.data) + static_cast<int64_t>(h) * p.g.head_rows * C::ROW + lane % CH * 16;
-  const bool whole = p.g.ps_shift >= 4;  // a tile lies in one page
+  const bool whole = p.g.ps_shift >= 4;  // a piece lies in one page
   // Key i of the slice: the list's entry, and whether the query sees it.
   auto entry_of = [&](int i) { return list[min(i >> p.g.ps_shift, entries - 1)]; };
   auto seen = [&](int i, int word) { return i < keys && (word >= 0 || (i & (p.g.ps - 1)) <= limit); };
-  // Rows of a tile that lies in one page which the query sees: the first `live`.
-  auto live_of = [&](int tile, int word) { return word >= 0 ? kTile : limit + 1 - ((tile * kTile) & (p.g.ps - 1)); };
+  // Of a piece in one page: its entry, and how many of its first rows the query sees.
+  auto word_of = [&](int piece) { return list[min(piece, pieces - 1) >> (p.g.ps_shift - 4)]; };
+  auto live_of = [&](int piece, int word) {
+    return C::PIECES > 1 && piece >= pieces ? 0 : (word >= 0 ? 16 : limit + 1 - ((piece * 16) & (p.g.ps - 1)));
+  };
   auto copy = [&](int tile, int stage) {
     if (tile < tiles) {
-      const uint32_t dst = ring + stage * C::STAGE + row0 * C::ROW;
-      const uint32_t piece = (lane % CH) ^ row0;
-      if (whole) {
-        const int word = list[tile >> (p.g.ps_shift - 4)], slot0 = (tile * kTile) & (p.g.ps - 1);
-        const int live = live_of(tile, word);
-        const uint8_t* k = data + static_cast<int64_t>(word & INT_MAX) * (2 * v_off) + (slot0 + row0) * slot_bytes;
-        const uint8_t* v = k + v_off;
-        if (live >= kTile) {
+      const uint32_t chunk16 = (lane % CH) ^ row0;
 #pragma unroll
-          for (int i = 0; i < kTile / RPI; ++i) {
-            const uint32_t at = dst + i * RPI * C::ROW + (piece ^ (i * RPI & 7)) * 16;
-            cp_async16(at, k + i * RPI * slot_bytes, 16);
-            cp_async16(at + kTile * C::ROW, v + i * RPI * slot_bytes, 16);
+      for (int m = 0; m < C::PIECES; ++m) {
+        const uint32_t dst = ring + stage * C::STAGE + (m * 16 + row0) * C::ROW;
+        const int piece = tile * C::PIECES + m;
+        if (whole) {
+          const int word = word_of(piece), slot0 = (piece * 16) & (p.g.ps - 1), live = live_of(piece, word);
+          const uint8_t* k = data + static_cast<int64_t>(word & INT_MAX) * (2 * v_off) + (slot0 + row0) * slot_bytes;
+          const uint8_t* v = k + v_off;
+          if (live >= 16) {
+#pragma unroll
+            for (int i = 0; i < 16 / RPI; ++i) {
+              const uint32_t at = dst + i * RPI * C::ROW + (chunk16 ^ (i * RPI & 7)) * 16;
+              cp_async16(at, k + i * RPI * slot_bytes, 16);
+              cp_async16(at + C::TILE * C::ROW, v + i * RPI * slot_bytes, 16);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16 / RPI; ++i) {
+              const uint32_t at = dst + i * RPI * C::ROW + (chunk16 ^ (i * RPI & 7)) * 16;
+              const uint32_t bytes = i * RPI + row0 < live ? 16 : 0;
+              cp_async16(at, k + i * RPI * slot_bytes, bytes);
+              cp_async16(at + C::TILE * C::ROW, v + i * RPI * slot_bytes, bytes);
+            }
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < kTile / RPI; ++i) {
-            const uint32_t at = dst + i * RPI * C::ROW + (piece ^ (i * RPI & 7)) * 16;
-            const uint32_t bytes = i * RPI + row0 < live ? 16 : 0;
-            cp_async16(at, k + i * RPI * slot_bytes, bytes);
-            cp_async16(at + kTile * C::ROW, v + i * RPI * slot_bytes, bytes);
+          for (int i = 0; i < 16 / RPI; ++i) {
+            const int key = piece * 16 + i * RPI + row0;
+            const int word = entry_of(key);
+            const uint32_t bytes = seen(key, word) ? 16 : 0;
+            const uint8_t* src = data + static_cast<int64_t>(word & INT_MAX) * (2 * v_off) + (key & (p.g.ps - 1)) * slot_bytes;
+            const uint32_t at = dst + i * RPI * C::ROW + (chunk16 ^ (i * RPI & 7)) * 16;
+            cp_async16(at, src, bytes);
+            cp_async16(at + C::TILE * C::ROW, src + v_off, bytes);
           }
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < kTile / RPI; ++i) {
-          const int key = tile * kTile + i * RPI + row0;
-          const int word = entry_of(key);
-          const uint32_t bytes = seen(key, word) ? 16 : 0;
-          const uint8_t* src = data + static_cast<int64_t>(word & INT_MAX) * (2 * v_off) + (key & (p.g.ps - 1)) * slot_bytes;
-          const uint32_t at = dst + i * RPI * C::ROW + (piece ^ (i * RPI & 7)) * 16;
-          cp_async16(at, src, bytes);
-          cp_async16(at + kTile * C::ROW, src + v_off, bytes);
         }
       }
     }
@@ -304,48 +313,60 @@ __device__ __forceinline__ void attend_item(const BlockParams& p, unsigned work,
     copy(tile + (C::STAGES - 1) * kWarps, stage == 0 ? C::STAGES - 1 : stage - 1);
     const uint32_t at = ring + stage * C::STAGE;
     stage = stage == C::STAGES - 1 ? 0 : stage + 1;
-    float s[NT][4];
+    float s[NT][C::PIECES][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
+      for (int m = 0; m < C::PIECES; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[n][m][i] = 0.f;
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
-      uint32_t a[4];
-      ldmatrix<false>(a, at + (lane & 15) * C::ROW + ((2 * k + (lane >> 4)) ^ (lane & 7)) * 16);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) mma<T>(s[n], a, qf[n][k][0], qf[n][k][1]);
-    }
-    bool see0 = true, see1 = true, masked = false;
-    if (whole) {
-      const int word = list[tile >> (p.g.ps_shift - 4)];
-      if (word < 0) {
-        const int live = live_of(tile, word);
-        masked = live < kTile;
-        see0 = g < live, see1 = g + 8 < live;
+      for (int m = 0; m < C::PIECES; ++m) {
+        uint32_t a[4];
+        ldmatrix<false>(a, at + (m * 16 + (lane & 15)) * C::ROW + ((2 * k + (lane >> 4)) ^ (lane & 7)) * 16);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma<T>(s[n][m], a, qf[n][k][0], qf[n][k][1]);
       }
-    } else {
-      const int k0 = tile * kTile + g;
-      masked = true;
-      see0 = seen(k0, entry_of(k0)), see1 = seen(k0 + 8, entry_of(k0 + 8));
     }
-    if (masked) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+    for (int m = 0; m < C::PIECES; ++m) {
+      const int piece = tile * C::PIECES + m;
+      bool see0 = true, see1 = true, masked = false;
+      if (whole) {
+        const int live = live_of(piece, word_of(piece));
+        masked = live < 16;
+        see0 = g < live, see1 = g + 8 < live;
+      } else {
+        const int k0 = piece * 16 + g;
+        masked = true;
+        see0 = seen(k0, entry_of(k0)), see1 = seen(k0 + 8, entry_of(k0 + 8));
+      }
+      if (masked) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[n][i] = (i < 2 ? see0 : see1) ? s[n][i] : -INFINITY;
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[n][m][i] = (i < 2 ? see0 : see1) ? s[n][m][i] : -INFINITY;
+      }
     }
+    // the largest of a lane's keys for each of its heads
+    auto largest = [&](int n, int i) {
+      float top = fmaxf(s[n][0][i], s[n][0][i + 2]);
+      if constexpr (C::PIECES > 1) top = fmaxf(top, fmaxf(s[n][1][i], s[n][1][i + 2]));
+      return top;
+    };
     bool over = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) over = over || fmaxf(s[n][i], s[n][i + 2]) > above[n][i];
+      for (int i = 0; i < 2; ++i) over = over || largest(n, i) > above[n][i];
     if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float top = fmaxf(s[n][i], s[n][i + 2]);
+          float top = largest(n, i);
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
           if (top > above[n][i]) {
@@ -362,32 +383,36 @@ __device__ __forceinline__ void attend_item(const BlockParams& p, unsigned work,
         }
       }
     }
-    uint32_t b[NT][2], b_low[NT][2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[n][i] = ex2(fmaf(s[n][i], p.scale_log2, -m[n][i & 1]));
-      l[n][0] += s[n][0] + s[n][2];
-      l[n][1] += s[n][1] + s[n][3];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t w = Elt<T>::from_f2(s[n][2 * i], s[n][2 * i + 1]);
-        b[n][i] = movmatrix(w);
-        if constexpr (Elt<T>::kBf16) {
-          const float2 r = Elt<T>::to_f2(w);
-          b_low[n][i] = movmatrix(Elt<T>::from_f2(s[n][2 * i] - r.x, s[n][2 * i + 1] - r.y));
-        }
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      uint32_t a[4];
-      const int r = (lane & 7) + (lane >> 4) * 8;
-      ldmatrix<true>(a, at + (kTile + r) * C::ROW + ((2 * k + ((lane >> 3) & 1)) ^ (lane & 7)) * 16);
+    for (int w = 0; w < C::PIECES; ++w) {
+      uint32_t b[NT][2], b_low[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        mma<T>(o[n][k], a, b[n][0], b[n][1]);
-        if constexpr (Elt<T>::kBf16) mma<T>(o[n][k], a, b_low[n][0], b_low[n][1]);
+        float(&x)[4] = s[n][w];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = ex2(fmaf(x[i], p.scale_log2, -m[n][i & 1]));
+        l[n][0] += x[0] + x[2];
+        l[n][1] += x[1] + x[3];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t both = Elt<T>::from_f2(x[2 * i], x[2 * i + 1]);
+          b[n][i] = movmatrix(both);
+          if constexpr (Elt<T>::kBf16) {
+            const float2 r = Elt<T>::to_f2(both);
+            b_low[n][i] = movmatrix(Elt<T>::from_f2(x[2 * i] - r.x, x[2 * i + 1] - r.y));
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        uint32_t a[4];
+        const int r = w * 16 + (lane & 7) + (lane >> 4) * 8;
+        ldmatrix<true>(a, at + (C::TILE + r) * C::ROW + ((2 * k + ((lane >> 3) & 1)) ^ (lane & 7)) * 16);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          mma<T>(o[n][k], a, b[n][0], b[n][1]);
+          if constexpr (Elt<T>::kBf16) mma<T>(o[n][k], a, b_low[n][0], b_low[n][1]);
+        }
       }
     }
   }
@@ -521,7 +546,7 @@ AttendShape attend_shape(const BlockShape& s) {
   AttendShape a;
   a.rows = s.D == 256 || s.G <= 8 ? 8 : 16;
   a.chunks = (s.G + a.rows - 1) / a.rows;
-  a.ctas = s.num_sms * (s.D == 64 ? 3 : (s.D == 128 ? 2 : 1));
+  a.ctas = s.num_sms * (s.D == 256 ? 1 : 2);
   // slices of 128 keys or more (3 requests of 4096 keys 16.4 us, in one slice each 34.5)
   int64_t n = int64_t(s.num_blocks) * s.page_size / 128;
   if (n > s.num_blocks) n = s.num_blocks;
@@ -531,7 +556,7 @@ AttendShape attend_shape(const BlockShape& s) {
 }
 
 int64_t attend_part_rows(const BlockShape& s) {
-  return int64_t(s.num_sms) * 3 * 16;  // no more slices in all than CTAs that fit the card
+  return int64_t(s.num_sms) * 2 * 16;  // no more slices in all than CTAs that fit the card
 }
 
 cudaError_t launch_block_attention(BlockParams p, const BlockShape& s, int dtype, cudaStream_t stream) {
