@@ -13,7 +13,9 @@
 // passes it by 15: a row's largest P lies in [2^7, 2^15], and the keys' ones
 // down to 2^-21 of it are rounded like it.  P is rounded to fp16 for fp16
 // values (by 2^-11 of it at most); for bf16, where that would be 2^-8, it is split
-// in two bf16 terms and multiplied twice.
+// in two bf16 terms and multiplied twice.  Logits are scaled and rounded as m was
+// before m is taken off (no fused step): however large they are, a key's is at most 15
+// above m, and the largest not below it.
 //
 // What bounds it: HBM.  64 decodes of 2048 keys at 64 / 8 heads (464 MB) take 75
 // us, 6.2 TB/s, 91 % of the copy rate; 3 requests of 4096 of up to 131071 keys (50 MB)
@@ -297,7 +299,8 @@ __device__ __forceinline__ void attend_item(const BlockParams& p, unsigned work,
   float o[NT][KS][4], m[NT][2], l[NT][2], above[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    m[n][0] = m[n][1] = above[n][0] = above[n][1] = kNone;
+    m[n][0] = m[n][1] = kNone;
+    above[n][0] = above[n][1] = -INFINITY;
     l[n][0] = l[n][1] = 0.f;
 #pragma unroll
     for (int k = 0; k < KS; ++k)
@@ -370,8 +373,8 @@ __device__ __forceinline__ void attend_item(const BlockParams& p, unsigned work,
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
           if (top > above[n][i]) {
-            const float next = top * p.scale_log2 - kHead, f = ex2(m[n][i] - next);
-            above[n][i] = top + kRise / p.scale_log2;
+            const float next = __fmul_rn(top, p.scale_log2) - kHead, f = ex2(m[n][i] - next);
+            above[n][i] = fabsf(next) < 0x1p20f ? top + kRise / p.scale_log2 : top;
             m[n][i] = next;
             l[n][i] *= f;
 #pragma unroll
@@ -390,7 +393,7 @@ __device__ __forceinline__ void attend_item(const BlockParams& p, unsigned work,
       for (int n = 0; n < NT; ++n) {
         float(&x)[4] = s[n][w];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = ex2(fmaf(x[i], p.scale_log2, -m[n][i & 1]));
+        for (int i = 0; i < 4; ++i) x[i] = ex2(__fmul_rn(x[i], p.scale_log2) - m[n][i & 1]);
         l[n][0] += x[0] + x[2];
         l[n][1] += x[1] + x[3];
 #pragma unroll

@@ -789,6 +789,46 @@ def test_attention_keeps_a_long_tail(kv, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("qo, kv, Hq, D, page, gain", [
+    ([1, 1, 1], [700, 9, 3000], 16, 64, 16, 1e4), ([1], [5000], 8, 128, 2, 1e4), ([1, 1], [900, 40], 8, 256, 32, 1e4),
+    ([1, 2], [333, 600], 24, 128, 16, 500.0), ([300], [900], 16, 128, 16, 500.0)], ids=str)
+def test_attention_of_large_logits(qo, kv, Hq, D, page, gain, dtype):
+    """Logits of 10^8 and more (or 10^6): rows whose largest stands out take its value.
+
+    Its weight is off by half a step of the type at most, as is the output: twice eps / 2.  The others' logits lie
+    two bounds of the fp32 sums and 40 below it: less than 2^-40 together.  lse: that bound, 2^-20 for
+    exp2 and log2, and six roundings of 2^-24 (two factors, their products, the reference, its sum with the log)."""
+    b = Batch(qo, kv, Hq, Hq // 2 if len(qo) == 1 and qo[0] > 1 else 2, D, page, "NHD", dtype, seed=8, q_gain=gain)
+    b.cache.data.mul_(gain)
+    b.cache.data[:, 1].div_(gain)
+    b.cache.data.clamp_(-6e4, 6e4)
+    b.q.clamp_(-6e4, 6e4)
+    blocks = -(-max(kv) // page)
+    lists = np.broadcast_to(np.arange(blocks, dtype=np.int32), (b.T, b.Hkv, blocks)).copy()
+    for i, (_, _, n, _) in enumerate(paged.queries(b.qo_indptr, b.page_indptr, b.last, page)):
+        lists[i, :, n:] = -1
+    ref, ref_lse, sp = b.want(lists)
+    ds = 2.0 ** -22 * (D / 16 + 2) * sp["s"]
+    G = b.Hq // b.Hkv
+    data, q = b.cache.data.double().cpu().numpy(), host(b.q)
+    clear = np.zeros((b.T, b.Hq), bool)
+    for i, (_, start, n, pos) in enumerate(paged.queries(b.qo_indptr, b.page_indptr, b.last, page)):
+        k = data[b.pages[start: start + n], 0].reshape(-1, b.Hkv, D)[: pos + 1]
+        z = np.sort(np.einsum("nhd,hgd->hgn", k, q[i].reshape(b.Hkv, G, D)).reshape(b.Hq, -1) / np.sqrt(D))
+        clear[i] = z[:, -1] - z[:, -2] > 2 * ds[i] + 40
+    assert clear.mean() > 0.8 and np.abs(ref_lse).max() > (1e8 if gain > 1e3 else 1e5)
+    a = b.attention(blocks)
+    out, lse = a.run(b.q, b.cache, b.tables(), dev(lists))
+    assert a.device_status() == 0
+    out, lse = host(out), host(lse)
+    assert np.isfinite(out).all()
+    assert (np.abs(lse - ref_lse) <= ds + 6 * 2.0 ** -24 * np.abs(ref_lse) + 2.0 ** -20)[clear].all()
+    eps = torch.finfo(dtype).eps
+    assert (np.abs(out - ref) <= eps * (1 + eps) * np.abs(ref) + 2.0 ** -25)[clear].all()
+
+
+@gpu
 def test_attention_nan_stays_its_own():
     """A NaN of q reaches its row, one of K or V the rows of its kv head that list its page and see it."""
     b = Batch([1, 2, 1], [100, 100, 100], 8, 2, 128, 16, "NHD", torch.float16, seed=2)
