@@ -99,13 +99,13 @@ class Rope(_Object):
         at = self._index
         if q.dim() != 3:
             _refuse("q must be of shape [tokens, heads, head_dim]")
-        n, heads, dim = q.shape
+        size = n, _, dim = q.shape
         k_heads = 0 if k is None else (k.shape[1] if k.dim() == 3 else -1)
         shape = (n, k_heads, dim)
-        q_stride = _rows(q, "q", q.shape, at)
+        q_stride = _rows(q, "q", size, at)
         k_stride = 0 if k is None else _rows(k, "k", shape, at)
         if q_out is not None:
-            _rows(q_out, "q_out", q.shape, at)
+            _rows(q_out, "q_out", size, at)
         if k_out is not None:
             if k is None:
                 _refuse("k_out without k")
@@ -118,22 +118,24 @@ class Rope(_Object):
         handle, guard = _on(at, stream, (self,), (q, k, positions, q_out, k_out))
         if guard is not None:
             with guard:  # the outputs are allocated on the stream that writes them
-                return self._launch(q, k, q_stride, k_stride, q_out, k_out, pos, pos_stride, inverse, code, handle)
-        return self._launch(q, k, q_stride, k_stride, q_out, k_out, pos, pos_stride, inverse, code, handle)
+                return self._launch(q, k, size, k_heads, q_stride, k_stride, q_out, k_out, pos, pos_stride, inverse,
+                                    code, handle)
+        return self._launch(q, k, size, k_heads, q_stride, k_stride, q_out, k_out, pos, pos_stride, inverse, code,
+                            handle)
 
-    def _launch(self, q, k, q_stride, k_stride, q_out, k_out, pos, pos_stride, inverse, code, handle):
+    def _launch(self, q, k, size, k_heads, q_stride, k_stride, q_out, k_out, pos, pos_stride, inverse, code, handle):
         import torch
-        n, heads, dim = q.shape
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        n, heads, dim = size
+        if q_out is None:  # (alike but for the tokens' stride: twice as quick as with type, shape and device by name)
+            q_out = torch.empty_like(q)
         if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+            k_out = torch.empty_like(k)
         more = n > 1
         rows = _ROPE_ROWS.pack(q.data_ptr(), 0 if k is None else k.data_ptr(), q_out.data_ptr(),
                                0 if k is None else k_out.data_ptr(), q_stride, k_stride,
                                q_out.stride(0) if more else heads * dim,
-                               0 if k is None else (k_out.stride(0) if more else k.shape[1] * dim), pos, pos_stride, n,
-                               heads, 0 if k is None else k.shape[1], dim, bool(inverse), code)
+                               0 if k is None else (k_out.stride(0) if more else k_heads * dim), pos, pos_stride, n, heads,
+                               k_heads, dim, bool(inverse), code)
         status = self._lib.pagedattn_rope(ctypes.byref(self._args), rows, handle)
         if status != _b.PA_OK:
             _b.check(status)
@@ -233,7 +235,7 @@ class KvCache(_Object):
     def _append(self, k, v, slots, rope, q, q_out, k_stride, v_stride, q_stride, q_heads, pos, pos_stride, n, handle):
         import torch
         if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = torch.empty_like(q)
         out_stride = 0 if q is None else (q_out.stride(0) if n > 1 else q_heads * self.head_dim)
         rows = _KV_ROWS.pack(k.data_ptr(), v.data_ptr(), 0 if q is None else q.data_ptr(),
                              0 if q is None else q_out.data_ptr(), k_stride, v_stride, q_stride, out_stride,
@@ -305,6 +307,9 @@ class BlockAttention(_Object):
             _b.check(self._lib.pagedattn_blocks_workspace_size(self.num_kv_heads, self.head_dim, self.page_size, sizes,
                                                                ctypes.byref(need)))
             self._take_workspace(workspace, need.value, BlockAttention)
+        # what allocated outputs are like
+        self._a_list = self.status.expand(self._lists)
+        self._an_lse = self.status.view(torch.float32).expand(self._shape[:2])
 
     def _sizes(self, qo_indptr, page_indptr, pages, last, nnz):
         return _BLOCK_BATCH.pack(qo_indptr, page_indptr, pages, last, self.batch_size, nnz, self.num_tokens,
@@ -335,7 +340,7 @@ class BlockAttention(_Object):
             _is(page_indptr, "kv_page_indptr", i32, (B + 1,), at)
             _is(pages, "kv_page_indices", i32, (nnz,), at)
             _is(last, "kv_last_page_len", i32, (B,), at)
-        batch = self._sizes(*(t.data_ptr() for t in tables), nnz)
+        batch = self._sizes(tables[0].data_ptr(), tables[1].data_ptr(), tables[2].data_ptr(), tables[3].data_ptr(), nnz)
         return stride, batch, objects, tables
 
     def select(self, q, cache, tables, out=None, stream=None):
@@ -356,10 +361,10 @@ class BlockAttention(_Object):
         handle, guard = _on(self._index, stream, objects, (q, out, *tables))
         if out is None:
             if guard is None:
-                out = torch.empty(self._lists, dtype=torch.int32, device=self.device)
+                out = torch.empty_like(self._a_list)
             else:
                 with guard:  # allocated on the stream that writes it
-                    out = torch.empty(self._lists, dtype=torch.int32, device=self.device)
+                    out = torch.empty_like(self._a_list)
                 handle, guard = _on(self._index, stream, ())
         _call(guard, self._lib.pagedattn_select_blocks, ctypes.byref(cache._args), batch, q.data_ptr(), stride,
               out.data_ptr(), self._ws_ptr, self._ws_bytes, handle)
@@ -388,9 +393,9 @@ class BlockAttention(_Object):
     def _launch(self, q, stride, cache, batch, blocks, out, lse, return_lse, handle):
         import torch
         if out is None:
-            out = torch.empty(self._shape, dtype=self._dtype, device=self.device)
+            out = torch.empty_like(q)
         if lse is None and return_lse:
-            lse = torch.empty(self._shape[:2], dtype=torch.float32, device=self.device)
+            lse = torch.empty_like(self._an_lse)
         status = self._lib.pagedattn_blocks_run(ctypes.byref(cache._args), batch, blocks.data_ptr(), q.data_ptr(), stride,
                                                 out.data_ptr(), None if lse is None else lse.data_ptr(), self._ws_ptr,
                                                 self._ws_bytes, handle)
