@@ -198,7 +198,8 @@ class KvCache(_Object):
         distinct.  rope: a Rope that turns k, and q [n, heads, head_dim] where
         given, by the positions (int32 [n], or [num_axes, n]); q_out (allocated
         where not given) may be q.  Tokens at any stride that is a multiple of 8.
-        Bounds, where the cache has them, follow (see update_bounds).  See
+        Bounds, where the cache has them, follow, and then the slots of a page
+        have to stand together in ascending order (see update_bounds).  See
         pagedattn_kv_append.
         """
         import torch
@@ -250,8 +251,9 @@ class KvCache(_Object):
         """The bounds of the pages that the slots (int64 [n]) name, each over its slots up to the one named last.
 
         For keys that came into ``data`` by other ways than append.  The slots of
-        a page stand one behind the other in ascending order, as BatchTables lays
-        them out; negative ones are skipped.  See pagedattn_kv_bounds.
+        a page stand together in ascending order, as BatchTables lays them out, none
+        of another page between them; negative ones may stand anywhere and are
+        skipped.  See pagedattn_kv_bounds.
         """
         import torch
         if self.bounds is None:

@@ -608,16 +608,21 @@ typedef struct {
  * beyond are skipped and raise PA_DEV_BAD_INDEX.  The non-negative slots of
  * one call must be distinct: two rows for one slot may leave a mixture of both
  * there.  Where the cache has bounds, those of the pages written to are made
- * anew, as by pagedattn_kv_bounds.
+ * anew, as by pagedattn_kv_bounds, whose order of the slots is then asked for here too
+ * (rows in any other order: a cache without bounds over the same data, then
+ * pagedattn_kv_bounds with the slots sorted).
  */
 PAGEDATTN_API pagedattn_status pagedattn_kv_append(const pagedattn_kv_cache* cache, const pagedattn_rotation* rotation,
                                      const pagedattn_kv_rows* rows, pagedattn_stream_t stream);
 
 /*
  * The bounds of the pages that the slots name, each over its slots from 0 to
- * the one named last.  The slots of one page have to stand one behind the other
- * in ascending order, as pagedattn_build_tables lays them out.  Negative ones
- * are skipped, those beyond the cache too, which raises PA_DEV_BAD_INDEX.
+ * the one named last.  The slots of one page have to stand together in
+ * ascending order, as pagedattn_build_tables lays them out: none of another page
+ * between them.  Negative ones may stand anywhere and are skipped; those beyond the
+ * cache too, which raises PA_DEV_BAD_INDEX, as does a slot behind a larger one or itself of
+ * its page.  (Of a page whose slots stand apart, with another page's between them, the bounds
+ * may be those of its keys up to any of the slots' groups.)
  */
 PAGEDATTN_API pagedattn_status pagedattn_kv_bounds(const pagedattn_kv_cache* cache, const int64_t* slot_mapping,
                                      int32_t num_tokens, int32_t* status, pagedattn_stream_t stream);

@@ -1113,3 +1113,57 @@ def test_turns_are_the_nearest_fractions():
         got = _paged._turns(float(w))
         assert -(1 << 63) <= got < 1 << 63
         assert abs((exact - got + (1 << 63)) % (1 << 64) - (1 << 63)) <= Fraction(1, 2) + Fraction(1, 1 << 40) * max(1, abs(exact) / (1 << 64))
+
+
+# ---------------------------------------------------------------- bounds of slots with others between them
+
+
+@gpu
+@pytest.mark.parametrize("h, page, n, gaps", [
+    (1, 16, 40, [1]), (8, 16, 30, [1, 2, 7]), (2, 64, 100, [1, 250, 256, 3]), (1, 128, 5, [300, 1400, 9000]),
+    (8, 16, 3000, [1, 1, 40]), (3, 32, 5000, [2, 500, 1]), (4, 8, 20, [256, 255, 257, 1023, 1024, 1025, 2])], ids=str)
+def test_bounds_pass_over_rows_without_a_slot(h, page, n, gaps):
+    """Negative slots, and slots beyond the cache, between two of one page: the bounds are those of all its slots.
+
+    From one token a warp to 32, the next row within the CTA's tokens, within what it loads ahead, and beyond."""
+    rng = np.random.default_rng(n)
+    num_pages = -(-n // page) + 2
+    ids = rng.permutation(num_pages)
+    t = np.arange(n)
+    slots, named, at = [], ids[t // page] * page + t % page, 0
+    while at < n:
+        take = int(rng.integers(1, 5))
+        slots += list(named[at: at + take])
+        gap = gaps[int(rng.integers(len(gaps)))] if rng.random() < min(1.0, 200 / n) else 0
+        slots += list(rng.choice([-1, -7, -(1 << 40)], gap))
+        at += take
+    slots = np.array(slots + [-1] * 3000, np.int64)
+    used = -(-n // page)
+    filled = [page] * (used - 1) + [n - (used - 1) * page]
+    for beyond in (False, True):
+        if beyond:
+            free = np.flatnonzero(slots < 0)
+            slots[free[:: 3]] = num_pages * page + rng.integers(0, 1 << 40, len(free[:: 3]))
+        for use in ("update_bounds", "append"):
+            cache = pa.KvCache(num_pages, page, h, 64, torch.bfloat16, bounds=True)
+            cache.data.copy_(torch.randn(cache.data.shape, device="cuda"))
+            cache.bounds.fill_(77)
+            cache.bound_scales.fill_(77)
+            for _ in range(3):
+                if use == "append":
+                    k = torch.randn(len(slots), h, 64, device="cuda").bfloat16()
+                    cache.append(k, k, dev(slots, torch.int64))
+                else:
+                    cache.update_bounds(dev(slots, torch.int64))
+                assert cache.device_status() == (raw.PA_DEV_BAD_INDEX if beyond else 0)
+                check_bounds(cache, ids[:used], filled, ids[used:])
+
+
+@gpu
+def test_bounds_of_slots_out_of_order_are_reported():
+    cache = pa.KvCache(4, 16, 2, 64, torch.float16, bounds=True)
+    for slots, bad in (([3, 4, 5, 16, 17], False), ([4, 3], True), ([4, -1, 3], True), ([4, 4], True),
+                       ([15, 14], True), ([4] + [-1] * 700 + [2], True), ([4] + [-1] * 700 + [18], False),
+                       ([15, 0 + 16, 31, 32], False)):
+        cache.update_bounds(torch.tensor(slots, device="cuda"))
+        assert cache.device_status() == (raw.PA_DEV_BAD_INDEX if bad else 0), slots
