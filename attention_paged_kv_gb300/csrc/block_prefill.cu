@@ -27,8 +27,11 @@
 // 603 us.  256 items are two waves of 152 CTAs for work of 1.7.
 //
 // P is rounded to the values' type (the MMA takes both operands of one type): by
-// at most 2^-11 of each weight in fp16, 2^-8 in bf16.  The running maximum is moved only
-// when it grows by more than 2^8.  A key that a row's mask leaves out is given a
+// at most 2^-8 of each weight in bf16.  In fp16 the reference that is subtracted from the logits
+// is set 7 below the running maximum, as the single tokens' kernel does: a weight is
+// rounded by 2^-11 of it down to 2^-21 of the row's largest, below that by 2^-32 of the largest,
+// and the largest stays below 2^15.  The reference is moved only when the
+// maximum grows by more than 2^8.  A key that a row's mask leaves out is given a
 // weight of exactly 0 by its exponent's addend; a NaN or an infinity of K or V
 // reaches the tokens of its row tiles all the same.
 #include <climits>
@@ -41,6 +44,7 @@ namespace pa {
 namespace {
 
 constexpr float kLn2f = 0.6931471805599453f;
+constexpr float kHead = 7.f;  // fp16: the reference below the maximum
 constexpr int kUnionThreads = 256;
 
 // ---------------------------------------------------------------------------
@@ -430,12 +434,15 @@ __global__ void __launch_bounds__(TileCfg<D, NT>::THREADS, 1)
       most = max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], most), most) * sl2;
       float alpha = 1.f;
       bool resc = false;
-      if (most > m_ref + 8.f) {
+      // (references of 2^20 and more are rounded by more than 2^-4: there they follow each growth)
+      const float rise = Elt<T>::kBf16 ? 8.f : (fabsf(most) < 0x1p20f ? kHead + 8.f : kHead);
+      if (most > m_ref + rise) {
+        const float next = Elt<T>::kBf16 ? most : most - kHead;
         if (m_ref != -INFINITY) {
-          alpha = ex2(m_ref - most);
+          alpha = ex2(m_ref - next);
           resc = true;
         }
-        m_ref = most;
+        m_ref = next;
       }
       const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
       const float2 sc2 = make_float2(sl2, sl2);

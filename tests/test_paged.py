@@ -1167,3 +1167,35 @@ def test_bounds_of_slots_out_of_order_are_reported():
                        ([15, 0 + 16, 31, 32], False)):
         cache.update_bounds(torch.tensor(slots, device="cuda"))
         assert cache.device_status() == (raw.PA_DEV_BAD_INDEX if bad else 0), slots
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("H, kv, page, D", [(5, 9000, 16, 128), (5, 8200, 128, 64), (3, 9000, 32, 256), (1, 9000, 16, 128)])
+def test_chunks_keep_a_long_tail(H, kv, page, D, dtype):
+    """As test_attention_keeps_a_long_tail, for a chunk: the tail's weights are 2^-20.45 of the largest, between two
+    fp16 subnormals (11.7 of them) where the reference is the largest logit itself.
+
+    With the reference 7 below it they are 2^-13.45, rounded by at most 2^-25, which is 2^-11.55 of them; bf16 rounds by
+    2^-8.  Logits, weights and sums add less than 2^-10, the output rounds by half a step."""
+    n, qo, G = -(-kv // page), 600, 16  # (few kv heads: keys cut into parts of their own references)
+    cache = pa.KvCache(n, page, H, D, dtype)
+    k = torch.zeros(kv, H, D, dtype=dtype, device="cuda")
+    v = torch.full((kv, H, D), 16384.0, dtype=dtype, device="cuda")
+    k[kv // 5, :, 0] = 4.0
+    v[kv // 5] = 0.0
+    cache.append(k, v, torch.arange(kv, device="cuda"))
+    q = torch.zeros(qo, G * H, D, dtype=dtype, device="cuda")
+    q[..., 0] = 20.45 * np.log(2) * D ** 0.5 / 4
+    a = pa.BlockAttention(1, qo, G * H, H, D, page, dtype, n, kv)
+    tables = tuple(dev(x) for x in ([0, qo], [0, n], range(n), [kv - (n - 1) * page]))
+    assert qo * H * n * page >= 1 << 20  # a chunk, by the rule of its kernel
+    lists = torch.arange(n, dtype=I32, device="cuda").expand(qo, H, n).contiguous()
+    out, lse = a.run(q, cache, tables, lists)
+    assert a.device_status() == 0
+    logit = float(q[0, 0, 0]) * 4 / D ** 0.5
+    w = torch.arange(kv - qo, kv, device="cuda", dtype=torch.float64).view(-1, 1, 1) * np.exp(-logit)
+    rel = (out.double() / (16384 * w / (1 + w)) - 1).abs().max().item()
+    eps = torch.finfo(dtype).eps / 2
+    assert rel <= (2.0 ** -11.5 if dtype == torch.float16 else eps) + 2.0 ** -10 + eps, rel
+    assert (lse.double() - (logit + torch.log1p(w[..., 0]))).abs().max().item() <= 2.0 ** -17
