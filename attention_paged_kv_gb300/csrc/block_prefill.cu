@@ -30,12 +30,18 @@
 // at most 2^-8 of each weight in bf16.  In fp16 the reference that is subtracted from the logits
 // is set 7 below the running maximum, as the single tokens' kernel does: a weight is
 // rounded by 2^-11 of it down to 2^-21 of the row's largest, below that by 2^-32 of the largest,
-// and the largest stays below 2^15.  The reference is moved only when the
-// maximum grows by more than 2^8.  A key that a row's mask leaves out is given a
-// weight of exactly 0 by its exponent's addend; a NaN or an infinity of K or V
-// reaches the tokens of its row tiles all the same.
+// and the largest stays below 2^15.  The reference is moved only when the maximum
+// grows by more than 2^8.  Over many keys these roundings average out; items with a
+// token of fewer than 128 keys (a prompt's first tokens, short lists) hold P in two terms of the
+// type, side by side in TMEM, and multiply V twice (8 prompts of 300 tokens 84 us, with one
+// term 75; longer requests as with one).
+//
+// A key that a row's mask leaves out is given a weight of exactly 0 by its
+// exponent's addend; a NaN or an infinity of K or V reaches the tokens of its row
+// tiles all the same.
 #include <climits>
 #include <cstring>
+#include <type_traits>
 
 #include "internal.h"
 #include "paged_common.cuh"
@@ -55,6 +61,7 @@ __global__ void __launch_bounds__(kUnionThreads) union_lists_kernel(const BlockP
   extern __shared__ uint32_t words[];
   __shared__ uint32_t bad[8];
   __shared__ int warp_count[2][kUnionThreads / 32];
+  __shared__ int full;  // tokens that see 128 keys or more
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tile = blockIdx.x / p.g.Hkv, h = blockIdx.x % p.g.Hkv;
   pdl_wait();
@@ -71,6 +78,7 @@ __global__ void __launch_bounds__(kUnionThreads) union_lists_kernel(const BlockP
   if (end >= 0 && end / p.g.ps + 1 > p.max_pages && tid == 0) atomicOr(p.status, PA_DEV_NO_ROOM);
   for (int i = tid; i < blocks * W; i += kUnionThreads) words[i] = 0;
   if (tid < 8) bad[tid] = 0;
+  if (tid == 0) full = 0;
   __syncthreads();
   // 32 entries of a list at a time, kBatch such strips of a warp's lists in flight
   constexpr int kUnionWarps = kUnionThreads / 32, kBatch = 8;
@@ -95,7 +103,10 @@ __global__ void __launch_bounds__(kUnionThreads) union_lists_kernel(const BlockP
       if (e[k] >= 0) {
         if (i > 0 && (last < 0 || e[k] <= last)) sound = false;
         if (e[k] >= r.pages) atomicOr(p.status, PA_DEV_BAD_INDEX);
-        if (e[k] <= own && e[k] < blocks) atomicOr(words + e[k] * W + (t >> 5), 1u << (t & 31));
+        if (e[k] <= own && e[k] < blocks) {
+          atomicOr(words + e[k] * W + (t >> 5), 1u << (t & 31));
+          if (i == 128 / p.g.ps) atomicAdd(&full, 1);  // 128 keys in the pages before it
+        }
       }
       if (!__all_sync(0xffffffffu, sound) && lane == 0) {
         atomicOr(bad + (t >> 5), 1u << (t & 31));
@@ -154,7 +165,7 @@ __global__ void __launch_bounds__(kUnionThreads) union_lists_kernel(const BlockP
   __syncthreads();
   if (lane == 0) atomicMin(&diag_s, diag);
   __syncthreads();
-  if (tid == 0) p.items[item] = BlockItem{r.qo_start + q0, tokens, count, diag_s, pos0, r.kv_len, 0, 0};
+  if (tid == 0) p.items[item] = BlockItem{r.qo_start + q0, tokens, count, diag_s, pos0, r.kv_len, full < tokens, 0};
 }
 
 // ---------------------------------------------------------------------------
@@ -211,6 +222,153 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
   const long long t0 = clock64();
   while (!mbar_try_wait(a, parity))
     if (clock64() - t0 > PA_WAIT_LIMIT_CYCLES) break;
+}
+
+// A row tile's softmax over all steps, by a warpgroup (thread = row = TMEM lane): what it works on,
+// and what it leaves.
+struct RowArgs {
+  uint64_t *s_full, *p_full, *full_v;  // s_full and p_full: the row tile's
+  volatile int32_t* abort_flag;
+  int32_t* status;
+  const int2* entries;
+  const uint16_t* masks;  // the row's token's
+  uint8_t* smem;
+  uint32_t s_col, o_col;
+  int steps, count, diag, per, ps_shift, pos, kv_len, tile_tokens, x;
+  float sl2;
+  bool real;
+};
+struct RowState {
+  float m_ref, l_sum;
+  bool ok;
+};
+// kFew: P's second terms behind the first ones.
+template <typename T, int D, int NT, bool kFew>
+__device__ __forceinline__ RowState softmax_rows(const RowArgs& a) {
+  using C = TileCfg<D, NT>;
+  constexpr int NKB = C::NKB, NST = C::NST;
+  const int r = threadIdx.x & 127, lane = threadIdx.x & 31, ps = 1 << a.ps_shift;
+  float m_ref = -INFINITY, l_sum = 0.f;
+  bool ok = true;
+  uint32_t mask = a.real && a.steps > 0 ? a.masks[0] : 0u;
+  for (int j = 0; j < a.steps; ++j) {
+    const uint32_t next = a.real && j + 1 < a.steps ? a.masks[(j + 1) * a.tile_tokens] : 0u;
+    ok = warp_wait(a.s_full, j & 1, a.abort_flag, a.status);
+    if (!ok) break;
+    tc_fence_after();
+    uint32_t s[128];
+    tmem_ld32(a.s_col + 0, *reinterpret_cast<uint32_t(*)[32]>(s + 0));
+    tmem_ld32(a.s_col + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+    tmem_ld32(a.s_col + 64, *reinterpret_cast<uint32_t(*)[32]>(s + 64));
+    tmem_ld32(a.s_col + 96, *reinterpret_cast<uint32_t(*)[32]>(s + 96));
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 128; ++i) asm volatile("" : "+r"(s[i]));
+    if (j >= a.diag || j == a.steps - 1) {
+      // keys behind the row's position, and what no page of the step holds
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const int e = j * a.per + (c * 8 >> a.ps_shift);
+        const bool there = e < a.count && (mask >> c & 1);
+        const int limit = there ? a.pos + 1 - (a.entries[min(e, a.count - 1)].y * ps + (c * 8 & (ps - 1))) : 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i >= limit) s[8 * c + i] = __float_as_uint(-INFINITY);
+      }
+    }
+    float top[16];
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      auto f = [&](int i) { return __uint_as_float(s[8 * c + i]); };
+      const float v = max3(max3(f(0), f(1), f(2)), max3(f(3), f(4), f(5)), fmaxf(f(6), f(7)));
+      top[c] = mask >> c & 1 ? v : -INFINITY;
+    }
+    float most = top[15];
+#pragma unroll
+    for (int c = 0; c < 5; ++c) top[c] = max3(top[3 * c], top[3 * c + 1], top[3 * c + 2]);
+    most = max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], most), most) * a.sl2;
+    float alpha = 1.f;
+    bool resc = false;
+    // (references of 2^20 and more are rounded by more than 2^-4: there they follow each growth)
+    const float rise = Elt<T>::kBf16 ? 8.f : (fabsf(most) < 0x1p20f ? kHead + 8.f : kHead);
+    if (most > m_ref + rise) {
+      const float next = Elt<T>::kBf16 ? most : most - kHead;
+      if (m_ref != -INFINITY) {
+        alpha = ex2(m_ref - next);
+        resc = true;
+      }
+      m_ref = next;
+    }
+    const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+    const float2 sc2 = make_float2(a.sl2, a.sl2);
+    float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t ph[16], pl[16];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float nm = mask >> (4 * c + u) & 1 ? -m_use : -INFINITY;
+        const float2 nm2 = make_float2(nm, nm);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int i = 4 * u + v, k = 32 * c + 2 * i;
+          const float2 t2 = __ffma2_rn(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), sc2, nm2);
+          const float y = ex2(t2.x), z = ex2(t2.y);
+          acc[u & 1] = __fadd2_rn(acc[u & 1], make_float2(y, z));
+          ph[i] = Elt<T>::from_f2(y, z);
+          if constexpr (kFew) {
+            const float2 hi = Elt<T>::to_f2(ph[i]);
+            pl[i] = Elt<T>::from_f2(y - hi.x, z - hi.y);
+          }
+        }
+      }
+      tmem_st16(a.s_col + c * 16, ph);
+      if constexpr (kFew) tmem_st16(a.s_col + 64 + c * 16, pl);
+    }
+    const float2 sum = __fadd2_rn(acc[0], acc[1]);
+    // (P V of the step before is complete: S was issued behind it)
+    if (__any_sync(0xffffffffu, resc)) {
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32(a.o_col + c * 32, o);
+        tmem_wait_ld(o);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+        tmem_st32(a.o_col + c * 32, o);
+      }
+    }
+    // V rows of the last step that hold no key (0 * NaN would reach O)
+    if (a.x == 0 && j == a.steps - 1) {
+      const int last = a.count - 1 - j * a.per;
+      const int valid = last * ps + min(ps, a.kv_len - a.entries[a.count - 1].y * ps);
+      if (valid < 128) {
+        const int st = j % NST;
+        ok = warp_wait(&a.full_v[st], (j / NST) & 1, a.abort_flag, a.status);
+        if (!ok) break;
+        if (r >= valid) {
+          uint8_t* row = a.smem + C::OFF_V + st * C::TILE + r * 128;
+#pragma unroll
+          for (int kb = 0; kb < NKB; ++kb)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(row + kb * C::BLK + c * 16) = make_uint4(0, 0, 0, 0);
+        }
+      }
+    }
+    l_sum = l_sum * alpha + sum.x + sum.y;
+    mask = next;
+    tmem_wait_st();
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(a.p_full);
+  }
+  return RowState{m_ref, l_sum, ok};
+}
+// Not in line: the registers of both loops in one function cost the usual one 2 to 7 %.
+template <typename T, int D, int NT>
+__device__ __noinline__ RowState softmax_rows_of_few(const RowArgs a) {
+  return softmax_rows<T, D, NT, true>(a);
 }
 
 template <typename T, int D, int NT>
@@ -337,11 +495,16 @@ __global__ void __launch_bounds__(TileCfg<D, NT>::THREADS, 1)
         }
         tc_commit(&s_full[x]);
       };
-      auto issue_pv = [&](int x, int j, int st) {
+      auto issue_pv = [&](int x, int j, int st, auto few) {
         const uint64_t vd = dv0 + uint64_t(st) * (C::TILE >> 4);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           tc_mma_ts(tmem + C::O_COL + x * 128, tmem + x * 128 + k * 8, vd + (k * 2048 >> 4), id_o, (j > 0 || k > 0) ? 1u : 0u);
+        if constexpr (decltype(few)::value) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            tc_mma_ts(tmem + C::O_COL + x * 128, tmem + x * 128 + 64 + k * 8, vd + (k * 2048 >> 4), id_o, 1u);
+        }
         if (j == steps - 1) tc_commit(&o_done[x]);
       };
       bool ok = spin_wait(q_full, 0, abort_flag, p.status);
@@ -352,33 +515,37 @@ __global__ void __launch_bounds__(TileCfg<D, NT>::THREADS, 1)
         if (has_b) issue_s(1, 0);
         tc_commit(&empty_k[0]);
       }
-      for (int j = 0; ok && j < steps; ++j) {
-        const int st = j % NST, st1 = (j + 1) % NST;
-        const bool more = j + 1 < steps;
-        ok = spin_wait(&p_full[0], j & 1, abort_flag, p.status);
-        if (ok) ok = spin_wait(&full_v[st], (j / NST) & 1, abort_flag, p.status);
-        if (!ok) break;
-        tc_fence_after();
-        issue_pv(0, j, st);
-        if (more) {
-          ok = spin_wait(&full_k[st1], ((j + 1) / NST) & 1, abort_flag, p.status);
+      auto run = [&](auto few) {
+        for (int j = 0; ok && j < steps; ++j) {
+          const int st = j % NST, st1 = (j + 1) % NST;
+          const bool more = j + 1 < steps;
+          ok = spin_wait(&p_full[0], j & 1, abort_flag, p.status);
+          if (ok) ok = spin_wait(&full_v[st], (j / NST) & 1, abort_flag, p.status);
           if (!ok) break;
           tc_fence_after();
-          issue_s(0, st1);
-          if (!has_b) tc_commit(&empty_k[st1]);
+          issue_pv(0, j, st, few);
+          if (more) {
+            ok = spin_wait(&full_k[st1], ((j + 1) / NST) & 1, abort_flag, p.status);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(0, st1);
+            if (!has_b) tc_commit(&empty_k[st1]);
+          }
+          if (has_b) {
+            ok = spin_wait(&p_full[1], j & 1, abort_flag, p.status);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(1, j, st, few);
+          }
+          tc_commit(&empty_v[st]);
+          if (has_b && more) {
+            issue_s(1, st1);
+            tc_commit(&empty_k[st1]);
+          }
         }
-        if (has_b) {
-          ok = spin_wait(&p_full[1], j & 1, abort_flag, p.status);
-          if (!ok) break;
-          tc_fence_after();
-          issue_pv(1, j, st);
-        }
-        tc_commit(&empty_v[st]);
-        if (has_b && more) {
-          issue_s(1, st1);
-          tc_commit(&empty_k[st1]);
-        }
-      }
+      };
+      if (it.few) run(std::true_type{});
+      else run(std::false_type{});
       tc_commit(fin);
       drain_wait(fin, 0);
     }
@@ -390,119 +557,13 @@ __global__ void __launch_bounds__(TileCfg<D, NT>::THREADS, 1)
     const bool real = t_local < TQ && t < it.tokens;
     const int pos = it.pos + t;
     const uint16_t* masks = p.masks + (item * (p.max_entries / per) + step0) * p.tile_tokens + (real ? t : 0);
-    const float sl2 = p.scale_log2;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + lane_base + x * 128, o_col = tmem + lane_base + C::O_COL + x * 128;
-    float m_ref = -INFINITY, l_sum = 0.f;
-    bool ok = true;
-    uint32_t mask = real && steps > 0 ? masks[0] : 0u;
-    for (int j = 0; j < steps; ++j) {
-      const uint32_t next = real && j + 1 < steps ? masks[(j + 1) * p.tile_tokens] : 0u;
-      ok = warp_wait(&s_full[x], j & 1, abort_flag, p.status);
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t s[128];
-      tmem_ld32(s_col + 0, *reinterpret_cast<uint32_t(*)[32]>(s + 0));
-      tmem_ld32(s_col + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
-      tmem_ld32(s_col + 64, *reinterpret_cast<uint32_t(*)[32]>(s + 64));
-      tmem_ld32(s_col + 96, *reinterpret_cast<uint32_t(*)[32]>(s + 96));
-      tmem_wait_ld();
-#pragma unroll
-      for (int i = 0; i < 128; ++i) asm volatile("" : "+r"(s[i]));
-      if (j >= diag || j == steps - 1) {
-        // keys behind the row's position, and what no page of the step holds
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const int e = j * per + (c * 8 >> p.g.ps_shift);
-          const bool there = e < count && (mask >> c & 1);
-          const int limit = there ? pos + 1 - (entries[min(e, count - 1)].y * p.g.ps + (c * 8 & (p.g.ps - 1))) : 0;
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (i >= limit) s[8 * c + i] = __float_as_uint(-INFINITY);
-        }
-      }
-      float top[16];
-#pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        auto f = [&](int i) { return __uint_as_float(s[8 * c + i]); };
-        const float v = max3(max3(f(0), f(1), f(2)), max3(f(3), f(4), f(5)), fmaxf(f(6), f(7)));
-        top[c] = mask >> c & 1 ? v : -INFINITY;
-      }
-      float most = top[15];
-#pragma unroll
-      for (int c = 0; c < 5; ++c) top[c] = max3(top[3 * c], top[3 * c + 1], top[3 * c + 2]);
-      most = max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], most), most) * sl2;
-      float alpha = 1.f;
-      bool resc = false;
-      // (references of 2^20 and more are rounded by more than 2^-4: there they follow each growth)
-      const float rise = Elt<T>::kBf16 ? 8.f : (fabsf(most) < 0x1p20f ? kHead + 8.f : kHead);
-      if (most > m_ref + rise) {
-        const float next = Elt<T>::kBf16 ? most : most - kHead;
-        if (m_ref != -INFINITY) {
-          alpha = ex2(m_ref - next);
-          resc = true;
-        }
-        m_ref = next;
-      }
-      const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-      const float2 sc2 = make_float2(sl2, sl2);
-      float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t ph[16];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float nm = mask >> (4 * c + u) & 1 ? -m_use : -INFINITY;
-          const float2 nm2 = make_float2(nm, nm);
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const int i = 4 * u + v, k = 32 * c + 2 * i;
-            const float2 t2 = __ffma2_rn(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), sc2, nm2);
-            const float a = ex2(t2.x), e = ex2(t2.y);
-            acc[u & 1] = __fadd2_rn(acc[u & 1], make_float2(a, e));
-            ph[i] = Elt<T>::from_f2(a, e);
-          }
-        }
-        tmem_st16(s_col + c * 16, ph);
-      }
-      const float2 sum = __fadd2_rn(acc[0], acc[1]);
-      // (P V of the step before is complete: S was issued behind it)
-      if (__any_sync(0xffffffffu, resc)) {
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(o_col + c * 32, o);
-          tmem_wait_ld(o);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-          tmem_st32(o_col + c * 32, o);
-        }
-      }
-      // V rows of the last step that hold no key (0 * NaN would reach O)
-      if (x == 0 && j == steps - 1) {
-        const int last = count - 1 - j * per;
-        const int valid = last * p.g.ps + min(p.g.ps, it.kv_len - entries[count - 1].y * p.g.ps);
-        if (valid < 128) {
-          const int st = j % NST;
-          ok = warp_wait(&full_v[st], (j / NST) & 1, abort_flag, p.status);
-          if (!ok) break;
-          if (r >= valid) {
-            uint8_t* row = smem + C::OFF_V + st * C::TILE + r * 128;
-#pragma unroll
-            for (int kb = 0; kb < NKB; ++kb)
-#pragma unroll
-              for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(row + kb * C::BLK + c * 16) = make_uint4(0, 0, 0, 0);
-          }
-        }
-      }
-      l_sum = l_sum * alpha + sum.x + sum.y;
-      mask = next;
-      tmem_wait_st();
-      fence_proxy_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[x]);
-    }
+    const RowArgs args{&s_full[x], &p_full[x], full_v, abort_flag, p.status, entries, masks, smem, s_col, o_col, steps, count,
+                       diag, per, p.g.ps_shift, pos, it.kv_len, p.tile_tokens, x, p.scale_log2, real};
+    const RowState state = it.few ? softmax_rows_of_few<T, D, NT>(args) : softmax_rows<T, D, NT, false>(args);
+    const float m_ref = state.m_ref, l_sum = state.l_sum;
+    bool ok = state.ok;
     if (ok && steps > 0) ok = warp_wait(&o_done[x], 0, abort_flag, p.status);
     pdl_launch();
     if (ok) {

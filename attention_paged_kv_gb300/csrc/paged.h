@@ -62,7 +62,8 @@ struct BlockItem {
   int32_t entries;         // of the union of their lists
   int32_t diag;            // first step of 128 keys with a block that some token sees in part
   int32_t pos, kv_len;     // position of the first token, keys of the request
-  int32_t unused[2];
+  int32_t few;             // some token may see fewer than 128 keys
+  int32_t unused;
 };
 
 struct BlockParams {

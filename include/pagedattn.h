@@ -697,7 +697,8 @@ PAGEDATTN_API pagedattn_status pagedattn_select_blocks(const pagedattn_kv_cache*
  * itself; longer ones, where max_qo_len allows for them and pages have 8 slots or
  * more, those of many tokens together.  There a NaN or an infinity of K or V may reach
  * other tokens of its request and kv head, weights are rounded to the values' type
- * (of bf16 values by up to 2^-8), and logits have to stay below 2^26 in magnitude.
+ * (of bf16 values by up to 2^-8) but for tokens of fewer than 128 keys, and logits have to stay
+ * below 2^26 in magnitude.
  */
 PAGEDATTN_API pagedattn_status pagedattn_blocks_run(const pagedattn_kv_cache* cache, const pagedattn_block_batch* batch,
                                       const int32_t* blocks, const void* q, int64_t q_stride, void* out, float* lse,

@@ -1199,3 +1199,41 @@ def test_chunks_keep_a_long_tail(H, kv, page, D, dtype):
     eps = torch.finfo(dtype).eps / 2
     assert rel <= (2.0 ** -11.5 if dtype == torch.float16 else eps) + 2.0 ** -10 + eps, rel
     assert (lse.double() - (logit + torch.log1p(w[..., 0]))).abs().max().item() <= 2.0 ** -17
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("qo, kv, Hq, Hkv, D, page, layout, blocks, short", [
+    ([600], [600], 8, 1, 128, 16, "NHD", 128, False), ([700, 300], [700, 303], 16, 2, 64, 8, "HND", 130, False),
+    ([500], [500], 4, 1, 256, 32, "NHD", 100, False), ([600], [6000], 8, 1, 128, 16, "NHD", 128, True),
+    ([300], [5000], 12, 3, 64, 128, "HND", 12, True), ([400], [3000], 8, 1, 256, 64, "NHD", 60, True)], ids=str)
+def test_chunks_keep_rows_of_few_keys(qo, kv, Hq, Hkv, D, page, layout, blocks, short, dtype):
+    """Rows of a chunk that see fewer than 128 keys: the weights' rounding does not average out there, and they are held in
+    two terms, 2^-16 of bf16's weights (2^-22 of fp16's, and 2^-25 of the largest where the second is a subnormal).
+
+    The other terms are those of Batch.check.  short: the callers' lists of none to three blocks at far positions, with
+    others of many in the same tiles."""
+    b = Batch(qo, kv, Hq, Hkv, D, page, layout, dtype, seed=5)
+    a = b.attention(blocks)
+    assert sum(qo) * Hkv * blocks * page >= 1 << 20 or short
+    rng = np.random.default_rng(2)
+    lists = np.full((b.T, Hkv, blocks), -1, np.int32)
+    for i, (_, _, _, pos) in enumerate(paged.queries(b.qo_indptr, b.page_indptr, b.last, page)):
+        n = pos // page + 1
+        for h in range(Hkv):
+            count = min(n, blocks) if not short or i % 11 == 3 else int(rng.integers(0, 4))
+            mine = np.sort(rng.permutation(n)[:count])
+            if count and i % 2:
+                mine[-1] = n - 1  # the query's own, in part
+            lists[i, h, :count] = mine
+    ref, ref_lse, sp = b.want(lists)
+    out, lse = a.run(b.q, b.cache, b.tables(), dev(lists))
+    assert a.device_status() == 0
+    b.check(out, lse, (ref, ref_lse, sp))
+    eps = torch.finfo(dtype).eps / 2
+    ds = 2.0 ** -22 * (D / 16 + 2) * sp["s"]
+    rel = 2 * (ds + 2.0 ** -21) + (2.0 ** -22 if dtype == torch.float16 else 2.0 ** -16) + 2.0 ** -23 * (sp["n"] / 16 + 8)
+    bound = (rel[..., None] * sp["av"] + 2.0 ** -25 * sp["v"]) * (1 + eps) + eps * np.abs(ref) + 2.0 ** -25
+    few = sp["n"] < 128
+    err = np.abs(host(out) - ref)
+    assert few.sum() >= 100 * Hkv and (err <= bound)[few].all(), (err / bound)[few].max()
