@@ -343,8 +343,8 @@ __device__ __forceinline__ void select_item(const BlockParams& p, unsigned work,
   int32_t* out = p.blocks + (static_cast<int64_t>(t) * p.g.Hkv + h) * p.num_blocks;
   if (n <= p.num_blocks || n > p.max_pages) {
     if (slice == 0)
-      for (int i = tid; i < p.num_blocks; i += kThreads) out[i] = i < n && n <= p.num_blocks ? i : -1;
-    if (n > p.num_blocks && tid == 0) atomicOr(p.status, PA_DEV_NO_ROOM);
+      for (int i = tid; i < p.num_blocks; i += kThreads) out[i] = i < n && n <= p.max_pages ? i : -1;
+    if (n > p.max_pages && tid == 0) atomicOr(p.status, PA_DEV_NO_ROOM);
     return;
   }
   const int lo = static_cast<int>(static_cast<int64_t>(n) * slice / slices);
@@ -641,8 +641,8 @@ __device__ __forceinline__ void select_tile(const BlockParams& p, int work, uint
     const int pos = pos0 + i, n = pos < 0 ? 0 : (pos >> p.g.ps_shift) + 1;
     int32_t* out = p.blocks + (static_cast<int64_t>(token + i) * p.g.Hkv + h) * p.num_blocks;
     if (n <= p.num_blocks || n > p.max_pages) {
-      for (int c = lane; c < p.num_blocks; c += 32) out[c] = c < n && n <= p.num_blocks ? c : -1;
-      if (n > p.num_blocks && lane == 0) atomicOr(p.status, PA_DEV_NO_ROOM);
+      for (int c = lane; c < p.num_blocks; c += 32) out[c] = c < n && n <= p.max_pages ? c : -1;
+      if (n > p.max_pages && lane == 0) atomicOr(p.status, PA_DEV_NO_ROOM);
     } else {
       // (a strip of 32 keys past n costs little, so few sizes do)
       if (n <= 256) warp_select<8>(kept + i * row, n, p.num_blocks, p.first, p.last, out, sh.bins[warp]);

@@ -1237,3 +1237,22 @@ def test_chunks_keep_rows_of_few_keys(qo, kv, Hq, Hkv, D, page, layout, blocks, 
     few = sp["n"] < 128
     err = np.abs(host(out) - ref)
     assert few.sum() >= 100 * Hkv and (err <= bound)[few].all(), (err / bound)[few].max()
+
+
+@gpu
+@pytest.mark.parametrize("qo, kv", [([1, 2, 1], [200, 330, 100]), ([40, 700], [330, 200 + 700])])
+def test_no_room_although_the_list_has_some(qo, kv):
+    """More pages than the object allows for, but no more than a list holds: no list and no output, as with longer ones."""
+    b = Batch(qo, kv, 4, 2, 64, 16, "NHD", torch.float16, seed=6)
+    a = b.attention(60, 1, 1, max_kv=208)
+    got = a.select(b.q, b.cache, b.tables())
+    assert a.device_status() == raw.PA_DEV_NO_ROOM and a.device_status() == 0
+    want = b.lists(60, 1, 1)
+    over = np.array([pos // 16 + 1 > 13 for _, _, _, pos in paged.queries(b.qo_indptr, b.page_indptr, b.last, 16)])
+    assert over.any() and not over.all()
+    want[over] = -1
+    np.testing.assert_array_equal(got.cpu().numpy(), want)
+    out, lse = a.run(b.q, b.cache, b.tables(), got)
+    assert a.device_status() == raw.PA_DEV_NO_ROOM
+    at = torch.from_numpy(over).cuda()
+    assert not out[at].any() and torch.isneginf(lse[at]).all() and torch.isfinite(lse[~at]).all()
