@@ -252,13 +252,16 @@ __global__ void __launch_bounds__(1024) order_requests_kernel(const BlockParams 
   __syncthreads();
   pdl_launch();  // (the next kernel's CTAs may take their places)
   pdl_wait();
+  // (tokens and tiles are fewer than 2^30: limited to that, the sum of two counts fits 32 bits,
+  // of requests that overlap too, in tables that cannot be)
+  constexpr int kMost = (1 << 30) - 1;
   int mine = 0;
   for (int b = tid; b < p.batch; b += 1024) {
     const int n = load_span(p, b, true).qo_len;
-    if (n >= p.long_tokens) mine = min(mine + n, 1 << 30);
+    if (n >= p.long_tokens) mine = min(mine + n, kMost);
   }
 #pragma unroll
-  for (int d = 16; d; d >>= 1) mine = min(mine + __shfl_xor_sync(0xffffffffu, mine, d), 1 << 30);
+  for (int d = 16; d; d >>= 1) mine = min(mine + __shfl_xor_sync(0xffffffffu, mine, d), kMost);
   if (lane == 0 && mine) atomicAdd(reinterpret_cast<unsigned long long*>(&long_s), static_cast<unsigned long long>(mine));
   __syncthreads();
   const int long_tokens = long_s < p.least_long ? INT_MAX : p.long_tokens;
@@ -276,18 +279,18 @@ __global__ void __launch_bounds__(1024) order_requests_kernel(const BlockParams 
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int a = __shfl_up_sync(0xffffffffu, t, d), c = __shfl_up_sync(0xffffffffu, s, d);
-      if (lane >= d) t += a, s += c;
+      if (lane >= d) t = min(t + a, p.max_tiles), s = min(s + c, p.num_tokens);
     }
     __syncthreads();
     if (lane == 31) sums[0][warp] = t, sums[1][warp] = s;
     __syncthreads();
     int all_t = 0, all_s = 0;
+    // (requests that overlap may have more tiles than there is room for: what is past
+    // it is left out)
     for (int w = 0; w < 32; ++w) {
-      if (w < warp) t += sums[0][w], s += sums[1][w];
-      all_t += sums[0][w], all_s += sums[1][w];
+      if (w < warp) t = min(t + sums[0][w], p.max_tiles), s = min(s + sums[1][w], p.num_tokens);
+      all_t = min(all_t + sums[0][w], p.max_tiles), all_s = min(all_s + sums[1][w], p.num_tokens);
     }
-    // (requests that overlap, in tables that cannot be, may have more tiles than
-    // there is room for: what is past it is left out)
     if (b < p.batch) {
       p.tile_indptr[b + 1] = min(base_t + t, p.max_tiles);
       p.small_indptr[b + 1] = min(base_s + s, p.num_tokens);

@@ -1256,3 +1256,25 @@ def test_no_room_although_the_list_has_some(qo, kv):
     assert a.device_status() == raw.PA_DEV_NO_ROOM
     at = torch.from_numpy(over).cuda()
     assert not out[at].any() and torch.isneginf(lse[at]).all() and torch.isfinite(lse[~at]).all()
+
+
+@gpu
+def test_overlapping_requests_of_many_tokens():
+    """A qo_indptr that goes back and forth over 2^27 tokens 512 times: its tiles alone would pass 2^32."""
+    n, B = 1 << 27, 1024
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB")
+    cache = pa.KvCache(4, 16, 1, 64, torch.float16, bounds=True)
+    a = pa.BlockAttention(B, n, 1, 1, 64, 16, torch.float16, 1, 64, 0, 1, max_qo_len=n)
+    qo = torch.tensor([0, n] * (B // 2) + [0], dtype=I32, device="cuda")
+    # every request has 4 pages of its own: a long one's last token is at position 63
+    tables = (qo, 4 * torch.arange(B + 1, dtype=I32, device="cuda"), torch.arange(4, dtype=I32, device="cuda").repeat(B),
+              torch.full((B,), 16, dtype=I32, device="cuda"))
+    q = torch.zeros(n, 1, 64, dtype=torch.float16, device="cuda")
+    out = torch.full((n, 1, 1), 7, dtype=I32, device="cuda")
+    a.select(q, cache, tables, out=out)
+    assert a.device_status() == raw.PA_DEV_BAD_INDEX
+    # the first request's tokens are there: only the last 64 see a key, each its own block
+    want = torch.full((n,), -1, dtype=I32, device="cuda")
+    want[-64:] = torch.arange(64, device="cuda", dtype=I32) // 16
+    assert torch.equal(out.view(-1), want)
