@@ -18,7 +18,9 @@ as with the objects of the 4-bit cache.  ``cache.data`` is laid out as
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import struct
 
 from . import _binding as _b
@@ -39,6 +41,32 @@ def _turns(w):
     a, b = n * (_TWO_PI[1] << 64), d * _TWO_PI[0]
     t = (2 * a + b) // (2 * b) & ((1 << 64) - 1)
     return t - (1 << 64) if t >> 63 else t
+
+
+@functools.lru_cache(None)
+def _recorded():
+    """Rope.apply as a function of autograd: the gradient of a rotation is the rotation by the negative angle."""
+    import torch
+
+    class Turn(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, rope, q, k, positions, inverse):
+            ctx.rope, ctx.inverse = rope, inverse
+            ctx.save_for_backward(positions)
+            ctx.set_materialize_grads(False)
+            return rope.apply(q, k, positions, inverse=inverse)
+
+        @staticmethod
+        def backward(ctx, dq, dk):
+            # a gradient may be missing, or not laid out as rows (that of a sum is one value, expanded)
+            dq, dk = (None if d is None else d.contiguous() for d in (dq, dk))
+            if dq is None and dk is not None:
+                dk, _ = ctx.rope.apply(dk, None, *ctx.saved_tensors, inverse=not ctx.inverse)
+            elif dq is not None:
+                dq, dk = ctx.rope.apply(dq, dk, *ctx.saved_tensors, inverse=not ctx.inverse)
+            return None, dq, dk, None, None
+
+    return Turn
 
 
 class Rope(_Object):
@@ -93,7 +121,10 @@ class Rope(_Object):
         multiple of 8; head_dim a multiple of 16 up to 256.  q_out and k_out
         (allocated where not given) may be q and k themselves.  inverse: by the
         negative angle, as gradients pass through the rotation (with scale 1, the
-        rotation back).  See pagedattn_rope.
+        rotation back).  Autograd records the call where q or k needs a gradient
+        and no outputs are given (positions are copied for it); outputs that are
+        given carry none, nor do the results of the other calls here.  See
+        pagedattn_rope.
         """
         import torch
         at = self._index
@@ -116,6 +147,10 @@ class Rope(_Object):
         code = _b.PA_BF16 if q.dtype == torch.bfloat16 else _b.dtype_code(q.dtype)
         pos, pos_stride = self._positions(positions, n, at)
         handle, guard = _on(at, stream, (self,), (q, k, positions, q_out, k_out))
+        if q_out is None and k_out is None and torch.is_grad_enabled() and \
+                (q.requires_grad or (k is not None and k.requires_grad)):
+            with guard or contextlib.nullcontext():
+                return _recorded().apply(self, q, k, positions.clone(), inverse)
         if guard is not None:
             with guard:  # the outputs are allocated on the stream that writes them
                 return self._launch(q, k, size, k_heads, q_stride, k_stride, q_out, k_out, pos, pos_stride, inverse,

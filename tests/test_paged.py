@@ -1278,3 +1278,112 @@ def test_overlapping_requests_of_many_tokens():
     want = torch.full((n,), -1, dtype=I32, device="cuda")
     want[-64:] = torch.arange(64, device="cuda", dtype=I32) // 16
     assert torch.equal(out.view(-1), want)
+
+
+# ---------------------------------------------------------------- the rotation under autograd
+
+
+def oracle_gradient(y, positions, w, interleaved, inverse, dtype, scale=1.0):
+    """The gradient of sum(y * rope(x)) in x, and check_rotated's size of it."""
+    return paged.rope(host(y), positions, w, None, interleaved, scale, inverse=not inverse)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("interleaved, inverse, scale, needs", [
+    (False, False, 1.0, "qk"), (True, False, 1.5, "q"), (False, True, 0.75, "k"), (True, True, 1.0, "qk")])
+def test_rope_is_recorded_by_autograd(interleaved, inverse, scale, needs, dtype):
+    """backward() gives the formula's gradient, of q, k or both, as slices of a projection that is the leaf."""
+    rng = np.random.default_rng(4)
+    n, H, h, d = 37, 4, 2, 96
+    w = frequencies(40)
+    r = pa.Rope(w, interleaved=interleaved, scale=scale)
+    positions = rng.integers(0, 9000, (1, n))
+    pos = dev(positions[0])
+    leaf = torch.from_numpy(rng.standard_normal((n, (H + h) * d))).to(dtype).cuda().requires_grad_()
+    q, k = leaf[:, : H * d].view(n, H, d), leaf[:, H * d:].view(n, h, d)
+    q, k = q if "q" in needs else q.detach(), k if "k" in needs else k.detach()
+    a, b = r.apply(q, k, pos, inverse=inverse)
+    with torch.no_grad():
+        plain = r.apply(q, k, pos, inverse=inverse)
+    assert plain[0].grad_fn is None and torch.equal(a, plain[0]) and torch.equal(b, plain[1])
+    pos.fill_(7)  # the next step's: the backward pass has those of its own
+    y, z = (torch.from_numpy(rng.standard_normal(t.shape)).to(dtype).cuda() for t in (a, b))
+    torch.autograd.backward([a, b], [y, z])
+    got = leaf.grad.view(n, H + h, d)
+    for part, g, need in ((got[:, :H], y, "q"), (got[:, H:], z, "k")):
+        if need in needs:
+            check_rotated(part, *oracle_gradient(g, positions, w, interleaved, inverse, dtype, scale), dtype)
+        else:
+            assert not part.any()
+
+
+@gpu
+def test_rope_gradients_of_unusual_calls():
+    """One value expanded, a part of the results used, no k, given outputs, a given stream, the gradient's gradient, and
+    differences: a rotation is linear, so a step along e changes the sum by the gradient's product with e."""
+    rng = np.random.default_rng(5)
+    n, d = 20, 64
+    w, positions = frequencies(32), rng.integers(0, 500, (1, n))
+    r, pos = pa.Rope(w), dev(positions[0])
+    x = torch.from_numpy(rng.standard_normal((n, 3, d))).half().cuda().requires_grad_()
+    ones = torch.ones_like(x)
+    out, none = r.apply(x, None, pos)
+    assert none is None
+    out.sum().backward()
+    check_rotated(x.grad, *oracle_gradient(ones, positions, w, False, False, x.dtype), x.dtype)
+    a, b = r.apply(x, x, pos)
+    only_b, = torch.autograd.grad(b, x, ones, retain_graph=True)
+    both, = torch.autograd.grad([a, b], x, [ones, ones])
+    assert torch.equal(only_b, x.grad) and torch.equal(both, x.grad + x.grad)
+    given = torch.empty_like(x)
+    assert r.apply(x, None, pos, q_out=given)[0] is given and not given.requires_grad
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    far, _ = r.apply(x, None, pos, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    there, = torch.autograd.grad(far, x, ones)
+    torch.cuda.synchronize()
+    assert torch.equal(there, x.grad)
+    # y -> gradient in x is a rotation of y: its own gradient along v is rope(v)
+    y = ones.clone().requires_grad_()
+    g, = torch.autograd.grad(r.apply(x, None, pos)[0], x, y, create_graph=True)
+    v = torch.from_numpy(rng.standard_normal((n, 3, d))).half().cuda()
+    gg, = torch.autograd.grad(g, y, v)
+    assert torch.equal(gg, r.apply(v, None, pos)[0])
+    # differences, of values whose sums are exact in fp16: each result is half a step off, and 2^-20 of its pairs as of check_rotated
+    x0, e = (torch.from_numpy(rng.integers(-64, 65, (n, 3, d)) / 32).half().cuda() for _ in range(2))
+    here, moved = (host(r.apply(t, None, pos)[0]) for t in (x0, x0 + e))
+    bound = 2.0 ** -11 * (np.abs(here).sum() + np.abs(moved).sum() + (np.abs(host(x.grad)) * np.abs(host(e))).sum()) + \
+        2.0 ** -20 * 2 * (np.abs(host(x0)).sum() + np.abs(host(x0 + e)).sum() + np.abs(host(e)).sum())
+    assert abs((moved - here).sum() - (host(x.grad) * host(e)).sum()) <= bound
+
+
+@gpu
+def test_rope_with_its_gradient_in_a_graph():
+    n, d = 33, 128
+    r, pos = pa.Rope(frequencies(64)), torch.arange(n, dtype=I32, device="cuda")
+    x, y = (torch.randn(n, 2, d, device="cuda").half() for _ in range(2))
+    x.requires_grad_()
+
+    def step():
+        out, _ = r.apply(x, None, pos)
+        return out, torch.autograd.grad(out, x, y)[0]
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out, grad = step()
+    for gain in (1.0, -2.0):
+        with torch.no_grad():
+            x.mul_(gain)
+            y.mul_(gain)
+        pos.add_(5)
+        g.replay()
+        torch.cuda.synchronize()
+        with torch.no_grad():
+            assert torch.equal(out, r.apply(x, None, pos)[0]) and torch.equal(grad, r.apply(y, None, pos, inverse=True)[0])
