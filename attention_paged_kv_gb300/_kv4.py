@@ -128,6 +128,8 @@ class _Object:
         word too) or a tensor, which is cleared.  To be called with the object's device current."""
         import torch
         shared = workspace if isinstance(workspace, kind) else None
+        if shared is None and isinstance(workspace, _Object):
+            _refuse("the workspace of an object of another class cannot be shared")
         given = workspace is not None
         if shared is not None:
             workspace = shared.workspace

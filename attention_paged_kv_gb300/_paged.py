@@ -316,8 +316,6 @@ class BlockAttention(_Object):
     def __init__(self, batch_size, num_tokens, num_qo_heads, num_kv_heads, head_dim, page_size, dtype, num_blocks,
                  max_kv_len, first=1, last=1, max_qo_len=None, workspace=None, device=None):
         import torch
-        if isinstance(workspace, _Object) and not isinstance(workspace, BlockAttention):
-            _refuse("the workspace of an object of another class cannot be shared")
         self.batch_size, self.num_tokens = int(batch_size), int(num_tokens)
         self.num_qo_heads, self.num_kv_heads = int(num_qo_heads), int(num_kv_heads)
         self.head_dim, self.page_size = int(head_dim), int(page_size)

@@ -676,7 +676,8 @@ PAGEDATTN_API pagedattn_status pagedattn_blocks_workspace_size(int32_t num_kv_he
  *           elements apart (a multiple of 8), 16-byte aligned.
  * workspace device, 256-byte aligned, pagedattn_blocks_workspace_size() bytes: zero it once.
  *           Its first word is the status word.  Calls that overlap on the device need
- *           different workspaces; one after the other they may share one.
+ *           different workspaces; one after the other they may share one, of any sizes of
+ *           this call and the next, but not with pagedattn_kv4_run.
  */
 PAGEDATTN_API pagedattn_status pagedattn_select_blocks(const pagedattn_kv_cache* cache, const pagedattn_block_batch* batch,
                                          const void* q, int64_t q_stride, int32_t* blocks, void* workspace,

@@ -1387,3 +1387,19 @@ def test_rope_with_its_gradient_in_a_graph():
         torch.cuda.synchronize()
         with torch.no_grad():
             assert torch.equal(out, r.apply(x, None, pos)[0]) and torch.equal(grad, r.apply(y, None, pos, inverse=True)[0])
+
+
+@gpu
+def test_workspaces_are_shared_within_a_class():
+    kv4 = pa.Kv4Attention(1, 1, 2, 1, 64, 16, torch.float16)
+    block = pa.BlockAttention(1, 1, 2, 1, 64, 16, torch.float16, 4, 100)
+    cache = pa.KvCache(2, 16, 1, 64, torch.float16)
+    for make in (lambda w: pa.Kv4Attention(1, 1, 2, 1, 64, 16, torch.float16, workspace=w),
+                 lambda w: pa.BlockAttention(1, 1, 2, 1, 64, 16, torch.float16, 4, 100, workspace=w)):
+        refusals = 0
+        for w in (kv4, block, cache):
+            try:
+                make(w)
+            except pa.PagedAttnError as e:
+                refusals += "another class" in str(e)
+        assert refusals == 2
