@@ -677,12 +677,17 @@ TileShape tile_shape(const BlockShape& s) {
   t.rows = (s.D == 256 ? 1 : 2) * 128;
   // A million keys of single tokens and kv heads: 64 tokens of 2048 keys at 8 kv
   // heads take 47 us in tiles (32 where their lists are alike) and 46 by
-  // themselves, 32 tokens 43 (32) and 24, 128 tokens 63 (37) and 91.
+  // themselves, 32 tokens 43 (32) and 24, 128 tokens 63 (37) and 91.  That is behind 8000
+  // keys.  The union grows with the keys, which the rule leaves out: 1000 tokens behind 32000,
+  // 64000 and 128000 take 764, 1113 and 1385 us in tiles and 643, 798 and 958 by themselves where
+  // lists are by chance; by the selection, of keys around a centre of their page, 494, 652 and 825 against 621,
+  // 630 and 653; alike 90, 93 and 101 against 600.
   t.least_long = int32_t((1 << 20) / (int64_t(s.Hkv) * s.num_blocks * s.page_size) + 1);
   const int words = (t.tokens + 31) / 32;
   t.union_smem = int64_t(s.max_pages) * (words + 1) * 4;
   // pages of 8 slots or more (a TMA copy's rows keep the swizzle's period of 8),
-  // and unions that shared memory holds
+  // and unions that shared memory holds (1000 tokens of 8 / 8 heads, 5688 pages and room for one
+  // more: behind 32000 keys, by chance, 321 us and by themselves 622; behind 90000, by the selection, 707 and 780)
   t.use = s.max_qo_len >= t.long_tokens && s.num_tokens >= t.least_long && s.page_size >= 8 && t.union_smem <= 200 * 1024;
   if (!t.use) {
     t.max_tiles = t.max_entries = 0;

@@ -7,7 +7,7 @@
 // with f the pair's turns a position as a 64-bit fraction of a turn: x * f
 // modulo 2^64 is exact in integers, so a position of 10^6 has as good an angle
 // as one of 10, where a product in fp32 would be off by 0.1 rad; its top 32
-// bits go to sincospi.  Angles cost no table and no loads but the position.
+// bits go to sincospi, in fp32 (off by 2^-26 turns).  Angles cost no table and no loads but the position.
 //
 // Bytes bound it (2 read and 2 written a value).  A thread takes 8 pairs of one
 // token, two 16-byte pieces of a head, and goes through the heads of a group
@@ -17,7 +17,7 @@
 // CTAs of 256 threads 104, 42.2 and 2.8.
 //
 // Bounds: a page's keys are read once, D / 8 lanes a row.  8 prompts of 1001 to
-// 4000 tokens (39 MB) 11 us: slots, then two rounds of 16 rows, each a memory
+// 4000 tokens (39 MB) 9.9 us: slots, then two rounds of 16 rows, each a memory
 // latency; 256 decodes 2.8.  16 loads in flight in the place of 8 did not help
 // (11.7 and 3.2).
 #include <cstring>
@@ -342,7 +342,7 @@ cudaError_t launch_rows(RowsParams p, int parts, bool interleaved, int dtype, in
 
 cudaError_t launch_bounds(BoundsParams p, int D, int dtype, int num_sms, cudaStream_t stream) {
   // A warp a token where there are few (each may end a page: 256 decodes 2.8 us,
-  // 31 with 32 tokens a warp), up to 32 where most do not (8 prompts 11 us, 22
+  // 31 with 32 tokens a warp), up to 32 where most do not (8 prompts 10 us, 22
   // with one).
   p.warp_tokens = 1;
   while (p.warp_tokens < 32 && int64_t(p.n) * p.g.Hkv > int64_t(num_sms) * 32 * p.warp_tokens) p.warp_tokens *= 2;

@@ -711,7 +711,9 @@ SelectShape select_shape(const BlockShape& s) {
   t.tokens = kTileRows;
   // More keys than two CTAs an SM keep go to global memory, that is, to L2: 2000 tokens
   // at 8 kv heads take 199 us for 1500 pages with keys in shared memory and 210 so,
-  // for 2000 pages (one CTA an SM) 396 and 275.
+  // for 2000 pages (one CTA an SM) 396 and 275.  Beyond kKeptKeys pages tokens select by
+  // themselves: the CTAs' keys would pass 160 MB (2000 tokens over all of 8192 pages 1876 us, with
+  // room for one page more 2906; over 2000 of them 284 and 869).
   t.ctas = int64_t(kTileRows) * t.row * 4 > kTileSmem ? s.num_sms * (s.D == 256 ? 1 : 2) : 0;
   t.long_tokens = 4;
   // Fewer than the single tokens' CTAs of a full card are quicker there: of 500 pages

@@ -531,8 +531,9 @@ PAGEDATTN_API pagedattn_status pagedattn_kv4_run(const pagedattn_kv4_cache* cach
  * 2 i + 1.  Pair i = (a, b) at position x becomes
  *   (a cos - b sin, b cos + a sin) * scale,  angle = 2 pi * x * turns[i] / 2^64
  * in fp32, rounded once; values behind the pairs stay as they are.  turns[i] is
- * the pair's turns a position modulo 1, as a 64-bit fraction, so that the
- * angle of any position is exact to 2^-33 turns before its cosine is taken.
+ * the pair's turns a position modulo 1, as a 64-bit fraction: the product modulo 2^64 is
+ * exact, and its cosine is taken of the fraction in fp32, off by less than 2^-25 turns at any
+ * position.
  */
 typedef struct {
   const uint64_t* turns; /* device, [rotary_dim / 2], 8-byte aligned                             */
@@ -573,8 +574,8 @@ PAGEDATTN_API pagedattn_status pagedattn_rope(const pagedattn_rotation* rotation
  *   bound_scales  [num_pages][num_kv_heads] what code 1 stands for
  * With a the largest magnitude over the page's keys and channels, and f = 127 * (1 / a):
  * the scale is a * (1 / 127) and the codes min(127, ceil(x * f)) of the largest x and
- * max(-127, floor(x * f)) of the smallest, each step rounded to fp32: they
- * enclose the keys.  (a below 2^-100 counts as 0: scale and codes 0.  Where a
+ * max(-127, floor(x * f)) of the smallest, each step rounded to fp32: but for these
+ * roundings they enclose the keys (127 * scale may lie 2^-23 of it below a).  (a below 2^-100 counts as 0: scale and codes 0.  Where a
  * key is NaN or infinite the scale is infinite and the codes 127 and -127.)
  */
 typedef struct {
@@ -663,7 +664,8 @@ PAGEDATTN_API pagedattn_status pagedattn_blocks_workspace_size(int32_t num_kv_he
  *       lies in [2^14, 2^15); u, l = the sums over the heads of max(x, 0) and min(x, 0)
  *   codes c = rint((u, l) * (127 * (1 / max(|u|, |l|))))      (each step in fp32; 0 where all are 0)
  *   score = scale of the block * sum over channels of (c_u * largest + c_l * smallest)
- * The sums are of whole numbers, so a score has the same bits in any batch.
+ * The sums are of whole numbers, so a score has the same bits in any batch.  (Requests of many
+ * tokens are scored in tiles of 16 tokens where max_pages is at most 8192, else token by token.)
  * A NaN of the product (0 times an infinite scale) counts as infinity; a group
  * with a NaN or infinity in q has codes of 0.
  *
@@ -695,11 +697,12 @@ PAGEDATTN_API pagedattn_status pagedattn_select_blocks(const pagedattn_kv_cache*
  * qo_indptr[batch_size] on are neither read nor written.  out must not overlap q.
  *
  * Requests of few tokens (up to 32 packed rows) read the keys of each token by
- * itself; longer ones, where max_qo_len allows for them and pages have 8 slots or
- * more, those of many tokens together.  There a NaN or an infinity of K or V may reach
- * other tokens of its request and kv head, weights are rounded to the values' type
- * (of bf16 values by up to 2^-8) but for tokens of fewer than 128 keys, and logits have to stay
- * below 2^26 in magnitude.
+ * itself; there an infinity of a bf16 V gives NaN.  Longer ones read those of many tokens together,
+ * where max_qo_len allows for them, pages have 8 slots or more and max_pages is at most 51200 /
+ * (1 + W), with W the number of 32s, rounded up, in 256 / (heads of a group) tokens (half as many at
+ * head_dim 256).  There a NaN or an infinity of K or V may reach other tokens of its request and
+ * kv head, weights are rounded to the values' type (of bf16 values by up to 2^-8) but for
+ * tokens of fewer than 128 keys, and logits have to stay below 2^26 in magnitude.
  */
 PAGEDATTN_API pagedattn_status pagedattn_blocks_run(const pagedattn_kv_cache* cache, const pagedattn_block_batch* batch,
                                       const int32_t* blocks, const void* q, int64_t q_stride, void* out, float* lse,
