@@ -89,6 +89,15 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// A weight as two bf16 terms: the first cut towards zero, the second what is left, never
+// below 2^-100 of a weight above that: an infinity of V times terms of one sign, none
+// of them zero, stays one.
+__device__ __forceinline__ uint32_t first_terms(float a, float b) {
+  uint32_t r;
+  asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ float second_term(float x, float first) { return fmaxf(x - first, fminf(x, 0x1p-100f)); }
 template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // Row `row` of a state: its four columns from `col` on as 16-bit values.
@@ -398,11 +407,13 @@ __device__ __forceinline__ void attend_item(const BlockParams& p, unsigned work,
         l[n][1] += x[1] + x[3];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint32_t both = Elt<T>::from_f2(x[2 * i], x[2 * i + 1]);
-          b[n][i] = movmatrix(both);
           if constexpr (Elt<T>::kBf16) {
+            const uint32_t both = first_terms(x[2 * i], x[2 * i + 1]);
             const float2 r = Elt<T>::to_f2(both);
-            b_low[n][i] = movmatrix(Elt<T>::from_f2(x[2 * i] - r.x, x[2 * i + 1] - r.y));
+            b[n][i] = movmatrix(both);
+            b_low[n][i] = movmatrix(Elt<T>::from_f2(second_term(x[2 * i], r.x), second_term(x[2 * i + 1], r.y)));
+          } else {
+            b[n][i] = movmatrix(Elt<T>::from_f2(x[2 * i], x[2 * i + 1]));
           }
         }
       }

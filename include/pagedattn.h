@@ -697,8 +697,7 @@ PAGEDATTN_API pagedattn_status pagedattn_select_blocks(const pagedattn_kv_cache*
  * qo_indptr[batch_size] on are neither read nor written.  out must not overlap q.
  *
  * Requests of few tokens (up to 32 packed rows) read the keys of each token by
- * itself; there an infinity of a bf16 V gives NaN.  Longer ones read those of many tokens together,
- * where max_qo_len allows for them, pages have 8 slots or more and max_pages is at most 51200 /
+ * itself.  Longer ones read those of many tokens together, where max_qo_len allows for them, pages have 8 slots or more and max_pages is at most 51200 /
  * (1 + W), with W the number of 32s, rounded up, in 256 / (heads of a group) tokens (half as many at
  * head_dim 256).  There a NaN or an infinity of K or V may reach other tokens of its request and
  * kv head, weights are rounded to the values' type (of bf16 values by up to 2^-8) but for

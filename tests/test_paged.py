@@ -1403,3 +1403,25 @@ def test_workspaces_are_shared_within_a_class():
             except pa.PagedAttnError as e:
                 refusals += "another class" in str(e)
         assert refusals == 2
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("qo, kv, D, page, blocks", [
+    ([1, 2, 1], [100, 100, 100], 128, 16, 7), ([1, 1], [5000, 300], 64, 32, 160), ([1], [900], 256, 4, 225)], ids=str)
+def test_attention_of_an_infinite_value(qo, kv, D, page, blocks, dtype):
+    """An infinity of V, of either sign, is the result of its channel in the rows of its kv head that see it, and of none
+    else: their weights are positive, however they are held."""
+    b = Batch(qo, kv, 8, 2, D, page, "NHD", dtype, seed=2)
+    a = b.attention(blocks)
+    lists = a.select(b.q, b.cache, b.tables())
+    clean, clean_lse = a.run(b.q, b.cache, b.tables(), lists)
+    assert torch.isfinite(clean).all()
+    at = kv[0] // 3  # a key of the first request
+    page_id, slot = int(b.pages[at // page]), at % page
+    b.cache.data[page_id, 1, slot, 1, 9] = float("inf")
+    b.cache.data[page_id, 1, slot, 1, 40] = -float("inf")
+    out, lse = a.run(b.q, b.cache, b.tables(), lists)
+    want = clean.clone()
+    want[0, 4:, 9], want[0, 4:, 40] = float("inf"), -float("inf")
+    assert torch.equal(out, want) and torch.equal(lse, clean_lse)
