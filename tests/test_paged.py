@@ -1425,3 +1425,25 @@ def test_attention_of_an_infinite_value(qo, kv, D, page, blocks, dtype):
     want = clean.clone()
     want[0, 4:, 9], want[0, 4:, 40] = float("inf"), -float("inf")
     assert torch.equal(out, want) and torch.equal(lse, clean_lse)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("D, page, heads", [(128, 16, 8), (64, 32, 32), (256, 4, 4)], ids=str)
+def test_single_tokens_hold_weights_in_two_terms(D, page, heads, dtype):
+    """Batch.check's bound with the weights' rounding by two terms, the first cut: 2^-21 of fp16's (and 2^-24 where the second
+    is a subnormal, 2^-31 of the largest, which is 2^7 or more), 2^-15 of bf16's.  Requests of 1 to 120 keys, where one
+    term's roundings do not average out."""
+    kv = list(range(1, 121))
+    b = Batch([1] * len(kv), kv, heads, 2, D, page, "NHD", dtype, seed=3, q_gain=0.3)
+    blocks = -(-kv[-1] // page)
+    a = b.attention(blocks)
+    lists = a.select(b.q, b.cache, b.tables())
+    ref, ref_lse, sp = b.want(lists.cpu().numpy())
+    out, lse = a.run(b.q, b.cache, b.tables(), lists)
+    eps = torch.finfo(dtype).eps / 2
+    ds = 2.0 ** -22 * (D / 16 + 2) * sp["s"]
+    rel = 2 * (ds + 2.0 ** -21) + (2.0 ** -21 if dtype == torch.float16 else 2.0 ** -15) + 2.0 ** -23 * (sp["n"] / 16 + 8)
+    bound = (rel[..., None] * sp["av"] + 2.0 ** -31 * sp["v"]) * (1 + eps) + eps * np.abs(ref) + 2.0 ** -25
+    err = np.abs(host(out) - ref)
+    assert (err <= bound).all(), (err / bound).max()
