@@ -123,8 +123,9 @@ class Rope(_Object):
         negative angle, as gradients pass through the rotation (with scale 1, the
         rotation back).  Autograd records the call where q or k needs a gradient
         and no outputs are given (positions are copied for it); outputs that are
-        given carry none, nor do the results of the other calls here.  See
-        pagedattn_rope.
+        given carry none, nor do the results of the other calls here.  A backward
+        pass is captured into a graph with torch.autograd.grad, or with leaves
+        that no eager graph still holds.  See pagedattn_rope.
         """
         import torch
         at = self._index
